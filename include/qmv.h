@@ -415,6 +415,242 @@ int moe_qmv_run_static(const qmv_desc* gateup_desc, const qmv_desc* down_desc, c
                        const void* x_bf16, int M, int64_t ldx, float* y, int64_t ldy, void* stream);
 
 /*
+ * The attention side of a decode step: a paged KV cache in 8 bits. Weights are
+ * one of the two streams that a decode step reads; the other is the cache of
+ * keys and values of every earlier token, which grows with the context and the
+ * number of requests. The calls below keep that cache in one byte per value and
+ * serve a step from the fused qkv matvec's output to the input of the o matvec:
+ *
+ *   kv_plan      once per step: pages, slots and positions of the new tokens
+ *   kv8_append   per layer: rotate q and k, write k and v into the cache
+ *   kv8_attend   per layer: attention of the new tokens over the cache
+ *
+ * with rope_run (the rotation alone) and kv8_read (values back out of the
+ * cache) beside them.
+ *
+ * A page holds QMV_KV_PAGE consecutive tokens of one request. A request's row
+ * of the block table names its pages in order; a slot is page * QMV_KV_PAGE +
+ * offset. Per page and KV head there is one fp32 scale for K and one for V.
+ * Index arrays (int32) need only their natural alignment.
+ */
+#define QMV_KV_PAGE 64
+#define QMV_KV_MAX_REQUESTS 8192
+#define QMV_ROPE_MAX_PAIRS 128
+#define QMV_ROPE_MAX_AXES 4
+
+typedef enum {
+  QMV_KV_INT8 = 1,           /* code q in -127..127 stored as the byte q + 128; value q * scale */
+  QMV_KV_E4M3 = 2            /* e4m3 bits (never NaN); value e4m3 * scale */
+} qmv_kv_type;
+
+typedef enum { QMV_F32 = 1, QMV_BF16 = 2, QMV_F16 = 3 } qmv_dtype;
+
+/*
+ * Layout of one layer's cache, a buffer of two sections:
+ *   0 codes : per (page, head) a K tile, then a V tile, of 64 x D bytes each, in
+ *             the order in which the tensor-core fragments of kv8_attend take
+ *             them. V tile: byte d * 64 + token (transposed). K tile: the byte
+ *             of (token, d) is at ((((token % 16) / 2) * (D / 64) + d / 64) * 8
+ *             + (token / 16) * 2 + token % 2) * 64 + d % 64.
+ *   1 scales: fp32 [page][head][2], K then V.
+ * Nothing has to be initialised: a page's scale is set when its first slot is
+ * written, and slots past a request's length are never used.
+ */
+typedef struct {
+  uint32_t abi_version;      /* QMV_ABI_VERSION */
+  uint32_t type;             /* qmv_kv_type */
+  int32_t n_kv_heads;        /* 1..1024 */
+  int32_t head_dim;          /* 64 or 128 */
+  int64_t n_pages;
+  int64_t off[2], bytes[2];
+  int64_t total_bytes;
+} qmv_kv_desc;
+
+int kv8_desc(int type, int64_t n_pages, int32_t n_kv_heads, int32_t head_dim, qmv_kv_desc* out);
+
+/*
+ * Block tables and slot maps of one step, built on the GPU from the requests'
+ * lengths. All pointers are device int32 arrays; B = n_requests, T = n_tokens.
+ * Free pages are kept first in, first out in a ring of n_pages entries: those
+ * at ring[(head + i) % n_pages], i < count, with ring_state = {head, count}.
+ *
+ * Request b has lens[b] tokens in the cache and brings add[b] new ones (their
+ * rows of q, k and v lie at q_start[b].. in the order of requests; a negative
+ * add means that the request leaves). With held = ceil(lens / 64) and after =
+ * ceil((lens + add) / 64), in the order of requests:
+ *   status 0 (served): its after - held new pages are taken from the ring's
+ *     head and entered in its row of the table; lens_out = ctx = lens + add.
+ *   status 1 (no pages): it needs pages and the needs of all requests up to it
+ *     exceed count; nothing of it changes, lens_out = lens, ctx = 0.
+ *   status 2 (out of bounds): lens is negative, held or after is over
+ *     max_pages, or its rows end past T; nothing of it changes, ctx = 0, and
+ *     it needs nothing.
+ *   status 3 (left): its held pages go to the ring's tail (free from the next
+ *     step on), in the order of its row; lens_out = ctx = 0.
+ * q_start[0..B] are the exclusive sums of max(add, 0), at most T. slots[t] and
+ * positions[t] (the token's index in its request) are -1 where token t belongs
+ * to no served request. runs lists the runs of new tokens that share a page, as
+ * (first token, count), in order; the rest of its max_runs entries are (0, 0).
+ * max_runs has to be at least kv_max_runs(B, T).
+ * lens_out may be lens, and ring_state_out may be ring_state. A call whose
+ * outputs are separate may be repeated with the same inputs and gives the same
+ * result. A ring_state that is out of range, or pages that come back to a ring
+ * that cannot hold them, set QMV_ERR_CORRUPT in the device error word.
+ */
+typedef struct {
+  int32_t n_requests;        /* B, 1..QMV_KV_MAX_REQUESTS */
+  int32_t n_tokens;          /* T, >= 0 */
+  int32_t n_pages;           /* size of the ring */
+  int32_t max_pages;         /* entries of a table row */
+  int64_t ld_table;          /* row stride of the table, >= max_pages */
+  int32_t max_runs;
+  const int32_t* lens;       /* [B] */
+  const int32_t* add;        /* [B] */
+  int32_t* table;            /* [B][ld_table] */
+  int32_t* ring;             /* [n_pages] */
+  const int32_t* ring_state; /* [2] */
+  int32_t* ring_state_out;   /* [2] */
+  int32_t* lens_out;         /* [B] */
+  int32_t* ctx;              /* [B] */
+  int32_t* status;           /* [B] */
+  int32_t* q_start;          /* [B + 1] */
+  int32_t* slots;            /* [T] */
+  int32_t* positions;        /* [T] */
+  int32_t* runs;             /* [max_runs][2] */
+} kv_plan_args;
+
+int64_t kv_max_runs(int64_t n_requests, int64_t n_tokens);
+int kv_plan(const kv_plan_args* args, void* stream);
+
+/*
+ * Rotary positions with one to QMV_ROPE_MAX_AXES axes (text; time, height and
+ * width of images and video). The first rot_dim values of a head form rot_dim /
+ * 2 pairs: (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved. Pair i of a
+ * token at positions p[axis] turns by the angle p[axis[i]] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin);
+ * values past rot_dim pass through. The angle is kept in turns as a 64-bit
+ * fraction (turn[i] = inv_freq[i] / 2 pi mod 1), so its reduction is exact at
+ * every int32 position; sine, cosine and products are fp32.
+ * rope_desc: host arrays inv_freq [rot_dim / 2] and axis [rot_dim / 2] (NULL:
+ * all 0). head_dim <= 2 * QMV_ROPE_MAX_PAIRS; head_dim and rot_dim are
+ * multiples of 16, rot_dim <= head_dim; inv_freq finite.
+ */
+typedef struct {
+  uint32_t abi_version;
+  int32_t head_dim, rot_dim, n_axes, interleaved;
+  uint8_t axis[QMV_ROPE_MAX_PAIRS];
+  uint64_t turn[QMV_ROPE_MAX_PAIRS];  /* 2^-64 turns per position */
+} qmv_rope;
+
+int rope_desc(int32_t head_dim, int32_t rot_dim, int32_t n_axes, int32_t interleaved, const double* inv_freq,
+              const int32_t* axis, qmv_rope* out);
+
+/*
+ * Rotate n_heads heads of n_tokens tokens: x [n_tokens][ldx], head h at column h *
+ * head_dim, to out [n_tokens][ldo]. x_type and out_type are qmv_dtype; out may
+ * be x where type and stride agree. positions: int32 [n_axes][ldp]. inverse
+ * nonzero turns by the negative angle, which is also the gradient: dx is the
+ * inverse rotation of dout. n_tokens may be 0. Rows are 16-byte aligned.
+ */
+int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int32_t n_heads, int64_t ldx,
+             const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, void* stream);
+
+/*
+ * Write new keys and values into the cache, and rotate q and k on the way.
+ * k, v: [n_tokens][ldk / ldv], KV head h at column h * head_dim, of x_type (like
+ * q). runs (device, [n_runs][2]) lists runs of tokens that share a page as
+ * (first token, count): their slots are slots[first], slots[first] + 1, ... in
+ * one page. A run of count 0 or with slots[first] < 0 is skipped; a page may
+ * appear in one run of a call only. With s the page's scale for K or V (0 when
+ * the run starts at offset 0: the page begins anew), a the largest magnitude of
+ * the run's values and top = 127 (int8) or 448 (e4m3), the scale becomes
+ * s' = max(s, a / top); where it grows, the codes already in the page are
+ * rounded again from code * s * (1 / s'); the new codes are x * (1 / s'), rounded
+ * to nearest even and held to +-top. All of it is fp32. An infinite value takes
+ * the largest code and does not count for a; a NaN is stored as 0; either sets
+ * QMV_ERR_CORRUPT in the device error word, and so does a run outside the
+ * tokens, its page or the cache (nothing is written for that run).
+ * rope (nullable) rotates k by `positions` before it is stored and, where q is
+ * given, q [n_tokens][ldq] (n_q_heads heads) to q_out [n_tokens][ldqo] of
+ * q_out_type. Without rope q must be NULL.
+ */
+typedef struct {
+  const void* k;
+  const void* v;
+  const void* q;             /* nullable */
+  void* q_out;
+  int64_t ldk, ldv, ldq, ldqo;
+  int32_t x_type, q_out_type;
+  int32_t n_tokens, n_q_heads;
+  int32_t n_runs;
+  const int32_t* slots;      /* [n_tokens] */
+  const int32_t* runs;       /* [n_runs][2] */
+  const int32_t* positions;  /* [n_axes][ldp], where rope is given */
+  int64_t ldp;
+} kv8_append_args;
+
+int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const kv8_append_args* args, void* stream);
+
+/*
+ * Values back out of the cache: k_out, v_out [n][ldo] of out_type (KV head h at
+ * column h * head_dim) receive code * scale of slots[0..n). A negative slot or
+ * one past the cache gives zeros (the latter sets QMV_ERR_CORRUPT).
+ */
+int kv8_read(const qmv_kv_desc* desc, const void* cache, const int32_t* slots, int64_t n, void* k_out, void* v_out,
+             int out_type, int64_t ldo, void* stream);
+
+/*
+ * Attention of new tokens over the cache. Request b's query rows are tokens
+ * q_start[b] .. q_start[b+1] - 1 of q, at positions ctx[b] - n + i for the i-th
+ * of its n rows; its keys are the first ctx[b] tokens of its pages (the new
+ * tokens' own among them: append first). Query head h reads KV head h /
+ * (n_q_heads / n_kv_heads). For query position i and key j
+ *   s = scale * (q . k_j);  s = softcap * tanh(s / softcap) where softcap > 0;
+ *   s -= slopes[h] * |i - j| where slopes is given;
+ * j is seen where j < ctx[b], (j <= i or j < prefix[b]) and (window == 0 or
+ * i - j < window); out = sum_j softmax(s)_j v_j over the seen keys, and lse (nullable,
+ * [n_tokens][n_q_heads]) is the natural logarithm of the sum of exp(s). A row
+ * that sees no key gives out = 0 and lse = -inf. Rows of q past q_start[B] are
+ * left as they are in out.
+ * q and out are [n_tokens][ldq / ldo] of x_type and out_type, head h at column
+ * h * head_dim. Products are exact with fp32 sums (q is scaled per row by a
+ * power of two into fp16: exact for fp16, and for bf16 down to 2^-27 of the
+ * row's largest value; fp32 queries are rounded to 11 bits); probabilities are
+ * rounded to fp16 for the product with V; sums and softmax statistics are fp32.
+ * The result is reproducible bit for bit.
+ * max_new is the host's bound on the rows of one request. It chooses the
+ * kernel's row tile; a request with more rows is still served in full.
+ * A table entry outside the cache sets QMV_ERR_CORRUPT and its page is not
+ * read: its keys count as unseen.
+ * workspace: device, >= kv8_attend_workspace_size(desc) bytes, given to
+ * kv8_attend_init once; every call leaves it ready for the next. Calls that
+ * overlap on the GPU need one each. After QMV_ERR_TIMEOUT init it again.
+ */
+typedef struct {
+  const void* q;
+  void* out;
+  float* lse;                /* nullable */
+  int64_t ldq, ldo;
+  int32_t x_type, out_type;
+  int32_t n_requests, n_tokens, n_q_heads, max_new;
+  const int32_t* q_start;    /* [B + 1] */
+  const int32_t* ctx;        /* [B] */
+  const int32_t* table;      /* [B][ld_table] */
+  int64_t ld_table;
+  int32_t max_pages;         /* entries of a table row; ctx past max_pages * 64 is cut */
+  int32_t window;            /* 0: none */
+  float scale, softcap;
+  const float* slopes;       /* nullable, [n_q_heads] */
+  const int32_t* prefix;     /* nullable, [B] */
+  void* workspace;
+  size_t ws_bytes;
+} kv8_attend_args;
+
+size_t kv8_attend_workspace_size(const qmv_kv_desc* desc);
+int kv8_attend_init(const qmv_kv_desc* desc, void* workspace, size_t ws_bytes, void* stream);
+int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args* args, void* stream);
+
+/*
  * Packed-weight files ("Ternary Bonsai 2", section 3.6: the packed indices,
  * scales and flags are exported as the file that inference loads). A file
  * holds named packed matrices of any format above, each with its qmv_desc and

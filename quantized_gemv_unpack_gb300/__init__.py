@@ -25,11 +25,17 @@ QMV_ERR_CORRUPT, QMV_ERR_CUDA, QMV_ERR_TIMEOUT = -4, -5, -6
 QMV_TERNARY2, QMV_INT4, QMV_CASS, QMV_CASS_MX, QMV_TERNARY2_SPARSE, QMV_TERNARY2_LUT, QMV_INT4_LUT = 1, 2, 3, 4, 5, 6, 7
 QMV_FLAG_PATH_FMA, QMV_FLAG_PATH_MMA = 1, 2   # qmv_desc.flags: force the fp16-FMA or the tensor-core matvec kernel
 QMV_FLAG_TEST_WAIT_TIMEOUT = 0x100           # qmv_desc.flags, testing only: the matvec's first wait gives up
+QMV_KV_PAGE, QMV_KV_MAX_REQUESTS = 64, 8192  # tokens of a cache page; requests of a step
+QMV_ROPE_MAX_PAIRS, QMV_ROPE_MAX_AXES = 128, 4
+QMV_KV_INT8, QMV_KV_E4M3 = 1, 2              # code types of the KV cache
+QMV_F32, QMV_BF16, QMV_F16 = 1, 2, 3         # activation types of the rope_* and kv8_* calls
 
 # the exported C symbols (one per declaration in include/qmv.h)
 EXPORTS = ("qmv_pack_desc", "qmv_pack_ternary", "qmv_pack_int4", "qmv_unpack", "qmv_run_ternary",
            "qmv_run_int4", "qmv_run_batch", "qmv_sparse_pack_host", "cass_pack_host", "cass_mx_pack_host", "cass_kv_encode", "cass_decode_draft", "cass_reconstruct",
            "cass_speculate_step", "moe_workspace_size", "moe_qmv_run", "moe_qmv_run_static",
+           "kv8_desc", "kv_max_runs", "kv_plan", "rope_desc", "rope_run", "kv8_append", "kv8_read",
+           "kv8_attend_workspace_size", "kv8_attend_init", "kv8_attend",
            "qmv_file_write", "qmv_file_open", "qmv_file_count", "qmv_file_tensor", "qmv_file_find", "qmv_file_load",
            "qmv_file_read_host", "qmv_file_close", "qmv_crc32", "qmv_check_status", "qmv_last_error")
 
@@ -54,6 +60,41 @@ class qmv_desc(ctypes.Structure):
 class qmv_task(ctypes.Structure):
     _fields_ = [("desc", ctypes.POINTER(qmv_desc)), ("w", ctypes.c_void_p), ("x", ctypes.c_void_p),
                 ("y", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class qmv_kv_desc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("type", ctypes.c_uint32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("off", ctypes.c_int64 * 2),
+                ("bytes", ctypes.c_int64 * 2), ("total_bytes", ctypes.c_int64)]
+
+
+class qmv_rope(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axis", ctypes.c_uint8 * QMV_ROPE_MAX_PAIRS), ("turn", ctypes.c_uint64 * QMV_ROPE_MAX_PAIRS)]
+
+
+class kv_plan_args(ctypes.Structure):
+    _fields_ = [("n_requests", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("ld_table", ctypes.c_int64), ("max_runs", ctypes.c_int32)] + [
+                    (n, ctypes.c_void_p) for n in ("lens", "add", "table", "ring", "ring_state", "ring_state_out", "lens_out",
+                                                   "ctx", "status", "q_start", "slots", "positions", "runs")]
+
+
+class kv8_append_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "q", "q_out")] + [
+        (n, ctypes.c_int64) for n in ("ldk", "ldv", "ldq", "ldqo")] + [
+        (n, ctypes.c_int32) for n in ("x_type", "q_out_type", "n_tokens", "n_q_heads", "n_runs")] + [
+        (n, ctypes.c_void_p) for n in ("slots", "runs", "positions")] + [("ldp", ctypes.c_int64)]
+
+
+class kv8_attend_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "out", "lse")] + [("ldq", ctypes.c_int64), ("ldo", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("x_type", "out_type", "n_requests", "n_tokens", "n_q_heads", "max_new")] + [
+        (n, ctypes.c_void_p) for n in ("q_start", "ctx", "table")] + [
+        ("ld_table", ctypes.c_int64), ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("prefix", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
 _lib = None
@@ -81,6 +122,17 @@ _SIGS = {
     "moe_qmv_run": (_I32, [_DESC, _DESC, _P, _I64, _I64, _I32, _P, _I32, _P, _I32, _I64, _P, _I64, _P,
                            ctypes.c_size_t, _P]),
     "moe_qmv_run_static": (_I32, [_DESC, _DESC, _P, _I64, _I64, _I32, _P, _I32, _P, _I32, _I64, _P, _I64, _P]),
+    "kv8_desc": (_I32, [_I32, _I64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(qmv_kv_desc)]),
+    "kv_max_runs": (_I64, [_I64, _I64]),
+    "kv_plan": (_I32, [ctypes.POINTER(kv_plan_args), _P]),
+    "rope_desc": (_I32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                         ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(qmv_rope)]),
+    "rope_run": (_I32, [ctypes.POINTER(qmv_rope), _P, _I32, _I64, ctypes.c_int32, _I64, _P, _I64, _P, _I32, _I64, _I32, _P]),
+    "kv8_append": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.POINTER(qmv_rope), ctypes.POINTER(kv8_append_args), _P]),
+    "kv8_read": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, _P, _I64, _P, _P, _I32, _I64, _P]),
+    "kv8_attend_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(qmv_kv_desc)]),
+    "kv8_attend_init": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.c_size_t, _P]),
+    "kv8_attend": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.POINTER(kv8_attend_args), _P]),
     "qmv_file_write": (_I32, [ctypes.c_char_p, _I32, ctypes.POINTER(ctypes.c_char_p), _DESC, ctypes.POINTER(_P)]),
     "qmv_file_open": (_I32, [ctypes.c_char_p, ctypes.POINTER(_P)]),
     "qmv_file_count": (_I32, [_P]),
@@ -318,7 +370,245 @@ def moe_qmv_run_static(gateup_desc: qmv_desc, down_desc: qmv_desc, experts, expe
                                     _stream(stream)))
 
 
-# ----------------------------------------------------------------------------- status
+# ----------------------------------------------------------------------------- paged 8-bit KV cache
+
+# The calls of a serving step take many arguments that stay the same from step to step (buffers that a captured
+# graph or a decode loop keeps), so each has a class that marshals them once, keeps its tensors alive like Batch,
+# and issues the call with run(). Shapes, strides, types and devices are checked when it is made.
+
+def _dtype(t):
+    import torch
+    code = {torch.float32: QMV_F32, torch.bfloat16: QMV_BF16, torch.float16: QMV_F16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"float32, bfloat16 or float16 expected, got {t.dtype}")
+    return code
+
+
+def _ints(name, t, shape, device):
+    """An int32 tensor of the given shape (None: any extent), contiguous, on `device`."""
+    import torch
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != device:
+        raise TypeError(f"{name}: a contiguous int32 tensor on {device} expected")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    return t
+
+
+def _heads(name, t, heads, head_dim, device, tokens=None):
+    """(address, token stride) of a [tokens][heads][head_dim] tensor whose heads lie side by side."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (tokens, {heads}, {head_dim})")
+    if tokens is not None and t.shape[0] != tokens:
+        raise ValueError(f"{name}: {t.shape[0]} tokens, expected {tokens}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name}: the heads of a token must lie side by side (strides {t.stride()})")
+    row = t.shape[1] * head_dim
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(row, t.stride(0))
+
+
+def _cache(desc, cache):
+    import torch
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.numel() < desc.total_bytes:
+        raise ValueError(f"cache: a contiguous uint8 tensor of at least {desc.total_bytes} bytes expected")
+    return cache
+
+
+def kv8_desc(type: int, n_pages: int, n_kv_heads: int, head_dim: int) -> qmv_kv_desc:
+    """Layout of one layer's cache: allocate desc.total_bytes bytes (uint8) for it."""
+    d = qmv_kv_desc()
+    _check(lib().kv8_desc(type, n_pages, n_kv_heads, head_dim, ctypes.byref(d)))
+    return d
+
+
+def kv_max_runs(n_requests: int, n_tokens: int) -> int:
+    return int(lib().kv_max_runs(n_requests, n_tokens))
+
+
+class KvPlan:
+    """kv_plan: block tables and slot maps of one step (see include/qmv.h). int32 device tensors lens, add [B],
+    table [B][max_pages], ring [n_pages], ring_state [2] = (head, count); n_tokens is the number of new tokens' rows.
+    run() fills slots, positions [n_tokens], runs [max_runs][2], q_start [B + 1], ctx, status [B], and lens_out and
+    ring_state_out, which may be given as lens and ring_state to advance the state in place."""
+
+    def __init__(self, lens, add, table, ring, ring_state, n_tokens: int, lens_out=None, ring_state_out=None):
+        import torch
+        dev = lens.device
+        B = lens.shape[0]
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)  # noqa: E731
+        self.lens, self.add = _ints("lens", lens, (B,), dev), _ints("add", add, (B,), dev)
+        self.table, self.ring = _ints("table", table, (B, None), dev), _ints("ring", ring, (None,), dev)
+        self.ring_state = _ints("ring_state", ring_state, (2,), dev)
+        self.lens_out = new(B) if lens_out is None else _ints("lens_out", lens_out, (B,), dev)
+        self.ring_state_out = new(2) if ring_state_out is None else _ints("ring_state_out", ring_state_out, (2,), dev)
+        max_runs = kv_max_runs(B, n_tokens)
+        self.ctx, self.status, self.q_start = new(B), new(B), new(B + 1)
+        self.slots, self.positions, self.runs = new(n_tokens), new(n_tokens), new(max_runs, 2)
+        a = self.args = kv_plan_args(B, n_tokens, ring.shape[0], table.shape[1], table.shape[1], max_runs)
+        for n in ("lens", "add", "table", "ring", "ring_state", "ring_state_out", "lens_out", "ctx", "status", "q_start",
+                  "slots", "positions", "runs"):
+            setattr(a, n, getattr(self, n).data_ptr())
+        self._call, self._args = lib().kv_plan, ctypes.byref(a)
+
+    def run(self, stream=None):
+        _check(self._call(self._args, _stream(stream)))
+
+
+def rope_desc(head_dim: int, inv_freq, axis=None, interleaved: bool = False, n_axes: int | None = None) -> qmv_rope:
+    """Rotation of the first 2 * len(inv_freq) values of each head; axis names the position axis of each pair
+    (default: axis 0 for all)."""
+    n = len(inv_freq)
+    f = (ctypes.c_double * n)(*[float(x) for x in inv_freq])
+    ax = None if axis is None else [int(x) for x in axis]
+    if ax is not None and len(ax) != n:
+        raise ValueError("axis and inv_freq differ in length")
+    if n_axes is None:
+        n_axes = max(ax) + 1 if ax else 1
+    if n > QMV_ROPE_MAX_PAIRS:
+        raise ValueError(f"{n} pairs, at most {QMV_ROPE_MAX_PAIRS}")
+    r = qmv_rope()
+    _check(lib().rope_desc(head_dim, 2 * n, n_axes, int(interleaved), f,
+                           (ctypes.c_int32 * n)(*ax) if ax is not None else None, ctypes.byref(r)))
+    return r
+
+
+def _positions(rope, positions, tokens, device):
+    p = positions if positions.dim() == 2 else positions.unsqueeze(0)
+    if p.shape[0] < rope.n_axes or p.shape[1] < tokens:
+        raise ValueError(f"positions: shape {tuple(positions.shape)}, expected at least ({rope.n_axes}, {tokens})")
+    return _ints("positions", p, (None, None), device)
+
+
+class Rope:
+    """rope_run: x [tokens][heads][head_dim] rotated into out (same shape; may be x). positions: int32 [n_axes][tokens]
+    (or [tokens] with one axis). inverse turns back, which is also the gradient."""
+
+    def __init__(self, rope: qmv_rope, x, positions, out, inverse: bool = False):
+        dev = x.device
+        T, H = x.shape[0], x.shape[1]
+        xp, ldx = _heads("x", x, None, rope.head_dim, dev)
+        op, ldo = _heads("out", out, H, rope.head_dim, dev, T)
+        pos = _positions(rope, positions, T, dev)
+        self.keep = (rope, x, pos, out)
+        self._call = lib().rope_run
+        self._args = (ctypes.byref(rope), xp, _dtype(x), T, H, ldx, pos.data_ptr(), pos.stride(0), op, _dtype(out), ldo,
+                      int(inverse))
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
+
+def rope_run(rope: qmv_rope, x, positions, out, inverse: bool = False, stream=None):
+    """One call of Rope(...).run()."""
+    Rope(rope, x, positions, out, inverse).run(stream)
+
+
+class KvAppend:
+    """kv8_append: write k, v [tokens][kv_heads][head_dim] to their slots (a KvPlan's slots and runs). With rope, k is
+    rotated by positions first, and q [tokens][q_heads][head_dim], where given, is rotated into q_out."""
+
+    def __init__(self, desc: qmv_kv_desc, cache, k, v, slots, runs, rope: qmv_rope | None = None, positions=None, q=None,
+                 q_out=None):
+        dev = cache.device
+        H, D, T = desc.n_kv_heads, desc.head_dim, k.shape[0]
+        a = self.args = kv8_append_args()
+        a.k, a.ldk = _heads("k", k, H, D, dev)
+        a.v, a.ldv = _heads("v", v, H, D, dev, T)
+        a.x_type, a.n_tokens = _dtype(k), T
+        if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+            raise TypeError("q, k and v must have one type")
+        a.slots = _ints("slots", slots, (T,), dev).data_ptr()
+        a.runs, a.n_runs = _ints("runs", runs, (None, 2), dev).data_ptr(), runs.shape[0]
+        pos = None
+        if rope is not None:
+            if positions is None:
+                raise ValueError("rope needs positions")
+            pos = _positions(rope, positions, T, dev)
+            a.positions, a.ldp = pos.data_ptr(), pos.stride(0)
+        if q is not None:
+            if q_out is None:
+                raise ValueError("q needs q_out")
+            a.q, a.ldq = _heads("q", q, None, D, dev, T)
+            a.q_out, a.ldqo = _heads("q_out", q_out, q.shape[1], D, dev, T)
+            a.q_out_type, a.n_q_heads = _dtype(q_out), q.shape[1]
+        self.keep = (desc, _cache(desc, cache), k, v, slots, runs, rope, pos, q, q_out)
+        self._call = lib().kv8_append
+        self._args = (ctypes.byref(desc), cache.data_ptr(), ctypes.byref(rope) if rope is not None else None, ctypes.byref(a))
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
+
+class KvRead:
+    """kv8_read: the values that the codes of slots [n] stand for, into k_out and v_out [n][kv_heads][head_dim]."""
+
+    def __init__(self, desc: qmv_kv_desc, cache, slots, k_out, v_out):
+        dev = cache.device
+        n = slots.shape[0]
+        kp, ldk = _heads("k_out", k_out, desc.n_kv_heads, desc.head_dim, dev, n)
+        vp, ldv = _heads("v_out", v_out, desc.n_kv_heads, desc.head_dim, dev, n)
+        if ldk != ldv or k_out.dtype != v_out.dtype:
+            raise ValueError("k_out and v_out must have one type and one stride")
+        _ints("slots", slots, (n,), dev)
+        self.keep = (desc, _cache(desc, cache), slots, k_out, v_out)
+        self._call = lib().kv8_read
+        self._args = (ctypes.byref(desc), cache.data_ptr(), slots.data_ptr(), n, kp, vp, _dtype(k_out), ldk)
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
+
+def kv8_workspace(desc: qmv_kv_desc, device):
+    """A workspace for kv8_attend (uint8), ready for use. Calls that overlap on the GPU need one each."""
+    import torch
+    n = int(lib().kv8_attend_workspace_size(ctypes.byref(desc)))
+    if n == 0:
+        _check(QMV_ERR_ARG)
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        _check(lib().kv8_attend_init(ctypes.byref(desc), ws.data_ptr(), n, _stream(None)))
+    return ws
+
+
+class KvAttend:
+    """kv8_attend: attention of q [tokens][q_heads][head_dim] over the cache into out (same shape), with a KvPlan's
+    q_start [B + 1], ctx [B] and table [B][max_pages]. max_new bounds the new tokens of one request. slopes [q_heads]
+    (fp32) and prefix [B] (int32) are device tensors; lse [tokens][q_heads] (fp32) is optional. Without a workspace
+    one is made; layers of one stream can share it (its `workspace`)."""
+
+    def __init__(self, desc: qmv_kv_desc, cache, q, out, q_start, ctx, table, scale: float, max_new: int = 1,
+                 softcap: float = 0.0, slopes=None, window: int = 0, prefix=None, lse=None, workspace=None):
+        import torch
+        dev = cache.device
+        T, Hq, D = q.shape[0], q.shape[1], desc.head_dim
+        B = ctx.shape[0]
+        a = self.args = kv8_attend_args()
+        a.q, a.ldq = _heads("q", q, None, D, dev)
+        a.out, a.ldo = _heads("out", out, Hq, D, dev, T)
+        a.x_type, a.out_type = _dtype(q), _dtype(out)
+        a.n_requests, a.n_tokens, a.n_q_heads, a.max_new = B, T, Hq, max_new
+        a.q_start = _ints("q_start", q_start, (B + 1,), dev).data_ptr()
+        a.ctx = _ints("ctx", ctx, (B,), dev).data_ptr()
+        a.table = _ints("table", table, (B, None), dev).data_ptr()
+        a.ld_table, a.max_pages = table.shape[1], table.shape[1]
+        a.window, a.scale, a.softcap = window, scale, softcap
+        for name, t, shape in (("slopes", slopes, (Hq,)), ("lse", lse, (T, Hq))):
+            if t is not None:
+                if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+                    raise ValueError(f"{name}: a contiguous float32 tensor of shape {shape} on {dev} expected")
+                setattr(a, name, t.data_ptr())
+        if prefix is not None:
+            a.prefix = _ints("prefix", prefix, (B,), dev).data_ptr()
+        self.workspace = kv8_workspace(desc, dev) if workspace is None else workspace
+        a.workspace, a.ws_bytes = self.workspace.data_ptr(), self.workspace.numel() * self.workspace.element_size()
+        self.keep = (desc, _cache(desc, cache), q, out, q_start, ctx, table, slopes, prefix, lse)
+        self._call = lib().kv8_attend
+        self._args = (ctypes.byref(desc), cache.data_ptr(), ctypes.byref(a))
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
 
 # ----------------------------------------------------------------------------- packed-weight files
 
@@ -391,6 +681,8 @@ class QmvFile:
     def __exit__(self, *exc):
         self.close()
 
+
+# ----------------------------------------------------------------------------- status
 
 def qmv_check_status(stream=None) -> int:
     """Synchronize the stream and return (and clear) the device error word; raises on CUDA failure."""
