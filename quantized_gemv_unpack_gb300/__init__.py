@@ -185,10 +185,17 @@ def _ptr(t):
     raise TypeError(f"cannot take the address of {type(t)}")
 
 
+_raw_stream = None   # torch's current stream of a device as an integer, without making a Stream object
+
+
 def _stream(stream):
     if stream is None:
+        global _raw_stream
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+                lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -19,7 +19,7 @@ Layout layout(const qmv_kv_desc* d) {
   Layout l;
   l.blocks = sm_count();
   if (l.blocks > (int)(kCounterBytes / sizeof(int))) l.blocks = (int)(kCounterBytes / sizeof(int));
-  const size_t rows = (size_t)l.blocks * (attend::kStreamRows + attend::kBlockRows);
+  const size_t rows = (size_t)l.blocks * attend::kPartRows;
   l.ml_off = kCounterBytes;
   l.o_off = l.ml_off + rows * sizeof(float2);
   l.total = l.o_off + rows * d->head_dim * sizeof(float);
@@ -119,8 +119,8 @@ int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args
   a.part_o = reinterpret_cast<float*>(ws + l.o_off);
   a.err = err;
   const int64_t rows = (int64_t)(g->max_new < g->n_tokens ? g->max_new : g->n_tokens) * a.G;
-  const int tile = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  a.min_units = 128 / tile;
+  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  a.limit = 24;
   const bool mods = g->softcap > 0.f || g->slopes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->type == QMV_KV_INT8;
