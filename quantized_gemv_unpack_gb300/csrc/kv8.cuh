@@ -53,6 +53,59 @@ __device__ __forceinline__ float decode(uint32_t b) {
   }
 }
 
+// Eight finite values of magnitude at most top * (1 + 2^-22) as codes, in two words. int8: adding 1.5 * 2^23 leaves the
+// nearest whole number (ties to even) in the low byte of the sum.
+template <int TYPE>
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float inv) {
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = __fmul_rn(v[4 * i + j], inv);
+    if constexpr (TYPE == QMV_KV_INT8) {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(__fadd_rn(y[j], 12582912.f));
+      w[i] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410) ^ 0x80808080u;
+    } else {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+      w[i] = lo | (hi << 16);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+// The same for any values.
+template <int TYPE>
+__device__ __forceinline__ uint2 encode8_any(const float (&v)[8], float inv) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= encode<TYPE>(v[i] * inv) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+
+// The values of eight codes, without the scale: exact.
+template <int TYPE>
+__device__ __forceinline__ void decode8(uint2 w, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = i ? w.y : w.x;
+    if constexpr (TYPE == QMV_KV_INT8) {
+      // 2^23 + byte in the bits of a float
+      v[4 * i] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440)) - 8388736.f;
+      v[4 * i + 1] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441)) - 8388736.f;
+      v[4 * i + 2] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442)) - 8388736.f;
+      v[4 * i + 3] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443)) - 8388736.f;
+    } else {
+      const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x & 0xFFFFu), __NV_E4M3);
+      const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(x >> 16), __NV_E4M3);
+      const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
+      v[4 * i] = a.x, v[4 * i + 1] = a.y, v[4 * i + 2] = b.x, v[4 * i + 3] = b.y;
+    }
+  }
+}
+
 // ---- eight consecutive values of an activation row (16-byte aligned)
 
 template <typename T>
@@ -131,66 +184,167 @@ __device__ __forceinline__ RopeChunk rope_chunk(const qmv_rope& r, int c) {
   if (turned && !r.interleaved) return {8 * c, 8 * c + r.rot_dim / 2, true};
   return {16 * c, 16 * c + 8, turned};
 }
-// Cosine and sine of chunk c's eight pairs for the token whose positions are at
-// pos[axis * ldp]. The product position * turn is exact modulo one turn; the
-// top 32 bits, as half turns in [-1, 1), go to sincospif (an angle error of at
-// most 2^-25 half turns from the conversion to fp32).
-__device__ __forceinline__ void rope_angles(const qmv_rope& r, int c, const int32_t* pos, int64_t ldp, float sign,
-                                            float (&cs)[8], float (&sn)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int pair = 8 * c + i;
-    const int64_t p = pos[(int64_t)r.axis[pair] * ldp];
-    const uint64_t ph = (uint64_t)p * r.turn[pair];
-    const float h = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(h, &sn[i], &cs[i]);
-    sn[i] *= sign;
+// A pair's angle at a position: position * turn is exact modulo one turn; its top 32 bits, as half turns in [-1, 1), go
+// to sincospif (an angle error of at most 2^-25 half turns from the conversion to fp32).
+// The angles of n tokens (positions at pos, pos + 1, ...) into shared memory, by the block's threads, each pair's once
+// for all heads that the block serves. Pairs 8c + 2i and 8c + 2i + 1 of token k are at 2 ((k * 4 + i) * chunks + c), so
+// that the threads of neighbouring chunks read neighbouring 16-byte words. A thread keeps its pair from token to token: reading the descriptor (a
+// kernel argument) at 32 places takes a warp 32 turns.
+__device__ __forceinline__ void rope_angles(const qmv_rope& r, int n, const int32_t* pos, int64_t ldp, float sign,
+                                            float2* angles, int tid, int threads) {
+  const int pairs = r.rot_dim / 2, chunks = r.head_dim / 16;
+  const int rows = threads >= pairs ? threads / pairs : 1;   // tokens at a time
+  const int k0 = threads >= pairs ? tid / pairs : 0;
+  if (k0 >= rows) return;
+  for (int pair = tid - k0 * pairs; pair < pairs; pair += threads) {
+    const uint64_t turn = r.turn[pair];
+    const int32_t* p = pos + (int64_t)r.axis[pair] * ldp;
+    for (int k = k0; k < n; k += rows) {
+      const uint64_t ph = (uint64_t)(int64_t)p[k] * turn;
+      const float h = (float)(int32_t)(ph >> 32) * 4.656612873077393e-10f;  // 2^-31
+      float s, c;
+      sincospif(h, &s, &c);
+      angles[2 * ((k * 4 + ((pair & 7) >> 1)) * chunks + (pair >> 3)) + (pair & 1)] = make_float2(c, s * sign);
+    }
   }
+}
+__device__ __forceinline__ void chunk_angles(const float2* angles, int k, int c, int chunks, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(angles)[(k * 4 + i) * chunks + c];
+    cs[2 * i] = v.x;
+    sn[2 * i] = v.y;
+    cs[2 * i + 1] = v.z;
+    sn[2 * i + 1] = v.w;
+  }
+}
+__device__ __forceinline__ void rope_pair(float c, float s, float& a, float& b) {
+  const float x = a;
+  a = fmaf(-b, s, x * c);
+  b = fmaf(x, s, b * c);
 }
 __device__ __forceinline__ void rope_turn(bool interleaved, const float (&cs)[8], const float (&sn)[8], float (&a)[8],
                                           float (&b)[8]) {
   if (!interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = __fsub_rn(__fmul_rn(x, cs[i]), __fmul_rn(y, sn[i]));
-      b[i] = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
-    }
+    for (int i = 0; i < 8; ++i) rope_pair(cs[i], sn[i], a[i], b[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float x = a[2 * i], y = a[2 * i + 1];
-      a[2 * i] = __fsub_rn(__fmul_rn(x, cs[i]), __fmul_rn(y, sn[i]));
-      a[2 * i + 1] = __fadd_rn(__fmul_rn(y, cs[i]), __fmul_rn(x, sn[i]));
-      x = b[2 * i], y = b[2 * i + 1];
-      b[2 * i] = __fsub_rn(__fmul_rn(x, cs[i + 4]), __fmul_rn(y, sn[i + 4]));
-      b[2 * i + 1] = __fadd_rn(__fmul_rn(y, cs[i + 4]), __fmul_rn(x, sn[i + 4]));
+      rope_pair(cs[i], sn[i], a[2 * i], a[2 * i + 1]);
+      rope_pair(cs[i + 4], sn[i + 4], b[2 * i], b[2 * i + 1]);
     }
   }
 }
 
-// Rotate the heads of tokens [t0, t1) that this block serves: thread (c, y) of
-// head_dim / 16 x rows threads takes chunk c of heads y, y + rows, ... and
-// computes the chunk's angles once per token.
+// Sixteen values of a head as they lie in memory.
 template <typename TI>
-__device__ __forceinline__ void rope_tokens(const qmv_rope& r, const TI* x, int64_t ldx, int64_t t0, int64_t t1, int h0,
-                                            int h1, const int32_t* positions, int64_t ldp, void* out, int out_type,
-                                            int64_t ldo, float sign, int c, int y, int rows) {
+struct Raw16 {
+  static constexpr int W = sizeof(TI) / 2;   // 16-byte words per eight values
+  uint4 w[2 * W];
+};
+template <typename TI>
+__device__ __forceinline__ Raw16<TI> load_raw(const TI* p, int d0, int d1) {
+  Raw16<TI> r;
+  constexpr int W = Raw16<TI>::W;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    r.w[i] = reinterpret_cast<const uint4*>(p + d0)[i];
+    r.w[W + i] = reinterpret_cast<const uint4*>(p + d1)[i];
+  }
+  return r;
+}
+template <typename TI>
+__device__ __forceinline__ void unpack(const Raw16<TI>& r, float (&a)[8], float (&b)[8]) {
+  load8(reinterpret_cast<const TI*>(&r.w[0]), a);
+  load8(reinterpret_cast<const TI*>(&r.w[Raw16<TI>::W]), b);
+}
+
+// Largest magnitude among sixteen values as the bits of their type without the sign (an order that puts infinity and
+// NaN on top): at or above odd_bits() some value is not finite.
+template <typename TI>
+__device__ __forceinline__ uint32_t raw_top(const Raw16<TI>& r) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 2 * Raw16<TI>::W; ++i) {
+    const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = sizeof(TI) == 4 ? max(m, w[j] & 0x7FFFFFFFu) : __vmaxu2(m, w[j] & 0x7FFF7FFFu);
+  }
+  return sizeof(TI) == 4 ? m : max(m & 0xFFFFu, m >> 16);
+}
+template <typename TI>
+__device__ __forceinline__ constexpr uint32_t odd_bits();
+template <>
+__device__ __forceinline__ constexpr uint32_t odd_bits<float>() { return 0x7F800000u; }
+template <>
+__device__ __forceinline__ constexpr uint32_t odd_bits<__nv_bfloat16>() { return 0x7F80u; }
+template <>
+__device__ __forceinline__ constexpr uint32_t odd_bits<__half>() { return 0x7C00u; }
+// Finite bits of raw_top as a float.
+template <typename TI>
+__device__ __forceinline__ float top_value(uint32_t bits) {
+  if constexpr (sizeof(TI) == 4) return __uint_as_float(bits);
+  else if constexpr (odd_bits<TI>() == 0x7F80u) return __uint_as_float(bits << 16);
+  else return __half2float(__ushort_as_half((unsigned short)bits));
+}
+
+// Rotate heads [h0, h1) of the n tokens from t0 on, by the block's threads: a thread keeps its chunk and takes a (token,
+// head) at a time, neighbouring threads neighbouring chunks. Its first two loads are in flight while the block
+// computes the angles. `angles` (shared) holds n * head_dim / 2 pairs.
+template <typename TI>
+__device__ __forceinline__ void rope_tokens(const qmv_rope& r, const TI* x, int64_t ldx, int64_t t0, int n, int h0, int h1,
+                                            const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo,
+                                            float sign, float2* angles, int tid, int threads) {
+  constexpr int kAhead = 2;
+  const int chunks = r.head_dim / 16, heads = h1 - h0;
+  const int step = threads / chunks, y = tid / chunks, c = tid - y * chunks;
   const RopeChunk ch = rope_chunk(r, c);
-  for (int64_t t = t0; t < t1; ++t) {
-    float cs[8], sn[8];
-    if (ch.turned) rope_angles(r, c, positions + t, ldp, sign, cs, sn);
-    for (int h = h0 + y; h < h1; h += rows) {
+  const bool inter = r.interleaved != 0;
+  // (token, head) of this thread's next load, and of its next store
+  int k = y / heads, h = y - k * heads;
+  int k2 = k, h2 = h;
+  if (y >= step) k = k2 = n;
+  const int dk = step / heads, dh = step - dk * heads;
+  auto next = [&](int& tk, int& th) {
+    tk += dk;
+    th += dh;
+    if (th >= heads) {
+      th -= heads;
+      ++tk;
+    }
+  };
+  const TI* px = x + t0 * ldx + (int64_t)h0 * r.head_dim;
+  const int64_t po = t0 * ldo + (int64_t)h0 * r.head_dim;
+  Raw16<TI> raw[kAhead];
+  bool first = true;
+  do {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k < n) raw[j] = load_raw(px + k * ldx + h * r.head_dim, ch.d0, ch.d1);
+      next(k, h);
+    }
+    if (first) {
+      rope_angles(r, n, positions + t0, ldp, sign, angles, tid, threads);
+      __syncthreads();
+      first = false;
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (k2 >= n) break;
       float a[8], b[8];
-      const TI* px = x + t * ldx + (int64_t)h * r.head_dim;
-      load8(px + ch.d0, a);
-      load8(px + ch.d1, b);
-      if (ch.turned) rope_turn(r.interleaved != 0, cs, sn, a, b);
-      const int64_t o = t * ldo + (int64_t)h * r.head_dim;
+      unpack(raw[j], a, b);
+      if (ch.turned) {
+        float cs[8], sn[8];
+        chunk_angles(angles, k2, c, chunks, cs, sn);
+        rope_turn(inter, cs, sn, a, b);
+      }
+      const int64_t o = po + k2 * ldo + h2 * r.head_dim;
       store8_as(out_type, out, o + ch.d0, a);
       store8_as(out_type, out, o + ch.d1, b);
+      next(k2, h2);
     }
-  }
+  } while (k2 < n);
 }
 
 }  // namespace kv8

@@ -1,15 +1,14 @@
 // Rotary positions with several axes (rope_run) and the rotation's descriptor.
 //
 // out = x rotated pair by pair: 2 * bytes(x) of traffic and three products per
-// pair, so the kernel is a copy with some arithmetic. A thread owns sixteen
-// values of a head (two 16-byte pieces in 16-bit types), computes their eight
-// angles once per token and reuses them for every head it takes, which keeps
-// sine and cosine (about 40 instructions each pair) off the critical count: with
-// 48 heads and 16 rows of threads, one angle serves three heads. No table of
-// angles is read and none has to be made for a longer context.
+// pair, so the kernel is a copy with some arithmetic. A block takes some tokens,
+// computes their angles once (sine and cosine cost about 40 instructions a pair)
+// into shared memory and applies them to all its heads, sixteen values per thread
+// in two 16-byte pieces (16-bit types). No table of angles is read and none has to
+// be made for a longer context.
 //
-// Few tokens are split over the heads (one block per 16 heads at most), so that
-// a decode token's 48 heads are three blocks rather than one long loop.
+// Few tokens are split over the heads (16 of them per block), so that a decode
+// token's 48 heads are three blocks rather than one long loop.
 #include "kv8.cuh"
 
 #include <cmath>
@@ -18,22 +17,27 @@
 namespace qmv {
 namespace {
 
+constexpr int kRopeThreads = 256;
+constexpr int kMaxTokensPerBlock = 4;
+
 struct RopeArgs {
   qmv_rope r;
   const void* x;
   void* out;
   const int32_t* positions;
   int64_t ldx, ldo, ldp, n_tokens;
-  int n_heads, out_type, heads_per_block;
+  int n_heads, out_type, tokens_per_block, heads_per_block;
   float sign;
 };
 
 template <typename TI>
-__global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 4 ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];
   const int h0 = blockIdx.y * a.heads_per_block;
-  for (int64_t t = blockIdx.x; t < a.n_tokens; t += gridDim.x)
-    kv8::rope_tokens<TI>(a.r, static_cast<const TI*>(a.x), a.ldx, t, t + 1, h0, min(a.n_heads, h0 + a.heads_per_block),
-                         a.positions, a.ldp, a.out, a.out_type, a.ldo, a.sign, threadIdx.x, threadIdx.y, blockDim.y);
+  const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
+  kv8::rope_tokens<TI>(a.r, static_cast<const TI*>(a.x), a.ldx, t0, (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0),
+                       h0, min(a.n_heads, h0 + a.heads_per_block), a.positions, a.ldp, a.out, a.out_type, a.ldo, a.sign,
+                       angles, threadIdx.x, blockDim.x);
 }
 
 }  // namespace
@@ -112,16 +116,15 @@ int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, 
   a.n_heads = n_heads;
   a.out_type = out_type;
   a.sign = inverse ? -1.f : 1.f;
-  const int c = rope->head_dim / 16;
-  int rows = 128 / c;
-  if (rows > n_heads) rows = n_heads;
-  // enough tokens for four blocks per SM: a block takes all heads of a token (one set of angles for them);
-  // fewer: a block per `rows` heads
+  // Enough tokens for four blocks per SM: all heads in one block, four tokens at a time. Fewer: one token and 16 heads.
   const bool split = n_tokens < 4 * sm_count();
-  a.heads_per_block = split ? rows : n_heads;
-  const int64_t most = 1 << 20;
-  dim3 grid((unsigned)(n_tokens < most ? n_tokens : most), (unsigned)((n_heads + a.heads_per_block - 1) / a.heads_per_block));
-  dim3 block(c, rows);
+  a.tokens_per_block = split ? 1 : kMaxTokensPerBlock;
+  a.heads_per_block = split && n_heads > 16 ? 16 : n_heads;
+  const dim3 grid((unsigned)((n_tokens + a.tokens_per_block - 1) / a.tokens_per_block),
+                  (unsigned)((n_heads + a.heads_per_block - 1) / a.heads_per_block));
+  // a block of few heads has one chunk per thread
+  const int chunks = a.heads_per_block * (rope->head_dim / 16);
+  const int block = chunks >= kRopeThreads ? kRopeThreads : (chunks + 31) / 32 * 32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (x_type == QMV_F32) rope_kernel<float><<<grid, block, 0, s>>>(a);
   else if (x_type == QMV_BF16) rope_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(a);
