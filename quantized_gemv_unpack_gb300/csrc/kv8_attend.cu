@@ -2,7 +2,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "kv8_attend.cuh"
+#include "kv8_prompt.cuh"
 
 using namespace qmv;
 using namespace qmv::kv8;
@@ -32,6 +32,10 @@ int check_workspace(const qmv_kv_desc* desc, const void* workspace, size_t ws_by
   if (!aligned16(workspace)) return fail(QMV_ERR_ALIGN, "workspace must be 16-byte aligned");
   if (ws_bytes < l.total) return fail(QMV_ERR_ARG, "workspace %zu < %zu bytes", ws_bytes, l.total);
   return QMV_OK;
+}
+
+bool prompt_kernel(int64_t rows, int requests, int H) {
+  return rows > 64 && (rows + 255) / 256 * requests * H >= sm_count() / 2;
 }
 
 }  // namespace
@@ -124,6 +128,7 @@ int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args
   const bool mods = g->softcap > 0.f || g->slopes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->type == QMV_KV_INT8;
+  if (prompt_kernel(rows, g->n_requests, H)) return i8 ? prompt::launch_int8(a, D, mods, l.blocks, s) : prompt::launch_e4m3(a, D, mods, l.blocks, s);
   if (D == 64) return i8 ? attend::launch_64_int8(a, tile, mods, l.blocks, s) : attend::launch_64_e4m3(a, tile, mods, l.blocks, s);
   return i8 ? attend::launch_128_int8(a, tile, mods, l.blocks, s) : attend::launch_128_e4m3(a, tile, mods, l.blocks, s);
 }

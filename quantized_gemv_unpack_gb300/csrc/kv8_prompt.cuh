@@ -1,0 +1,529 @@
+// Attention of a prompt's many query rows over the paged 8-bit cache
+// (kv8_attend), on the fifth-generation tensor cores (tcgen05, accumulators in
+// tensor memory).
+//
+// A block takes two tiles of 128 query rows (new tokens times the query heads of
+// one KV head) of one request and walks the keys they see, 128 at a time (two
+// pages). Both products are K-major in shared memory with the 128-byte swizzle:
+// S = Q K^T with Q and K as fp16, and O += P V with P read from tensor memory and
+// V as it is stored, transposed. Work is split by warps:
+//   warps 0-3, 4-7   softmax of tile 0 and tile 1: a thread owns a row
+//   warps 8-10       load the pages' codes and turn them into fp16 tiles
+//   warp 11          one thread issues the products
+// (twelve warps: a thirteenth would leave each 128 registers in place of 168).
+// The order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1) keeps the tensor cores on one tile
+// while the other's softmax runs, and the commit behind QK_t(j+1) also covers
+// PV_t(j): when a tile's softmax sees its next scores, its O may be rescaled.
+//
+// Rescaling is put off: a row's reference maximum moves only when the maximum has
+// grown by more than 2^7, and the pages' V scales (s_v) enter as p * s_v / s_ref in
+// the exponent, with s_ref moving only when a page's scale is over 128 times it; so
+// P stays below 2^14 in fp16 and the accumulator in tensor memory is read back a
+// few times per row and not once per step.
+//
+// What bounds it: per step and tile 2 * 128 * 128 * D multiply-adds, 1024 tensor
+// clocks for D = 128, against 128 exponentials per row thread (the exponential
+// unit) and 16 codes per conversion lane and register.
+#pragma once
+
+#include "kv8_attend.cuh"
+
+namespace qmv {
+namespace prompt {
+
+using attend::Args;
+using attend::ex2;
+using attend::kLn2;
+using attend::kLog2e;
+using attend::Req;
+using kv8::kPage;
+
+constexpr int kThreads = 12 * 32, kConvert = 96;
+constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
+constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
+
+// ---- tcgen05
+__device__ __forceinline__ void tmem_alloc(uint32_t* where) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(core::smem_addr(where)) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(base) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(core::smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 columns of a warp's 32 lanes: a thread gets its lane's row.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+      "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+// Shared-memory operand: K-major rows of 128 bytes (64 fp16), 128-byte swizzle, eight rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t smem) {
+  return (uint64_t)((smem & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// fp16 x fp16 -> fp32, both K-major, 128 x n.
+__device__ __forceinline__ constexpr uint32_t mma_shape(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
+
+template <int D>
+struct Smem {
+  // fp16 tiles in pieces of 64 columns: rows of 128 bytes
+  alignas(1024) unsigned char q[2][D / 64][kRows * 128];
+  alignas(1024) unsigned char k[2][D / 64][kStep * 128];
+  alignas(1024) unsigned char v[2][kStep / 64][D * 128];
+  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  float2 scale[4][2];   // of the step's two pages; x < 0: no such page
+  uint32_t tmem;
+  int tiles_max[12];
+};
+
+// One block's piece of work: up to two row tiles of one (request, KV head).
+struct Item {
+  Req r;
+  int h, row0, tiles;   // first row; row tiles of 128
+  int p0, pages, steps; // pages seen by any of its rows (p0 < 0: none)
+};
+
+template <int D, int TYPE, bool MODS>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
+  constexpr int KH = D / 64;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (warp == 11) tmem_alloc(&sm.tmem);
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      core::mbar_init(&sm.q_full[i], 128);
+      core::mbar_init(&sm.k_full[i], kConvert);
+      core::mbar_init(&sm.k_empty[i], 1);
+      core::mbar_init(&sm.v_full[i], kConvert);
+      core::mbar_init(&sm.v_empty[i], 1);
+      core::mbar_init(&sm.s_full[i], 1);
+      core::mbar_init(&sm.p_full[i], 128);
+      core::mbar_init(&sm.o_full[i], 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // the largest number of row-tile pairs of a request
+  int most = 0;
+  for (int b = tid; b < a.B; b += kThreads) most = max(most, (attend::load_req4(a, b).y * a.G + 2 * kRows - 1) / (2 * kRows));
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if (lane == 0) sm.tiles_max[warp] = most;
+  fence_before();
+  __syncthreads();
+  fence_after();
+#pragma unroll
+  for (int i = 0; i < 12; ++i) most = max(most, sm.tiles_max[i]);
+  const uint32_t tmem = sm.tmem;
+  // Items in the order of their tiles from the last (which sees the most keys) to the first, then request and head; a
+  // block takes every gridDim-th of them.
+  const long long n_items = (long long)most * a.B * a.H;
+  auto item_of = [&](long long i, Item& it) {
+    const int per = a.B * a.H;
+    const int pair = most - 1 - (int)(i / per), rest = (int)(i % per);
+    it.r = attend::make_req(a, rest / a.H, attend::load_req4(a, rest / a.H), kRows);
+    it.h = rest % a.H;
+    it.row0 = pair * 2 * kRows;
+    if (it.row0 >= it.r.rows) return false;
+    it.tiles = it.r.rows - it.row0 > kRows ? 2 : 1;
+    attend::tile_pages(a, it.r, pair, 2 * kRows, it.p0, it.pages);
+    it.steps = (it.pages + 1) / 2;
+    return true;
+  };
+
+  uint32_t n = 0;        // steps taken so far, over all items: stage n & 1, parity (n >> 1) & 1
+
+  if (warp < 8) {
+    // ------------------------------------------------------------------ softmax of tile `tile`: a thread owns a row
+    const int tile = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * 128;
+    uint32_t n_mine = 0;   // steps this tile has taken
+    uint32_t n_out = 0;
+    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
+      Item it;
+      if (!item_of(i, it)) continue;
+      const bool in_use = tile < it.tiles;
+      const int rr = it.row0 + tile * kRows + row;
+      const bool real = rr < it.r.rows;
+      const int tok = min(rr, it.r.rows - 1) / a.G, hq = it.h * a.G + min(rr, it.r.rows - 1) % a.G;
+      float mult = 0.f;
+      if (in_use) {
+        // the row as fp16 with its largest magnitude in [2^13, 2^14)
+        const int64_t at = (int64_t)(it.r.qs + tok) * a.ldq + (int64_t)hq * D;
+        float top = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          attend::load8_as(a.x_type, a.q, at + 8 * c, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
+        }
+        const int e = min(max(13 + 127 - (int)(__float_as_uint(top) >> 23), -126), 126);
+        const float f = real ? core::exp2i(e) : 0.f;
+        mult = core::exp2i(-e) * a.scale;
+        if (!MODS) mult *= kLog2e;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          attend::load8_as(a.x_type, a.q, at + 8 * c, v);
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (real)
+            w = make_uint4(attend::pack_h2(v[0] * f, v[1] * f), attend::pack_h2(v[2] * f, v[3] * f),
+                           attend::pack_h2(v[4] * f, v[5] * f), attend::pack_h2(v[6] * f, v[7] * f));
+          *reinterpret_cast<uint4*>(&sm.q[tile][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = w;
+        }
+      }
+      if (in_use) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        attend::mbar_arrive(&sm.q_full[tile]);
+      }
+
+      const int pos = it.r.ctx - it.r.qlen + tok;
+      const int hi = min(max(pos + 1, it.r.pfx), it.r.ctx);
+      const int lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int hi_all = __reduce_min_sync(0xFFFFFFFFu, hi), lo_all = __reduce_max_sync(0xFFFFFFFFu, lo);
+      const float slope = MODS && a.slopes ? a.slopes[hq] * kLog2e : 0.f;
+      float m = -INFINITY, l = 0.f, s_ref = 0.f;
+      if (in_use) {
+        for (int j = 0; j < it.steps; ++j) {
+          core::mbar_wait(&sm.s_full[tile], n_mine & 1, a.err);
+          fence_after();
+          const float2 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
+          const int key0 = (it.p0 + 2 * j) * kPage;
+          float f0 = fmaxf(mult * sc0.x, 1e-37f), f1 = fmaxf(mult * sc1.x, 1e-37f);
+          const bool slow = MODS || sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          uint32_t x[64];
+          if (slow) {
+            // masks, cap and distance bias: the scores go back as they are wanted, in units of log2
+            const float k2 = MODS && a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(s_at + 32 * c, x);
+              wait_ld();
+              const bool there = (c < 2 ? sc0.x : sc1.x) >= 0.f;
+              const float f = c < 2 ? f0 : f1;
+#pragma unroll
+              for (int q = 0; q < 32; ++q) {
+                const int key = key0 + 32 * c + q;
+                float y = __uint_as_float(x[q]) * f;
+                if (MODS) {
+                  if (a.softcap > 0.f) y = a.softcap - __fdividef(2.f * a.softcap, ex2(y * k2) + 1.f);
+                  y = y * kLog2e - slope * (float)abs(pos - key);
+                }
+                if (!there || key < lo || key >= hi) y = -INFINITY;
+                x[q] = __float_as_uint(y);
+              }
+              tmem_st32(s_at + 32 * c, x);
+            }
+            wait_st();
+            f0 = f1 = 1.f;
+          }
+          tmem_ld32(s_at, x);
+          tmem_ld32(s_at + 32, x + 32);
+          wait_ld();
+#pragma unroll
+          for (int q = 0; q < 64; ++q) mx0 = fmaxf(mx0, __uint_as_float(x[q]));
+          tmem_ld32(s_at + 64, x);
+          tmem_ld32(s_at + 96, x + 32);
+          wait_ld();
+#pragma unroll
+          for (int q = 0; q < 64; ++q) mx1 = fmaxf(mx1, __uint_as_float(x[q]));
+          const float mx = fmaxf(mx0 * f0, mx1 * f1);
+
+          // the references of the maximum and of the V scale, and what O is off by after moving them
+          float fix = 1.f;
+          const float sv = fmaxf(sc0.y, sc1.y);
+          if (sv > s_ref * 128.f) {
+            if (s_ref > 0.f) fix = s_ref / sv;
+            s_ref = sv;
+          }
+          if (mx > m + kSlack || m == -INFINITY) {
+            if (m != -INFINITY) {
+              const float down = ex2(m - mx);
+              fix *= down;
+              l *= down;
+            }
+            m = mx;
+          }
+          if (j > 0 && __any_sync(0xFFFFFFFFu, fix != 1.f)) {
+            uint32_t y[32];
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              tmem_ld32(o_at + 32 * c, y);
+              wait_ld();
+#pragma unroll
+              for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * fix);
+              tmem_st32(o_at + 32 * c, y);
+            }
+          }
+          const float use = m == -INFINITY ? 0.f : m;
+          // page 1 from the registers, then page 0 again: P takes the columns of page 1's scores
+          {
+            const float r = sc1.y > 0.f && s_ref > 0.f ? sc1.y / s_ref : 1.f, off = __log2f(r) - use;
+            float sum = 0.f;
+            uint32_t p[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[2 * q]), f1, off)), p1 = ex2(fmaf(__uint_as_float(x[2 * q + 1]), f1, off));
+              sum += p0 + p1;
+              p[q] = attend::pack_h2(p0, p1);
+            }
+            l += __fdividef(sum, r);
+            tmem_st32(s_at + 96, p);
+          }
+          tmem_ld32(s_at, x);
+          tmem_ld32(s_at + 32, x + 32);
+          wait_ld();
+          {
+            const float r = sc0.y > 0.f && s_ref > 0.f ? sc0.y / s_ref : 1.f, off = __log2f(r) - use;
+            float sum = 0.f;
+            uint32_t p[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) {
+              const float p0 = ex2(fmaf(__uint_as_float(x[2 * q]), f0, off)), p1 = ex2(fmaf(__uint_as_float(x[2 * q + 1]), f0, off));
+              sum += p0 + p1;
+              p[q] = attend::pack_h2(p0, p1);
+            }
+            l += __fdividef(sum, r);
+            tmem_st32(s_at + 64, p);
+          }
+          wait_st();
+          fence_before();
+          attend::mbar_arrive(&sm.p_full[tile]);
+          ++n_mine;
+        }
+        // ---- output
+        core::mbar_wait(&sm.o_full[tile], n_out & 1, a.err);
+        ++n_out;
+        fence_after();
+        const float f = l == 0.f ? 0.f : s_ref / l;
+        const int64_t at = (int64_t)(it.r.qs + tok) * a.ldo + (int64_t)hq * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t y[32];
+          tmem_ld32(o_at + 32 * c, y);
+          wait_ld();
+          if (real) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + k]) * f;
+              kv8::store8_as(a.out_type, a.out, at + 32 * c + 8 * q, v);
+            }
+          }
+        }
+        if (real && a.lse) a.lse[(int64_t)(it.r.qs + tok) * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        fence_before();
+      }
+      n += it.steps;
+    }
+  } else if (warp < 11) {
+    // ------------------------------------------------------------------ pages' codes to fp16 tiles
+    const int w = tid - 256;
+    constexpr int P = kPage * D / 16, U = (P + kConvert - 1) / kConvert;   // 16-byte pieces of a page's tile, and per thread
+    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
+      Item it;
+      if (!item_of(i, it)) continue;
+      int win = -1;          // lane's page of a window of 32
+      uint4 rk[2][U], rv[2][U];
+      float2 sc0 = make_float2(-1.f, 0.f), sc1 = sc0;
+      auto fetch = [&](int j, bool keys, uint4 (&to)[2][U]) {
+        if (keys && (j & 15) == 0) {
+          win = -1;
+          const int p = 2 * j + lane;
+          if (it.p0 >= 0 && p < it.pages) {
+            win = a.table[(int64_t)it.r.b * a.ld_table + it.p0 + p];
+            if (win < 0 || win >= a.n_pages) {
+              atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+              win = -1;
+            }
+          }
+        }
+        constexpr uint32_t zero = TYPE == QMV_KV_INT8 ? 0x80808080u : 0u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int page = __shfl_sync(0xFFFFFFFFu, win, (2 * j + e) & 31);
+          const int64_t at = (int64_t)max(page, 0) * a.H + it.h;
+          const uint4* src = reinterpret_cast<const uint4*>(a.cache + at * (2 * kPage * D) + (keys ? 0 : kPage * D)) + w;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            to[e][u] = page >= 0 && w + kConvert * u < P ? src[kConvert * u] : make_uint4(zero, zero, zero, zero);
+          if (keys) {
+            float2 s = make_float2(-1.f, 0.f);
+            if (page >= 0) s = reinterpret_cast<const float2*>(a.cache + a.scale_off)[at];
+            if (e == 0) sc0 = s;
+            else sc1 = s;
+          }
+        }
+      };
+      // sixteen codes to two 16-byte pieces of a row of 128 bytes
+      auto put = [&](unsigned char* tile, int row, int piece, uint4 x) {
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) attend::codes_to_half<TYPE>(attend::word4(x, k), o[2 * k], o[2 * k + 1]);
+        unsigned char* at = tile + row * 128;
+        *reinterpret_cast<uint4*>(at + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(at + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      };
+      fetch(0, true, rk);
+      fetch(0, false, rv);
+      for (int j = 0; j < it.steps; ++j, ++n) {
+        const int stage = n & 1;
+        const uint32_t parity = ((n >> 1) & 1) ^ 1;
+        core::mbar_wait(&sm.k_empty[stage], parity, a.err);
+        if (w < 2) sm.scale[n & 3][w] = w == 0 ? sc0 : sc1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            // 16-byte piece ((g3 * KH + half) * 8 + g) * 4 + t of the K tile: token 16 (g / 2) + 2 g3 + g % 2, values 64 half + 16 t ..
+            const int q = w + kConvert * u, t = q & 3, g = (q >> 2) & 7, half = KH == 2 ? (q >> 5) & 1 : 0, g3 = q >> (KH == 2 ? 6 : 5);
+            if (q < P) put(sm.k[stage][half], e * 64 + 16 * (g >> 1) + 2 * g3 + (g & 1), t, rk[e][u]);
+          }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        attend::mbar_arrive(&sm.k_full[stage]);
+        // the V codes of step j are on their way since step j - 1; now the K codes of the next step
+        const bool tail = (it.p0 + 2 * j + 2) * kPage > it.r.ctx;   // slots past the request's end may hold any byte
+        const bool more = j + 1 < it.steps;
+        if (more) fetch(j + 1, true, rk);
+        core::mbar_wait(&sm.v_empty[stage], parity, a.err);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int q = w + kConvert * u;   // 16-byte piece: value q / 4, tokens 16 (q % 4) ..
+            uint4 x = rv[e][u];
+            if (TYPE == QMV_KV_E4M3 && tail)
+              x = make_uint4(attend::drop_nan(x.x), attend::drop_nan(x.y), attend::drop_nan(x.z), attend::drop_nan(x.w));
+            if (q < P) put(sm.v[stage][e], q >> 2, q & 3, x);
+          }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        attend::mbar_arrive(&sm.v_full[stage]);
+        if (more) fetch(j + 1, false, rv);
+      }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ the products
+    constexpr uint32_t qk = mma_shape(kStep), pv = mma_shape(D);
+    uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};   // steps and items each tile has taken
+    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
+      Item it;
+      if (!item_of(i, it)) continue;
+      auto scores = [&](int tile, int stage) {
+#pragma unroll
+        for (int hh = 0; hh < KH; ++hh) {
+          const uint64_t qa = operand(core::smem_addr(sm.q[tile][hh])), kb = operand(core::smem_addr(sm.k[stage][hh]));
+#pragma unroll
+          for (int s = 0; s < 4; ++s) mma_ss(tmem + tile * 128, qa + 2 * s, kb + 2 * s, qk, hh + s > 0);
+        }
+        commit(&sm.s_full[tile]);
+      };
+      core::mbar_wait(&sm.k_full[n & 1], (n >> 1) & 1, a.err);
+#pragma unroll
+      for (int tile = 0; tile < 2; ++tile) {
+        if (tile >= it.tiles) continue;
+        core::mbar_wait(&sm.q_full[tile], n_q[tile] & 1, a.err);
+        ++n_q[tile];
+        fence_after();
+        scores(tile, n & 1);
+      }
+      commit(&sm.k_empty[n & 1]);
+      for (int j = 0; j < it.steps; ++j, ++n) {
+        const int stage = n & 1, next = (n + 1) & 1;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+          if (tile >= it.tiles) continue;
+          core::mbar_wait(&sm.p_full[tile], n_p[tile] & 1, a.err);
+          ++n_p[tile];
+          if (tile == 0) core::mbar_wait(&sm.v_full[stage], (n >> 1) & 1, a.err);
+          fence_after();
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t vb = operand(core::smem_addr(sm.v[stage][e]));
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + 64 + (e * 4 + s) * 8, vb + 2 * s, pv, j > 0 || e + s > 0);
+          }
+          if (j + 1 < it.steps) {
+            if (tile == 0) {
+              core::mbar_wait(&sm.k_full[next], ((n + 1) >> 1) & 1, a.err);
+              fence_after();
+            }
+            scores(tile, next);
+          } else {
+            commit(&sm.o_full[tile]);
+          }
+        }
+        commit(&sm.v_empty[stage]);
+        if (j + 1 < it.steps) commit(&sm.k_empty[next]);
+      }
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 11) tmem_free(tmem);
+}
+
+template <int D, int TYPE, bool MODS>
+int launch(const Args& a, int blocks, cudaStream_t s) {
+  const void* f = reinterpret_cast<const void*>(prompt_kernel<D, TYPE, MODS>);
+  int per_sm = 0;
+  int rc = kernel_fit(f, kThreads, sizeof(Smem<D>), &per_sm);
+  if (rc) return rc;
+  prompt_kernel<D, TYPE, MODS><<<blocks, kThreads, sizeof(Smem<D>), s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "kv8_attend launch");
+  return QMV_OK;
+}
+
+// One translation unit per type of codes.
+int launch_int8(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s);
+int launch_e4m3(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s);
+
+template <int TYPE>
+int launch_dim(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s) {
+  if (head_dim == 64) return mods ? launch<64, TYPE, true>(a, blocks, s) : launch<64, TYPE, false>(a, blocks, s);
+  return mods ? launch<128, TYPE, true>(a, blocks, s) : launch<128, TYPE, false>(a, blocks, s);
+}
+
+}  // namespace prompt
+}  // namespace qmv

@@ -1,0 +1,10 @@
+// kv8_attend's prompt kernels for e4m3 codes.
+#include "kv8_prompt.cuh"
+
+namespace qmv {
+namespace prompt {
+int launch_e4m3(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s) {
+  return launch_dim<QMV_KV_E4M3>(a, head_dim, mods, blocks, s);
+}
+}  // namespace prompt
+}  // namespace qmv

@@ -511,6 +511,69 @@ def test_attend_masks_and_scores(env, opt, D, kind, new):
     c.check(**opt)
 
 
+PROMPTS = [   # enough row tiles for the kernel of long prompts: ctx, new, q heads, kv heads
+    ([130], [80], 76, 76), ([300, 64], [129, 64], 80, 40), ([500, 257], [300, 257], 20, 20), ([90, 700, 128], [90, 65, 128], 39, 13),
+    ([1100], [33], 152, 38), ([300, 5, 1], [130, 0, 1], 90, 30), ([129], [129], 152, 76),
+]
+
+
+@pytest.mark.parametrize("shape", range(len(PROMPTS)))
+@pytest.mark.parametrize("D,kind,x,out", [(128, 1, "bf16", "f32"), (64, 2, "f32", "bf16")])
+def test_attend_prompts_match_oracle(env, shape, D, kind, x, out):
+    ctx, new, Hq, H = PROMPTS[shape]
+    c = _Case(env, ctx, new, Hq, H, D, kind, x, seed=40 + shape, pad=shape % 3)
+    c.check(out=out)
+
+
+@pytest.mark.parametrize("opt", [dict(softcap=5.0), dict(softcap=50.0, slopes=True), dict(window=1), dict(window=64), dict(window=100, softcap=20.0),
+                                 dict(prefix=[300, 3]), dict(prefix=[120, 500], window=37), dict(slopes=True, prefix=[900, 1]), dict(scale=3.0)])
+@pytest.mark.parametrize("D,kind", [(128, 2), (64, 1)])
+def test_attend_prompts_masks_and_scores(env, opt, D, kind):
+    opt = dict(opt)
+    c = _Case(env, [421, 200], [70, 200], 44, 22, D, kind, "bf16", seed=60 + len(str(opt)))
+    if opt.get("slopes"):
+        opt["slopes"] = [2.0 ** -(h % 8 + 1) for h in range(44)]
+    c.check(**opt)
+
+
+def test_attend_prompts_rows_that_see_nothing(env):
+    """Fewer cached keys than query rows, a request without a cache, missing pages, scales of many sizes."""
+    q, torch, dev = env
+    c = _Case(env, [70, 0, 300], [100, 70, 65], 60, 30, 64, seed=71)
+    o = c.check()
+    assert not o[:30].any() and not o[100:170].any()
+    assert q.qmv_check_status() == 0
+    table = c.table.copy()
+    table[2, 1] = table[2, 4] = -1
+    table[0, 0] = c.desc.n_pages
+    c.check(table=table)
+    assert q.qmv_check_status() == q.QMV_ERR_CORRUPT
+    c = _Case(env, [400], [80], 80, 40, 128, seed=72, spread=0.0)
+    for i, f in enumerate([1e-6, 1e-2, 1.0, 0.0, 1e3, 30.0, 1e-3]):
+        c.cache_ref.scales[c.table[0, i], :, 1] *= f
+    c.cache_ref.scales[c.table[0, 3], :, 0] = 0
+    c.cache.copy_(torch.from_numpy(c.cache_ref.buf))
+    c.q[0] = 0
+    c.check(scale=0.5)
+    c.check()
+
+
+def test_attend_prompts_are_reproducible_and_follow_max_new(env):
+    q, torch, dev = env
+    c = _Case(env, [900, 650, 80], [300, 200, 80], 40, 20, 128, seed=73)
+    first = c.check()
+    for _ in range(2):
+        assert torch.equal(c.run()[0], first)
+    # the host's bound chooses the kernel; rows past it are served all the same
+    for m in (1, 10, 64, 65):
+        c.check(max_new=m)
+    c.q[7, 3, 1] = math.nan
+    got, _ = c.run()
+    assert torch.isnan(got[7, 3]).all() and int(torch.isnan(got).sum()) == 128
+    got[7, 3] = first[7, 3]
+    assert torch.equal(got, first)
+
+
 def test_attend_rows_that_see_nothing(env):
     """ctx 0, fewer cached keys than query rows, pages that the table does not have."""
     q, torch, dev = env
