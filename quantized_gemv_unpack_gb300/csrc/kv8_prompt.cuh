@@ -8,9 +8,9 @@
 // S = Q K^T with Q and K as fp16, and O += P V with P read from tensor memory and
 // V as it is stored, transposed. Work is split by warps:
 //   warps 0-3, 4-7   softmax of tile 0 and tile 1: a thread owns a row
-//   warps 8-10       load the pages' codes and turn them into fp16 tiles
-//   warp 11          one thread issues the products
-// (twelve warps: a thirteenth would leave each 128 registers in place of 168).
+//   warps 8-14       load the pages' codes and turn them into fp16 tiles
+//   warp 15          one thread issues the products (issued by one lane)
+// with the registers moved from the last eight warps to the softmax (setmaxnreg).
 // The order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1) keeps the tensor cores on one tile
 // while the other's softmax runs, and the commit behind QK_t(j+1) also covers
 // PV_t(j): when a tile's softmax sees its next scores, its O may be rescaled.
@@ -38,9 +38,29 @@ using attend::kLog2e;
 using attend::Req;
 using kv8::kPage;
 
-constexpr int kThreads = 12 * 32, kConvert = 96;
+constexpr int kWarps = 16, kThreads = kWarps * 32, kConvert = 7 * 32;
+// 512 threads are launched with 128 registers each; 256 * 176 + 256 * 80 = 512 * 128
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
+
+// ---- two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // ---- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t* where) {
@@ -54,6 +74,14 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// True in one lane, the same one each time. Products are issued under it by a warp that runs the loop around them as a
+// whole: under a test of the lane number the compiler takes the operands for divergent, and an issue costs 116 clocks in
+// place of the product's own 64.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(core::smem_addr(bar)) : "memory");
 }
@@ -91,6 +119,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // Shared-memory operand: K-major rows of 128 bytes (64 fp16), 128-byte swizzle, eight rows 1024 bytes apart.
 __device__ __forceinline__ uint64_t operand(uint32_t smem) {
   return (uint64_t)((smem & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
@@ -104,10 +150,10 @@ struct Smem {
   alignas(1024) unsigned char q[2][D / 64][kRows * 128];
   alignas(1024) unsigned char k[2][D / 64][kStep * 128];
   alignas(1024) unsigned char v[2][kStep / 64][D * 128];
-  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2];
+  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
   float2 scale[4][2];   // of the step's two pages; x < 0: no such page
   uint32_t tmem;
-  int tiles_max[12];
+  int tiles_max[kWarps];
 };
 
 // One block's piece of work: up to two row tiles of one (request, KV head).
@@ -122,9 +168,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   constexpr int KH = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
-  if (warp == 11) tmem_alloc(&sm.tmem);
+  if (warp == kWarps - 1) tmem_alloc(&sm.tmem);
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       core::mbar_init(&sm.q_full[i], 128);
@@ -133,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       core::mbar_init(&sm.v_full[i], kConvert);
       core::mbar_init(&sm.v_empty[i], 1);
       core::mbar_init(&sm.s_full[i], 1);
-      core::mbar_init(&sm.p_full[i], 128);
+      core::mbar_init(&sm.p_full[i][0], 128);
+      core::mbar_init(&sm.p_full[i][1], 128);
       core::mbar_init(&sm.o_full[i], 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -147,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   fence_after();
 #pragma unroll
-  for (int i = 0; i < 12; ++i) most = max(most, sm.tiles_max[i]);
+  for (int i = 0; i < kWarps; ++i) most = max(most, sm.tiles_max[i]);
   const uint32_t tmem = sm.tmem;
   // Items in the order of their tiles from the last (which sees the most keys) to the first, then request and head; a
   // block takes every gridDim-th of them.
@@ -167,6 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
   uint32_t n = 0;        // steps taken so far, over all items: stage n & 1, parity (n >> 1) & 1
 
+  if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp < 8) {
     // ------------------------------------------------------------------ softmax of tile `tile`: a thread owns a row
     const int tile = warp >> 2, row = tid & 127;
@@ -227,44 +276,36 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const int key0 = (it.p0 + 2 * j) * kPage;
           float f0 = fmaxf(mult * sc0.x, 1e-37f), f1 = fmaxf(mult * sc1.x, 1e-37f);
           const bool slow = MODS || sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          uint32_t x[64];
+          uint32_t x[128];   // the row's scores, until their p goes back to the same columns
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x + 32 * c);
+          wait_ld();
           if (slow) {
-            // masks, cap and distance bias: the scores go back as they are wanted, in units of log2
+            // masks, cap and distance bias: the scores as they are wanted, in units of log2
             const float k2 = MODS && a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(s_at + 32 * c, x);
-              wait_ld();
-              const bool there = (c < 2 ? sc0.x : sc1.x) >= 0.f;
-              const float f = c < 2 ? f0 : f1;
-#pragma unroll
-              for (int q = 0; q < 32; ++q) {
-                const int key = key0 + 32 * c + q;
-                float y = __uint_as_float(x[q]) * f;
-                if (MODS) {
-                  if (a.softcap > 0.f) y = a.softcap - __fdividef(2.f * a.softcap, ex2(y * k2) + 1.f);
-                  y = y * kLog2e - slope * (float)abs(pos - key);
-                }
-                if (!there || key < lo || key >= hi) y = -INFINITY;
-                x[q] = __float_as_uint(y);
+            for (int q = 0; q < 128; ++q) {
+              const int key = key0 + q;
+              float y = __uint_as_float(x[q]) * (q < 64 ? f0 : f1);
+              if (MODS) {
+                if (a.softcap > 0.f) y = a.softcap - __fdividef(2.f * a.softcap, ex2(y * k2) + 1.f);
+                y = y * kLog2e - slope * (float)abs(pos - key);
               }
-              tmem_st32(s_at + 32 * c, x);
+              if ((q < 64 ? sc0.x : sc1.x) < 0.f || key < lo || key >= hi) y = -INFINITY;
+              x[q] = __float_as_uint(y);
             }
-            wait_st();
             f0 = f1 = 1.f;
           }
-          tmem_ld32(s_at, x);
-          tmem_ld32(s_at + 32, x + 32);
-          wait_ld();
+          float top[4];   // of halves of the pages
 #pragma unroll
-          for (int q = 0; q < 64; ++q) mx0 = fmaxf(mx0, __uint_as_float(x[q]));
-          tmem_ld32(s_at + 64, x);
-          tmem_ld32(s_at + 96, x + 32);
-          wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            top[c] = __uint_as_float(x[32 * c]);
 #pragma unroll
-          for (int q = 0; q < 64; ++q) mx1 = fmaxf(mx1, __uint_as_float(x[q]));
-          const float mx = fmaxf(mx0 * f0, mx1 * f1);
+            for (int q = 1; q < 31; q += 2)
+              top[c] = fmaxf(top[c], fmaxf(__uint_as_float(x[32 * c + q]), __uint_as_float(x[32 * c + q + 1])));
+            top[c] = fmaxf(top[c], __uint_as_float(x[32 * c + 31]));
+          }
+          const float mx = fmaxf(fmaxf(top[0], top[1]) * f0, fmaxf(top[2], top[3]) * f1);
 
           // the references of the maximum and of the V scale, and what O is off by after moving them
           float fix = 1.f;
@@ -282,50 +323,48 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             m = mx;
           }
           if (j > 0 && __any_sync(0xFFFFFFFFu, fix != 1.f)) {
-            uint32_t y[32];
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              tmem_ld32(o_at + 32 * c, y);
+            // eight columns at a time: the scores fill the registers
+#pragma unroll 1
+            for (int c = 0; c < D / 8; ++c) {
+              uint32_t y[8];
+              tmem_ld8(o_at + 8 * c, y);
               wait_ld();
 #pragma unroll
-              for (int q = 0; q < 32; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * fix);
-              tmem_st32(o_at + 32 * c, y);
+              for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * fix);
+              tmem_st8(o_at + 8 * c, y);
             }
           }
           const float use = m == -INFINITY ? 0.f : m;
-          // page 1 from the registers, then page 0 again: P takes the columns of page 1's scores
-          {
-            const float r = sc1.y > 0.f && s_ref > 0.f ? sc1.y / s_ref : 1.f, off = __log2f(r) - use;
-            float sum = 0.f;
-            uint32_t p[32];
+          // p = exp2(score + log2 of the V scale over s_ref): sixteen-bit pairs to tensor memory, their sum to l
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[2 * q]), f1, off)), p1 = ex2(fmaf(__uint_as_float(x[2 * q + 1]), f1, off));
-              sum += p0 + p1;
-              p[q] = attend::pack_h2(p0, p1);
-            }
-            l += __fdividef(sum, r);
-            tmem_st32(s_at + 96, p);
-          }
-          tmem_ld32(s_at, x);
-          tmem_ld32(s_at + 32, x + 32);
-          wait_ld();
-          {
-            const float r = sc0.y > 0.f && s_ref > 0.f ? sc0.y / s_ref : 1.f, off = __log2f(r) - use;
-            float sum = 0.f;
-            uint32_t p[32];
+          for (int page = 0; page < 2; ++page) {
+            const float f = page ? f1 : f0, v_scale = page ? sc1.y : sc0.y;
+            const float r = v_scale > 0.f && s_ref > 0.f ? v_scale / s_ref : 1.f;
+            const uint64_t f2 = two(f, f), off = two(__log2f(r) - use, __log2f(r) - use);
+            uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const float p0 = ex2(fmaf(__uint_as_float(x[2 * q]), f0, off)), p1 = ex2(fmaf(__uint_as_float(x[2 * q + 1]), f0, off));
-              sum += p0 + p1;
-              p[q] = attend::pack_h2(p0, p1);
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                const int at = 64 * page + 32 * c + 2 * q;
+                float p0, p1;
+                split(fma2(two(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), f2, off), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                if (q & 1) sum1 = add2(sum1, two(p0, p1));
+                else sum0 = add2(sum0, two(p0, p1));
+                p[q] = attend::pack_h2(p0, p1);
+              }
+              tmem_st16(s_at + 32 * page + 16 * c, p);
             }
-            l += __fdividef(sum, r);
-            tmem_st32(s_at + 64, p);
+            float a0, a1;
+            split(add2(sum0, sum1), a0, a1);
+            l += __fdividef(a0 + a1, r);
+            wait_st();
+            fence_before();
+            attend::mbar_arrive(&sm.p_full[tile][page]);   // the product with this page may begin
           }
-          wait_st();
-          fence_before();
-          attend::mbar_arrive(&sm.p_full[tile]);
           ++n_mine;
         }
         // ---- output
@@ -354,10 +393,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       n += it.steps;
     }
-  } else if (warp < 11) {
+  } else if (warp < kWarps - 1) {
     // ------------------------------------------------------------------ pages' codes to fp16 tiles
     const int w = tid - 256;
     constexpr int P = kPage * D / 16, U = (P + kConvert - 1) / kConvert;   // 16-byte pieces of a page's tile, and per thread
+    int k_at[U], v_at[U];   // where this thread's pieces go in the fp16 tiles
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int q = w + kConvert * u;
+      // 16-byte piece ((g3 * KH + half) * 8 + g) * 4 + t of the K tile: token 16 (g / 2) + 2 g3 + g % 2, values 64 half + 16 t ..
+      const int t = q & 3, g = (q >> 2) & 7, half = KH == 2 ? (q >> 5) & 1 : 0, g3 = q >> (KH == 2 ? 6 : 5);
+      const int row = 16 * (g >> 1) + 2 * g3 + (g & 1);
+      k_at[u] = half * (kStep * 128) + row * 128 + (((2 * t) ^ (row & 7)) << 4);
+      // and of the V tile: value q / 4, tokens 16 (q % 4) ..
+      v_at[u] = (q >> 2) * 128 + (((2 * (q & 3)) ^ ((q >> 2) & 7)) << 4);
+    }
     for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
       Item it;
       if (!item_of(i, it)) continue;
@@ -393,14 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
         }
       };
-      // sixteen codes to two 16-byte pieces of a row of 128 bytes
-      auto put = [&](unsigned char* tile, int row, int piece, uint4 x) {
+      // sixteen codes to two 16-byte pieces of a row of 128 bytes (`at`: the first piece's place, swizzled)
+      auto put = [&](unsigned char* tile, int at, uint4 x) {
         uint32_t o[8];
 #pragma unroll
         for (int k = 0; k < 4; ++k) attend::codes_to_half<TYPE>(attend::word4(x, k), o[2 * k], o[2 * k + 1]);
-        unsigned char* at = tile + row * 128;
-        *reinterpret_cast<uint4*>(at + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(at + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(tile + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(tile + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
       };
       fetch(0, true, rk);
       fetch(0, false, rv);
@@ -412,11 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            // 16-byte piece ((g3 * KH + half) * 8 + g) * 4 + t of the K tile: token 16 (g / 2) + 2 g3 + g % 2, values 64 half + 16 t ..
-            const int q = w + kConvert * u, t = q & 3, g = (q >> 2) & 7, half = KH == 2 ? (q >> 5) & 1 : 0, g3 = q >> (KH == 2 ? 6 : 5);
-            if (q < P) put(sm.k[stage][half], e * 64 + 16 * (g >> 1) + 2 * g3 + (g & 1), t, rk[e][u]);
-          }
+          for (int u = 0; u < U; ++u)
+            if (w + kConvert * u < P) put(sm.k[stage][0] + e * 64 * 128, k_at[u], rk[e][u]);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         attend::mbar_arrive(&sm.k_full[stage]);
         // the V codes of step j are on their way since step j - 1; now the K codes of the next step
@@ -428,18 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int q = w + kConvert * u;   // 16-byte piece: value q / 4, tokens 16 (q % 4) ..
             uint4 x = rv[e][u];
             if (TYPE == QMV_KV_E4M3 && tail)
               x = make_uint4(attend::drop_nan(x.x), attend::drop_nan(x.y), attend::drop_nan(x.z), attend::drop_nan(x.w));
-            if (q < P) put(sm.v[stage][e], q >> 2, q & 3, x);
+            if (w + kConvert * u < P) put(sm.v[stage][e], v_at[u], x);
           }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         attend::mbar_arrive(&sm.v_full[stage]);
         if (more) fetch(j + 1, false, rv);
       }
     }
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------------ the products
     constexpr uint32_t qk = mma_shape(kStep), pv = mma_shape(D);
     uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};   // steps and items each tile has taken
@@ -447,13 +492,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       Item it;
       if (!item_of(i, it)) continue;
       auto scores = [&](int tile, int stage) {
+        if (elected()) {
 #pragma unroll
-        for (int hh = 0; hh < KH; ++hh) {
-          const uint64_t qa = operand(core::smem_addr(sm.q[tile][hh])), kb = operand(core::smem_addr(sm.k[stage][hh]));
+          for (int hh = 0; hh < KH; ++hh) {
+            const uint64_t qa = operand(core::smem_addr(sm.q[tile][hh])), kb = operand(core::smem_addr(sm.k[stage][hh]));
 #pragma unroll
-          for (int s = 0; s < 4; ++s) mma_ss(tmem + tile * 128, qa + 2 * s, kb + 2 * s, qk, hh + s > 0);
+            for (int s = 0; s < 4; ++s) mma_ss(tmem + tile * 128, qa + 2 * s, kb + 2 * s, qk, hh + s > 0);
+          }
+          commit(&sm.s_full[tile]);
         }
-        commit(&sm.s_full[tile]);
+        __syncwarp();
       };
       core::mbar_wait(&sm.k_full[n & 1], (n >> 1) & 1, a.err);
 #pragma unroll
@@ -464,35 +512,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         fence_after();
         scores(tile, n & 1);
       }
-      commit(&sm.k_empty[n & 1]);
+      if (elected()) commit(&sm.k_empty[n & 1]);
+      __syncwarp();
       for (int j = 0; j < it.steps; ++j, ++n) {
         const int stage = n & 1, next = (n + 1) & 1;
+        const bool more = j + 1 < it.steps;
 #pragma unroll
         for (int tile = 0; tile < 2; ++tile) {
           if (tile >= it.tiles) continue;
-          core::mbar_wait(&sm.p_full[tile], n_p[tile] & 1, a.err);
-          ++n_p[tile];
-          if (tile == 0) core::mbar_wait(&sm.v_full[stage], (n >> 1) & 1, a.err);
-          fence_after();
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint64_t vb = operand(core::smem_addr(sm.v[stage][e]));
+            core::mbar_wait(&sm.p_full[tile][e], n_p[tile] & 1, a.err);
+            if (tile == 0 && e == 0) core::mbar_wait(&sm.v_full[stage], (n >> 1) & 1, a.err);
+            fence_after();
+            if (elected()) {
+              const uint64_t vb = operand(core::smem_addr(sm.v[stage][e]));
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + 64 + (e * 4 + s) * 8, vb + 2 * s, pv, j > 0 || e + s > 0);
+              for (int s = 0; s < 4; ++s)
+                mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + (e * 4 + s) * 8, vb + 2 * s, pv, j > 0 || e + s > 0);
+              if (!more && e == 1) commit(&sm.o_full[tile]);
+            }
+            __syncwarp();
           }
-          if (j + 1 < it.steps) {
+          ++n_p[tile];
+          if (more) {
             if (tile == 0) {
               core::mbar_wait(&sm.k_full[next], ((n + 1) >> 1) & 1, a.err);
               fence_after();
             }
             scores(tile, next);
-          } else {
-            commit(&sm.o_full[tile]);
           }
         }
-        commit(&sm.v_empty[stage]);
-        if (j + 1 < it.steps) commit(&sm.k_empty[next]);
+        if (elected()) {
+          commit(&sm.v_empty[stage]);
+          if (more) commit(&sm.k_empty[next]);
+        }
+        __syncwarp();
       }
     }
   }
@@ -500,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 11) tmem_free(tmem);
+  if (warp == kWarps - 1) tmem_free(tmem);
 }
 
 template <int D, int TYPE, bool MODS>
