@@ -34,7 +34,8 @@ int check_workspace(const qmv_kv_desc* desc, const void* workspace, size_t ws_by
   return QMV_OK;
 }
 
-bool prompt_kernel(int64_t rows, int requests, int H) {
+bool prompt_kernel(int64_t rows, int64_t all_rows, int requests, int H) {
+  if ((all_rows / 256 + 1) * requests * H > INT32_MAX) return false;  // its items are numbered in 31 bits
   return rows > 64 && (rows + 255) / 256 * requests * H >= sm_count() / 2;
 }
 
@@ -108,6 +109,10 @@ int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args
   a.Hq = g->n_q_heads;
   a.H = H;
   a.G = g->n_q_heads / H;
+  int log_g = 0;
+  while ((1 << log_g) < a.G) ++log_g;
+  a.g_shift = 31 + log_g;
+  a.g_mul = (uint32_t)(((1ull << a.g_shift) + a.G - 1) / a.G);   // 2^31 for G = 1
   a.q_start = g->q_start;
   a.ctx = g->ctx;
   a.table = g->table;
@@ -128,7 +133,7 @@ int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args
   const bool mods = g->softcap > 0.f || g->slopes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->type == QMV_KV_INT8;
-  if (prompt_kernel(rows, g->n_requests, H)) return i8 ? prompt::launch_int8(a, D, mods, l.blocks, s) : prompt::launch_e4m3(a, D, mods, l.blocks, s);
+  if (prompt_kernel(rows, (int64_t)g->n_tokens * a.G, g->n_requests, H)) return i8 ? prompt::launch_int8(a, D, mods, l.blocks, s) : prompt::launch_e4m3(a, D, mods, l.blocks, s);
   if (D == 64) return i8 ? attend::launch_64_int8(a, tile, mods, l.blocks, s) : attend::launch_64_e4m3(a, tile, mods, l.blocks, s);
   return i8 ? attend::launch_128_int8(a, tile, mods, l.blocks, s) : attend::launch_128_e4m3(a, tile, mods, l.blocks, s);
 }

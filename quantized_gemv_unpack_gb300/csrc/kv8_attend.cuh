@@ -60,6 +60,9 @@ struct Args {
   float* part_o;         // [blocks][kPartRows][D]: the streams' first tiles, then two tiles of the block
   float2* part_ml;       // the same with one (maximum, sum) per row
   int* counters;         // [blocks], zero between calls
+  uint32_t g_mul, g_shift;
+  // n / G for n below 2^31: G's rounded-up reciprocal, exact in this range
+  __device__ __forceinline__ int by_g(int n) const { return (int)(((uint64_t)(uint32_t)n * g_mul) >> g_shift); }
   int limit;             // pages of one tile that a block takes at least before the tile is cut between blocks
   int* err;
 };
@@ -100,7 +103,7 @@ __device__ __forceinline__ int4 load_req4(const Args& a, int b) {
 }
 // Pages [p0, p0 + n) that hold the keys seen by a row tile; p0 = -1, n = 1 where it sees none.
 __device__ __forceinline__ void tile_pages(const Args& a, const Req& r, int tile, int tile_rows, int& p0, int& n) {
-  const int first = tile * tile_rows / a.G, last = (min(r.rows, (tile + 1) * tile_rows) - 1) / a.G;
+  const int first = a.by_g(tile * tile_rows), last = a.by_g(min(r.rows, (tile + 1) * tile_rows) - 1);
   const int base = r.ctx - r.qlen;
   const int hi = min(max(base + last + 1, r.pfx), r.ctx);
   const int lo = a.window > 0 ? max(0, base + first - a.window + 1) : 0;
@@ -191,10 +194,25 @@ __device__ __forceinline__ void store_as(int type, void* base, int64_t i, float 
     *reinterpret_cast<__half2*>(static_cast<__half*>(base) + i) = __floats2half2_rn(x, y);
   }
 }
-__device__ __forceinline__ void load8_as(int type, const void* base, int64_t i, float (&v)[8]) {
-  if (type == QMV_F32) kv8::load8(static_cast<const float*>(base) + i, v);
-  else if (type == QMV_BF16) kv8::load8(static_cast<const __nv_bfloat16*>(base) + i, v);
-  else kv8::load8(static_cast<const __half*>(base) + i, v);
+// N pieces of eight query values at the offsets at[0..N) of q, of the type known at run time (a negative offset: zeros).
+// The type is chosen once around all of them, so that their loads are in flight together.
+template <typename T, int N>
+__device__ __forceinline__ void load_pieces(const void* base, const int64_t (&at)[N], float (&v)[N][8]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (at[i] >= 0) {
+      kv8::load8(static_cast<const T*>(base) + at[i], v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_pieces_as(int type, const void* base, const int64_t (&at)[N], float (&v)[N][8]) {
+  if (type == QMV_BF16) load_pieces<__nv_bfloat16>(base, at, v);
+  else if (type == QMV_F16) load_pieces<__half>(base, at, v);
+  else load_pieces<float>(base, at, v);
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(core::smem_addr(bar)) : "memory");
@@ -252,8 +270,8 @@ __device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OF
       stat[row] = make_float2(use, to_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
       if (!to_out) dst_ml[row] = make_float2(m, l);
       else if (a.lse) {
-        const int rr = row0 + row;
-        a.lse[(int64_t)(qs + rr / a.G) * a.Hq + h * a.G + rr % a.G] = l == 0.f ? -INFINITY : (use + log2f(l)) * kLn2;
+        const int rr = row0 + row, tok = a.by_g(rr);
+        a.lse[(int64_t)(qs + tok) * a.Hq + h * a.G + rr - tok * a.G] = l == 0.f ? -INFINITY : (use + log2f(l)) * kLn2;
       }
     }
   }
@@ -273,8 +291,8 @@ __device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OF
       s.w += w * v.w;
     }
     if (to_out) {
-      const int rr = row0 + row;
-      const int64_t at = (int64_t)(qs + rr / a.G) * a.ldo + (int64_t)(h * a.G + rr % a.G) * D + d;
+      const int rr = row0 + row, tok = a.by_g(rr);
+      const int64_t at = (int64_t)(qs + tok) * a.ldo + (int64_t)(h * a.G + rr - tok * a.G) * D + d;
       store_as(a.out_type, a.out, at, s.x, s.y);
       store_as(a.out_type, a.out, at + 2, s.z, s.w);
     } else {
@@ -493,20 +511,15 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
       int lo[N][2], hi[N][2], pos[N][2];  // keys seen
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int row = min(row0 + 8 * n + g, cw.r.rows - 1);
+        const int row = min(row0 + 8 * n + g, cw.r.rows - 1), row_tok = a.by_g(row);
         const bool real = 8 * n + g < nr;
-        const int64_t at = (int64_t)(cw.r.qs + row / a.G) * a.ldq + (int64_t)(cw.h * a.G + row % a.G) * D;
+        const int64_t at = (int64_t)(cw.r.qs + row_tok) * a.ldq + (int64_t)(cw.h * a.G + row - row_tok * a.G) * D;
         float v[KH * 2][8];
+        int64_t piece[KH * 2];
+#pragma unroll
+        for (int p = 0; p < KH * 2; ++p) piece[p] = real ? at + (p >> 1) * 64 + t * 16 + (p & 1) * 8 : -1;
+        load_pieces_as(a.x_type, a.q, piece, v);
         float m = 0.f;
-#pragma unroll
-        for (int p = 0; p < KH * 2; ++p) {
-          if (real) {
-            load8_as(a.x_type, a.q, at + (p >> 1) * 64 + t * 16 + (p & 1) * 8, v[p]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[p][i] = 0.f;
-          }
-        }
 #pragma unroll
         for (int p = 0; p < KH * 2; ++p)
 #pragma unroll
@@ -525,13 +538,13 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           mult[n][c] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4 * c);
-          const int rr = min(row0 + 8 * n + 2 * t + c, cw.r.rows - 1);
-          pos[n][c] = cw.r.ctx - cw.r.qlen + rr / a.G;
+          const int rr = min(row0 + 8 * n + 2 * t + c, cw.r.rows - 1), tok = a.by_g(rr);
+          pos[n][c] = cw.r.ctx - cw.r.qlen + tok;
           hi[n][c] = min(max(pos[n][c] + 1, cw.r.pfx), cw.r.ctx);
           lo[n][c] = a.window > 0 ? pos[n][c] - a.window + 1 : 0;
           slope[n][c] = 0.f;
           if (MODS) {
-            if (a.slopes) slope[n][c] = a.slopes[cw.h * a.G + rr % a.G] * kLog2e;
+            if (a.slopes) slope[n][c] = a.slopes[cw.h * a.G + rr - tok * a.G] * kLog2e;
           } else {
             mult[n][c] *= kLog2e;
           }
@@ -712,8 +725,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
         const bool real = r8 < nr;
         const float lc = c ? l[n][1] : l[n][0], mc = c ? m[n][1] : m[n][0];
         const float f = whole ? (lc == 0.f ? 0.f : 1.f / lc) : 1.f;
-        const int row = row0 + r8;
-        const int64_t at = (int64_t)(cw.r.qs + row / a.G) * a.ldo + (int64_t)(cw.h * a.G + row % a.G) * D;
+        const int row = row0 + r8, tok = a.by_g(row);
+        const int64_t at = (int64_t)(cw.r.qs + tok) * a.ldo + (int64_t)(cw.h * a.G + row - tok * a.G) * D;
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
           }
         if (real && g < 2) {
           if (!whole) pml[wr * 8 * N + r8] = make_float2(mc, lc);
-          else if (a.lse) a.lse[(int64_t)(cw.r.qs + row / a.G) * a.Hq + cw.h * a.G + row % a.G] = lc == 0.f ? -INFINITY : (mc + log2f(lc)) * kLn2;
+          else if (a.lse) a.lse[(int64_t)(cw.r.qs + tok) * a.Hq + cw.h * a.G + row - tok * a.G] = lc == 0.f ? -INFINITY : (mc + log2f(lc)) * kLn2;
         }
       }
       first_piece = false;

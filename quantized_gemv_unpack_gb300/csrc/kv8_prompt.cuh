@@ -8,7 +8,7 @@
 // S = Q K^T with Q and K as fp16, and O += P V with P read from tensor memory and
 // V as it is stored, transposed. Work is split by warps:
 //   warps 0-3, 4-7   softmax of tile 0 and tile 1: a thread owns a row
-//   warps 8-14       load the pages' codes and turn them into fp16 tiles
+//   warps 8-14       load the query rows and the pages' codes and turn them into fp16 tiles
 //   warp 15          one thread issues the products (issued by one lane)
 // with the registers moved from the last eight warps to the softmax (setmaxnreg).
 // The order PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1) keeps the tensor cores on one tile
@@ -26,6 +26,8 @@
 // unit) and 16 codes per conversion lane and register.
 #pragma once
 
+#include <type_traits>
+
 #include "kv8_attend.cuh"
 
 namespace qmv {
@@ -38,10 +40,11 @@ using attend::kLog2e;
 using attend::Req;
 using kv8::kPage;
 
-constexpr int kWarps = 16, kThreads = kWarps * 32, kConvert = 7 * 32;
-// 512 threads are launched with 128 registers each; 256 * 176 + 256 * 80 = 512 * 128
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+constexpr int kWarps = 16, kThreads = kWarps * 32, kKeyThreads = 128, kValueThreads = 96;
+// 512 threads are launched with 128 registers each; 256 * 168 + 256 * 88 = 512 * 128
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
+constexpr int kItems = 8;                // items the roles may be apart
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
 
 // ---- two fp32 operations in one instruction
@@ -150,8 +153,9 @@ struct Smem {
   alignas(1024) unsigned char q[2][D / 64][kRows * 128];
   alignas(1024) unsigned char k[2][D / 64][kStep * 128];
   alignas(1024) unsigned char v[2][kStep / 64][D * 128];
-  alignas(8) uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
-  float2 scale[4][2];   // of the step's two pages; x < 0: no such page
+  alignas(8) uint64_t item_full[kItems], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
+  float4 scale[4][2];   // of the step's two pages, see below
+  int item[kItems];
   uint32_t tmem;
   int tiles_max[kWarps];
 };
@@ -174,15 +178,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       core::mbar_init(&sm.q_full[i], 128);
-      core::mbar_init(&sm.k_full[i], kConvert);
+      core::mbar_init(&sm.k_full[i], kKeyThreads);
       core::mbar_init(&sm.k_empty[i], 1);
-      core::mbar_init(&sm.v_full[i], kConvert);
+      core::mbar_init(&sm.v_full[i], kValueThreads);
       core::mbar_init(&sm.v_empty[i], 1);
       core::mbar_init(&sm.s_full[i], 1);
       core::mbar_init(&sm.p_full[i][0], 128);
       core::mbar_init(&sm.p_full[i][1], 128);
       core::mbar_init(&sm.o_full[i], 1);
     }
+    for (int i = 0; i < kItems; ++i) core::mbar_init(&sm.item_full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // the largest number of row-tile pairs of a request
@@ -196,12 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) most = max(most, sm.tiles_max[i]);
   const uint32_t tmem = sm.tmem;
-  // Items in the order of their tiles from the last (which sees the most keys) to the first, then request and head; a
-  // block takes every gridDim-th of them.
-  const long long n_items = (long long)most * a.B * a.H;
-  auto item_of = [&](long long i, Item& it) {
+  // Items in the order of their tiles from the last (which sees the most keys) to the first, then request and head.
+  // Blocks take them one after another from a counter: an item's cost varies by its request's context, and which block
+  // computes it does not change its result.
+  const int n_items = most * a.B * a.H;   // at most (rows + 255 B) / 256 * H: below 2^31 for any call the host lets through
+  auto item_of = [&](int i, Item& it) {
     const int per = a.B * a.H;
-    const int pair = most - 1 - (int)(i / per), rest = (int)(i % per);
+    const int pair = most - 1 - i / per, rest = i % per;
     it.r = attend::make_req(a, rest / a.H, attend::load_req4(a, rest / a.H), kRows);
     it.h = rest % a.H;
     it.row0 = pair * 2 * kRows;
@@ -212,7 +218,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     return true;
   };
 
-  uint32_t n = 0;        // steps taken so far, over all items: stage n & 1, parity (n >> 1) & 1
+  // the k-th item of this block, as the converters' first lane publishes it
+  auto next_item = [&](uint32_t k, Item& it) {
+    if (!core::mbar_wait(&sm.item_full[k % kItems], (k / kItems) & 1, a.err)) return false;
+    const int i = sm.item[k % kItems];
+    return i >= 0 && item_of(i, it);
+  };
+
+  uint32_t n = 0;   // steps taken so far, over all items: stage n & 1, parity (n >> 1) & 1
 
   if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -223,45 +236,80 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     const uint32_t s_at = tmem + lanes + tile * 128, o_at = tmem + lanes + 256 + tile * 128;
     uint32_t n_mine = 0;   // steps this tile has taken
     uint32_t n_out = 0;
-    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
-      Item it;
-      if (!item_of(i, it)) continue;
+    // The thread's query row at `at` (negative: zeros) as fp16 with its largest magnitude in [2^13, 2^14); returns the
+    // factor from product to score. 16-bit rows are read in one flight, fp32 rows twice.
+    auto query_row = [&](int64_t at) {
+      const bool wide = a.x_type == QMV_F32;
+      uint4 raw[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 8; ++c) {
+        raw[c] = make_uint4(0, 0, 0, 0);
+        if (at >= 0 && !wide) raw[c] = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at)[c];
+      }
+      auto put = [&](int c, const float (&v)[8], float f) {
+        *reinterpret_cast<uint4*>(&sm.q[tile][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) =
+            make_uint4(attend::pack_h2(v[0] * f, v[1] * f), attend::pack_h2(v[2] * f, v[3] * f),
+                       attend::pack_h2(v[4] * f, v[5] * f), attend::pack_h2(v[6] * f, v[7] * f));
+      };
+      float top = 0.f;
+      if (wide) {
+        const float* x = static_cast<const float*>(a.q) + max(at, (int64_t)0);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          kv8::load8(x + 8 * c, v);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(v[q]));
+        }
+        if (at < 0) top = 0.f;
+      } else {
+        uint32_t most16 = 0;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint32_t x[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) most16 = __vmaxu2(most16, x[q] & 0x7FFF7FFFu);
+        }
+        most16 = max(most16 & 0xFFFFu, most16 >> 16);
+        top = a.x_type == QMV_BF16 ? __uint_as_float(most16 << 16) : __half2float(__ushort_as_half((unsigned short)most16));
+      }
+      const int e = min(max(13 + 127 - (int)(__float_as_uint(top) >> 23), -126), 126);
+      const float f = core::exp2i(e);
+      if (wide) {
+        const float* x = static_cast<const float*>(a.q) + max(at, (int64_t)0);
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          kv8::load8(x + 8 * c, v);
+          put(c, v, at < 0 ? 0.f : f);
+        }
+      } else if (a.x_type == QMV_BF16) {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          kv8::load8(reinterpret_cast<const __nv_bfloat16*>(&raw[c]), v);
+          put(c, v, f);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          float v[8];
+          kv8::load8(reinterpret_cast<const __half*>(&raw[c]), v);
+          put(c, v, f);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      attend::mbar_arrive(&sm.q_full[tile]);
+      return core::exp2i(-e) * a.scale * (MODS ? 1.f : kLog2e);
+    };
+    Item it;
+    for (uint32_t k = 0; next_item(k, it); ++k) {
       const bool in_use = tile < it.tiles;
       const int rr = it.row0 + tile * kRows + row;
       const bool real = rr < it.r.rows;
-      const int tok = min(rr, it.r.rows - 1) / a.G, hq = it.h * a.G + min(rr, it.r.rows - 1) % a.G;
+      const int last = min(rr, it.r.rows - 1), tok = a.by_g(last), hq = it.h * a.G + last - tok * a.G;
       float mult = 0.f;
-      if (in_use) {
-        // the row as fp16 with its largest magnitude in [2^13, 2^14)
-        const int64_t at = (int64_t)(it.r.qs + tok) * a.ldq + (int64_t)hq * D;
-        float top = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          float v[8];
-          attend::load8_as(a.x_type, a.q, at + 8 * c, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[j]));
-        }
-        const int e = min(max(13 + 127 - (int)(__float_as_uint(top) >> 23), -126), 126);
-        const float f = real ? core::exp2i(e) : 0.f;
-        mult = core::exp2i(-e) * a.scale;
-        if (!MODS) mult *= kLog2e;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          float v[8];
-          attend::load8_as(a.x_type, a.q, at + 8 * c, v);
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (real)
-            w = make_uint4(attend::pack_h2(v[0] * f, v[1] * f), attend::pack_h2(v[2] * f, v[3] * f),
-                           attend::pack_h2(v[4] * f, v[5] * f), attend::pack_h2(v[6] * f, v[7] * f));
-          *reinterpret_cast<uint4*>(&sm.q[tile][c >> 3][row * 128 + (((c & 7) ^ (row & 7)) << 4)]) = w;
-        }
-      }
-      if (in_use) {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        attend::mbar_arrive(&sm.q_full[tile]);
-      }
-
+      if (in_use) mult = query_row(real ? (int64_t)(it.r.qs + tok) * a.ldq + (int64_t)hq * D : (int64_t)-1);
       const int pos = it.r.ctx - it.r.qlen + tok;
       const int hi = min(max(pos + 1, it.r.pfx), it.r.ctx);
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
@@ -272,7 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         for (int j = 0; j < it.steps; ++j) {
           core::mbar_wait(&sm.s_full[tile], n_mine & 1, a.err);
           fence_after();
-          const float2 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
+          // per page: K scale (negative: no such page), log2 of r = V scale over its reference, 1 / r; and what O is off by
+          // since the reference moved, and the reference
+          const float4 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
           const int key0 = (it.p0 + 2 * j) * kPage;
           float f0 = fmaxf(mult * sc0.x, 1e-37f), f1 = fmaxf(mult * sc1.x, 1e-37f);
           const bool slow = MODS || sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
@@ -307,13 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           }
           const float mx = fmaxf(fmaxf(top[0], top[1]) * f0, fmaxf(top[2], top[3]) * f1);
 
-          // the references of the maximum and of the V scale, and what O is off by after moving them
-          float fix = 1.f;
-          const float sv = fmaxf(sc0.y, sc1.y);
-          if (sv > s_ref * 128.f) {
-            if (s_ref > 0.f) fix = s_ref / sv;
-            s_ref = sv;
-          }
+          // the reference of the maximum, and what O is off by after moving it
+          float fix = sc0.w;
+          s_ref = sc1.w;
           if (mx > m + kSlack || m == -INFINITY) {
             if (m != -INFINITY) {
               const float down = ex2(m - mx);
@@ -338,9 +384,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           // p = exp2(score + log2 of the V scale over s_ref): sixteen-bit pairs to tensor memory, their sum to l
 #pragma unroll
           for (int page = 0; page < 2; ++page) {
-            const float f = page ? f1 : f0, v_scale = page ? sc1.y : sc0.y;
-            const float r = v_scale > 0.f && s_ref > 0.f ? v_scale / s_ref : 1.f;
-            const uint64_t f2 = two(f, f), off = two(__log2f(r) - use, __log2f(r) - use);
+            const float f = page ? f1 : f0, shift = (page ? sc1.y : sc0.y) - use;
+            const uint64_t f2 = two(f, f), off = two(shift, shift);
             uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -360,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             }
             float a0, a1;
             split(add2(sum0, sum1), a0, a1);
-            l += __fdividef(a0 + a1, r);
+            l += (a0 + a1) * (page ? sc1.z : sc0.z);
             wait_st();
             fence_before();
             attend::mbar_arrive(&sm.p_full[tile][page]);   // the product with this page may begin
@@ -383,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int q = 0; q < 4; ++q) {
               float v[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + k]) * f;
+              for (int x = 0; x < 8; ++x) v[x] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + x]) * f;
               kv8::store8_as(a.out_type, a.out, at + 32 * c + 8 * q, v);
             }
           }
@@ -394,103 +439,142 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       n += it.steps;
     }
   } else if (warp < kWarps - 1) {
-    // ------------------------------------------------------------------ pages' codes to fp16 tiles
-    const int w = tid - 256;
-    constexpr int P = kPage * D / 16, U = (P + kConvert - 1) / kConvert;   // 16-byte pieces of a page's tile, and per thread
-    int k_at[U], v_at[U];   // where this thread's pieces go in the fp16 tiles
+    // ------------------------------------------------------------------ codes to fp16 tiles
+    constexpr int P = kPage * D / 16;   // 16-byte pieces of a page's K or V tile
+    int win = -1;                       // this lane's page of a window of 32
+    // Pages 2 j and 2 j + 1 of the item: their pieces w, w + T, ... of the tile at byte `part` of a page's codes.
+    auto fetch = [&](const Item& it, int j, int part, int w, auto& to, auto threads, float2* sc) {
+      constexpr int T = decltype(threads)::value, U = (P + T - 1) / T;
+      constexpr uint32_t zero = TYPE == QMV_KV_INT8 ? 0x80808080u : 0u;
+      if ((j & 15) == 0) {
+        win = -1;
+        const int p = 2 * j + lane;
+        if (it.p0 >= 0 && p < it.pages) {
+          win = a.table[(int64_t)it.r.b * a.ld_table + it.p0 + p];
+          if (win < 0 || win >= a.n_pages) {
+            atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+            win = -1;
+          }
+        }
+      }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int q = w + kConvert * u;
-      // 16-byte piece ((g3 * KH + half) * 8 + g) * 4 + t of the K tile: token 16 (g / 2) + 2 g3 + g % 2, values 64 half + 16 t ..
-      const int t = q & 3, g = (q >> 2) & 7, half = KH == 2 ? (q >> 5) & 1 : 0, g3 = q >> (KH == 2 ? 6 : 5);
-      const int row = 16 * (g >> 1) + 2 * g3 + (g & 1);
-      k_at[u] = half * (kStep * 128) + row * 128 + (((2 * t) ^ (row & 7)) << 4);
-      // and of the V tile: value q / 4, tokens 16 (q % 4) ..
-      v_at[u] = (q >> 2) * 128 + (((2 * (q & 3)) ^ ((q >> 2) & 7)) << 4);
-    }
-    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
-      Item it;
-      if (!item_of(i, it)) continue;
-      int win = -1;          // lane's page of a window of 32
-      uint4 rk[2][U], rv[2][U];
-      float2 sc0 = make_float2(-1.f, 0.f), sc1 = sc0;
-      auto fetch = [&](int j, bool keys, uint4 (&to)[2][U]) {
-        if (keys && (j & 15) == 0) {
-          win = -1;
-          const int p = 2 * j + lane;
-          if (it.p0 >= 0 && p < it.pages) {
-            win = a.table[(int64_t)it.r.b * a.ld_table + it.p0 + p];
-            if (win < 0 || win >= a.n_pages) {
-              atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
-              win = -1;
+      for (int e = 0; e < 2; ++e) {
+        const int page = __shfl_sync(0xFFFFFFFFu, win, (2 * j + e) & 31);
+        const int64_t at = (int64_t)max(page, 0) * a.H + it.h;
+        const uint4* src = reinterpret_cast<const uint4*>(a.cache + at * (2 * kPage * D) + part) + w;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          to[e * U + u] = make_uint4(zero, zero, zero, zero);
+          if (page >= 0 && w + T * u < P) to[e * U + u] = src[T * u];
+        }
+        if (sc) {
+          sc[e] = make_float2(-1.f, 0.f);
+          if (page >= 0) sc[e] = reinterpret_cast<const float2*>(a.cache + a.scale_off)[at];
+        }
+      }
+    };
+    // sixteen codes to two 16-byte pieces of a row of 128 bytes (`at`: the first piece's place, swizzled)
+    auto put = [&](unsigned char* tile, int at, uint4 x) {
+      uint32_t o[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) attend::codes_to_half<TYPE>(attend::word4(x, k), o[2 * k], o[2 * k + 1]);
+      *reinterpret_cast<uint4*>(tile + at) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(tile + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+    };
+    Item it;
+    if (warp < 12) {
+      // ---------------------------------------------------------------- K, the scales, the items
+      constexpr int T = kKeyThreads, U = (P + T - 1) / T;
+      const int w = tid - 256;
+      int k_at[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // piece ((g3 * KH + half) * 8 + g) * 4 + t: token 16 (g / 2) + 2 g3 + g % 2, values 64 half + 16 t ..
+        const int q = w + T * u, t = q & 3, g = (q >> 2) & 7, half = KH == 2 ? (q >> 5) & 1 : 0, g3 = q >> (KH == 2 ? 6 : 5);
+        const int row = 16 * (g >> 1) + 2 * g3 + (g & 1);
+        k_at[u] = half * (kStep * 128) + row * 128 + (((2 * t) ^ (row & 7)) << 4);
+      }
+      // the first lane takes the block's next item
+      auto take = [&](uint32_t k) {
+        if (w != 0) return;
+        Item next;
+        int i;
+        do i = atomicAdd(a.counters, 1);
+        while (i < n_items && !item_of(i, next));
+        sm.item[k % kItems] = i < n_items ? i : -1;
+        attend::mbar_arrive(&sm.item_full[k % kItems]);
+      };
+      take(0);
+      for (uint32_t k = 0; next_item(k, it); ++k) {
+        uint4 raw[2 * U];
+        float2 sc[2];
+        fetch(it, 0, 0, w, raw, std::integral_constant<int, T>(), sc);
+        float s_ref = 0.f;
+        for (int j = 0; j < it.steps; ++j, ++n) {
+          const int stage = n & 1;
+          core::mbar_wait(&sm.k_empty[stage], ((n >> 1) & 1) ^ 1, a.err);
+          {
+            // the V scales' reference moves where a scale is over 128 times it, and O with it
+            const float sv = fmaxf(sc[0].y, sc[1].y);
+            float fix = 1.f;
+            if (sv > s_ref * 128.f) {
+              if (s_ref > 0.f) fix = s_ref / sv;
+              s_ref = sv;
+            }
+            if (w < 2) {
+              const float y = w ? sc[1].y : sc[0].y, r = y > 0.f ? __fdividef(y, s_ref) : 1.f;
+              sm.scale[n & 3][w] = make_float4(w ? sc[1].x : sc[0].x, __log2f(r), __fdividef(1.f, r), w ? s_ref : fix);
             }
           }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+              if (w + T * u < P) put(sm.k[stage][0] + e * 64 * 128, k_at[u], raw[e * U + u]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          attend::mbar_arrive(&sm.k_full[stage]);
+          if (j + 1 < it.steps) fetch(it, j + 1, 0, w, raw, std::integral_constant<int, T>(), sc);
         }
-        constexpr uint32_t zero = TYPE == QMV_KV_INT8 ? 0x80808080u : 0u;
+        take(k + 1);
+      }
+    } else {
+      // ---------------------------------------------------------------- V
+      constexpr int T = kValueThreads, U = (P + T - 1) / T;
+      const int w = tid - 384;
+      int v_at[U];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int page = __shfl_sync(0xFFFFFFFFu, win, (2 * j + e) & 31);
-          const int64_t at = (int64_t)max(page, 0) * a.H + it.h;
-          const uint4* src = reinterpret_cast<const uint4*>(a.cache + at * (2 * kPage * D) + (keys ? 0 : kPage * D)) + w;
+      for (int u = 0; u < U; ++u) {
+        const int q = w + T * u;   // piece: value q / 4, tokens 16 (q % 4) ..
+        v_at[u] = (q >> 2) * 128 + (((2 * (q & 3)) ^ ((q >> 2) & 7)) << 4);
+      }
+      for (uint32_t k = 0; next_item(k, it); ++k) {
+        uint4 raw[2 * U];
+        fetch(it, 0, kPage * D, w, raw, std::integral_constant<int, T>(), nullptr);
+        for (int j = 0; j < it.steps; ++j, ++n) {
+          const int stage = n & 1;
+          const bool tail = (it.p0 + 2 * j + 2) * kPage > it.r.ctx;   // slots past the request's end may hold any byte
+          core::mbar_wait(&sm.v_empty[stage], ((n >> 1) & 1) ^ 1, a.err);
 #pragma unroll
-          for (int u = 0; u < U; ++u)
-            to[e][u] = page >= 0 && w + kConvert * u < P ? src[kConvert * u] : make_uint4(zero, zero, zero, zero);
-          if (keys) {
-            float2 s = make_float2(-1.f, 0.f);
-            if (page >= 0) s = reinterpret_cast<const float2*>(a.cache + a.scale_off)[at];
-            if (e == 0) sc0 = s;
-            else sc1 = s;
-          }
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              uint4 x = raw[e * U + u];
+              if (TYPE == QMV_KV_E4M3 && tail)
+                x = make_uint4(attend::drop_nan(x.x), attend::drop_nan(x.y), attend::drop_nan(x.z), attend::drop_nan(x.w));
+              if (w + T * u < P) put(sm.v[stage][e], v_at[u], x);
+            }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          attend::mbar_arrive(&sm.v_full[stage]);
+          if (j + 1 < it.steps) fetch(it, j + 1, kPage * D, w, raw, std::integral_constant<int, T>(), nullptr);
         }
-      };
-      // sixteen codes to two 16-byte pieces of a row of 128 bytes (`at`: the first piece's place, swizzled)
-      auto put = [&](unsigned char* tile, int at, uint4 x) {
-        uint32_t o[8];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) attend::codes_to_half<TYPE>(attend::word4(x, k), o[2 * k], o[2 * k + 1]);
-        *reinterpret_cast<uint4*>(tile + at) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint4*>(tile + (at ^ 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-      };
-      fetch(0, true, rk);
-      fetch(0, false, rv);
-      for (int j = 0; j < it.steps; ++j, ++n) {
-        const int stage = n & 1;
-        const uint32_t parity = ((n >> 1) & 1) ^ 1;
-        core::mbar_wait(&sm.k_empty[stage], parity, a.err);
-        if (w < 2) sm.scale[n & 3][w] = w == 0 ? sc0 : sc1;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (w + kConvert * u < P) put(sm.k[stage][0] + e * 64 * 128, k_at[u], rk[e][u]);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        attend::mbar_arrive(&sm.k_full[stage]);
-        // the V codes of step j are on their way since step j - 1; now the K codes of the next step
-        const bool tail = (it.p0 + 2 * j + 2) * kPage > it.r.ctx;   // slots past the request's end may hold any byte
-        const bool more = j + 1 < it.steps;
-        if (more) fetch(j + 1, true, rk);
-        core::mbar_wait(&sm.v_empty[stage], parity, a.err);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            uint4 x = rv[e][u];
-            if (TYPE == QMV_KV_E4M3 && tail)
-              x = make_uint4(attend::drop_nan(x.x), attend::drop_nan(x.y), attend::drop_nan(x.z), attend::drop_nan(x.w));
-            if (w + kConvert * u < P) put(sm.v[stage][e], v_at[u], x);
-          }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        attend::mbar_arrive(&sm.v_full[stage]);
-        if (more) fetch(j + 1, false, rv);
       }
     }
   } else {
     // ------------------------------------------------------------------ the products
     constexpr uint32_t qk = mma_shape(kStep), pv = mma_shape(D);
     uint32_t n_p[2] = {0, 0}, n_q[2] = {0, 0};   // steps and items each tile has taken
-    for (long long i = blockIdx.x; i < n_items; i += gridDim.x) {
-      Item it;
-      if (!item_of(i, it)) continue;
+    Item it;
+    for (uint32_t k = 0; next_item(k, it); ++k) {
       auto scores = [&](int tile, int stage) {
         if (elected()) {
 #pragma unroll
@@ -556,6 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   __syncthreads();
   fence_after();
   if (warp == kWarps - 1) tmem_free(tmem);
+  // the last block leaves the counters as it found them
+  if (tid == 0 && atomicAdd(a.counters + 1, 1) == (int)gridDim.x - 1) a.counters[0] = a.counters[1] = 0;
 }
 
 template <int D, int TYPE, bool MODS>
