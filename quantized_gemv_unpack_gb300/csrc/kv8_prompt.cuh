@@ -41,8 +41,8 @@ using attend::Req;
 using kv8::kPage;
 
 constexpr int kWarps = 16, kThreads = kWarps * 32, kKeyThreads = 128, kValueThreads = 96;
-// 512 threads are launched with 128 registers each; 256 * 168 + 256 * 88 = 512 * 128
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+// 512 threads are launched with 128 registers each; 256 * 176 + 256 * 80 = 512 * 128
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
 constexpr int kItems = 8;                // items the roles may be apart
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
