@@ -68,6 +68,7 @@ struct Args {
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kWeights = 1024;   // factors of a join held in shared memory
 constexpr int kStreamRows = 128, kBlockRows = 256, kPartRows = kStreamRows + kBlockRows;
 
 template <int D, int N, int R>
@@ -240,34 +241,46 @@ struct Smem {
   long long start_off[S::kStreams];
   int start_b[S::kStreams];
   Piece piece[S::kStreams][2];
-  int entry[S::kStreams * 2];
+  const float* entry_o[S::kStreams * 2];
+  const float2* entry_ml[S::kStreams * 2];
   float2 stat[S::kRows];
+  float weights[kWeights];
   long long warp_sum[S::kWarps];
   int warp_segs[S::kWarps];
   int last;
 };
 
 // Join E partial tiles of `rows` rows (ml(e, row): maximum and sum, o(e, row, d): four values) into the output or into
-// (dst_o, dst_ml), by all threads of the block.
+// (dst_o, dst_ml), by all threads of the block. The tiles' factors lie in `weights` (kWeights floats, shared) where they
+// fit, else a factor is taken from its maximum each time.
 template <int D, int THREADS, typename MlFn, typename OFn>
-__device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OFn o, float2* stat, bool to_out, int h, int qs,
-                                     int row0, float* dst_o, float2* dst_ml) {
+__device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OFn o, float2* stat, float* weights, bool to_out,
+                                     int h, int qs, int row0, float* dst_o, float2* dst_ml) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool held = E * rows <= kWeights;
   for (int row = warp; row < rows; row += THREADS / 32) {
-    float m = -INFINITY;
-    for (int e = lane; e < E; e += 32) m = fmaxf(m, ml(e, row).x);
+    float2 mine = make_float2(-INFINITY, 0.f);
+    if (lane < E) mine = ml(lane, row);
+    float m = mine.x;
+    for (int e = lane + 32; e < E; e += 32) m = fmaxf(m, ml(e, row).x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     const float use = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int e = lane; e < E; e += 32) {
+    const float w0 = ex2(mine.x - use);
+    float l = w0 * mine.y;
+    for (int e = lane + 32; e < E; e += 32) {
       const float2 v = ml(e, row);
       l += ex2(v.x - use) * v.y;
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+    const float inv = !to_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
+    if (held) {
+      if (lane < E) weights[lane * rows + row] = w0 * inv;
+      for (int e = lane + 32; e < E; e += 32) weights[e * rows + row] = ex2(ml(e, row).x - use) * inv;
+    }
     if (lane == 0) {
-      stat[row] = make_float2(use, to_out ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+      stat[row] = make_float2(use, inv);
       if (!to_out) dst_ml[row] = make_float2(m, l);
       else if (a.lse) {
         const int rr = row0 + row, tok = a.by_g(rr);
@@ -279,16 +292,20 @@ __device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OF
   constexpr int Q = D / 4;
   for (int u = tid; u < rows * Q; u += THREADS) {
     const int row = u / Q, d = (u % Q) * 4;
-    const float2 st = stat[row];
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int e = 0; e < E; ++e) {
-      const float4 v = o(e, row, d);
-      const float w = ex2(ml(e, row).x - st.x) * st.y;
+    auto add = [&](float4 v, float w) {
       s.x += w * v.x;
       s.y += w * v.y;
       s.z += w * v.z;
       s.w += w * v.w;
+    };
+    if (held) {
+#pragma unroll 6
+      for (int e = 0; e < E; ++e) add(o(e, row, d), weights[e * rows + row]);
+    } else {
+      const float2 st = stat[row];
+#pragma unroll 4
+      for (int e = 0; e < E; ++e) add(o(e, row, d), ex2(ml(e, row).x - st.x) * st.y);
     }
     if (to_out) {
       const int rr = row0 + row, tok = a.by_g(rr);
@@ -356,9 +373,9 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   // blocks costs a trip of the partial tile through L2, about two pages' time of every stream.)
   int A = gridDim.x;
   if (segs < A) {
-    const long long span = (long long)segs * a.limit;
-    const long long want = segs * ((W + span - 1) / span);
-    if (want < A) A = (int)want;
+    const int span = segs * a.limit;   // below 2^13
+    const int want = W < (1ll << 30) ? segs * (int)(((unsigned)W + span - 1) / (unsigned)span) : A;
+    if (want < A) A = want;
   }
   const int cta = blockIdx.x;
   if (cta >= A) return;
@@ -586,21 +603,25 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
           float s[N][4][4];   // tokens of column groups 2i and 2i + 1
           const uint4* kt = reinterpret_cast<const uint4*>(sm.ring[stream][cstage]) + lane;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int n = 0; n < N; ++n)
 #pragma unroll
-            for (int n = 0; n < N; ++n) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
+            for (int i = 0; i < 4; ++i) s[n][i][0] = s[n][i][1] = s[n][i][2] = s[n][i][3] = 0.f;
+          // the four row tiles' chains of products side by side
 #pragma unroll
-            for (int hh = 0; hh < KH; ++hh) {
-              const uint4 wa = kt[(2 * i * KH + hh) * 32], wb = kt[((2 * i + 1) * KH + hh) * 32];
+          for (int hh = 0; hh < KH; ++hh) {
+            uint4 w[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+            for (int j = 0; j < 8; ++j) w[j] = kt[(j * KH + hh) * 32];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
                 uint32_t a0, a1, a2, a3;
-                codes_to_half<TYPE>(word4(wa, k), a0, a2);
-                codes_to_half<TYPE>(word4(wb, k), a1, a3);
+                codes_to_half<TYPE>(word4(w[2 * i], k), a0, a2);
+                codes_to_half<TYPE>(word4(w[2 * i + 1], k), a1, a3);
 #pragma unroll
                 for (int n = 0; n < N; ++n) mma16816(s[n][i], a0, a1, a2, a3, qf[n][hh * 4 + k][0], qf[n][hh * 4 + k][1]);
               }
-            }
           }
 #pragma unroll
           for (int n = 0; n < N; ++n) {
@@ -666,29 +687,37 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
         core::mbar_wait(&sm.full[stream][cstage], cphase, a.err);
         if (there) {
           const uint4* vt = reinterpret_cast<const uint4*>(sm.ring[stream][cstage]) + lane;
+          constexpr int S4 = MT < 4 ? MT : 4;   // row tiles side by side
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            uint4 wa = vt[2 * i * 32], wb = vt[(2 * i + 1) * 32];
-            if (TYPE == QMV_KV_E4M3 && cut_page) {
+          for (int i0 = 0; i0 < MT; i0 += S4) {
+            uint4 w[2 * S4];
+#pragma unroll
+            for (int j = 0; j < 2 * S4; ++j) {
+              w[j] = vt[(2 * i0 + j) * 32];
               // slots past the request's end may hold any byte: a NaN code there would not be hidden by p = 0
-              wa = make_uint4(drop_nan(wa.x), drop_nan(wa.y), drop_nan(wa.z), drop_nan(wa.w));
-              wb = make_uint4(drop_nan(wb.x), drop_nan(wb.y), drop_nan(wb.z), drop_nan(wb.w));
+              if (TYPE == QMV_KV_E4M3 && cut_page) w[j] = make_uint4(drop_nan(w[j].x), drop_nan(w[j].y), drop_nan(w[j].z), drop_nan(w[j].w));
             }
-            float c[N][4];
-#pragma unroll
-            for (int n = 0; n < N; ++n) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t a0, a1, a2, a3;
-              codes_to_half<TYPE>(word4(wa, k), a0, a2);
-              codes_to_half<TYPE>(word4(wb, k), a1, a3);
-#pragma unroll
-              for (int n = 0; n < N; ++n) mma16816(c[n], a0, a1, a2, a3, pf[n][2 * k], pf[n][2 * k + 1]);
-            }
+            float c[N][S4][4];
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) o[n][i][j] = fmaf(c[n][j], scale.y, o[n][i][j] * corr[n][j & 1]);
+              for (int i = 0; i < S4; ++i) c[n][i][0] = c[n][i][1] = c[n][i][2] = c[n][i][3] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int i = 0; i < S4; ++i) {
+                uint32_t a0, a1, a2, a3;
+                codes_to_half<TYPE>(word4(w[2 * i], k), a0, a2);
+                codes_to_half<TYPE>(word4(w[2 * i + 1], k), a1, a3);
+#pragma unroll
+                for (int n = 0; n < N; ++n) mma16816(c[n][i], a0, a1, a2, a3, pf[n][2 * k], pf[n][2 * k + 1]);
+              }
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+              for (int i = 0; i < S4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) o[n][i0 + i][j] = fmaf(c[n][i][j], scale.y, o[n][i0 + i][j] * corr[n][j & 1]);
           }
         }
         release();
@@ -754,20 +783,25 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   __syncthreads();
 
   // ---- join the partial tiles of this block's streams, tile by tile (in the order of the line)
-  for (int e0 = 0; e0 < S::kStreams * 2;) {
-    const Piece pc = (&sm.piece[0][0])[e0];
-    if (pc.len == 0) {
-      ++e0;
-      continue;
-    }
-    int e1 = e0, covered = 0, n_e = 0;
-    for (; e1 < S::kStreams * 2; ++e1) {
-      const Piece& p = (&sm.piece[0][0])[e1];
-      if (p.len == 0) continue;
-      if (p.start != pc.start) break;
-      covered += p.len;
-      if (tid == 0) sm.entry[n_e] = e1;
-      ++n_e;
+  // Lane e of every warp holds entry e's place.
+  long long p_start = -1;
+  int p_len = 0;
+  if (lane < S::kStreams * 2) {
+    p_start = (&sm.piece[0][0])[lane].start;
+    p_len = (&sm.piece[0][0])[lane].len;
+  }
+  unsigned todo = __ballot_sync(0xFFFFFFFFu, p_len > 0);
+  while (todo) {
+    const int e0 = __ffs(todo) - 1;
+    const long long start = __shfl_sync(0xFFFFFFFFu, p_start, e0);
+    const unsigned same = __ballot_sync(0xFFFFFFFFu, p_len > 0 && p_start == start);
+    const int covered = __reduce_add_sync(0xFFFFFFFFu, (same >> lane) & 1 ? p_len : 0), n_e = __popc(same);
+    todo &= ~same;
+    const Piece& pc = (&sm.piece[0][0])[e0];
+    if (warp == 0 && (same >> lane) & 1) {
+      const int at = __popc(same & ((1u << lane) - 1));
+      sm.entry_o[at] = (&sm.piece[0][0])[lane].o;
+      sm.entry_ml[at] = (&sm.piece[0][0])[lane].ml;
     }
     __syncthreads();
     const Req r = get_req(pc.b);
@@ -775,11 +809,9 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     const bool whole = covered == pc.n;
     const int64_t mine_at = (int64_t)cta * kPartRows + kStreamRows + (pc.start < u0 ? 0 : S::kRows);
     join<D, S::kThreads>(
-        a, n_e, rows, [&](int e, int row) { return (&sm.piece[0][0])[sm.entry[e]].ml[row]; },
-        [&](int e, int row, int d) {
-          return *reinterpret_cast<const float4*>((&sm.piece[0][0])[sm.entry[e]].o + row * D + d);
-        },
-        sm.stat, whole, pc.h, r.qs, row0, a.part_o + mine_at * D, a.part_ml + mine_at);
+        a, n_e, rows, [&](int e, int row) { return sm.entry_ml[e][row]; },
+        [&](int e, int row, int d) { return *reinterpret_cast<const float4*>(sm.entry_o[e] + row * D + d); }, sm.stat,
+        sm.weights, whole, pc.h, r.qs, row0, a.part_o + mine_at * D, a.part_ml + mine_at);
     if (!whole) {
       // blocks that hold a part of this tile
       const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
@@ -801,10 +833,9 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
         join<D, S::kThreads>(
             a, c1 - c0 + 1, rows, [&](int e, int row) { return __ldcg(a.part_ml + at(e) + row); },
             [&](int e, int row, int d) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + (at(e) + row) * D + d)); },
-            sm.stat, true, pc.h, r.qs, row0, nullptr, nullptr);
+            sm.stat, sm.weights, true, pc.h, r.qs, row0, nullptr, nullptr);
       }
     }
-    e0 = e1;
   }
 }
 
