@@ -73,14 +73,16 @@ constexpr int kStreamRows = 128, kBlockRows = 256, kPartRows = kStreamRows + kBl
 
 template <int D, int N, int R>
 struct Shape {
-  // eight rows per warp need few registers: twelve warps hide the latency of a page's chain better than eight
-  static constexpr int kWarps = N == 1 ? 12 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStreams = kWarps / R;
-  static constexpr int kTile = kPage * D;                                // bytes of a K or V tile
-  static constexpr int kStages = 192 * 1024 / kStreams / kTile;          // 2 tiles of 128 for N = 1, 3 R for N = 2
+  static constexpr int kTile = kPage * D;   // bytes of a K or V tile
+  // A ring of 128 KB: a tile of K and one of V for each warp (D = 128). With 64 requests up to 16384 tokens (1.16 GB): 188 us;
+  // 195 with 192 KB, and 199 with twelve warps and 192 KB, because more bytes in flight are shared out less evenly between
+  // near and far SMs and the slowest block ends the call; 194 with six warps.
+  static constexpr int kStages = 128 * 1024 / kStreams / kTile;
   static constexpr int kRows = 8 * N * R;
-  static constexpr int kReqs = 256;                                      // requests kept in shared memory
+  static constexpr int kReqs = 256;   // requests kept in shared memory
 };
 
 struct Req {
@@ -331,23 +333,26 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the line of units, and where this block's streams begin
-  const int per = (a.B + S::kThreads - 1) / S::kThreads;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  long long mine = 0;
-  int segs = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int4 v = load_req4(a, b);
-    if (b < S::kReqs) sm.req[b] = v;
-    const Req r = make_req(a, b, v, S::kRows);
-    mine += req_units(a, r, S::kRows);
-    segs += r.tiles * a.H;
-  }
   if (tid < S::kStreams * S::kStages) {
     core::mbar_init(&sm.full[0][0] + tid, 2);
     core::mbar_init(&sm.empty[0][0] + tid, R);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < S::kStreams * 2) (&sm.piece[0][0] + tid)->len = 0;
+  // Up to 32 requests: lane b of every warp holds request b, and each warp sums for itself.
+  const bool few = a.B <= 32;
+  int4 held = make_int4(0, 0, 0, 0);
+  long long mine = 0, before = 0, W = 0;   // units of this thread's requests, of those before them, of all
+  int segs = 0;
+  const int per = few ? 1 : (a.B + S::kThreads - 1) / S::kThreads;
+  const int b0 = few ? lane : min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  for (int b = b0; b < b1; ++b) {
+    held = load_req4(a, b);
+    if (!few && b < S::kReqs) sm.req[b] = held;
+    const Req r = make_req(a, b, held, S::kRows);
+    mine += req_units(a, r, S::kRows);
+    segs += r.tiles * a.H;
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -355,19 +360,23 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     if (lane >= o) incl += u;
   }
   segs = __reduce_add_sync(0xFFFFFFFFu, segs);
-  if (lane == 31) {
-    sm.warp_sum[warp] = incl;
-    sm.warp_segs[warp] = segs;
-  }
-  __syncthreads();
-  long long before = 0, W = 0;
-  segs = 0;
+  if (few) {
+    W = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  } else {
+    if (lane == 31) {
+      sm.warp_sum[warp] = incl;
+      sm.warp_segs[warp] = segs;
+    }
+    __syncthreads();
+    segs = 0;
 #pragma unroll
-  for (int w = 0; w < S::kWarps; ++w) {
-    if (w < warp) before += sm.warp_sum[w];
-    W += sm.warp_sum[w];
-    segs += sm.warp_segs[w];
+    for (int w = 0; w < S::kWarps; ++w) {
+      if (w < warp) before += sm.warp_sum[w];
+      W += sm.warp_sum[w];
+      segs += sm.warp_segs[w];
+    }
   }
+  before += incl - mine;
   if (W == 0) return;
   // blocks in use: as many per tile as it has `limit`s of pages on average, all of them at most. (A cut between
   // blocks costs a trip of the partial tile through L2, about two pages' time of every stream.)
@@ -383,27 +392,45 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   const long long u0 = blocks.at(cta);
   const int units = (int)(blocks.at(cta + 1) - u0);
   const Cut streams = cut(units, S::kStreams);
-  {
-    long long P = before + incl - mine;
-    if (P < u0 + units && P + mine > u0) {
-      for (int b = b0; b < b1; ++b) {
-        const long long ub = per == 1 ? mine : req_units(a, make_req(a, b, load_req4(a, b), S::kRows), S::kRows);
-        for (int i = 0; i < S::kStreams; ++i) {
-          const long long x = u0 + streams.at(i);
-          if (P <= x && x < P + ub) {
-            sm.start_b[i] = b;
-            sm.start_off[i] = x - P;
-            sm.start_base[i] = P;
-          }
+  int start_b = 0;
+  long long start_off = 0, start_base = 0;   // this stream's first unit: its request, its place there, where that begins
+  if (few) {
+    const long long x = u0 + streams.at(stream);
+    start_b = __popc(__ballot_sync(0xFFFFFFFFu, before + mine <= x));
+    start_base = __shfl_sync(0xFFFFFFFFu, before, start_b & 31);
+    start_off = x - start_base;
+  } else if (before < u0 + units && before + mine > u0) {
+    long long P = before;
+    for (int b = b0; b < b1; ++b) {
+      const long long ub = per == 1 ? mine : req_units(a, make_req(a, b, load_req4(a, b), S::kRows), S::kRows);
+      for (int i = 0; i < S::kStreams; ++i) {
+        const long long x = u0 + streams.at(i);
+        if (P <= x && x < P + ub) {
+          sm.start_b[i] = b;
+          sm.start_off[i] = x - P;
+          sm.start_base[i] = P;
         }
-        P += ub;
       }
+      P += ub;
     }
   }
   __syncthreads();
+  if (!few) {
+    start_b = sm.start_b[stream];
+    start_off = sm.start_off[stream];
+    start_base = sm.start_base[stream];
+  }
   int left = (int)(streams.at(stream + 1) - streams.at(stream));
 
-  auto get_req = [&](int b) { return make_req(a, b, b < S::kReqs ? sm.req[b] : load_req4(a, b), S::kRows); };
+  auto get_req = [&](int b) {
+    int4 v;
+    if (few)
+      v = make_int4(__shfl_sync(0xFFFFFFFFu, held.x, b), __shfl_sync(0xFFFFFFFFu, held.y, b), __shfl_sync(0xFFFFFFFFu, held.z, b),
+                    __shfl_sync(0xFFFFFFFFu, held.w, b));
+    else
+      v = b < S::kReqs ? sm.req[b] : load_req4(a, b);
+    return make_req(a, b, v, S::kRows);
+  };
   auto walk_next = [&](Walk& w) {
     w.start += w.n;
     if (++w.h < a.H) return;
@@ -426,8 +453,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     Walk cw;   // the tile being computed
     int cp;    // page within it
     {
-      long long off = sm.start_off[stream], base = sm.start_base[stream];
-      cw.r = get_req(sm.start_b[stream]);
+      long long off = start_off, base = start_base;
+      cw.r = get_req(start_b);
       cw.tile = 0;
       for (;;) {
         tile_pages(a, cw.r, cw.tile, S::kRows, cw.p0, cw.n);
