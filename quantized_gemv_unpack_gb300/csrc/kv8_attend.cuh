@@ -73,7 +73,7 @@ constexpr int kStreamRows = 128, kBlockRows = 256, kPartRows = kStreamRows + kBl
 
 template <int D, int N, int R>
 struct Shape {
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = D == 64 && N == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kStreams = kWarps / R;
   static constexpr int kTile = kPage * D;   // bytes of a K or V tile
@@ -81,6 +81,7 @@ struct Shape {
   // 195 with 192 KB, and 199 with twelve warps and 192 KB, because more bytes in flight are shared out less evenly between
   // near and far SMs and the slowest block ends the call; 194 with six warps.
   static constexpr int kStages = 128 * 1024 / kStreams / kTile;
+  static_assert(kStages % 2 == 0, "K in even stages, V in odd ones");
   static constexpr int kRows = 8 * N * R;
   static constexpr int kReqs = 256;   // requests kept in shared memory
 };
@@ -217,6 +218,12 @@ __device__ __forceinline__ void load_pieces_as(int type, const void* base, const
   else if (type == QMV_F16) load_pieces<__half>(base, at, v);
   else load_pieces<float>(base, at, v);
 }
+// True in one lane of a warp, the same one each time.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(core::smem_addr(bar)) : "memory");
 }
@@ -249,7 +256,7 @@ struct Smem {
   float weights[kWeights];
   long long warp_sum[S::kWarps];
   int warp_segs[S::kWarps];
-  int last;
+  int last[2];
 };
 
 // Join E partial tiles of `rows` rows (ml(e, row): maximum and sum, o(e, row, d): four values) into the output or into
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
 
   // ---- the line of units, and where this block's streams begin
   if (tid < S::kStreams * S::kStages) {
-    core::mbar_init(&sm.full[0][0] + tid, 2);
+    core::mbar_init(&sm.full[0][0] + tid, tid % 2 ? 1 : 2);   // K tiles (even stages) come with their page's scales
     core::mbar_init(&sm.empty[0][0] + tid, R);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -470,7 +477,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     }
     Walk iw = cw;   // the tile being fetched
     int ip = cp, ileft = left;
-    int win_page = -1, win_at = 0, win_n = 0;   // this lane's page of a window of up to 32 units
+    int win_at = 0, win_n = 0;
+    long long win_off = -1;   // this lane's page of a window of up to 32 units: where its codes of this head begin
     bool fetch_v = false;
     int istage = 0;
     uint32_t iphase = 1;   // parity of the empty barrier's phase that a first use passes at once
@@ -480,33 +488,31 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
       if (!fetch_v && win_at == win_n) {
         win_at = 0;
         win_n = min(32, min(iw.n - ip, ileft));
-        win_page = -1;
+        win_off = -1;
         if (lane < win_n && iw.p0 >= 0) {
           const int id = a.table[(int64_t)iw.r.b * a.ld_table + iw.p0 + ip + lane];
-          if (id >= 0 && id < a.n_pages) win_page = id;
+          if (id >= 0 && id < a.n_pages) win_off = ((int64_t)id * a.H + iw.h) * (2 * S::kTile);
           else atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
         }
       }
-      const int page = __shfl_sync(0xFFFFFFFFu, win_page, win_at);
-      if (lane == 0) {
+      const long long off = __shfl_sync(0xFFFFFFFFu, win_off, win_at);
+      if (elected()) {
         if (R > 1) core::mbar_wait(&sm.empty[stream][istage], iphase, a.err);
         uint64_t* bar = &sm.full[stream][istage];
-        if (page >= 0) {
-          const int64_t at = (int64_t)page * a.H + iw.h;
-          const unsigned char* src = a.cache + at * (2 * S::kTile) + (fetch_v ? S::kTile : 0);
+        if (off >= 0) {
           core::mbar_arrive_expect_tx(bar, S::kTile);
-          core::bulk_g2s(sm.ring[stream][istage], src, S::kTile, bar);
+          core::bulk_g2s(sm.ring[stream][istage], a.cache + off + (fetch_v ? S::kTile : 0), S::kTile, bar);
           if (!fetch_v) {
             asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(core::smem_addr(&sm.scale[stream][istage])),
-                         "l"(a.cache + a.scale_off + at * 8)
+                         "l"(a.cache + a.scale_off + off / (2 * S::kTile) * 8)
                          : "memory");
             asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(core::smem_addr(bar)) : "memory");
-          } else {
-            mbar_arrive(bar);
           }
         } else {
-          sm.scale[stream][istage] = make_float2(-1.f, -1.f);
-          mbar_arrive(bar);
+          if (!fetch_v) {
+            sm.scale[stream][istage] = make_float2(-1.f, -1.f);
+            mbar_arrive(bar);
+          }
           mbar_arrive(bar);
         }
       }
@@ -818,6 +824,10 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     p_len = (&sm.piece[0][0])[lane].len;
   }
   unsigned todo = __ballot_sync(0xFFFFFFFFu, p_len > 0);
+  int shared_tiles[2] = {-1, -1};   // entries of the (at most two) tiles that other blocks hold a part of
+  auto slot_of = [&](const Piece& pc, int c) {   // the rows where block c leaves its part of the tile
+    return (int64_t)c * kPartRows + kStreamRows + (pc.start < blocks.at(c) ? 0 : S::kRows);
+  };
   while (todo) {
     const int e0 = __ffs(todo) - 1;
     const long long start = __shfl_sync(0xFFFFFFFFu, p_start, e0);
@@ -834,35 +844,41 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     const Req r = get_req(pc.b);
     const int row0 = pc.tile * S::kRows, rows = min(S::kRows, r.rows - row0);
     const bool whole = covered == pc.n;
-    const int64_t mine_at = (int64_t)cta * kPartRows + kStreamRows + (pc.start < u0 ? 0 : S::kRows);
+    const int64_t mine_at = slot_of(pc, cta);
+    if (!whole) {
+      if (shared_tiles[0] < 0) shared_tiles[0] = e0;
+      else shared_tiles[1] = e0;
+    }
     join<D, S::kThreads>(
         a, n_e, rows, [&](int e, int row) { return sm.entry_ml[e][row]; },
         [&](int e, int row, int d) { return *reinterpret_cast<const float4*>(sm.entry_o[e] + row * D + d); }, sm.stat,
         sm.weights, whole, pc.h, r.qs, row0, a.part_o + mine_at * D, a.part_ml + mine_at);
-    if (!whole) {
-      // blocks that hold a part of this tile
-      const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        const int old = atomicAdd(a.counters + c0, 1);
-        sm.last = old == c1 - c0;
-        if (sm.last) a.counters[c0] = 0;
-        __threadfence();
-      }
-      __syncthreads();
-      if (sm.last) {
-        auto at = [&](int e) {
-          const int c = c0 + e;
-          return (int64_t)c * kPartRows + kStreamRows + (pc.start < blocks.at(c) ? 0 : S::kRows);
-        };
-        // written by other blocks during this launch: read past L1
-        join<D, S::kThreads>(
-            a, c1 - c0 + 1, rows, [&](int e, int row) { return __ldcg(a.part_ml + at(e) + row); },
-            [&](int e, int row, int d) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + (at(e) + row) * D + d)); },
-            sm.stat, sm.weights, true, pc.h, r.qs, row0, nullptr, nullptr);
-      }
-    }
+  }
+  if (shared_tiles[0] < 0) return;
+  // ---- the last of a tile's blocks to arrive joins their parts
+  __threadfence();
+  __syncthreads();
+  if (tid < 2 && (tid ? shared_tiles[1] : shared_tiles[0]) >= 0) {
+    const Piece& pc = (&sm.piece[0][0])[tid ? shared_tiles[1] : shared_tiles[0]];
+    const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
+    const int old = atomicAdd(a.counters + c0, 1);
+    sm.last[tid] = old == c1 - c0;
+    if (old == c1 - c0) a.counters[c0] = 0;
+    __threadfence();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (shared_tiles[i] < 0 || !sm.last[i]) continue;
+    const Piece& pc = (&sm.piece[0][0])[shared_tiles[i]];
+    const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
+    const Req r = get_req(pc.b);
+    const int row0 = pc.tile * S::kRows, rows = min(S::kRows, r.rows - row0);
+    // written by other blocks during this launch: read past L1
+    join<D, S::kThreads>(
+        a, c1 - c0 + 1, rows, [&](int e, int row) { return __ldcg(a.part_ml + slot_of(pc, c0 + e) + row); },
+        [&](int e, int row, int d) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(pc, c0 + e) + row) * D + d)); },
+        sm.stat, sm.weights, true, pc.h, r.qs, row0, nullptr, nullptr);
   }
 }
 

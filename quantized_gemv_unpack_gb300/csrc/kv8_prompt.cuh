@@ -77,14 +77,8 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// True in one lane, the same one each time. Products are issued under it by a warp that runs the loop around them as a
-// whole: under a test of the lane number the compiler takes the operands for divergent, and an issue costs 116 clocks in
-// place of the product's own 64.
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
-  return r != 0;
-}
+// Products are issued under attend::elected() by a warp that runs the loop around them as a whole: under a test of the lane
+// number the compiler takes the operands for divergent, and an issue costs 116 clocks in place of the product's own 64.
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(core::smem_addr(bar)) : "memory");
 }
@@ -576,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     Item it;
     for (uint32_t k = 0; next_item(k, it); ++k) {
       auto scores = [&](int tile, int stage) {
-        if (elected()) {
+        if (attend::elected()) {
 #pragma unroll
           for (int hh = 0; hh < KH; ++hh) {
             const uint64_t qa = operand(core::smem_addr(sm.q[tile][hh])), kb = operand(core::smem_addr(sm.k[stage][hh]));
@@ -596,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         fence_after();
         scores(tile, n & 1);
       }
-      if (elected()) commit(&sm.k_empty[n & 1]);
+      if (attend::elected()) commit(&sm.k_empty[n & 1]);
       __syncwarp();
       for (int j = 0; j < it.steps; ++j, ++n) {
         const int stage = n & 1, next = (n + 1) & 1;
@@ -609,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             core::mbar_wait(&sm.p_full[tile][e], n_p[tile] & 1, a.err);
             if (tile == 0 && e == 0) core::mbar_wait(&sm.v_full[stage], (n >> 1) & 1, a.err);
             fence_after();
-            if (elected()) {
+            if (attend::elected()) {
               const uint64_t vb = operand(core::smem_addr(sm.v[stage][e]));
 #pragma unroll
               for (int s = 0; s < 4; ++s)
@@ -627,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             scores(tile, next);
           }
         }
-        if (elected()) {
+        if (attend::elected()) {
           commit(&sm.v_empty[stage]);
           if (more) commit(&sm.k_empty[next]);
         }
