@@ -1,12 +1,12 @@
 // Block tables, slot maps and run lists of one serving step, built on the GPU
 // from the requests' lengths (kv_plan).
 //
-// Per request the step needs three exclusive sums: of new tokens (q_start), of
-// new pages (place in the ring of free pages) and of runs or returned pages. A
-// block takes them over all requests with warp scans: 1 to 8 requests per
-// thread, a few hundred cycles. Then every token finds its request by binary
-// search in the sums (shared memory) and writes its slot, its position, its
-// table entry if it opens a page and its run if it heads one. Nothing here is
+// Per request the step needs exclusive sums of new tokens (q_start), of new pages
+// (place in the ring of free pages), of runs and of returned pages. A block takes
+// them over all requests with three scans: 1 to 8 requests per thread. Then every
+// thread finds the request of its four tokens by binary search in the sums
+// (shared memory) and writes their slots and positions, the table's entry of a
+// page that one of them opens and the run that one of them heads. Nothing here is
 // worth bandwidth: a step of 64 requests moves 6 KB, and the time is that of the
 // launch and of three dependent loads (lengths; ring state; table or ring).
 //
@@ -21,7 +21,7 @@ namespace qmv {
 namespace {
 
 constexpr int kMaxPlanThreads = 1024;
-constexpr int kPlanCluster = 8;
+constexpr int kPlanCluster = 8;   // blocks: the largest cluster that every device of this kind schedules
 
 struct Scratch {   // per request, in dynamic shared memory
   int32_t* start;  // first token (at most T)
@@ -31,36 +31,52 @@ struct Scratch {   // per request, in dynamic shared memory
   int32_t* status;
 };
 
-// Exclusive sum over the block's threads of one value per thread; *total gets the sum.
-__device__ long long block_scan(long long v, long long* total, long long* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = (blockDim.x + 31) >> 5;
-  long long s = v;
+// Sums stop at kMost (past any count of tokens or pages that a call can serve, and small enough to add two).
+constexpr int kMost = 1 << 30;
+__device__ __forceinline__ int add_most(int a, int b) { return min(a + b, kMost); }
+
+// Exclusive sums over the block's threads of K values per thread, with the totals. Every warp sums the warps' sums for
+// itself, so a scan has one barrier; `sums` is not used again by the next one.
+template <int K>
+__device__ __forceinline__ void block_scan(int (&v)[K], int (&total)[K], int (*sums)[32]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int s[K], w[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-    if (lane >= o) s += u;
-  }
-  __syncthreads();  // the previous scan's sums have been read
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = lane < warps ? warp_sums[lane] : 0;
+  for (int k = 0; k < K; ++k) s[k] = v[k];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xFFFFFFFFu, w, o);
-      if (lane >= o) w += u;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, s[k], o);
+      if (lane >= o) s[k] = add_most(s[k], u);
     }
-    warp_sums[lane] = w;
-  }
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < K; ++k) sums[k][warp] = s[k];
   __syncthreads();
-  *total = warp_sums[warps - 1];
-  return (warp ? warp_sums[warp - 1] : 0) + s - v;
+#pragma unroll
+  for (int k = 0; k < K; ++k) w[k] = lane < warps ? sums[k][lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, w[k], o);
+      if (lane >= o) w[k] = add_most(w[k], u);
+    }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    total[k] = __shfl_sync(0xFFFFFFFFu, w[k], 31);
+    const int before_warp = __shfl_sync(0xFFFFFFFFu, w[k], (warp + 31) & 31);
+    int before_lane = __shfl_up_sync(0xFFFFFFFFu, s[k], 1);   // a stopped sum cannot be undone by subtraction
+    if (lane == 0) before_lane = 0;
+    v[k] = add_most(warp ? before_warp : 0, before_lane);
+  }
 }
 
 __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_constant__ kv_plan_args a, int n_blocks,
                                                                   int* err) {
   extern __shared__ int32_t plan_smem[];
-  __shared__ long long warp_sums[32];
+  __shared__ int warp_sums[5][32];
   const int B = a.n_requests, T = a.n_tokens, N = a.n_pages;
   const Scratch s{plan_smem, plan_smem + B, plan_smem + 2 * B, plan_smem + 3 * B, plan_smem + 4 * B};
   const int tid = threadIdx.x, nt = blockDim.x;
@@ -76,52 +92,53 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
   }
 
   // tokens
-  long long sum = 0, total;
-  for (int b = b0; b < b1; ++b) sum += max(a.add[b], 0);
-  long long at = block_scan(sum, &total, warp_sums);
-  const int n_tokens = (int)min((long long)T, total);
-  long long need_sum = 0;
+  int sum[1] = {0}, total[1];
+  for (int b = b0; b < b1; ++b) sum[0] = add_most(sum[0], min(max(a.add[b], 0), kMost));
+  block_scan<1>(sum, total, warp_sums);
+  const int n_tokens = min(T, total[0]);
+  int at = sum[0], need[1] = {0};
   for (int b = b0; b < b1; ++b) {
     const int len = a.lens[b], add = a.add[b];
-    const long long tok = max(add, 0);
-    const long long held = ((long long)len + 63) >> 6, after = ((long long)len + tok + 63) >> 6;
-    const bool bad = len < 0 || held > a.max_pages || after > a.max_pages || at + tok > T;
-    s.start[b] = (int)min(at, (long long)T);
+    const int tok = min(max(add, 0), kMost);
+    const int held = (int)(((long long)len + 63) >> 6);
+    const long long after = ((long long)len + tok + 63) >> 6;
+    const bool bad = len < 0 || held > a.max_pages || after > a.max_pages || at + tok > T;   // at + tok is at most 2^31 - 2^30
+    s.start[b] = min(at, T);
     s.len[b] = len;
     s.status[b] = bad ? 2 : (add < 0 ? 3 : 0);
-    if (!bad && add > 0) need_sum += after - held;
-    at += tok;
+    if (!bad && add > 0) need[0] = add_most(need[0], (int)after - held);
+    at = add_most(at, tok);
   }
   // new pages: a request is short of pages where the needs up to its own exceed what is free
-  long long need_at = block_scan(need_sum, &total, warp_sums);
-  long long run_sum = 0, back_sum = 0, taken = 0;
+  block_scan<1>(need, total, warp_sums + 1);
+  int need_at = need[0];
+  int sums3[3] = {0, 0, 0}, total3[3];   // runs, returned pages, pages taken
   for (int b = b0; b < b1; ++b) {
-    const int len = s.len[b], add = max(a.add[b], 0);
-    const int held = (int)(((long long)len + 63) >> 6);
-    if (s.status[b] == 3) back_sum += held;
+    const int len = s.len[b];
+    if (s.status[b] == 3) sums3[1] = add_most(sums3[1], (len + 63) >> 6);
     if (s.status[b] != 0) continue;
-    const int need = (int)(((long long)len + add + 63) >> 6) - held;
-    s.page[b] = (int)min(need_at, (long long)INT32_MAX);
-    need_at += need;
-    if (need > 0 && need_at > count) {
+    const int add = max(a.add[b], 0);   // served so far: at most T
+    const int held = (len + 63) >> 6, want = ((len + add + 63) >> 6) - held;
+    s.page[b] = need_at;
+    need_at = add_most(need_at, want);
+    if (want > 0 && need_at > count) {
       s.status[b] = 1;
       continue;
     }
-    taken += need;
-    if (add > 0) run_sum += ((len + add - 1) >> 6) - (len >> 6) + 1;
+    sums3[2] += want;   // at most count in all
+    if (add > 0) sums3[0] += ((len + add - 1) >> 6) - (len >> 6) + 1;   // at most T in all
   }
-  // runs (low half, at most T in all) and pages taken (high half, at most count) in one scan
-  const long long both = block_scan(run_sum | (taken << 32), &total, warp_sums);
-  const int n_runs = (int)(total & 0x7FFFFFFFll), popped = (int)(total >> 32);
-  long long n_back;
-  long long back_at = block_scan(back_sum, &n_back, warp_sums), run_at = both & 0x7FFFFFFFll;
+  block_scan<3>(sums3, total3, warp_sums + 2);
+  const int n_runs = total3[0], n_back = total3[1], popped = total3[2];
+  int run_at = sums3[0], back_at = sums3[1];
   for (int b = b0; b < b1; ++b) {
+    const int len = s.len[b];
     if (s.status[b] == 3) {
-      s.run[b] = (int)min(back_at, (long long)N);
-      back_at += (s.len[b] + 63) >> 6;
+      s.run[b] = back_at;
+      back_at = add_most(back_at, (len + 63) >> 6);
     } else if (s.status[b] == 0) {
-      s.run[b] = (int)run_at;
-      const int len = s.len[b], add = max(a.add[b], 0);
+      s.run[b] = run_at;
+      const int add = max(a.add[b], 0);
       if (add > 0) run_at += ((len + add - 1) >> 6) - (len >> 6) + 1;
     }
   }
@@ -147,59 +164,92 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
     a.ctx[b] = st == 0 ? after : 0;
   }
   if (gtid == 0) {
-    const int kept = (int)min(n_back, (long long)room);
+    const int kept = min(n_back, room);
     int h = head + popped;
     a.ring_state_out[0] = h >= N ? h - N : h;
     a.ring_state_out[1] = count - popped + kept;
     if (n_back > room) atomicCAS(err, 0, (int)QMV_ERR_CORRUPT);
   }
-  for (int t = gtid; t < T; t += gnt) {
-    int slot = -1, pos = -1;
-    if (t < n_tokens) {
-      int lo = 0, hi = B;  // the last request that starts at or before t: the one that has it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.start[mid] <= t) lo = mid;
-        else hi = mid;
+  // tokens, one per thread or four neighbours: a search in shared memory, then from token to token. (Neighbours of a decode
+  // step are tokens of different requests, whose loads would follow one another.)
+  const int each = T > gnt ? 4 : 1;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+  int search = 1;   // steps that halve B requests to one
+  while ((1 << search) < B) ++search;
+  for (int t0 = gtid * each; t0 < T; t0 += gnt * each) {
+    // the last request that starts at or before the token: the one that has it
+    int b = 0;
+    for (int step = 1 << (search - 1); step; step >>= 1)
+      if (b + step < B && s.start[b + step] <= t0) b += step;
+    int start = s.start[b], end = b + 1 < B ? s.start[b + 1] : n_tokens, len = s.len[b], page_index = -1, page = 0;
+    bool served = s.status[b] == 0;
+    int slot[4], pos[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u;
+      slot[u] = pos[u] = -1;
+      if (u >= each || t >= n_tokens) continue;
+      while (t >= end) {   // on to the next request with tokens
+        ++b;
+        start = end;
+        end = b + 1 < B ? s.start[b + 1] : n_tokens;
+        len = s.len[b];
+        served = s.status[b] == 0;
+        page_index = -1;
       }
-      const int b = lo;
-      if (s.status[b] == 0) {
-        const int len = s.len[b], i = t - s.start[b];
-        const int end = b + 1 < B ? s.start[b + 1] : n_tokens;
-        pos = len + i;
-        const int held = (len + 63) >> 6, index = pos >> 6;
-        int page;
+      if (!served) continue;
+      pos[u] = len + t - start;
+      const int held = (len + 63) >> 6, index = pos[u] >> 6;
+      const bool opens = (pos[u] & 63) == 0;
+      if (index != page_index) {
+        page_index = index;
         if (index < held) {
           page = a.table[(int64_t)b * a.ld_table + index];
         } else {
           int k = head + s.page[b] + index - held;
           if (k >= N) k -= N;
           page = a.ring[k];
-          if ((pos & 63) == 0) a.table[(int64_t)b * a.ld_table + index] = page;
-        }
-        slot = page * 64 + (pos & 63);
-        if ((pos & 63) == 0 || i == 0) {
-          const int r = s.run[b] + index - (len >> 6);
-          if (r < a.max_runs)
-            reinterpret_cast<int2*>(a.runs)[r] = make_int2(t, min(64 - (pos & 63), end - t));
         }
       }
+      slot[u] = page * 64 + (pos[u] & 63);
+      if (opens && index >= held) a.table[(int64_t)b * a.ld_table + index] = page;
+      if (opens || t == start) {
+        const int r = s.run[b] + index - (len >> 6);
+        if (r < a.max_runs) reinterpret_cast<int2*>(a.runs)[r] = make_int2(t, min(64 - (pos[u] & 63), end - t));
+      }
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+    if (wide && each == 4 && t0 + 3 < T) {
+      *reinterpret_cast<int4*>(a.slots + t0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u < each && t0 + u < T) {
+          a.slots[t0 + u] = slot[u];
+          a.positions[t0 + u] = pos[u];
+        }
+    }
   }
   for (int r = n_runs + gtid; r < a.max_runs; r += gnt) reinterpret_cast<int2*>(a.runs)[r] = make_int2(0, 0);
-  // returned pages: one warp per leaving request
-  const int lane = tid & 31;
-  for (int b = gtid >> 5; b < B; b += gnt >> 5) {
-    if (s.status[b] != 3) continue;
-    const int held = (s.len[b] + 63) >> 6;
-    for (int i = lane; i < held; i += 32) {
-      const long long k = (long long)s.run[b] + i;
-      if (k >= room) break;
-      long long at_ring = (long long)head + count + k;
-      if (at_ring >= N) at_ring -= N;
-      a.ring[at_ring] = a.table[(int64_t)b * a.ld_table + i];
+  // returned pages: the warps share out groups of 32 requests, and within a group its leaving requests, whose rows they copy
+  const int lane = tid & 31, warps = gnt >> 5, groups = (B + 31) >> 5;
+  const int sharers = warps > groups ? warps / groups : 1;
+  for (int w = gtid >> 5; w < groups * sharers; w += warps) {
+    const int first = (w % groups) * 32;
+    int turn = w / groups;   // leaving requests until this warp's next
+    unsigned gone = __ballot_sync(0xFFFFFFFFu, first + lane < B && s.status[min(first + lane, B - 1)] == 3);
+    for (; gone; gone &= gone - 1) {
+      if (turn-- != 0) continue;
+      turn = sharers - 1;
+      const int b = first + __ffs(gone) - 1;
+      const int held = (s.len[b] + 63) >> 6, place = s.run[b], n = min(held, room - place);
+      const int32_t* row = a.table + (int64_t)b * a.ld_table;
+#pragma unroll 4
+      for (int i = lane; i < n; i += 32) {
+        int k = head + count + place + i - N;   // below N: place + i < N - count
+        if (k < 0) k += N;
+        a.ring[k] = row[i];
+      }
     }
   }
 }
@@ -225,6 +275,7 @@ int kv_plan(const kv_plan_args* a, void* stream) {
   if (a->n_tokens < 0 || a->n_pages < 1 || a->max_pages < 1 || a->ld_table < a->max_pages)
     return fail(QMV_ERR_ARG, "n_tokens=%d n_pages=%d max_pages=%d ld_table=%lld", a->n_tokens, a->n_pages, a->max_pages,
                 (long long)a->ld_table);
+  if (a->n_tokens > (1 << 30)) return fail(QMV_ERR_UNSUPPORTED, "n_tokens=%d over 2^30", a->n_tokens);
   if (a->n_pages > INT32_MAX / 64) return fail(QMV_ERR_UNSUPPORTED, "n_pages=%d: slots must fit 31 bits", a->n_pages);
   if (a->max_pages > INT32_MAX / 64) return fail(QMV_ERR_UNSUPPORTED, "max_pages=%d: positions must fit 31 bits", a->max_pages);
   if (a->max_runs < kv_max_runs(a->n_requests, a->n_tokens))
@@ -247,7 +298,7 @@ int kv_plan(const kv_plan_args* a, void* stream) {
 
   const int B = a->n_requests, T = a->n_tokens;
   const int most = B > T ? B : T;
-  // one block while its threads see at most 4 tokens each: more blocks only add the cluster barrier
+  // one block while its threads see at most four requests or four tokens each: more blocks only add the cluster barrier
   const int n_blocks = most > 4 * kMaxPlanThreads ? kPlanCluster : 1;
   const int threads = most <= 256 ? 256 : kMaxPlanThreads;
   const size_t smem = (size_t)B * 5 * sizeof(int32_t);
@@ -265,7 +316,7 @@ int kv_plan(const kv_plan_args* a, void* stream) {
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = n_blocks > 1 ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, *a, n_blocks, err);
   if (e != cudaSuccess) return cuda_fail(e, "kv_plan launch");
   return QMV_OK;
