@@ -192,28 +192,27 @@ def attend(cache: Cache, q, q_start, ctx, table, scale, softcap=0.0, slopes=None
         K = np.concatenate([cache.page_values(p if 0 <= p < cache.n_pages else 0, 0) for p in pages], 1)[:, :L]
         V = np.concatenate([cache.page_values(p if 0 <= p < cache.n_pages else 0, 1) for p in pages], 1)[:, :L]
         key = np.arange(L)
-        for t in range(t0, t1):
-            i = L - (t1 - t0) + t - t0
-            ok = (key <= i) | (key < (0 if prefix is None else prefix[b]))
-            if window:
-                ok &= i - key < window
-            ok &= there
-            if not ok.any():
-                continue
-            for hq in range(Hq):
-                kk, vv = K[hq // G][ok], V[hq // G][ok]
-                s = scale * (kk @ q[t, hq])
-                if softcap:
-                    s = softcap * np.tanh(s / softcap)
-                if slopes is not None:
-                    s = s - slopes[hq] * np.abs(i - key[ok])
-                m = s.max()
-                p = np.exp(s - m)
-                l = p.sum()
-                out[t, hq] = (p / l) @ vv
-                lse[t, hq] = m + math.log(l)
-                pv[t, hq] = (p / l) @ np.abs(vv)
-                vmax[t, hq] = np.abs(vv).max()
-                seen_n[t, hq] = ok.sum()
-                sabs[t, hq] = scale * (np.abs(kk) @ np.abs(q[t, hq])).max()
+        pos = (L - (t1 - t0) + np.arange(t1 - t0))[:, None]
+        ok = (key <= pos) | (key < (0 if prefix is None else prefix[b]))
+        if window:
+            ok &= pos - key < window
+        ok &= there
+        some = ok.any(1)
+        for hq in range(Hq):
+            kk, vv, qq = K[hq // G], V[hq // G], q[t0:t1, hq]
+            s = scale * (qq @ kk.T)
+            if softcap:
+                s = softcap * np.tanh(s / softcap)
+            if slopes is not None:
+                s = s - slopes[hq] * np.abs(pos - key)
+            s = np.where(ok, s, -np.inf)
+            m = np.where(some, s.max(1), 0.0)[:, None]
+            p = np.exp(s - m)
+            l = np.where(some, p.sum(1), 1.0)[:, None]
+            out[t0:t1, hq] = (p / l) @ vv
+            lse[t0:t1, hq] = np.where(some, m[:, 0] + np.log(l[:, 0]), -np.inf)
+            pv[t0:t1, hq] = (p / l) @ np.abs(vv)
+            vmax[t0:t1, hq] = np.where(ok, np.abs(vv).max(1), 0.0).max(1)
+            sabs[t0:t1, hq] = scale * np.where(ok, np.abs(qq) @ np.abs(kk).T, 0.0).max(1)
+        seen_n[t0:t1] = ok.sum(1)[:, None]
     return out, lse, pv, vmax, seen_n, sabs
