@@ -1,4 +1,4 @@
-// kv8_attend: checks of arguments, workspace and choice of the row tile.
+// kv8_attend: checks of arguments, workspace and choice of the kernel.
 #include <cmath>
 #include <cstring>
 
@@ -9,7 +9,7 @@ using namespace qmv::kv8;
 
 namespace {
 
-constexpr size_t kCounterBytes = 4096;  // one int per block
+constexpr size_t kCounterBytes = 16384;  // one int per block, or two and two per item of a wave (prompts)
 
 struct Layout {
   int blocks;
@@ -18,7 +18,7 @@ struct Layout {
 Layout layout(const qmv_kv_desc* d) {
   Layout l;
   l.blocks = sm_count();
-  if (l.blocks > (int)(kCounterBytes / sizeof(int))) l.blocks = (int)(kCounterBytes / sizeof(int));
+  if (l.blocks > 1024) l.blocks = 1024;
   const size_t rows = (size_t)l.blocks * attend::kPartRows;
   l.ml_off = kCounterBytes;
   l.o_off = l.ml_off + rows * sizeof(float2);
@@ -34,9 +34,16 @@ int check_workspace(const qmv_kv_desc* desc, const void* workspace, size_t ws_by
   return QMV_OK;
 }
 
-bool prompt_kernel(int64_t rows, int64_t all_rows, int requests, int H) {
-  if ((all_rows / 256 + 1) * requests * H > INT32_MAX) return false;  // its items are numbered in 31 bits
-  return rows > 64 && (rows + 255) / 256 * requests * H >= sm_count() / 2;
+// The kernel of a call, by the query rows per (request, KV head) that max_new bounds. Measured (times in us, warp-level
+// tensor cores / tcgen05): 30 rows of 40 query and 8 KV heads of 128, 1 request of 16384 tokens 38 / 46, 4 of them 48 / 72,
+// 16 of 2048 31 / 34; 48 rows of one KV head, 34 / 35 over 4 requests of 4096 tokens, 66 / 49 over 4 of 16384, 30 / 26 over
+// 4 of 1200; with 65 and 130 rows of 8 heads the first takes 1.5 to 4 times as long. Few rows are bound by the cache's
+// bytes and by joins, which the first has more streams for; many rows by the products.
+enum Kernel { kWarps, kPrompt, kPromptParts };
+Kernel choose(int64_t rows, int64_t all_rows, int requests, int H) {
+  if (rows <= 32 || (all_rows / 256 + 1) * requests * H > INT32_MAX / 2) return kWarps;  // items are numbered in 31 bits
+  // items of 256 rows for half the blocks or fewer: their keys are cut into parts
+  return (rows + 255) / 256 * requests * H > sm_count() / 2 ? kPrompt : kPromptParts;
 }
 
 }  // namespace
@@ -128,12 +135,16 @@ int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args
   a.part_o = reinterpret_cast<float*>(ws + l.o_off);
   a.err = err;
   const int64_t rows = (int64_t)(g->max_new < g->n_tokens ? g->max_new : g->n_tokens) * a.G;
-  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  a.limit = 24;
+  const int tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   const bool mods = g->softcap > 0.f || g->slopes;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->type == QMV_KV_INT8;
-  if (prompt_kernel(rows, (int64_t)g->n_tokens * a.G, g->n_requests, H)) return i8 ? prompt::launch_int8(a, D, mods, l.blocks, s) : prompt::launch_e4m3(a, D, mods, l.blocks, s);
+  const Kernel kernel = choose(rows, (int64_t)g->n_tokens * a.G, g->n_requests, H);
+  if (kernel != kWarps) {
+    const bool split = kernel == kPromptParts;
+    if (D == 64) return i8 ? prompt::launch_64_int8(a, mods, split, l.blocks, s) : prompt::launch_64_e4m3(a, mods, split, l.blocks, s);
+    return i8 ? prompt::launch_128_int8(a, mods, split, l.blocks, s) : prompt::launch_128_e4m3(a, mods, split, l.blocks, s);
+  }
   if (D == 64) return i8 ? attend::launch_64_int8(a, tile, mods, l.blocks, s) : attend::launch_64_e4m3(a, tile, mods, l.blocks, s);
   return i8 ? attend::launch_128_int8(a, tile, mods, l.blocks, s) : attend::launch_128_e4m3(a, tile, mods, l.blocks, s);
 }

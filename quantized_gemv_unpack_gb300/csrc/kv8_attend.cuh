@@ -63,13 +63,12 @@ struct Args {
   uint32_t g_mul, g_shift;
   // n / G for n below 2^31: G's rounded-up reciprocal, exact in this range
   __device__ __forceinline__ int by_g(int n) const { return (int)(((uint64_t)(uint32_t)n * g_mul) >> g_shift); }
-  int limit;             // pages of one tile that a block takes at least before the tile is cut between blocks
   int* err;
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWeights = 1024;   // factors of a join held in shared memory
-constexpr int kStreamRows = 128, kBlockRows = 256, kPartRows = kStreamRows + kBlockRows;
+constexpr int kStreamRows = 128, kPartRows = 256;   // rows per block of the workspace: of its streams, in all
 
 template <int D, int N, int R>
 struct Shape {
@@ -84,6 +83,9 @@ struct Shape {
   static_assert(kStages % 2 == 0, "K in even stages, V in odd ones");
   static constexpr int kRows = 8 * N * R;
   static constexpr int kReqs = 256;   // requests kept in shared memory
+  // How tiles are cut between blocks. Up to kAlone pages in a call's longest tile each has a block of its own; else a block
+  // takes kCut pages or more of one tile, or the line of all is cut evenly where that saves a block more than kUneven pages.
+  static constexpr int kAlone = kStreams * 6, kCut = kStreams * 2, kUneven = kStreams * 4;
 };
 
 struct Req {
@@ -119,14 +121,26 @@ __device__ __forceinline__ void tile_pages(const Args& a, const Req& r, int tile
   p0 = lo / kPage;
   n = (hi + kPage - 1) / kPage - p0;
 }
-__device__ __forceinline__ long long req_units(const Args& a, const Req& r, int tile_rows) {
+// Units of a request; `longest`: the most pages that a tile of it has, or what it was.
+__device__ __forceinline__ long long req_units(const Args& a, const Req& r, int tile_rows, int& longest) {
   long long u = 0;
   for (int k = 0; k < r.tiles; ++k) {
     int p0, n;
     tile_pages(a, r, k, tile_rows, p0, n);
     u += n;
+    longest = max(longest, n);
   }
   return u * a.H;
+}
+// Blocks of a request whose tiles are cut into parts of up to `most` pages.
+__device__ __forceinline__ int req_parts(const Args& a, const Req& r, int tile_rows, int most) {
+  int c = 0;
+  for (int k = 0; k < r.tiles; ++k) {
+    int p0, n;
+    tile_pages(a, r, k, tile_rows, p0, n);
+    c += (n + most - 1) / most;
+  }
+  return c * a.H;
 }
 
 // A place on the line of units: a tile of a request, a KV head, and its pages.
@@ -350,14 +364,14 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   const bool few = a.B <= 32;
   int4 held = make_int4(0, 0, 0, 0);
   long long mine = 0, before = 0, W = 0;   // units of this thread's requests, of those before them, of all
-  int segs = 0;
+  int segs = 0, longest = 0;
   const int per = few ? 1 : (a.B + S::kThreads - 1) / S::kThreads;
   const int b0 = few ? lane : min(a.B, tid * per), b1 = min(a.B, b0 + per);
   for (int b = b0; b < b1; ++b) {
     held = load_req4(a, b);
     if (!few && b < S::kReqs) sm.req[b] = held;
     const Req r = make_req(a, b, held, S::kRows);
-    mine += req_units(a, r, S::kRows);
+    mine += req_units(a, r, S::kRows, longest);
     segs += r.tiles * a.H;
   }
   long long incl = mine;
@@ -385,50 +399,6 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   }
   before += incl - mine;
   if (W == 0) return;
-  // blocks in use: as many per tile as it has `limit`s of pages on average, all of them at most. (A cut between
-  // blocks costs a trip of the partial tile through L2, about two pages' time of every stream.)
-  int A = gridDim.x;
-  if (segs < A) {
-    const int span = segs * a.limit;   // below 2^13
-    const int want = W < (1ll << 30) ? segs * (int)(((unsigned)W + span - 1) / (unsigned)span) : A;
-    if (want < A) A = want;
-  }
-  const int cta = blockIdx.x;
-  if (cta >= A) return;
-  const Cut blocks = cut(W, A);
-  const long long u0 = blocks.at(cta);
-  const int units = (int)(blocks.at(cta + 1) - u0);
-  const Cut streams = cut(units, S::kStreams);
-  int start_b = 0;
-  long long start_off = 0, start_base = 0;   // this stream's first unit: its request, its place there, where that begins
-  if (few) {
-    const long long x = u0 + streams.at(stream);
-    start_b = __popc(__ballot_sync(0xFFFFFFFFu, before + mine <= x));
-    start_base = __shfl_sync(0xFFFFFFFFu, before, start_b & 31);
-    start_off = x - start_base;
-  } else if (before < u0 + units && before + mine > u0) {
-    long long P = before;
-    for (int b = b0; b < b1; ++b) {
-      const long long ub = per == 1 ? mine : req_units(a, make_req(a, b, load_req4(a, b), S::kRows), S::kRows);
-      for (int i = 0; i < S::kStreams; ++i) {
-        const long long x = u0 + streams.at(i);
-        if (P <= x && x < P + ub) {
-          sm.start_b[i] = b;
-          sm.start_off[i] = x - P;
-          sm.start_base[i] = P;
-        }
-      }
-      P += ub;
-    }
-  }
-  __syncthreads();
-  if (!few) {
-    start_b = sm.start_b[stream];
-    start_off = sm.start_off[stream];
-    start_base = sm.start_base[stream];
-  }
-  int left = (int)(streams.at(stream + 1) - streams.at(stream));
-
   auto get_req = [&](int b) {
     int4 v;
     if (few)
@@ -438,6 +408,110 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
       v = b < S::kReqs ? sm.req[b] : load_req4(a, b);
     return make_req(a, b, v, S::kRows);
   };
+  const int cta = blockIdx.x;
+  Cut blocks = {0, 0};
+  int units;                                 // of this block
+  int start_b = 0;
+  long long start_off = 0, start_base = 0;   // this stream's first unit: its request, its place there, where that begins
+  int whose0 = 0, whose1 = -1;               // the blocks of this block's tile, where each block has pages of one tile only
+  // Cuts at the tiles' ends: `most` pages or fewer in each part, the fewest (in steps of a page per stream) with which
+  // there are no more parts than blocks.
+  int most = 0, parts = 0;
+  if (few && segs <= (int)gridDim.x && W < (1ll << 30)) {
+    longest = __reduce_max_sync(0xFFFFFFFFu, longest);
+    const Req r = make_req(a, lane, held, S::kRows);
+    if (longest <= S::kAlone) {
+      most = longest;
+      parts = r.tiles * a.H;
+    } else {
+      const int one = r.tiles == 1 ? (int)mine / a.H : 0;   // pages of a request that has one row tile
+      const int even = ((int)W + gridDim.x - 1) / (int)gridDim.x;
+      const int least = (max(even, S::kCut) + S::kStreams - 1) / S::kStreams * S::kStreams;
+      for (int p = least; p <= max(least, even + S::kUneven); p += S::kStreams) {
+        parts = r.tiles == 1 ? (one + p - 1) / p * a.H : req_parts(a, r, S::kRows, p);
+        if (__reduce_add_sync(0xFFFFFFFFu, parts) <= (int)gridDim.x) {
+          most = p;
+          break;
+        }
+      }
+    }
+  }
+  if (most > 0) {
+    int incl_parts = parts;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, incl_parts, o);
+      if (lane >= o) incl_parts += u;
+    }
+    if (cta >= __shfl_sync(0xFFFFFFFFu, incl_parts, 31)) return;
+    start_b = __popc(__ballot_sync(0xFFFFFFFFu, incl_parts <= cta));
+    start_base = __shfl_sync(0xFFFFFFFFu, before, start_b);
+    const Req r = get_req(start_b);
+    int part = cta - __shfl_sync(0xFFFFFFFFu, incl_parts - parts, start_b), n = 0, each = 1;   // of the request, then of a tile
+    for (int k = 0;; ++k) {
+      int p0;
+      tile_pages(a, r, k, S::kRows, p0, n);
+      each = n <= most ? 1 : (n + most - 1) / most;
+      if (part < each * a.H || k + 1 >= r.tiles) break;
+      part -= each * a.H;
+      start_off += (long long)n * a.H;
+    }
+    int h = part, first = 0;   // its first page
+    units = n;
+    if (each > 1) {
+      h = part / each;
+      part -= h * each;
+      const Cut cuts = cut(n, each);
+      first = (int)cuts.at(part);
+      units = (int)cuts.at(part + 1) - first;
+      whose0 = cta - part;
+      whose1 = whose0 + each - 1;
+    }
+    start_off += (long long)h * n + first + cut(units, S::kStreams).at(stream);
+  } else {
+    // the line in equal pieces for as many blocks as the tiles have kCut pages on average, all of them at most
+    int A = gridDim.x;
+    if (segs < A) {
+      const int span = segs * S::kCut;   // below 2^13
+      const int want = W < (1ll << 30) ? segs * (int)(((unsigned)W + span - 1) / (unsigned)span) : A;
+      if (want < A) A = want;
+    }
+    if (cta >= A) return;
+    blocks = cut(W, A);
+    const long long u0 = blocks.at(cta);
+    units = (int)(blocks.at(cta + 1) - u0);
+    const Cut streams = cut(units, S::kStreams);
+    if (few) {
+      const long long x = u0 + streams.at(stream);
+      start_b = __popc(__ballot_sync(0xFFFFFFFFu, before + mine <= x));
+      start_base = __shfl_sync(0xFFFFFFFFu, before, start_b & 31);
+      start_off = x - start_base;
+    } else if (before < u0 + units && before + mine > u0) {
+      long long P = before;
+      for (int b = b0; b < b1; ++b) {
+        const long long ub =
+            per == 1 ? mine : req_units(a, make_req(a, b, load_req4(a, b), S::kRows), S::kRows, longest);
+        for (int i = 0; i < S::kStreams; ++i) {
+          const long long x = u0 + streams.at(i);
+          if (P <= x && x < P + ub) {
+            sm.start_b[i] = b;
+            sm.start_off[i] = x - P;
+            sm.start_base[i] = P;
+          }
+        }
+        P += ub;
+      }
+    }
+  }
+  const Cut streams = cut(units, S::kStreams);
+  __syncthreads();
+  if (!few) {
+    start_b = sm.start_b[stream];
+    start_off = sm.start_off[stream];
+    start_base = sm.start_base[stream];
+  }
+  int left = (int)(streams.at(stream + 1) - streams.at(stream));
+
   auto walk_next = [&](Walk& w) {
     w.start += w.n;
     if (++w.h < a.H) return;
@@ -826,7 +900,11 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   unsigned todo = __ballot_sync(0xFFFFFFFFu, p_len > 0);
   int shared_tiles[2] = {-1, -1};   // entries of the (at most two) tiles that other blocks hold a part of
   auto slot_of = [&](const Piece& pc, int c) {   // the rows where block c leaves its part of the tile
-    return (int64_t)c * kPartRows + kStreamRows + (pc.start < blocks.at(c) ? 0 : S::kRows);
+    return (int64_t)c * kPartRows + kStreamRows + (whose1 >= 0 || pc.start < blocks.at(c) ? 0 : S::kRows);
+  };
+  auto blocks_of = [&](const Piece& pc, int& c0, int& c1) {   // the blocks that hold parts of the tile
+    c0 = whose1 >= 0 ? whose0 : blocks.part_of(pc.start);
+    c1 = whose1 >= 0 ? whose1 : blocks.part_of(pc.start + pc.n - 1);
   };
   while (todo) {
     const int e0 = __ffs(todo) - 1;
@@ -860,7 +938,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   __syncthreads();
   if (tid < 2 && (tid ? shared_tiles[1] : shared_tiles[0]) >= 0) {
     const Piece& pc = (&sm.piece[0][0])[tid ? shared_tiles[1] : shared_tiles[0]];
-    const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
+    int c0, c1;
+    blocks_of(pc, c0, c1);
     const int old = atomicAdd(a.counters + c0, 1);
     sm.last[tid] = old == c1 - c0;
     if (old == c1 - c0) a.counters[c0] = 0;
@@ -871,7 +950,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
   for (int i = 0; i < 2; ++i) {
     if (shared_tiles[i] < 0 || !sm.last[i]) continue;
     const Piece& pc = (&sm.piece[0][0])[shared_tiles[i]];
-    const int c0 = blocks.part_of(pc.start), c1 = blocks.part_of(pc.start + pc.n - 1);
+    int c0, c1;
+    blocks_of(pc, c0, c1);
     const Req r = get_req(pc.b);
     const int row0 = pc.tile * S::kRows, rows = min(S::kRows, r.rows - row0);
     // written by other blocks during this launch: read past L1
@@ -895,7 +975,7 @@ int launch(const Args& a, int blocks, cudaStream_t s) {
   return QMV_OK;
 }
 
-// One translation unit per (D, type): rows is the row tile (8, 16, 32, 64 or 128).
+// One translation unit per (D, type): rows is the row tile (8, 16 or 32).
 int launch_64_int8(const Args& a, int rows, bool mods, int blocks, cudaStream_t s);
 int launch_64_e4m3(const Args& a, int rows, bool mods, int blocks, cudaStream_t s);
 int launch_128_int8(const Args& a, int rows, bool mods, int blocks, cudaStream_t s);
@@ -906,9 +986,7 @@ int launch_rows(const Args& a, int rows, bool mods, int blocks, cudaStream_t s) 
   switch (rows) {
     case 8: return mods ? launch<D, TYPE, 1, 1, true>(a, blocks, s) : launch<D, TYPE, 1, 1, false>(a, blocks, s);
     case 16: return mods ? launch<D, TYPE, 2, 1, true>(a, blocks, s) : launch<D, TYPE, 2, 1, false>(a, blocks, s);
-    case 32: return mods ? launch<D, TYPE, 2, 2, true>(a, blocks, s) : launch<D, TYPE, 2, 2, false>(a, blocks, s);
-    case 64: return mods ? launch<D, TYPE, 2, 4, true>(a, blocks, s) : launch<D, TYPE, 2, 4, false>(a, blocks, s);
-    default: return mods ? launch<D, TYPE, 2, 8, true>(a, blocks, s) : launch<D, TYPE, 2, 8, false>(a, blocks, s);
+    default: return mods ? launch<D, TYPE, 2, 2, true>(a, blocks, s) : launch<D, TYPE, 2, 2, false>(a, blocks, s);
   }
 }
 

@@ -44,6 +44,8 @@ constexpr int kWarps = 16, kThreads = kWarps * 32, kKeyThreads = 128, kValueThre
 // 512 threads are launched with 128 registers each; 256 * 176 + 256 * 80 = 512 * 128
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
+constexpr int kHeld = 512;               // parts times rows that a join holds in shared memory: what L1 keeps counts (below)
+constexpr int kChunk = 4;                // steps of a part at least
 constexpr int kItems = 8;                // items the roles may be apart
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
 
@@ -154,18 +156,105 @@ struct Smem {
   int tiles_max[kWarps];
 };
 
+template <int D, bool SPLIT>
+struct Shared : Smem<D> {};
+template <int D>
+struct Shared<D, true> : Smem<D> {
+  float2 parts[2][kHeld];   // (maximum, sum) of a row tile's parts and rows, then their factors
+  int last[2];
+};
+
+// A barrier of softmax group `tile` alone.
+__device__ __forceinline__ void group_sync(int tile) { asm volatile("bar.sync %0, 128;" ::"r"(1 + tile) : "memory"); }
+
+// Join `entries` parts of a row tile (rows at first + e * stride of the workspace) into rows row1 .. row1 + rows - 1 of a
+// request's KV head h, by the 128 threads of a softmax group; written by other blocks too: read past L1. As many rows at a
+// time as their parts' maxima and sums fit `held`. A function of its own, so that its registers are not the step loop's.
+template <int D>
+__device__ __noinline__ void join_parts(const Args& a, int64_t first, int stride, int entries, int row1, int rows, int qs, int h,
+                                        float2* held, int group, int t) {
+  const int at_once = max(1, min(rows, kHeld / entries));
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int nr = min(at_once, rows - r0);
+    const float2* ml = a.part_ml + first + r0;
+#pragma unroll 4
+    for (int i = t; i < entries * nr; i += kRows) {
+      const int e = i / nr;
+      held[i] = __ldcg(ml + (int64_t)e * stride + i - e * nr);
+    }
+    group_sync(group);
+    if (t < nr) {
+      float top = -INFINITY, sum = 0.f;
+      for (int e = 0; e < entries; ++e) top = fmaxf(top, held[e * nr + t].x);
+      const float use = top == -INFINITY ? 0.f : top;
+      for (int e = 0; e < entries; ++e) {
+        const float2 v = held[e * nr + t];
+        const float w = ex2(v.x - use);
+        held[e * nr + t].x = w;
+        sum += w * v.y;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      for (int e = 0; e < entries; ++e) held[e * nr + t].x *= inv;
+      if (a.lse) {
+        const int rx = row1 + r0 + t, tx = a.by_g(rx);
+        a.lse[(int64_t)(qs + tx) * a.Hq + h * a.G + rx - tx * a.G] = sum == 0.f ? -INFINITY : (use + log2f(sum)) * kLn2;
+      }
+    }
+    group_sync(group);
+    // two pieces of four values per thread at a time, and ten parts of them in flight
+    constexpr int Q = D / 4, AT = 2;
+    for (int u0 = t; u0 < nr * Q; u0 += AT * kRows) {
+      float4 sum[AT];
+      const float4* from[AT];
+      int r[AT];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const int u = min(u0 + i * kRows, nr * Q - 1);   // past the end: the last piece again, not stored
+        r[i] = u / Q;
+        from[i] = reinterpret_cast<const float4*>(a.part_o + (first + r0 + r[i]) * D) + u % Q;
+        sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 10
+      for (int e = 0; e < entries; ++e) {
+#pragma unroll
+        for (int i = 0; i < AT; ++i) {
+          const float4 v = __ldcg(from[i] + (int64_t)e * stride * Q);
+          const float w = held[e * nr + r[i]].x;
+          sum[i].x += w * v.x;
+          sum[i].y += w * v.y;
+          sum[i].z += w * v.z;
+          sum[i].w += w * v.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        const int u = u0 + i * kRows;
+        if (u >= nr * Q) continue;
+        const int rx = row1 + r0 + r[i], tx = a.by_g(rx);
+        const int64_t to = (int64_t)(qs + tx) * a.ldo + (int64_t)(h * a.G + rx - tx * a.G) * D + (u % Q) * 4;
+        attend::store_as(a.out_type, a.out, to, sum[i].x, sum[i].y);
+        attend::store_as(a.out_type, a.out, to + 2, sum[i].z, sum[i].w);
+      }
+    }
+    group_sync(group);
+  }
+}
+
 // One block's piece of work: up to two row tiles of one (request, KV head).
 struct Item {
   Req r;
   int h, row0, tiles;   // first row; row tiles of 128
-  int p0, pages, steps; // pages seen by any of its rows (p0 < 0: none)
+  int p0, pages, steps; // pages of it that any of its rows sees (p0 < 0: none), in steps of two
+  int base, part, parts;  // number without its part, and the part of its keys
 };
 
-template <int D, int TYPE, bool MODS>
+// SPLIT: an item's keys may be cut into parts (a kernel of its own, because the step loop of one that also joins parts is
+// slower: 229 us in place of 212 on prompt chunks of 1500 tokens over up to 4096 keys).
+template <int D, int TYPE, bool MODS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
   constexpr int KH = D / 64;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+  Shared<D, SPLIT>& sm = *reinterpret_cast<Shared<D, SPLIT>*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
 
   if (warp == kWarps - 1) tmem_alloc(&sm.tmem);
@@ -198,10 +287,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   // Items in the order of their tiles from the last (which sees the most keys) to the first, then request and head.
   // Blocks take them one after another from a counter: an item's cost varies by its request's context, and which block
   // computes it does not change its result.
-  const int n_items = most * a.B * a.H;   // at most (rows + 255 B) / 256 * H: below 2^31 for any call the host lets through
+  // Where there are fewer items than blocks, an item's keys are cut into up to n_split parts, each an item of its own; what
+  // they leave is joined by the last of them to arrive.
+  const int per = a.B * a.H, n_base = most * per;   // at most (rows + 255 B) / 256 * H: below 2^31 for any call the host lets through
+  const int n_split = SPLIT && n_base > 0 && n_base <= (int)gridDim.x ? (int)gridDim.x / n_base : 1, n_items = n_base * n_split;
   auto item_of = [&](int i, Item& it) {
-    const int per = a.B * a.H;
-    const int pair = most - 1 - i / per, rest = i % per;
+    it.base = SPLIT ? i / n_split : i;
+    it.part = SPLIT ? i - it.base * n_split : 0;
+    const int pair = most - 1 - it.base / per, rest = it.base % per;
     it.r = attend::make_req(a, rest / a.H, attend::load_req4(a, rest / a.H), kRows);
     it.h = rest % a.H;
     it.row0 = pair * 2 * kRows;
@@ -209,6 +302,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     it.tiles = it.r.rows - it.row0 > kRows ? 2 : 1;
     attend::tile_pages(a, it.r, pair, 2 * kRows, it.p0, it.pages);
     it.steps = (it.pages + 1) / 2;
+    it.parts = 1;
+    if (SPLIT && n_split > 1) {
+      const int chunk = max((it.steps + n_split - 1) / n_split, kChunk), first = it.part * chunk;
+      it.parts = (it.steps + chunk - 1) / chunk;
+      if (it.part >= it.parts) return false;
+      it.steps = min(chunk, it.steps - first);
+      if (it.p0 >= 0) it.p0 += 2 * first;
+      it.pages = min(it.pages - 2 * first, 2 * it.steps);
+    }
     return true;
   };
 
@@ -410,8 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         core::mbar_wait(&sm.o_full[tile], n_out & 1, a.err);
         ++n_out;
         fence_after();
-        const float f = l == 0.f ? 0.f : s_ref / l;
         const int64_t at = (int64_t)(it.r.qs + tok) * a.ldo + (int64_t)hq * D;
+        const bool part = SPLIT && it.parts > 1;
+        const int64_t mine = (int64_t)(it.base * n_split + it.part) * 2 * kRows + tile * kRows + row;   // of a part's rows
+        const float f = part ? s_ref : l == 0.f ? 0.f : s_ref / l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t y[32];
@@ -423,11 +527,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               float v[8];
 #pragma unroll
               for (int x = 0; x < 8; ++x) v[x] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + x]) * f;
-              kv8::store8_as(a.out_type, a.out, at + 32 * c + 8 * q, v);
+              if (part) kv8::store8(a.part_o + mine * D + 32 * c + 8 * q, v);
+              else kv8::store8_as(a.out_type, a.out, at + 32 * c + 8 * q, v);
             }
           }
         }
-        if (real && a.lse) a.lse[(int64_t)(it.r.qs + tok) * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (!part && real && a.lse) a.lse[(int64_t)(it.r.qs + tok) * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if constexpr (SPLIT) {
+          if (part) {
+            // the last of the row tile's parts to arrive joins them in their order
+            if (real) a.part_ml[mine] = make_float2(m, l);
+            __threadfence();
+            group_sync(tile);
+            if (row == 0) {
+              int* counter = a.counters + 2 + it.base * 2 + tile;
+              const int old = atomicAdd(counter, 1);
+              sm.last[tile] = old == it.parts - 1;
+              if (old == it.parts - 1) *counter = 0;
+              __threadfence();
+            }
+            group_sync(tile);
+            if (sm.last[tile]) {
+              const int row1 = it.row0 + tile * kRows;
+              join_parts<D>(a, (int64_t)it.base * n_split * 2 * kRows + tile * kRows, 2 * kRows, it.parts, row1,
+                            min(kRows, it.r.rows - row1), it.r.qs, it.h, sm.parts[tile], tile, row);
+            }
+          }
+        }
         fence_before();
       }
       n += it.steps;
@@ -638,26 +764,28 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   if (tid == 0 && atomicAdd(a.counters + 1, 1) == (int)gridDim.x - 1) a.counters[0] = a.counters[1] = 0;
 }
 
-template <int D, int TYPE, bool MODS>
+template <int D, int TYPE, bool MODS, bool SPLIT>
 int launch(const Args& a, int blocks, cudaStream_t s) {
-  const void* f = reinterpret_cast<const void*>(prompt_kernel<D, TYPE, MODS>);
+  const void* f = reinterpret_cast<const void*>(prompt_kernel<D, TYPE, MODS, SPLIT>);
   int per_sm = 0;
-  int rc = kernel_fit(f, kThreads, sizeof(Smem<D>), &per_sm);
+  int rc = kernel_fit(f, kThreads, sizeof(Shared<D, SPLIT>), &per_sm);
   if (rc) return rc;
-  prompt_kernel<D, TYPE, MODS><<<blocks, kThreads, sizeof(Smem<D>), s>>>(a);
+  prompt_kernel<D, TYPE, MODS, SPLIT><<<blocks, kThreads, sizeof(Shared<D, SPLIT>), s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "kv8_attend launch");
   return QMV_OK;
 }
 
-// One translation unit per type of codes.
-int launch_int8(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s);
-int launch_e4m3(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s);
+// One translation unit per type of codes and head size.
+int launch_64_int8(const Args& a, bool mods, bool split, int blocks, cudaStream_t s);
+int launch_64_e4m3(const Args& a, bool mods, bool split, int blocks, cudaStream_t s);
+int launch_128_int8(const Args& a, bool mods, bool split, int blocks, cudaStream_t s);
+int launch_128_e4m3(const Args& a, bool mods, bool split, int blocks, cudaStream_t s);
 
-template <int TYPE>
-int launch_dim(const Args& a, int head_dim, bool mods, int blocks, cudaStream_t s) {
-  if (head_dim == 64) return mods ? launch<64, TYPE, true>(a, blocks, s) : launch<64, TYPE, false>(a, blocks, s);
-  return mods ? launch<128, TYPE, true>(a, blocks, s) : launch<128, TYPE, false>(a, blocks, s);
+template <int D, int TYPE>
+int launch_any(const Args& a, bool mods, bool split, int blocks, cudaStream_t s) {
+  if (split) return mods ? launch<D, TYPE, true, true>(a, blocks, s) : launch<D, TYPE, false, true>(a, blocks, s);
+  return mods ? launch<D, TYPE, true, false>(a, blocks, s) : launch<D, TYPE, false, false>(a, blocks, s);
 }
 
 }  // namespace prompt

@@ -536,6 +536,50 @@ def test_attend_prompts_masks_and_scores(env, opt, D, kind):
     c.check(**opt)
 
 
+PARTS = [   # few row tiles over many keys, which are cut into parts: ctx, new, q heads, kv heads, options
+    ([3000], [20], 4, 2, {}), ([3001], [7], 10, 2, {}), ([2500], [150], 4, 2, {}), ([64 * 27 + 5], [300], 1, 1, {}),
+    ([2500, 70, 900, 0, 1400], [150, 33, 10, 4, 0], 4, 2, {}), ([520, 513, 512, 511], [40] * 4, 8, 4, {}),
+    ([3000], [40], 1, 1, dict(window=700, softcap=20.0)), ([3000, 2000], [40, 90], 2, 1, dict(window=64)),
+    ([2200], [60], 1, 1, dict(prefix=[2200])), ([2200, 1800], [60, 33], 4, 1, dict(slopes=[0.5, 0.25, 0.125, 2.0 ** -8])),
+]
+
+
+@pytest.mark.parametrize("shape", range(len(PARTS)))
+@pytest.mark.parametrize("D,kind,x,out", [(128, 1, "bf16", "f32"), (64, 2, "f16", "bf16"), (128, 2, "bf16", "f32"), (64, 1, "f32", "f32")])
+def test_attend_prompts_in_parts(env, shape, D, kind, x, out):
+    q, torch, dev = env
+    ctx, new, Hq, H, opt = PARTS[shape]
+    c = _Case(env, ctx, new, Hq, H, D, kind, x, seed=140 + shape, pad=shape % 2)
+    first = c.check(out=out, **opt)
+    again, _ = c.run(out=out, workspace=c.call.workspace, **opt)     # the counters are zero again, the order is fixed
+    assert torch.equal(first, again)
+    assert q.qmv_check_status() == 0
+
+
+CUTS = [   # tiles of decode steps over blocks: ctx, new, q heads, kv heads, max_new
+    ([300, 1, 3008, 0, 777], [1] * 5, 8, 2, None),       # a block for each
+    ([9000, 130, 4000], [1, 1, 1], 10, 2, None),              # parts of one tile each
+    ([64 * 49], [1], 1, 1, None), ([64 * 49 + 1, 64 * 49], [4, 3], 8, 1, None),
+    ([6400, 640], [1, 2], 60, 60, None),                      # the line of all cut evenly
+    ([4000], [40], 1, 1, 1), ([4000, 70], [13, 30], 5, 1, 6),  # several row tiles
+    ([200] * 40 + [7000], [1] * 41, 2, 1, None),              # more requests than a warp has lanes
+]
+
+
+@pytest.mark.parametrize("shape", range(len(CUTS)))
+@pytest.mark.parametrize("D,kind", [(128, 2), (64, 1)])
+def test_attend_steps_cut_between_blocks(env, shape, D, kind):
+    q, torch, dev = env
+    ctx, new, Hq, H, max_new = CUTS[shape]
+    c = _Case(env, ctx, new, Hq, H, D, kind, seed=160 + shape)
+    opt = dict(max_new=max_new) if max_new else {}
+    first = c.check(**opt)
+    again, _ = c.run(workspace=c.call.workspace, **opt)
+    assert torch.equal(first, again)
+    c.check(window=1000, prefix=[64 * b % 200 for b in range(len(ctx))], **opt)
+    assert q.qmv_check_status() == 0
+
+
 def test_attend_prompts_rows_that_see_nothing(env):
     """Fewer cached keys than query rows, a request without a cache, missing pages, scales of many sizes."""
     q, torch, dev = env
