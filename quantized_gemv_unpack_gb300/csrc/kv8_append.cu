@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 4 * D ? 1024 / BLOCK : 1) kv8_
   const int tid = threadIdx.x;
   const int run = blockIdx.x / a.head_groups, first_head = (blockIdx.x % a.head_groups) * a.head_group;
   const int last_head = min(a.H, first_head + a.head_group);
+  follow_previous();
   const int2 rn = reinterpret_cast<const int2*>(a.runs)[run];
   const int t0 = rn.x, n = rn.y;
   if (n == 0) return;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kFewThreads) kv8_append_few_kernel(const __gri
   constexpr int C = D / 16, L = 8 / V;         // chunks, lanes per chunk
   __shared__ float2 angles[D / 2];
   const int tid = threadIdx.x, lane = tid & 31;
+  follow_previous();
   const int n_runs = a.n_runs * a.H, run_blocks = (n_runs + kFewThreads / 32 - 1) / (kFewThreads / 32);
   if ((int)blockIdx.x >= run_blocks) {
     const int w = blockIdx.x - run_blocks, groups = (a.n_q_heads + a.q_heads - 1) / a.q_heads;
@@ -453,6 +455,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, head = blockIdx.y;
   const int64_t e0 = (int64_t)blockIdx.x * kReadEntries;
   const int n = (int)min((int64_t)kReadEntries, a.n - e0);
+  follow_previous();
   // every warp finds the stretches: entries of one page that follow one another
   const int mine = lane < n ? a.slots[e0 + lane] : -1;
   const int page = mine < 0 ? -1 : mine / kPage;
@@ -670,7 +673,7 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   rc = kernel_fit(f, threads, smem, &per_sm);
   if (rc) return rc;
   void* args[] = {&a};
-  cudaError_t e = cudaLaunchKernel(f, dim3((unsigned)blocks), dim3(threads), args, smem, static_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_early(f, dim3((unsigned)blocks), threads, args, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");
   return QMV_OK;
 }
@@ -695,14 +698,10 @@ int kv8_read(const qmv_kv_desc* desc, const void* cache, const int32_t* slots, i
   const dim3 grid((unsigned)((n + kReadEntries - 1) / kReadEntries), (unsigned)desc->n_kv_heads);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->type == QMV_KV_INT8;
-  if (desc->head_dim == 64) {
-    if (i8) kv8_read_kernel<64, QMV_KV_INT8><<<grid, kReadThreads, 0, s>>>(a);
-    else kv8_read_kernel<64, QMV_KV_E4M3><<<grid, kReadThreads, 0, s>>>(a);
-  } else {
-    if (i8) kv8_read_kernel<128, QMV_KV_INT8><<<grid, kReadThreads, 0, s>>>(a);
-    else kv8_read_kernel<128, QMV_KV_E4M3><<<grid, kReadThreads, 0, s>>>(a);
-  }
-  cudaError_t e = cudaGetLastError();
+  const void* f = desc->head_dim == 64 ? (i8 ? (const void*)kv8_read_kernel<64, QMV_KV_INT8> : (const void*)kv8_read_kernel<64, QMV_KV_E4M3>)
+                                       : (i8 ? (const void*)kv8_read_kernel<128, QMV_KV_INT8> : (const void*)kv8_read_kernel<128, QMV_KV_E4M3>);
+  void* args[] = {&a};
+  cudaError_t e = launch_early(f, grid, kReadThreads, args, 0, s);
   if (e != cudaSuccess) return cuda_fail(e, "kv8_read launch");
   return QMV_OK;
 }

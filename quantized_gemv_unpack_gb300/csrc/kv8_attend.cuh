@@ -360,6 +360,8 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < S::kStreams * 2) (&sm.piece[0][0] + tid)->len = 0;
+  kv8::let_next_begin();
+  kv8::follow_previous();
   // Up to 32 requests: lane b of every warp holds request b, and each warp sums for itself.
   const bool few = a.B <= 32;
   int4 held = make_int4(0, 0, 0, 0);
@@ -969,8 +971,9 @@ int launch(const Args& a, int blocks, cudaStream_t s) {
   int per_sm = 0;
   int rc = kernel_fit(f, S::kThreads, sizeof(Smem<D, N, R>), &per_sm);
   if (rc) return rc;
-  attend_kernel<D, TYPE, N, R, MODS><<<blocks, S::kThreads, sizeof(Smem<D, N, R>), s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  Args copy = a;
+  void* args[] = {&copy};
+  cudaError_t e = kv8::launch_early(f, dim3(blocks), S::kThreads, args, sizeof(Smem<D, N, R>), s);
   if (e != cudaSuccess) return cuda_fail(e, "kv8_attend launch");
   return QMV_OK;
 }

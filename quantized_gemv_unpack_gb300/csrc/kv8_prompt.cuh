@@ -273,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     for (int i = 0; i < kItems; ++i) core::mbar_init(&sm.item_full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  kv8::let_next_begin();
+  kv8::follow_previous();
   // the largest number of row-tile pairs of a request
   int most = 0;
   for (int b = tid; b < a.B; b += kThreads) most = max(most, (attend::load_req4(a, b).y * a.G + 2 * kRows - 1) / (2 * kRows));
@@ -770,8 +772,9 @@ int launch(const Args& a, int blocks, cudaStream_t s) {
   int per_sm = 0;
   int rc = kernel_fit(f, kThreads, sizeof(Shared<D, SPLIT>), &per_sm);
   if (rc) return rc;
-  prompt_kernel<D, TYPE, MODS, SPLIT><<<blocks, kThreads, sizeof(Shared<D, SPLIT>), s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  Args copy = a;
+  void* args[] = {&copy};
+  cudaError_t e = kv8::launch_early(f, dim3(blocks), kThreads, args, sizeof(Shared<D, SPLIT>), s);
   if (e != cudaSuccess) return cuda_fail(e, "kv8_attend launch");
   return QMV_OK;
 }

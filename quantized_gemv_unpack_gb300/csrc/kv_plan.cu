@@ -84,6 +84,8 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
   const int per = (B + nt - 1) / nt;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
 
+  kv8::let_next_begin();
+  kv8::follow_previous();
   int head = a.ring_state[0], count = a.ring_state[1];
   if (head < 0 || head >= N || count < 0 || count > N) {
     if (block == 0 && tid == 0) atomicCAS(err, 0, (int)QMV_ERR_CORRUPT);
@@ -305,19 +307,11 @@ int kv_plan(const kv_plan_args* a, void* stream) {
   int per_sm = 0;
   int rc = kernel_fit(reinterpret_cast<const void*>(kv_plan_kernel), threads, smem, &per_sm);
   if (rc) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(n_blocks);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = n_blocks;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = n_blocks > 1 ? 1 : 0;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_plan_kernel, *a, n_blocks, err);
+  kv_plan_args copy = *a;
+  int blocks = n_blocks;
+  void* args[] = {&copy, &blocks, &err};
+  cudaError_t e = kv8::launch_early(reinterpret_cast<const void*>(kv_plan_kernel), dim3(n_blocks), threads, args, smem,
+                                    static_cast<cudaStream_t>(stream), n_blocks);
   if (e != cudaSuccess) return cuda_fail(e, "kv_plan launch");
   return QMV_OK;
 }

@@ -33,6 +33,7 @@ struct RopeArgs {
 template <typename TI>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 4 ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];
+  kv8::follow_previous();
   const int h0 = blockIdx.y * a.heads_per_block;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
   kv8::rope_tokens<TI>(a.r, static_cast<const TI*>(a.x), a.ldx, t0, (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0),
@@ -126,10 +127,10 @@ int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, 
   const int chunks = a.heads_per_block * (rope->head_dim / 16);
   const int block = chunks >= kRopeThreads ? kRopeThreads : (chunks + 31) / 32 * 32;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_type == QMV_F32) rope_kernel<float><<<grid, block, 0, s>>>(a);
-  else if (x_type == QMV_BF16) rope_kernel<__nv_bfloat16><<<grid, block, 0, s>>>(a);
-  else rope_kernel<__half><<<grid, block, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const void* f = x_type == QMV_F32 ? (const void*)rope_kernel<float>
+                  : x_type == QMV_BF16 ? (const void*)rope_kernel<__nv_bfloat16> : (const void*)rope_kernel<__half>;
+  void* args[] = {&a};
+  cudaError_t e = kv8::launch_early(f, grid, block, args, 0, s);
   if (e != cudaSuccess) return cuda_fail(e, "rope launch");
   return QMV_OK;
 }

@@ -755,6 +755,41 @@ def test_calls_follow_their_stream(env):
 
 # ----------------------------------------------------------------------------- together
 
+def test_calls_in_a_row_keep_their_order(env):
+    """Each call reads what the one before it wrote, and writes what the one before it read: with and without a wait between."""
+    q, torch, dev = env
+    H, Hq, D, T = 2, 8, 64, 70
+    rope = q.rope_desc(D, [50.0 ** (-i / 32) for i in range(32)])
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+
+    def steps(wait):
+        torch.manual_seed(5)
+        d, cache = _fresh_cache(env, 1, 9, H, D, fill=0)
+        x = torch.randn((T, Hq + 2 * H, D), device=dev, dtype=torch.bfloat16)
+        out = torch.zeros((T, Hq, D), device=dev, dtype=torch.bfloat16)
+        pos, table = i32([list(range(T))]), i32([[3, 5, 0, 7]])
+        slots = i32([3 * 64 + i for i in range(64)] + [5 * 64 + i for i in range(6)])
+        runs = i32([[0, 64], [64, 6]])
+        calls = [q.Rope(rope, x[:, :Hq], pos, x[:, :Hq]), q.KvAppend(d, cache, x[:, Hq:Hq + H], x[:, Hq + H:], slots, runs, rope=rope, positions=pos),
+                 q.KvAttend(d, cache, x[:, :Hq], out, i32([0, T]), i32([T]), table, 0.125, max_new=T),
+                 q.Rope(rope, out, pos, x[:, :Hq], inverse=True),
+                 q.KvRead(d, cache, slots, x[:, Hq:Hq + H], x[:, Hq + H:])]
+        seen = []
+        for _ in range(12):
+            for c in calls:
+                c.run()
+                if wait:
+                    torch.cuda.synchronize()
+            seen.append((x.clone(), out.clone()))
+            x.mul_(1.25)
+        torch.cuda.synchronize()
+        return seen, cache
+
+    (a, ca), (b, cb) = steps(False), steps(True)
+    assert torch.equal(ca, cb)
+    assert all(torch.equal(p, r) for s, t in zip(a, b) for p, r in zip(s, t))
+
+
 def test_steps_together_match_a_cache_in_full_precision(env):
     """Prompts, then decode steps with requests that come and go: plan, append with rotation, attend; against attention
     over the unquantized keys and values, within the quantization's error, and the same from a captured graph."""
