@@ -38,6 +38,7 @@ struct AppendArgs {
   int H;
   int head_group, head_groups;   // KV heads of one block, blocks per run
   int q_heads;                   // heads of a block that rotates query heads (few tokens)
+  int beside;                    // follows this call's own rotation of the query heads
   int* err;
 };
 
@@ -91,7 +92,7 @@ __device__ __forceinline__ int v_swap(int d) { return (2 * (d / 16) + ((d >> 1) 
 
 // BLOCK threads hold a full page's 64 * D / 16 pieces, U per thread.
 template <typename TI, int D, int TYPE, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, BLOCK == 4 * D ? 1024 / BLOCK : 1) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
+__device__ __forceinline__ void append_run(const AppendArgs& a) {
   constexpr int C = D / 16;                        // pieces of sixteen values per token
   constexpr int U = kPage * C / BLOCK;             // pieces per thread of a full page
   __shared__ __align__(16) uint32_t vt[D][kPage / 4];   // V codes, transposed
@@ -102,7 +103,6 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 4 * D ? 1024 / BLOCK : 1) kv8_
   const int tid = threadIdx.x;
   const int run = blockIdx.x / a.head_groups, first_head = (blockIdx.x % a.head_groups) * a.head_group;
   const int last_head = min(a.H, first_head + a.head_group);
-  follow_previous();
   const int2 rn = reinterpret_cast<const int2*>(a.runs)[run];
   const int t0 = rn.x, n = rn.y;
   if (n == 0) return;
@@ -297,6 +297,15 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 4 * D ? 1024 / BLOCK : 1) kv8_
       }
     }
   }
+}
+
+// Behind this call's own rotation of the query heads (a.beside) it does not wait for that, which it shares nothing with:
+// the rotation lets it begin when what came before has ended, and it waits at its end, so that both have ended with it.
+template <typename TI, int D, int TYPE, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
+  if (!a.beside) follow_previous();
+  append_run<TI, D, TYPE, BLOCK>(a);
+  if (a.beside) follow_previous();
 }
 
 // Runs of a few tokens (a decode step: one). One warp takes a run of one head, a lane the two values of D / 64 pairs of K
@@ -646,10 +655,12 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   const int D = desc->head_dim, sms = sm_count();
   // runs of less than eight tokens on average go to the kernel of one warp per run and head
   const bool few = g->n_tokens < 8 * (int64_t)g->n_runs;
-  // one head per block while that leaves an SM fewer than eight; more blocks than that share the angles of their tokens
-  // among two or four heads
-  const int64_t per_head = (int64_t)g->n_runs * desc->n_kv_heads;
-  a.head_group = !rope || per_head < 4 * (int64_t)sms ? 1 : per_head < 16 * (int64_t)sms ? 2 : 4;
+  // The heads of a block share the angles of its run's tokens: the fewest heads (a power of two, up to 8) with which all
+  // blocks are resident at once. 8190 tokens of 40 and 8 heads of 128, rotation included: 49 us with 4 heads a block (the
+  // rule's choice), 57, 53 and 63 with 1, 2 and 8; 512 tokens: 10.2 with 1, 12.2, 17.9 and 28 with 2, 4 and 8.
+  const int64_t per_head = (int64_t)g->n_runs * desc->n_kv_heads, resident = (int64_t)sms * (1024 / (4 * D));
+  a.head_group = 1;
+  while (rope && a.head_group < 8 && per_head > a.head_group * resident) a.head_group *= 2;
   a.head_groups = (desc->n_kv_heads + a.head_group - 1) / a.head_group;
   int64_t blocks = few ? (per_head + kFewThreads / 32 - 1) / (kFewThreads / 32) : (int64_t)g->n_runs * a.head_groups;
   if (g->q && few) {
@@ -658,9 +669,10 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   } else if (g->q) {
     // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 32 + 27
     // us, and 65 us as blocks of one launch, where the cache write's registers halve the rotation's loads in flight)
-    rc = rope_run(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
-                  g->ldqo, 0, stream);
+    rc = rope_launch(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
+                     g->ldqo, 0, blocks > 0, static_cast<cudaStream_t>(stream));
     if (rc) return rc;
+    a.beside = 1;
   }
   if (blocks == 0) return QMV_OK;
   if (blocks > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "too many runs");

@@ -27,6 +27,7 @@ struct RopeArgs {
   const int32_t* positions;
   int64_t ldx, ldo, ldp, n_tokens;
   int n_heads, out_type, tokens_per_block, heads_per_block;
+  int lead;   // the next kernel shares nothing with this one and waits for it at its own end
   float sign;
 };
 
@@ -34,6 +35,7 @@ template <typename TI>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 4 ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];
   kv8::follow_previous();
+  if (a.lead) kv8::let_next_begin();
   const int h0 = blockIdx.y * a.heads_per_block;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
   kv8::rope_tokens<TI>(a.r, static_cast<const TI*>(a.x), a.ldx, t0, (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0),
@@ -54,6 +56,53 @@ int check_rope(const qmv_rope* r) {
   if (r->n_axes < 1 || r->n_axes > QMV_ROPE_MAX_AXES) return fail(QMV_ERR_ARG, "n_axes=%d outside 1..%d", r->n_axes, QMV_ROPE_MAX_AXES);
   for (int i = 0; i < r->rot_dim / 2; ++i)
     if (r->axis[i] >= r->n_axes) return fail(QMV_ERR_ARG, "pair %d: axis %d of %d", i, r->axis[i], r->n_axes);
+  return QMV_OK;
+}
+
+int rope_launch(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int n_heads, int64_t ldx,
+                const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, bool lead, cudaStream_t s) {
+  int rc = check_rope(rope);
+  if (rc) return rc;
+  const int xs = dtype_size(x_type), os = dtype_size(out_type);
+  if (!xs || !os) return fail(QMV_ERR_ARG, "x_type=%d out_type=%d", x_type, out_type);
+  if (n_tokens < 0 || n_heads < 1 || n_tokens > INT32_MAX || n_heads > 65536)
+    return fail(QMV_ERR_ARG, "n_tokens=%lld n_heads=%d", (long long)n_tokens, n_heads);
+  const int64_t row = (int64_t)n_heads * rope->head_dim;
+  if (ldx < row || ldo < row || ldp < n_tokens) return fail(QMV_ERR_ARG, "ldx=%lld ldo=%lld ldp=%lld", (long long)ldx, (long long)ldo, (long long)ldp);
+  if (ldx * xs % 16 || ldo * os % 16) return fail(QMV_ERR_ALIGN, "rows of x and out must be 16-byte aligned");
+  if (n_tokens == 0) return QMV_OK;
+  if (!x || !out || !positions) return fail(QMV_ERR_ARG, "NULL x, out or positions");
+  if (!aligned16(x) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return fail(QMV_ERR_ALIGN, "x and out must be 16-byte aligned, positions 4-byte");
+  if (x == out && (x_type != out_type || ldx != ldo)) return fail(QMV_ERR_ARG, "in place needs one type and one stride");
+
+  RopeArgs a;
+  a.r = *rope;
+  a.x = x;
+  a.out = out;
+  a.positions = positions;
+  a.ldx = ldx;
+  a.ldo = ldo;
+  a.ldp = ldp;
+  a.n_tokens = n_tokens;
+  a.n_heads = n_heads;
+  a.out_type = out_type;
+  a.sign = inverse ? -1.f : 1.f;
+  a.lead = lead;
+  // Enough tokens for four blocks per SM: all heads in one block, four tokens at a time. Fewer: one token and 16 heads.
+  const bool split = n_tokens < 4 * sm_count();
+  a.tokens_per_block = split ? 1 : kMaxTokensPerBlock;
+  a.heads_per_block = split && n_heads > 16 ? 16 : n_heads;
+  const dim3 grid((unsigned)((n_tokens + a.tokens_per_block - 1) / a.tokens_per_block),
+                  (unsigned)((n_heads + a.heads_per_block - 1) / a.heads_per_block));
+  // a block of few heads has one chunk per thread
+  const int chunks = a.heads_per_block * (rope->head_dim / 16);
+  const int block = chunks >= kRopeThreads ? kRopeThreads : (chunks + 31) / 32 * 32;
+  const void* f = x_type == QMV_F32 ? (const void*)rope_kernel<float>
+                  : x_type == QMV_BF16 ? (const void*)rope_kernel<__nv_bfloat16> : (const void*)rope_kernel<__half>;
+  void* args[] = {&a};
+  cudaError_t e = launch_early(f, grid, block, args, 0, s);
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
   return QMV_OK;
 }
 }  // namespace kv8
@@ -90,49 +139,8 @@ int rope_desc(int32_t head_dim, int32_t rot_dim, int32_t n_axes, int32_t interle
 
 int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int32_t n_heads, int64_t ldx,
              const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, void* stream) {
-  int rc = kv8::check_rope(rope);
-  if (rc) return rc;
-  const int xs = kv8::dtype_size(x_type), os = kv8::dtype_size(out_type);
-  if (!xs || !os) return fail(QMV_ERR_ARG, "x_type=%d out_type=%d", x_type, out_type);
-  if (n_tokens < 0 || n_heads < 1 || n_tokens > INT32_MAX || n_heads > 65536)
-    return fail(QMV_ERR_ARG, "n_tokens=%lld n_heads=%d", (long long)n_tokens, n_heads);
-  const int64_t row = (int64_t)n_heads * rope->head_dim;
-  if (ldx < row || ldo < row || ldp < n_tokens) return fail(QMV_ERR_ARG, "ldx=%lld ldo=%lld ldp=%lld", (long long)ldx, (long long)ldo, (long long)ldp);
-  if (ldx * xs % 16 || ldo * os % 16) return fail(QMV_ERR_ALIGN, "rows of x and out must be 16-byte aligned");
-  if (n_tokens == 0) return QMV_OK;
-  if (!x || !out || !positions) return fail(QMV_ERR_ARG, "NULL x, out or positions");
-  if (!aligned16(x) || !aligned16(out) || (reinterpret_cast<uintptr_t>(positions) & 3u))
-    return fail(QMV_ERR_ALIGN, "x and out must be 16-byte aligned, positions 4-byte");
-  if (x == out && (x_type != out_type || ldx != ldo)) return fail(QMV_ERR_ARG, "in place needs one type and one stride");
-
-  RopeArgs a;
-  a.r = *rope;
-  a.x = x;
-  a.out = out;
-  a.positions = positions;
-  a.ldx = ldx;
-  a.ldo = ldo;
-  a.ldp = ldp;
-  a.n_tokens = n_tokens;
-  a.n_heads = n_heads;
-  a.out_type = out_type;
-  a.sign = inverse ? -1.f : 1.f;
-  // Enough tokens for four blocks per SM: all heads in one block, four tokens at a time. Fewer: one token and 16 heads.
-  const bool split = n_tokens < 4 * sm_count();
-  a.tokens_per_block = split ? 1 : kMaxTokensPerBlock;
-  a.heads_per_block = split && n_heads > 16 ? 16 : n_heads;
-  const dim3 grid((unsigned)((n_tokens + a.tokens_per_block - 1) / a.tokens_per_block),
-                  (unsigned)((n_heads + a.heads_per_block - 1) / a.heads_per_block));
-  // a block of few heads has one chunk per thread
-  const int chunks = a.heads_per_block * (rope->head_dim / 16);
-  const int block = chunks >= kRopeThreads ? kRopeThreads : (chunks + 31) / 32 * 32;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const void* f = x_type == QMV_F32 ? (const void*)rope_kernel<float>
-                  : x_type == QMV_BF16 ? (const void*)rope_kernel<__nv_bfloat16> : (const void*)rope_kernel<__half>;
-  void* args[] = {&a};
-  cudaError_t e = kv8::launch_early(f, grid, block, args, 0, s);
-  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
-  return QMV_OK;
+  return kv8::rope_launch(rope, x, x_type, n_tokens, n_heads, ldx, positions, ldp, out, out_type, ldo, inverse, false,
+                          static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
