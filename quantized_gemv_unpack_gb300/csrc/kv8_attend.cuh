@@ -67,7 +67,6 @@ struct Args {
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr int kWeights = 1024;   // factors of a join held in shared memory
 constexpr int kStreamRows = 128, kPartRows = 256;   // rows per block of the workspace: of its streams, in all
 
 template <int D, int N, int R>
@@ -266,80 +265,80 @@ struct Smem {
   Piece piece[S::kStreams][2];
   const float* entry_o[S::kStreams * 2];
   const float2* entry_ml[S::kStreams * 2];
-  float2 stat[S::kRows];
-  float weights[kWeights];
   long long warp_sum[S::kWarps];
   int warp_segs[S::kWarps];
   int last[2];
 };
 
 // Join E partial tiles of `rows` rows (ml(e, row): maximum and sum, o(e, row, d): four values) into the output or into
-// (dst_o, dst_ml), by all threads of the block. The tiles' factors lie in `weights` (kWeights floats, shared) where they
-// fit, else a factor is taken from its maximum each time.
-template <int D, int THREADS, typename MlFn, typename OFn>
-__device__ __forceinline__ void join(const Args& a, int E, int rows, MlFn ml, OFn o, float2* stat, float* weights, bool to_out,
-                                     int h, int qs, int row0, float* dst_o, float2* dst_ml) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool held = E * rows <= kWeights;
-  for (int row = warp; row < rows; row += THREADS / 32) {
-    float2 mine = make_float2(-INFINITY, 0.f);
-    if (lane < E) mine = ml(lane, row);
+// (dst_o, dst_ml): a warp of W takes row `first` and every W-th after it, with no step of the whole block. Lane e holds
+// the factor of part e (of 32 at a time); BATCH parts are in flight, which is what a join out of L2 waits for: 19 parts of 25
+// rows cost 11 us with six. With D = 64 the two halves of a warp take turns with the parts.
+template <int D, int W, int BATCH, typename MlFn, typename OFn>
+__device__ __forceinline__ void join(const Args& a, int E, int rows, int first, MlFn ml, OFn o, bool to_out, int h, int qs, int row0,
+                                     float* dst_o, float2* dst_ml) {
+  constexpr int HALVES = 128 / D, LANES = 32 / HALVES;
+  const int lane = threadIdx.x & 31, half = lane / LANES, d = (lane % LANES) * 4;
+  float2 next = make_float2(-INFINITY, 0.f);
+  if (lane < E && first < rows) next = ml(lane, first);
+  for (int row = first; row < rows; row += W) {
+    const float2 mine = next;
+    if (lane < E && row + W < rows) next = ml(lane, row + W);
     float m = mine.x;
     for (int e = lane + 32; e < E; e += 32) m = fmaxf(m, ml(e, row).x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     const float use = m == -INFINITY ? 0.f : m;
-    const float w0 = ex2(mine.x - use);
-    float l = w0 * mine.y;
+    float w = ex2(mine.x - use);
+    float l = w * mine.y;
     for (int e = lane + 32; e < E; e += 32) {
       const float2 v = ml(e, row);
       l += ex2(v.x - use) * v.y;
     }
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
-    const float inv = !to_out ? 1.f : l == 0.f ? 0.f : 1.f / l;
-    if (held) {
-      if (lane < E) weights[lane * rows + row] = w0 * inv;
-      for (int e = lane + 32; e < E; e += 32) weights[e * rows + row] = ex2(ml(e, row).x - use) * inv;
-    }
-    if (lane == 0) {
-      stat[row] = make_float2(use, inv);
-      if (!to_out) dst_ml[row] = make_float2(m, l);
-      else if (a.lse) {
-        const int rr = row0 + row, tok = a.by_g(rr);
-        a.lse[(int64_t)(qs + tok) * a.Hq + h * a.G + rr - tok * a.G] = l == 0.f ? -INFINITY : (use + log2f(l)) * kLn2;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < E; c += 32) {
+      const int n = min(32, E - c);
+      if (c > 0) w = lane < n ? ex2(ml(c + lane, row).x - use) : 0.f;
+      for (int i0 = 0; i0 < n; i0 += BATCH * HALVES) {
+        float4 v[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int i = i0 + j * HALVES + half;
+          v[j] = i < n ? o(c + i, row, d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+          const int i = i0 + j * HALVES + half;   // past the end: v is 0, and lanes from E on hold the factor of -inf, 0
+          const float f = __shfl_sync(0xFFFFFFFFu, w, i & 31);
+          s.x += f * v[j].x;
+          s.y += f * v[j].y;
+          s.z += f * v[j].z;
+          s.w += f * v[j].w;
+        }
       }
     }
-  }
-  __syncthreads();
-  constexpr int Q = D / 4;
-  for (int u = tid; u < rows * Q; u += THREADS) {
-    const int row = u / Q, d = (u % Q) * 4;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float4 v, float w) {
-      s.x += w * v.x;
-      s.y += w * v.y;
-      s.z += w * v.z;
-      s.w += w * v.w;
-    };
-    if (held) {
-#pragma unroll 6
-      for (int e = 0; e < E; ++e) add(o(e, row, d), weights[e * rows + row]);
-    } else {
-      const float2 st = stat[row];
-#pragma unroll 4
-      for (int e = 0; e < E; ++e) add(o(e, row, d), ex2(ml(e, row).x - st.x) * st.y);
+    if (HALVES == 2) {
+      s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, 16);
+      s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, 16);
+      s.z += __shfl_xor_sync(0xFFFFFFFFu, s.z, 16);
+      s.w += __shfl_xor_sync(0xFFFFFFFFu, s.w, 16);
     }
     if (to_out) {
-      const int rr = row0 + row, tok = a.by_g(rr);
-      const int64_t at = (int64_t)(qs + tok) * a.ldo + (int64_t)(h * a.G + rr - tok * a.G) * D + d;
-      store_as(a.out_type, a.out, at, s.x, s.y);
-      store_as(a.out_type, a.out, at + 2, s.z, s.w);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int rr = row0 + row, tok = a.by_g(rr), hq = h * a.G + rr - tok * a.G;
+      if (half == 0) {
+        const int64_t at = (int64_t)(qs + tok) * a.ldo + (int64_t)hq * D + d;
+        store_as(a.out_type, a.out, at, s.x * inv, s.y * inv);
+        store_as(a.out_type, a.out, at + 2, s.z * inv, s.w * inv);
+      }
+      if (lane == 0 && a.lse) a.lse[(int64_t)(qs + tok) * a.Hq + hq] = l == 0.f ? -INFINITY : (use + log2f(l)) * kLn2;
     } else {
-      *reinterpret_cast<float4*>(dst_o + (int64_t)row * D + d) = s;
+      if (half == 0) *reinterpret_cast<float4*>(dst_o + (int64_t)row * D + d) = s;
+      if (lane == 0) dst_ml[row] = make_float2(m, l);
     }
   }
-  __syncthreads();
 }
 
 template <int D, int TYPE, int N, int R, bool MODS>
@@ -899,7 +898,15 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     p_start = (&sm.piece[0][0])[lane].start;
     p_len = (&sm.piece[0][0])[lane].len;
   }
-  unsigned todo = __ballot_sync(0xFFFFFFFFu, p_len > 0);
+  const unsigned all = __ballot_sync(0xFFFFFFFFu, p_len > 0);
+  unsigned todo = all;
+  if (warp == 0 && p_len > 0) {
+    const int at = __popc(all & ((1u << lane) - 1));
+    sm.entry_o[at] = (&sm.piece[0][0])[lane].o;
+    sm.entry_ml[at] = (&sm.piece[0][0])[lane].ml;
+  }
+  __syncthreads();
+  int turn = 0;   // rows given out so far: the next tile's begin with the next warp
   int shared_tiles[2] = {-1, -1};   // entries of the (at most two) tiles that other blocks hold a part of
   auto slot_of = [&](const Piece& pc, int c) {   // the rows where block c leaves its part of the tile
     return (int64_t)c * kPartRows + kStreamRows + (whose1 >= 0 || pc.start < blocks.at(c) ? 0 : S::kRows);
@@ -915,12 +922,7 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     const int covered = __reduce_add_sync(0xFFFFFFFFu, (same >> lane) & 1 ? p_len : 0), n_e = __popc(same);
     todo &= ~same;
     const Piece& pc = (&sm.piece[0][0])[e0];
-    if (warp == 0 && (same >> lane) & 1) {
-      const int at = __popc(same & ((1u << lane) - 1));
-      sm.entry_o[at] = (&sm.piece[0][0])[lane].o;
-      sm.entry_ml[at] = (&sm.piece[0][0])[lane].ml;
-    }
-    __syncthreads();
+    const int base = __popc(all & ((1u << e0) - 1));   // a tile's pieces follow one another
     const Req r = get_req(pc.b);
     const int row0 = pc.tile * S::kRows, rows = min(S::kRows, r.rows - row0);
     const bool whole = covered == pc.n;
@@ -929,10 +931,11 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
       if (shared_tiles[0] < 0) shared_tiles[0] = e0;
       else shared_tiles[1] = e0;
     }
-    join<D, S::kThreads>(
-        a, n_e, rows, [&](int e, int row) { return sm.entry_ml[e][row]; },
-        [&](int e, int row, int d) { return *reinterpret_cast<const float4*>(sm.entry_o[e] + row * D + d); }, sm.stat,
-        sm.weights, whole, pc.h, r.qs, row0, a.part_o + mine_at * D, a.part_ml + mine_at);
+    join<D, S::kWarps, 8>(
+        a, n_e, rows, (warp + S::kWarps - turn % S::kWarps) % S::kWarps, [&](int e, int row) { return sm.entry_ml[base + e][row]; },
+        [&](int e, int row, int d) { return *reinterpret_cast<const float4*>(sm.entry_o[base + e] + row * D + d); }, whole, pc.h, r.qs,
+        row0, a.part_o + mine_at * D, a.part_ml + mine_at);
+    turn += rows;
   }
   if (shared_tiles[0] < 0) return;
   // ---- the last of a tile's blocks to arrive joins their parts
@@ -957,10 +960,10 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
     const Req r = get_req(pc.b);
     const int row0 = pc.tile * S::kRows, rows = min(S::kRows, r.rows - row0);
     // written by other blocks during this launch: read past L1
-    join<D, S::kThreads>(
-        a, c1 - c0 + 1, rows, [&](int e, int row) { return __ldcg(a.part_ml + slot_of(pc, c0 + e) + row); },
+    join<D, S::kWarps, 20>(
+        a, c1 - c0 + 1, rows, warp, [&](int e, int row) { return __ldcg(a.part_ml + slot_of(pc, c0 + e) + row); },
         [&](int e, int row, int d) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot_of(pc, c0 + e) + row) * D + d)); },
-        sm.stat, sm.weights, true, pc.h, r.qs, row0, nullptr, nullptr);
+        true, pc.h, r.qs, row0, nullptr, nullptr);
   }
 }
 
