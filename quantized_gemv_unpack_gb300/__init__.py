@@ -201,6 +201,11 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _ready(f, first, *rest):
+    """Arguments of f as the C types it takes, so that a call that is made many times does not convert them each time."""
+    return (first,) + tuple(t(v) for t, v in zip(f.argtypes[1:], rest))
+
+
 def _rows(t):
     """(M, leading dimension) of a 2-D (or 1-D) activation/output tensor."""
     if t.dim() == 1:
@@ -499,8 +504,8 @@ class Rope:
         pos = _positions(rope, positions, T, dev)
         self.keep = (rope, x, pos, out)
         self._call = lib().rope_run
-        self._args = (ctypes.byref(rope), xp, _dtype(x), T, H, ldx, pos.data_ptr(), pos.stride(0), op, _dtype(out), ldo,
-                      int(inverse))
+        self._args = _ready(self._call, ctypes.byref(rope), xp, _dtype(x), T, H, ldx, pos.data_ptr(), pos.stride(0), op,
+                            _dtype(out), ldo, int(inverse))
 
     def run(self, stream=None):
         _check(self._call(*self._args, _stream(stream)))
@@ -560,7 +565,7 @@ class KvRead:
         _ints("slots", slots, (n,), dev)
         self.keep = (desc, _cache(desc, cache), slots, k_out, v_out)
         self._call = lib().kv8_read
-        self._args = (ctypes.byref(desc), cache.data_ptr(), slots.data_ptr(), n, kp, vp, _dtype(k_out), ldk)
+        self._args = _ready(self._call, ctypes.byref(desc), cache.data_ptr(), slots.data_ptr(), n, kp, vp, _dtype(k_out), ldk)
 
     def run(self, stream=None):
         _check(self._call(*self._args, _stream(stream)))
