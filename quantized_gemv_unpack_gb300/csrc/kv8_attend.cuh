@@ -169,6 +169,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A product's factor f to a score, and c of cap * tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1), whose argument of the
+// base-2 exponential is x times it; the capped score with `cap` (and so the score) in units of log2. The sum is 1 or more,
+// so that the reciprocal of infinity is 0 and no other case arises.
+__device__ __forceinline__ float cap_factor(float softcap, float f) { return f * (2.f * kLog2e / softcap); }
+__device__ __forceinline__ float capped(float s, float factor, float cap) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(s * factor) + 1.f));
+  return fmaf(-2.f * cap, r, cap);
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -737,17 +746,26 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
             float f[2] = {fmaxf(mult[n][0] * scale.x, 1e-37f), fmaxf(mult[n][1] * scale.x, 1e-37f)};
             const int tok0 = key0 + 16 * (g >> 1) + (g & 1);
             if (MODS) {
-              const float k2 = a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+              if (a.softcap > 0.f) {
+                const float c2[2] = {cap_factor(a.softcap, f[0]), cap_factor(a.softcap, f[1])}, cap = a.softcap * kLog2e;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  float x = s[n][i][c] * f[c & 1];
-                  // cap * tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
-                  if (a.softcap > 0.f) x = a.softcap - __fdividef(2.f * a.softcap, ex2(x * k2) + 1.f);
-                  const int gap = pos[n][c & 1] - (tok0 + 4 * i + 2 * (c >> 1));
-                  s[n][i][c] = x * kLog2e - slope[n][c & 1] * (float)abs(gap);
-                }
+                  for (int c = 0; c < 4; ++c) s[n][i][c] = capped(s[n][i][c], c2[c & 1], cap);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) s[n][i][c] *= f[c & 1] * kLog2e;
+              }
+              if (a.slopes) {
+                const float gap[2] = {(float)(pos[n][0] - tok0), (float)(pos[n][1] - tok0)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int c = 0; c < 4; ++c)
+                    s[n][i][c] = fmaf(-slope[n][c & 1], fabsf(gap[c & 1] - (4 * i + 2 * (c >> 1))), s[n][i][c]);
+              }
               f[0] = f[1] = 1.f;
             }
             if (cut_page) {

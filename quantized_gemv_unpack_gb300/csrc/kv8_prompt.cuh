@@ -423,26 +423,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           const float4 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
           const int key0 = (it.p0 + 2 * j) * kPage;
           float f0 = fmaxf(mult * sc0.x, 1e-37f), f1 = fmaxf(mult * sc1.x, 1e-37f);
-          const bool slow = MODS || sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
+          const bool cut = sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
           uint32_t x[128];   // the row's scores, until their p goes back to the same columns
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x + 32 * c);
           wait_ld();
-          if (slow) {
-            // masks, cap and distance bias: the scores as they are wanted, in units of log2
-            const float k2 = MODS && a.softcap > 0.f ? 2.f * kLog2e / a.softcap : 0.f;
+          if (MODS) {
+            // cap and distance bias: the scores as they are wanted, in units of log2
+            if (a.softcap > 0.f) {
+              const float c0 = attend::cap_factor(a.softcap, f0), c1 = attend::cap_factor(a.softcap, f1), cap = a.softcap * kLog2e;
 #pragma unroll
-            for (int q = 0; q < 128; ++q) {
-              const int key = key0 + q;
-              float y = __uint_as_float(x[q]) * (q < 64 ? f0 : f1);
-              if (MODS) {
-                if (a.softcap > 0.f) y = a.softcap - __fdividef(2.f * a.softcap, ex2(y * k2) + 1.f);
-                y = y * kLog2e - slope * (float)abs(pos - key);
-              }
-              if ((q < 64 ? sc0.x : sc1.x) < 0.f || key < lo || key >= hi) y = -INFINITY;
-              x[q] = __float_as_uint(y);
+              for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(attend::capped(__uint_as_float(x[q]), q < 64 ? c0 : c1, cap));
+            } else {
+#pragma unroll
+              for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * ((q < 64 ? f0 : f1) * kLog2e));
+            }
+            if (a.slopes) {
+              const float gap = (float)(pos - key0);
+#pragma unroll
+              for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(fmaf(-slope, fabsf(gap - q), __uint_as_float(x[q])));
             }
             f0 = f1 = 1.f;
+          }
+          if (cut) {
+            const int from = max(lo, 0) - key0, to = hi - key0;
+            const int from0 = sc0.x < 0.f ? kStep : from, from1 = sc1.x < 0.f ? kStep : from;
+#pragma unroll
+            for (int q = 0; q < 128; ++q)
+              if (q < (q < 64 ? from0 : from1) || q >= to) x[q] = __float_as_uint(-INFINITY);
           }
           float top[4];   // of halves of the pages
 #pragma unroll
