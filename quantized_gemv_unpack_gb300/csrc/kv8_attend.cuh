@@ -220,6 +220,18 @@ __device__ __forceinline__ void store_as(int type, void* base, int64_t i, float 
     *reinterpret_cast<__half2*>(static_cast<__half*>(base) + i) = __floats2half2_rn(x, y);
   }
 }
+// Four values in one store; i is a multiple of four.
+__device__ __forceinline__ void store4_as(int type, void* base, int64_t i, float4 v) {
+  if (type == QMV_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = v;
+  } else if (type == QMV_BF16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__half*>(base) + i) = make_uint2(pack_h2(v.x, v.y), pack_h2(v.z, v.w));
+  }
+}
 // N pieces of eight query values at the offsets at[0..N) of q, of the type known at run time (a negative offset: zeros).
 // The type is chosen once around all of them, so that their loads are in flight together.
 template <typename T, int N>
@@ -339,8 +351,7 @@ __device__ __forceinline__ void join(const Args& a, int E, int rows, int first, 
       const int rr = row0 + row, tok = a.by_g(rr), hq = h * a.G + rr - tok * a.G;
       if (half == 0) {
         const int64_t at = (int64_t)(qs + tok) * a.ldo + (int64_t)hq * D + d;
-        store_as(a.out_type, a.out, at, s.x * inv, s.y * inv);
-        store_as(a.out_type, a.out, at + 2, s.z * inv, s.w * inv);
+        store4_as(a.out_type, a.out, at, make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv));
       }
       if (lane == 0 && a.lse) a.lse[(int64_t)(qs + tok) * a.Hq + hq] = l == 0.f ? -INFINITY : (use + log2f(l)) * kLn2;
     } else {

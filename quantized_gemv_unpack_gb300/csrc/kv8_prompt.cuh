@@ -45,7 +45,9 @@ constexpr int kWarps = 16, kThreads = kWarps * 32, kKeyThreads = 128, kValueThre
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 constexpr int kRows = 128, kStep = 128;  // rows of a tile, keys of a step
 constexpr int kHeld = 512;               // parts times rows that a join holds in shared memory: what L1 keeps counts (below)
-constexpr int kChunk = 4;                // steps of a part at least
+// Steps of a part at least, and steps up to which an item stays whole: 100 tokens of 24 and 4 heads over 600 take 22 us whole
+// and 33 in two parts; 20 tokens of 8 heads over 2048 32 us with parts of 4 steps and 35 with 6.
+constexpr int kChunk = 4, kWhole = 6;
 constexpr int kItems = 8;                // items the roles may be apart
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
 
@@ -201,39 +203,36 @@ __device__ __noinline__ void join_parts(const Args& a, int64_t first, int stride
       }
     }
     group_sync(group);
-    // two pieces of four values per thread at a time, and ten parts of them in flight
-    constexpr int Q = D / 4, AT = 2;
+    // Eight pieces of four values per thread at a time, part after part. A row's pieces and the rows of a part follow one
+    // another, so that piece u + 128 i lies 128 i pieces further on. (Fewer pieces and several parts in flight, unrolled, took
+    // 21 us in place of 10 for 128 rows of three parts.)
+    constexpr int Q = D / 4, AT = 8;
     for (int u0 = t; u0 < nr * Q; u0 += AT * kRows) {
+      const float4* from = reinterpret_cast<const float4*>(a.part_o + (first + r0) * D) + u0;
       float4 sum[AT];
-      const float4* from[AT];
-      int r[AT];
 #pragma unroll
-      for (int i = 0; i < AT; ++i) {
-        const int u = min(u0 + i * kRows, nr * Q - 1);   // past the end: the last piece again, not stored
-        r[i] = u / Q;
-        from[i] = reinterpret_cast<const float4*>(a.part_o + (first + r0 + r[i]) * D) + u % Q;
-        sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll 10
-      for (int e = 0; e < entries; ++e) {
+      for (int i = 0; i < AT; ++i) sum[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int e = 0; e < entries; ++e, from += (int64_t)stride * Q) {
+        float4 v[AT];
+#pragma unroll
+        for (int i = 0; i < AT; ++i) v[i] = u0 + i * kRows < nr * Q ? __ldcg(from + i * kRows) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < AT; ++i) {
-          const float4 v = __ldcg(from[i] + (int64_t)e * stride * Q);
-          const float w = held[e * nr + r[i]].x;
-          sum[i].x += w * v.x;
-          sum[i].y += w * v.y;
-          sum[i].z += w * v.z;
-          sum[i].w += w * v.w;
+          if (u0 + i * kRows >= nr * Q) continue;
+          const float w = held[e * nr + u0 / Q + i * (kRows / Q)].x;
+          sum[i].x += w * v[i].x;
+          sum[i].y += w * v[i].y;
+          sum[i].z += w * v[i].z;
+          sum[i].w += w * v[i].w;
         }
       }
 #pragma unroll
       for (int i = 0; i < AT; ++i) {
         const int u = u0 + i * kRows;
         if (u >= nr * Q) continue;
-        const int rx = row1 + r0 + r[i], tx = a.by_g(rx);
-        const int64_t to = (int64_t)(qs + tx) * a.ldo + (int64_t)(h * a.G + rx - tx * a.G) * D + (u % Q) * 4;
-        attend::store_as(a.out_type, a.out, to, sum[i].x, sum[i].y);
-        attend::store_as(a.out_type, a.out, to + 2, sum[i].z, sum[i].w);
+        const int rx = row1 + r0 + u / Q, tx = a.by_g(rx);
+        attend::store4_as(a.out_type, a.out, (int64_t)(qs + tx) * a.ldo + (int64_t)(h * a.G + rx - tx * a.G) * D + (u % Q) * 4, sum[i]);
       }
     }
     group_sync(group);
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     it.steps = (it.pages + 1) / 2;
     it.parts = 1;
     if (SPLIT && n_split > 1) {
-      const int chunk = max((it.steps + n_split - 1) / n_split, kChunk), first = it.part * chunk;
+      const int chunk = it.steps <= kWhole ? it.steps : max((it.steps + n_split - 1) / n_split, kChunk), first = it.part * chunk;
       it.parts = (it.steps + chunk - 1) / chunk;
       if (it.part >= it.parts) return false;
       it.steps = min(chunk, it.steps - first);
