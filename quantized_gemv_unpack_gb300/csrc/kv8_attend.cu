@@ -34,8 +34,8 @@ int check_workspace(const qmv_kv_desc* desc, const void* workspace, size_t ws_by
   return QMV_OK;
 }
 
-// The kernel of a call, by the query rows per (request, KV head) that max_new bounds. Measured (times in us, warp-level
-// tensor cores / tcgen05): 30 rows of 40 query and 8 KV heads of 128, 1 request of 16384 tokens 38 / 46, 4 of them 48 / 72,
+// The kernel of a call, by the query rows per (request, KV head) that max_new bounds. Measured when the rule was set (times in us, warp-level
+// tensor cores / tcgen05; both have gained 5 to 20 % since): 30 rows of 40 query and 8 KV heads of 128, 1 request of 16384 tokens 38 / 46, 4 of them 48 / 72,
 // 16 of 2048 31 / 34; 48 rows of one KV head, 34 / 35 over 4 requests of 4096 tokens, 66 / 49 over 4 of 16384, 30 / 26 over
 // 4 of 1200; with 65 and 130 rows of 8 heads the first takes 1.5 to 4 times as long. Few rows are bound by the cache's
 // bytes and by joins, which the first has more streams for; many rows by the products.

@@ -23,7 +23,12 @@
 //
 // What bounds it: per step and tile 2 * 128 * 128 * D multiply-adds, 1024 tensor
 // clocks for D = 128, against 128 exponentials per row thread (the exponential
-// unit) and 16 codes per conversion lane and register.
+// unit) and 16 codes per conversion lane and register. Three chunks of up to 1500
+// tokens over up to 4096 keys (40 and 8 heads of 128): 201 us, 0.98 PFLOP/s, half of
+// the measured peak. A step takes about 3300 clocks for 2048 of products, because
+// each tile's chain of scores, maximum, exponentials and P is as long as that, and
+// tensor memory has no room for a second tile of scores. With cap and slopes 410 us:
+// three special-function results per score in place of one.
 #pragma once
 
 #include <type_traits>
@@ -248,7 +253,8 @@ struct Item {
 };
 
 // SPLIT: an item's keys may be cut into parts (a kernel of its own, because the step loop of one that also joins parts is
-// slower: 229 us in place of 212 on prompt chunks of 1500 tokens over up to 4096 keys).
+// slower: 229 us in place of 212 on prompt chunks of 1500 tokens over up to 4096 keys, when it also held 24 KB more
+// shared memory, which L1 then lacks).
 template <int D, int TYPE, bool MODS, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Args a) {
   constexpr int KH = D / 64;
