@@ -32,9 +32,10 @@ struct Scratch {   // per request, in dynamic shared memory
   int32_t* status;
 };
 
-// Sums stop at kMost (past any count of tokens or pages that a call can serve, and small enough to add two).
-constexpr int kMost = 1 << 30;
-__device__ __forceinline__ int add_most(int a, int b) { return min(a + b, kMost); }
+// Sums stop at kMost: past any count of tokens or pages that a call can serve (2^30 tokens at most), so that a sum that has
+// stopped is over every limit. Two of them come to 2^31 + 2, which does not fit an int: they are added without sign.
+constexpr int kMost = (1 << 30) + 1;
+__device__ __forceinline__ int add_most(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost); }
 
 // Exclusive sums over the block's threads of K values per thread, with the totals. Every warp sums the warps' sums for
 // itself, so a scan has one barrier; `sums` is not used again by the next one.
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
     const int tok = min(max(add, 0), kMost);
     const int held = (int)(((long long)len + 63) >> 6);
     const long long after = ((long long)len + tok + 63) >> 6;
-    const bool bad = len < 0 || held > a.max_pages || after > a.max_pages || at + tok > T;   // at + tok is at most 2^31 - 2^30
+    const bool bad = len < 0 || held > a.max_pages || after > a.max_pages || (unsigned)at + (unsigned)tok > (unsigned)T;
     s.start[b] = min(at, T);
     s.len[b] = len;
     s.status[b] = bad ? 2 : (add < 0 ? 3 : 0);
