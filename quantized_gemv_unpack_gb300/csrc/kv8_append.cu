@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(const __grid_con
       const bool ok = __shfl_sync(0xFFFFFFFFu, (int)there, e) != 0;
       const float s = __shfl_sync(0xFFFFFFFFu, sc.y, e);
       if (e >= n || j < 0 || j > 1) continue;
-      const int tok = slot % kPage;
+      const int tok = ok ? slot % kPage : 0;   // a slot that is not there has no place in the tile (and gives zeros)
       uint32_t x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = vt[j][d0 + i][(tok >> 2) ^ ((d0 / 8) & 15)];
