@@ -325,7 +325,7 @@ __device__ __forceinline__ float top_value(uint32_t bits) {
 
 // Rotate heads [h0, h1) of the n tokens from t0 on, by the block's threads: a thread keeps its chunk and takes a (token,
 // head) at a time, neighbouring threads neighbouring chunks. Its first two loads are in flight while the block
-// computes the angles. `angles` (shared) holds n * head_dim / 2 pairs.
+// computes the angles. `angles` (shared, 16-byte aligned) holds n * head_dim / 2 pairs.
 template <typename TI>
 __device__ __forceinline__ void rope_tokens(const qmv_rope& r, const TI* x, int64_t ldx, int64_t t0, int n, int h0, int h1,
                                             const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo,

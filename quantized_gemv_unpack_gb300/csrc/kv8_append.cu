@@ -104,7 +104,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a) {
   __shared__ float red[2][BLOCK / 32];
   __shared__ float4 set;                           // new scales of K and V, and their reciprocals
   __shared__ float2 before;                        // the scales before
-  extern __shared__ float2 angles[];               // of the run's tokens, with rope
+  extern __shared__ __align__(16) float2 angles[]; // of the run's tokens, with rope; read two pairs at a time
   const int tid = threadIdx.x;
   const int run = blockIdx.x / a.head_groups, first_head = (blockIdx.x % a.head_groups) * a.head_group;
   const int last_head = min(a.H, first_head + a.head_group);
@@ -322,7 +322,7 @@ template <typename TI, int D, int TYPE>
 __global__ void __launch_bounds__(kFewThreads) kv8_append_few_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int V = D / 64;                    // values per lane from each half of a chunk
   constexpr int C = D / 16, L = 8 / V;         // chunks, lanes per chunk
-  __shared__ float2 angles[D / 2];
+  __shared__ __align__(16) float2 angles[D / 2];   // read two pairs at a time, like all tables of angles
   const int tid = threadIdx.x, lane = tid & 31;
   follow_previous();
   const int n_runs = a.n_runs * a.H, run_blocks = (n_runs + kFewThreads / 32 - 1) / (kFewThreads / 32);

@@ -37,7 +37,7 @@ struct RopeArgs {
 
 template <typename TI>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 4 ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];
+  __shared__ __align__(16) float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];   // read two pairs at a time
   kv8::follow_previous();
   if (a.lead) kv8::let_next_begin();
   const int h0 = blockIdx.y * a.heads_per_block;

@@ -48,3 +48,80 @@ def test_read_of_negative_slots_gives_zeros(env, kind, H, D):
             want = np.stack([ref.page_values(s // 64, w)[:, s % 64] if s >= 0 else np.zeros((H, D)) for s in slots])
             assert np.all(np.abs(_f64(o) - want) <= ULP[out] * np.abs(want))
     assert q.qmv_check_status() == 0
+
+
+# ----------------------------------------------------------------------------- append with rotation
+
+def _check_rotated_append(env, kind, H, Hq, D, before, new, inter, rot, axes, x="f32", seed=0, pad=0):
+    """A call that puts new[i] tokens behind before[i] in page i (a run each): the values that come back against the rotation
+    in float64, as in test_gpu_kv8.py, and the tokens that were there."""
+    q, torch, dev = env
+    from oracle import kv8
+    g = np.random.default_rng(seed)
+    P = len(new)
+    order = g.permutation(P + 2)[:P]
+    d, cache = _fresh_cache(env, kind, P + 2, H, D)
+    i32 = lambda a: torch.tensor(np.asarray(a, dtype=np.int32), device=dev)  # noqa: E731
+    had = [int(order[p]) * 64 + i for p, n in enumerate(before) for i in range(n)]
+    if had:
+        first = torch.from_numpy((g.standard_normal((len(had), H, D)) * 0.1).astype(np.float32)).to(dev)
+        at = np.concatenate([[0], np.cumsum([n for n in before if n])])
+        q.KvAppend(d, cache, first, first, i32(had), i32([[at[i], at[i + 1] - at[i]] for i in range(len(at) - 1)])).run()
+        old = _host(cache, d)
+    slots, runs, t = [], [], 0
+    for p, n in enumerate(new):
+        slots += [int(order[p]) * 64 + before[p] + i for i in range(n)]
+        runs.append([t, n])
+        t += n
+    T = len(slots)
+    qkv = torch.from_numpy(g.standard_normal((T, Hq + 2 * H, D)).astype(np.float32)).to(dev).to(_tt(torch, x))
+    pos = g.integers(0, 100000, (axes, T)).astype(np.int32)
+    inv, axis = [500.0 ** (-i / (rot // 2)) for i in range(rot // 2)], [i * axes // (rot // 2) for i in range(rot // 2)]
+    qo = torch.full((T, Hq, D), 9.0, device=dev)
+    q.KvAppend(d, cache, qkv[:, Hq:Hq + H], qkv[:, Hq + H:], i32(slots), i32(runs + [[0, 0]] * pad), rope=q.rope_desc(D, inv, axis=axis, interleaved=inter),
+               positions=torch.from_numpy(pos).to(dev), q=qkv[:, :Hq], q_out=qo).run()
+    v = _f64(qkv)
+    y = kv8.rotate(v[:, :Hq + H], pos, inv, axis, inter)
+    size = np.abs(v).max() * 2
+    assert np.all(np.abs(_f64(qo) - y[:, :Hq]) <= 1e-6 * size)
+    after = _host(cache, d)
+    page, off = np.array(slots) // 64, np.array(slots) % 64
+    for which, want in ((0, y[:, Hq:]), (1, v[:, Hq + H:])):
+        sc = after.scales[page, :, which].astype(np.float64)[:, :, None]
+        codes = np.stack([after.codes[page, h, which][np.arange(T)[:, None], after.at[which][off]] for h in range(H)], 1)
+        got = kv8.decode(codes, kind) * sc
+        step = 0.5 * sc if kind == 1 else np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * sc)
+        bad = np.abs(got - want) > step * (1 + 1e-5) + 2e-6 * size
+        assert not bad.any(), (which, np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
+        # the scale is the run's largest magnitude over the code's, or what it was
+        for p in range(P):
+            rows = slice(runs[p][0], runs[p][0] + runs[p][1])
+            top = np.abs(want[rows]).max((0, 2)) / (127 if kind == 1 else 448)
+            was = old.scales[order[p], :, which] if before[p] else 0
+            assert np.all(np.abs(after.scales[order[p], :, which] - np.maximum(top, was)) <= 2e-6 * size)
+            if before[p]:
+                a, b = old.page_values(order[p], which)[:, :before[p]], after.page_values(order[p], which)[:, :before[p]]
+                s = after.scales[order[p], :, which].astype(np.float64)[:, None, None]
+                assert np.all(np.abs(a - b) <= (0.5 * s if kind == 1 else np.maximum(2.0 ** -4 * np.abs(a), 2.0 ** -10 * s)) * (1 + 1e-5))
+    assert q.qmv_check_status() == 0
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("H,D,P", [(10, 128, 41), (10, 128, 83), (6, 128, 300), (10, 64, 90), (6, 64, 230), (10, 64, 300)])
+def test_append_of_prompts_whose_heads_share_angles(env, kind, H, D, P):
+    """Runs enough for blocks of 2, 4 and 8 heads (152 SMs), the last of them not full; full pages, pages that go on, short ones."""
+    new = [[64, 64, 34, 1, 59, 20][p % 6] for p in range(P)]
+    before = [[0, 0, 30, 63, 5, 17][p % 6] for p in range(P)]
+    _check_rotated_append(env, kind, H, 3, D, before, new, P % 2 == 1, D if P % 3 else D - 32, 1 + P % 3, "bf16" if D == 128 else "f32", seed=P)
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("inter,rot,axes", [(False, 128, 1), (True, 64, 2), (False, 96, 3), (True, 128, 4), (True, 16, 1), (False, 16, 1)])
+@pytest.mark.parametrize("H,D,Hq,x", [(2, 128, 10, "f32"), (3, 64, 33, "bf16"), (1, 128, 1, "f16")])
+def test_append_of_single_tokens_rotates(env, kind, inter, rot, axes, H, D, Hq, x):
+    """The kernel of a decode step with partial, interleaved and many-axis rotation; runs of one to five tokens."""
+    rot = min(rot, D)
+    new = [1, 1, 3, 1, 5, 2, 1, 1, 1]
+    before = [0, 40, 61, 63, 10, 0, 1, 16, 33]
+    _check_rotated_append(env, kind, H, Hq, D, before, new, inter, rot, axes, x, seed=rot + axes)
+    _check_rotated_append(env, kind, H, Hq, D, before, new, inter, rot, axes, x, seed=rot, pad=9)
