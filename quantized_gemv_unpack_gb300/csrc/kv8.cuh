@@ -45,9 +45,8 @@ constexpr int kPage = QMV_KV_PAGE;
 
 int check_kv_desc(const qmv_kv_desc* d);
 int check_rope(const qmv_rope* r);
-// rope_run; lead: its blocks let the next kernel begin, which shares nothing with them and waits for them at its own end.
 int rope_launch(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int n_heads, int64_t ldx,
-                const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, bool lead, cudaStream_t s);
+                const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, cudaStream_t s);
 inline int dtype_size(int t) { return t == QMV_F32 ? 4 : (t == QMV_BF16 || t == QMV_F16 ? 2 : 0); }
 
 // Byte of (token, d) in a K tile. Eight tokens (token / 16, token % 2) of one

@@ -18,7 +18,7 @@
 // rotation and cache write are one launch there.
 //
 // Measured (40 query and 8 KV heads of 128): 8190 prompt tokens, bf16 to e4m3, 20 us
-// beside the 31 of the rotation of q, 49 together; reading them back 15 us. Both
+// behind the 31 of the rotation of q, 50 together; reading them back 15 us. Both
 // are bound by instructions and block-wide steps (issue 54 and 63 % busy, DRAM 15 %). A step of 64
 // tokens: 4.5 us, and 5.5 to read them back, launch and dependent loads.
 #include "kv8.cuh"
@@ -43,7 +43,6 @@ struct AppendArgs {
   int H;
   int head_group, head_groups;   // KV heads of one block, blocks per run
   int q_heads;                   // heads of a block that rotates query heads (few tokens)
-  int beside;                    // follows this call's own rotation of the query heads
   int* err;
 };
 
@@ -304,13 +303,10 @@ __device__ __forceinline__ void append_run(const AppendArgs& a) {
   }
 }
 
-// Behind this call's own rotation of the query heads (a.beside) it does not wait for that, which it shares nothing with:
-// the rotation lets it begin when what came before has ended, and it waits at its end, so that both have ended with it.
 template <typename TI, int D, int TYPE, int BLOCK>
 __global__ void __launch_bounds__(BLOCK, 1024 / BLOCK) kv8_append_kernel(const __grid_constant__ AppendArgs a) {
-  if (!a.beside) follow_previous();
+  follow_previous();
   append_run<TI, D, TYPE, BLOCK>(a);
-  if (a.beside) follow_previous();
 }
 
 // Runs of a few tokens (a decode step: one). One warp takes a run of one head, a lane the two values of D / 64 pairs of K
@@ -675,9 +671,8 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
     // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 49
     // us, and 65 us as blocks of one launch, where the cache write's registers halve the rotation's loads in flight)
     rc = rope_launch(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
-                     g->ldqo, 0, blocks > 0, static_cast<cudaStream_t>(stream));
+                     g->ldqo, 0, static_cast<cudaStream_t>(stream));
     if (rc) return rc;
-    a.beside = 1;
   }
   if (blocks == 0) return QMV_OK;
   if (blocks > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "too many runs");

@@ -31,7 +31,6 @@ struct RopeArgs {
   const int32_t* positions;
   int64_t ldx, ldo, ldp, n_tokens;
   int n_heads, out_type, tokens_per_block, heads_per_block;
-  int lead;   // the next kernel shares nothing with this one and waits for it at its own end
   float sign;
 };
 
@@ -39,7 +38,6 @@ template <typename TI>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(TI) == 4 ? 3 : 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float2 angles[kMaxTokensPerBlock * QMV_ROPE_MAX_PAIRS];   // read two pairs at a time
   kv8::follow_previous();
-  if (a.lead) kv8::let_next_begin();
   const int h0 = blockIdx.y * a.heads_per_block;
   const int64_t t0 = (int64_t)blockIdx.x * a.tokens_per_block;
   kv8::rope_tokens<TI>(a.r, static_cast<const TI*>(a.x), a.ldx, t0, (int)min((int64_t)a.tokens_per_block, a.n_tokens - t0),
@@ -64,7 +62,7 @@ int check_rope(const qmv_rope* r) {
 }
 
 int rope_launch(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int n_heads, int64_t ldx,
-                const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, bool lead, cudaStream_t s) {
+                const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, cudaStream_t s) {
   int rc = check_rope(rope);
   if (rc) return rc;
   const int xs = dtype_size(x_type), os = dtype_size(out_type);
@@ -92,7 +90,6 @@ int rope_launch(const qmv_rope* rope, const void* x, int x_type, int64_t n_token
   a.n_heads = n_heads;
   a.out_type = out_type;
   a.sign = inverse ? -1.f : 1.f;
-  a.lead = lead;
   // Enough tokens for four blocks per SM: all heads in one block, four tokens at a time. Fewer: one token and 16 heads.
   const bool split = n_tokens < 4 * sm_count();
   a.tokens_per_block = split ? 1 : kMaxTokensPerBlock;
@@ -143,7 +140,7 @@ int rope_desc(int32_t head_dim, int32_t rot_dim, int32_t n_axes, int32_t interle
 
 int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, int32_t n_heads, int64_t ldx,
              const int32_t* positions, int64_t ldp, void* out, int out_type, int64_t ldo, int inverse, void* stream) {
-  return kv8::rope_launch(rope, x, x_type, n_tokens, n_heads, ldx, positions, ldp, out, out_type, ldo, inverse, false,
+  return kv8::rope_launch(rope, x, x_type, n_tokens, n_heads, ldx, positions, ldp, out, out_type, ldo, inverse,
                           static_cast<cudaStream_t>(stream));
 }
 

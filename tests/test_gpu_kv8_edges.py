@@ -125,3 +125,50 @@ def test_append_of_single_tokens_rotates(env, kind, inter, rot, axes, H, D, Hq, 
     before = [0, 40, 61, 63, 10, 0, 1, 16, 33]
     _check_rotated_append(env, kind, H, Hq, D, before, new, inter, rot, axes, x, seed=rot + axes)
     _check_rotated_append(env, kind, H, Hq, D, before, new, inter, rot, axes, x, seed=rot, pad=9)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_append_of_a_prompt_in_a_graph(env, inplace):
+    """The rotation and the cache write of a prompt follow what made their inputs and precede what reads their outputs: steps
+    of plan, append and read captured together and replayed, against the same calls with a wait after each."""
+    q, torch, dev = env
+    H, Hq, D, T = 4, 24, 128, 500
+    rope = q.rope_desc(D, [50.0 ** (-i / 64) for i in range(64)])
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+
+    def make():
+        d, cache = _fresh_cache(env, 1, 40, H, D, fill=0)
+        lens, state = i32([0, 0]), i32([0, 40])
+        p = q.KvPlan(lens, i32([T - 37, 37]), torch.full((2, 20), -1, dtype=torch.int32, device=dev), i32(list(range(40))), state, T,
+                     lens_out=lens, ring_state_out=state)
+        g = torch.Generator(device=dev).manual_seed(3)
+        src = torch.randn((T, Hq + 2 * H, D), generator=g, device=dev)
+        x = torch.zeros_like(src)
+        qo = x[:, :Hq] if inplace else torch.zeros((T, Hq, D), device=dev)
+        ko, vo = (torch.zeros((T, H, D), device=dev) for _ in range(2))
+        calls = [p, q.KvAppend(d, cache, x[:, Hq:Hq + H], x[:, Hq + H:], p.slots, p.runs, rope=rope, positions=p.positions, q=x[:, :Hq], q_out=qo),
+                 q.KvRead(d, cache, p.slots, ko, vo), q.Rope(rope, ko, p.positions, ko, inverse=True)]
+        return src, x, qo, ko, vo, calls
+
+    src, x, qo, ko, vo, calls = make()
+    x.copy_(src)
+    for c in calls:
+        c.run()
+        torch.cuda.synchronize()
+    want = [t.clone() for t in (qo, ko, vo)]
+    assert float((want[1] - src[:, Hq:Hq + H]).abs().max()) <= 0.02 * float(src.abs().max())
+    src, x, qo, ko, vo, calls = make()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.copy_(src)
+        for c in calls:
+            c.run()
+    g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(want, (qo, ko, vo)))
+    for _ in range(3):                         # and issued one behind the other
+        src, x, qo, ko, vo, calls = make()
+        x.copy_(src)
+        for c in calls:
+            c.run()
+        assert all(torch.equal(a, b) for a, b in zip(want, (qo, ko, vo)))
+    assert q.qmv_check_status() == 0
