@@ -53,7 +53,9 @@ constexpr int kHeld = 512;               // parts times rows that a join holds i
 // Steps of a part at least, and steps up to which an item stays whole: 100 tokens of 24 and 4 heads over 600 take 22 us whole
 // and 33 in two parts; 20 tokens of 8 heads over 2048 32 us with parts of 4 steps and 35 with 6.
 constexpr int kChunk = 4, kWhole = 6;
-constexpr int kItems = 8;                // items the roles may be apart
+// Items the roles may be apart. The converters and the products are three steps apart at most, and an item has a step; but a
+// softmax group sits out items of one row tile, and nothing of such an item waits for it: it gives back what it is past.
+constexpr int kItems = 8;
 constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
 
 // ---- two fp32 operations in one instruction
@@ -156,7 +158,7 @@ struct Smem {
   alignas(1024) unsigned char q[2][D / 64][kRows * 128];
   alignas(1024) unsigned char k[2][D / 64][kStep * 128];
   alignas(1024) unsigned char v[2][kStep / 64][D * 128];
-  alignas(8) uint64_t item_full[kItems], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
+  alignas(8) uint64_t item_full[kItems], item_done[kItems], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
   float4 scale[4][2];   // of the step's two pages, see below
   int item[kItems];
   uint32_t tmem;
@@ -275,7 +277,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       core::mbar_init(&sm.p_full[i][1], 128);
       core::mbar_init(&sm.o_full[i], 1);
     }
-    for (int i = 0; i < kItems; ++i) core::mbar_init(&sm.item_full[i], 1);
+    for (int i = 0; i < kItems; ++i) {
+      core::mbar_init(&sm.item_full[i], 1);
+      core::mbar_init(&sm.item_done[i], 8);   // the warps of the softmax
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   kv8::let_next_begin();
@@ -572,6 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         fence_before();
       }
       n += it.steps;
+      __syncwarp();
+      if (lane == 0) attend::mbar_arrive(&sm.item_done[k % kItems]);
     }
   } else if (warp < kWarps - 1) {
     // ------------------------------------------------------------------ codes to fp16 tiles
@@ -632,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       // the first lane takes the block's next item
       auto take = [&](uint32_t k) {
         if (w != 0) return;
+        if (k >= kItems) core::mbar_wait(&sm.item_done[k % kItems], (k / kItems - 1) & 1, a.err);   // its last use is over
         Item next;
         int i;
         do i = atomicAdd(a.counters, 1);

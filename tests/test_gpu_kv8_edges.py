@@ -5,7 +5,7 @@ The bounds are those of test_gpu_kv8.py unless a test derives its own.
 import numpy as np
 import pytest
 
-from test_gpu_kv8 import ULP, _check_plan, _f64, _fresh_cache, _host, _plan_state, _q, _run_plan, _tt, env  # noqa: F401 (env is a fixture)
+from test_gpu_kv8 import ULP, _Case, _check_plan, _f64, _fresh_cache, _host, _plan_state, _q, _run_plan, _tt, env  # noqa: F401 (env is a fixture)
 
 pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
 
@@ -172,3 +172,18 @@ def test_append_of_a_prompt_in_a_graph(env, inplace):
             c.run()
         assert all(torch.equal(a, b) for a, b in zip(want, (qo, ko, vo)))
     assert q.qmv_check_status() == 0
+
+
+# ----------------------------------------------------------------------------- attention: items of the prompt kernel
+
+@pytest.mark.parametrize("D,kind", [(64, 1), (128, 2)])
+@pytest.mark.parametrize("B,H", [(700, 1), (400, 3), (60, 1)])
+def test_prompts_of_two_row_tiles_among_many_of_one(env, D, kind, B, H):
+    """One group of rows sits out item after item, while the other takes them as fast as it can."""
+    g = np.random.default_rng(B)
+    new = np.where(np.arange(B) % 11 == 0, 200, g.integers(33, 60, B))
+    ctx = new + np.where(np.arange(B) % 11 == 0, 300, g.integers(0, 9, B))
+    c = _Case(env, [int(v) for v in ctx], [int(v) for v in new], H, H, D, kind, seed=B)
+    first = c.check()
+    for _ in range(3):
+        assert (c.run(workspace=c.call.workspace)[0] == first).all()
