@@ -564,8 +564,9 @@ int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, 
  * appear in one run of a call only. With s the page's scale for K or V (0 when
  * the run starts at offset 0: the page begins anew), a the largest magnitude of
  * the run's values and top = 127 (int8) or 448 (e4m3), the scale becomes
- * s' = max(s, a / top); where it grows, the codes already in the page are
- * rounded again from code * s * (1 / s'); the new codes are x * (1 / s'), rounded
+ * s' = max(s, a / top), or 2^-126 where that is smaller and not 0; where it
+ * grows, the codes already in the page are rounded again from code * s * (1 / s');
+ * the new codes are x * (1 / s'), rounded
  * to nearest even and held to +-top. All of it is fp32. An infinite value takes
  * the largest code and does not count for a; a NaN is stored as 0; either sets
  * QMV_ERR_CORRUPT in the device error word, and so does a run outside the

@@ -164,6 +164,8 @@ def append(cache: Cache, k, v, slots, runs):
                 a = fin.max() if fin.size else f32(0)
                 was = cache.scales[page, h, which] if off else f32(0)
                 now = max(was, f32(a / top))
+                if 0 < now < f32(2.0 ** -126):
+                    now = f32(2.0 ** -126)
                 with np.errstate(all="ignore"):
                     inv = f32(1) / now if now > 0 else f32(0)
                     if off and now > was and was > 0:

@@ -64,6 +64,13 @@ template <int TYPE>
 __device__ __forceinline__ float code_top() {
   return TYPE == QMV_KV_INT8 ? 127.f : 448.f;
 }
+// A page's scale is 0 or at least the smallest normal number, so that its reciprocal is finite: of a smaller one it would be
+// infinite, which makes a code of 0 a NaN when it is rounded again. Values below half of that are stored as 0.
+constexpr float kLeastScale = 1.17549435e-38f;   // 2^-126
+__device__ __forceinline__ float grown_scale(float was, float largest, float top) {
+  const float s = fmaxf(was, __fdiv_rn(largest, top));
+  return s > 0.f ? fmaxf(s, kLeastScale) : 0.f;
+}
 // x * inv as a code byte, rounded to nearest even and held to +-top; NaN gives 0.
 template <int TYPE>
 __device__ __forceinline__ uint32_t encode(float y) {

@@ -202,7 +202,7 @@ __device__ __forceinline__ void append_run(const AppendArgs& a) {
       }
       const float2 old = off > 0 ? *reinterpret_cast<const float2*>(scale) : make_float2(0.f, 0.f);
       const float top = code_top<TYPE>();
-      const float sk = fmaxf(old.x, __fdiv_rn(mk, top)), sv = fmaxf(old.y, __fdiv_rn(mv, top));
+      const float sk = grown_scale(old.x, mk, top), sv = grown_scale(old.y, mv, top);
       __syncwarp();
       if (tid == 0) {
         set = make_float4(sk, sv, sk > 0.f ? __frcp_rn(sk) : 0.f, sv > 0.f ? __frcp_rn(sv) : 0.f);
@@ -213,8 +213,6 @@ __device__ __forceinline__ void append_run(const AppendArgs& a) {
     __syncthreads();
     const float2 was = before;
     const float sk = set.x, sv = set.y, ik = set.z, iv = set.w;
-    // scales below 2^-125 (values below 2^-118): 1 / s is not finite or s too coarse for the fast conversion's bound
-    odd = odd || (sk > 0.f && sk < 2.4e-38f) || (sv > 0.f && sv < 2.4e-38f);
 
     // K: codes eight at a time, and V into the transposing tile
 #pragma unroll
@@ -406,7 +404,7 @@ __global__ void __launch_bounds__(kFewThreads) kv8_append_few_kernel(const __gri
     mv = fmaxf(mv, __shfl_xor_sync(0xFFFFFFFFu, mv, o));
   }
   const float top = code_top<TYPE>();
-  const float sk = fmaxf(was.x, __fdiv_rn(mk, top)), sv = fmaxf(was.y, __fdiv_rn(mv, top));
+  const float sk = grown_scale(was.x, mk, top), sv = grown_scale(was.y, mv, top);
   const float ik = sk > 0.f ? __frcp_rn(sk) : 0.f, iv = sv > 0.f ? __frcp_rn(sv) : 0.f;
   __syncwarp();  // every lane has read `was`
   if (lane == 0) *reinterpret_cast<float2*>(scale) = make_float2(sk, sv);

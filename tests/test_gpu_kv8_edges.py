@@ -187,3 +187,50 @@ def test_prompts_of_two_row_tiles_among_many_of_one(env, D, kind, B, H):
     first = c.check()
     for _ in range(3):
         assert (c.run(workspace=c.call.workspace)[0] == first).all()
+
+
+# ----------------------------------------------------------------------------- append: the smallest scales
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tiny_scales_grow_without_losing_what_is_there(env, kind, n, D):
+    """Values whose scale is below the smallest normal number, then larger ones in the same page: a code of zero stays zero,
+    no code is a NaN, and every value is off by half a step per rounding, with steps of 2^-126 at least."""
+    q, torch, dev = env
+    H, top = 2, (127 if kind == 1 else 448)
+    d, cache = _fresh_cache(env, kind, 3, H, D)
+    g = np.random.default_rng(kind * 7 + n)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    amps = [1e-40, 1e-38, 1e-37, 4e-37, 1.2e-36, 1e-35]
+    if n == 20:
+        amps = [1e-38, 3e-37, 1e-36]
+    given, steps = [[], []], [[], []]
+    for call, amp in enumerate(amps):
+        x = (g.uniform(-1, 1, (2, n, H, D)) * amp).astype(np.float32)
+        x[:, :, :, ::3] = 0
+        x[:, :, :, 1] = np.float32(amp)
+        k, v = (torch.from_numpy(a).to(dev) for a in x)
+        q.KvAppend(d, cache, k, v, i32([64 + call * n + i for i in range(n)]), i32([[0, n]])).run()
+        assert q.qmv_check_status() == 0
+        h = _host(cache, d)
+        for w in (0, 1):
+            given[w].append(x[w].astype(np.float64))
+            for s in steps[w]:
+                s.append(h.scales[1, :, w].astype(np.float64))
+            steps[w].append([h.scales[1, :, w].astype(np.float64)])
+            assert np.all(h.scales[1, :, w] <= max(amp / top * (1 + 1e-6), 2.0 ** -126))
+        if kind == 2:
+            codes = np.stack([h.page_codes(1, w)[:, :(call + 1) * n] for w in (0, 1)])
+            assert not ((codes & 127) == 127).any()
+    out = [torch.empty((n * len(amps), H, D), device=dev) for _ in (0, 1)]
+    q.KvRead(d, cache, i32([64 + i for i in range(n * len(amps))]), *out).run()
+    for w in (0, 1):
+        got = _f64(out[w]).reshape(len(amps), n, H, D)
+        for call, x in enumerate(given[w]):
+            assert not got[call][x == 0].any()
+            off = 0.0
+            for s in dict.fromkeys(tuple(s) for s in steps[w][call]):
+                s = np.array(s)[:, None]
+                off = off + (0.5 * s if kind == 1 else np.maximum(2.0 ** -4 * (np.abs(x) + off), 2.0 ** -10 * s)) * (1 + 1e-5)
+            assert np.all(np.abs(got[call] - x) <= off + 2.0 ** -149 * 2), (call, np.abs(got[call] - x).max(), amps[call])

@@ -113,3 +113,17 @@ def test_attention_by_hand():
     assert np.isclose(out[1, 0, 5], 10) and not out[0].any() and lse[0, 0] == -np.inf   # position -1 sees nothing
     out, *_ = kv8.attend(c, q * 1e6, [0, 2], [2], table, 1.0, softcap=math.log(3))
     assert np.isclose(out[1, 0, 5], 12.5)           # tanh(large) = 1: the score is the cap
+
+
+def test_append_keeps_the_least_scale():
+    """Scales below 2^-126 are 2^-126, and growing from one leaves zeros zero."""
+    for kind, top in ((kv8.INT8, 127), (kv8.E4M3, 448)):
+        c = _cache(kind)
+        k = np.zeros((2, 1, 64), dtype=np.float32)
+        k[0, 0, 1] = 1e-40
+        k[1, 0, 1] = np.float32(2.0 ** -125 * top)
+        kv8.append(c, k, k, np.array([64, 65]), [[0, 1]])
+        assert c.scales[1, 0].tolist() == [2.0 ** -126] * 2 and c.page_values(1, 0)[0, 0, 0] == 0
+        kv8.append(c, k, k, np.array([64, 65]), [[1, 1]])
+        assert c.scales[1, 0].tolist() == [2.0 ** -125] * 2
+        assert c.page_values(1, 1)[0, 1, 1] == 2.0 ** -125 * top and not c.page_values(1, 1)[0, :2, 2:].any()
