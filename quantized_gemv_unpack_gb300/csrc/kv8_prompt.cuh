@@ -27,8 +27,8 @@
 // tokens over up to 4096 keys (40 and 8 heads of 128): 201 us, 0.98 PFLOP/s, half of
 // the measured peak. A step takes about 3300 clocks for 2048 of products, because
 // each tile's chain of scores, maximum, exponentials and P is as long as that, and
-// tensor memory has no room for a second tile of scores. With cap and slopes 410 us:
-// three special-function results per score in place of one.
+// tensor memory has no room for a second tile of scores. With cap and slopes 420 us
+// (scores below half the cap; 550 where both sides of it meet: three special-function results per score in place of one).
 #pragma once
 
 #include <type_traits>
@@ -74,6 +74,19 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// attend::capped_near of two scores
+__device__ __forceinline__ uint64_t capped_near2(uint64_t s, uint64_t factor, uint64_t unit) {
+  using namespace attend;
+  const uint64_t X = mul2(s, factor), x = mul2(s, unit), y = mul2(X, X);
+  const uint64_t r = fma2(fma2(fma2(two(kCap3, kCap3), y, two(kCap2, kCap2)), y, two(kCap1, kCap1)), y, two(kCap0, kCap0));
+  return fma2(x, mul2(y, r), x);
 }
 
 // ---- tcgen05
@@ -442,8 +455,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             // cap and distance bias: the scores as they are wanted, in units of log2
             if (a.softcap > 0.f) {
               const float c0 = attend::cap_factor(a.softcap, f0), c1 = attend::cap_factor(a.softcap, f1), cap = a.softcap * kLog2e;
+              const float u0 = f0 * kLog2e, u1 = f1 * kLog2e;
+              float big[2] = {0.f, 0.f};
 #pragma unroll
-              for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(attend::capped(__uint_as_float(x[q]), q < 64 ? c0 : c1, cap));
+              for (int q = 0; q < 128; q += 2)
+                big[q >> 6] = fmaxf(big[q >> 6], fmaxf(fabsf(__uint_as_float(x[q])), fabsf(__uint_as_float(x[q + 1]))));
+              // one branch for the warp: scores far below the cap, as they mostly are, need no special function
+              if (__all_sync(0xFFFFFFFFu, fmaxf(big[0] * c0, big[1] * c1) <= attend::kNear)) {
+#pragma unroll
+                for (int q = 0; q < 128; q += 2) {
+                  const float c = q < 64 ? c0 : c1, u = q < 64 ? u0 : u1;
+                  float lo, hi;
+                  split(capped_near2(two(__uint_as_float(x[q]), __uint_as_float(x[q + 1])), two(c, c), two(u, u)), lo, hi);
+                  x[q] = __float_as_uint(lo);
+                  x[q + 1] = __float_as_uint(hi);
+                }
+              } else {
+#pragma unroll
+                for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(attend::capped(__uint_as_float(x[q]), q < 64 ? c0 : c1, q < 64 ? u0 : u1, cap));
+              }
             } else {
 #pragma unroll
               for (int q = 0; q < 128; ++q) x[q] = __float_as_uint(__uint_as_float(x[q]) * ((q < 64 ? f0 : f1) * kLog2e));

@@ -234,3 +234,25 @@ def test_tiny_scales_grow_without_losing_what_is_there(env, kind, n, D):
                 s = np.array(s)[:, None]
                 off = off + (0.5 * s if kind == 1 else np.maximum(2.0 ** -4 * (np.abs(x) + off), 2.0 ** -10 * s)) * (1 + 1e-5)
             assert np.all(np.abs(got[call] - x) <= off + 2.0 ** -149 * 2), (call, np.abs(got[call] - x).max(), amps[call])
+
+
+# ----------------------------------------------------------------------------- attention: the cap
+
+@pytest.mark.parametrize("cap", [0.5, 200.0, 1e4, 1e5, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("new,Hq,H", [([5, 2, 1], 6, 2), ([90, 64, 33], 6, 2), ([70, 60, 40], 80, 40)])
+def test_cap_is_exact_whatever_its_size(env, cap, new, Hq, H):
+    """cap * tanh(s / cap) of scores far below, near and over the cap: the error is that of the score, not of the cap."""
+    c = _Case(env, [513, 64, 200], new, Hq, H, 64, 1, "bf16", seed=len(str(cap)))
+    cap = float(np.float32(cap))
+    c.check(softcap=cap)
+    c.check(softcap=cap, scale=8.0)
+    c.check(softcap=cap, scale=0.01, slopes=[2.0 ** -(h % 8 + 2) for h in range(Hq)])
+
+
+@pytest.mark.parametrize("new", [[3], [60]])
+def test_smallest_cap(env, new):
+    """A cap near the smallest normal number, and queries of zero."""
+    c = _Case(env, [150], new, 4, 2, 128, seed=3)
+    c.q[0] = 0
+    c.q[2, 1] = 0
+    c.check(softcap=float(np.float32(1.2e-38)))
