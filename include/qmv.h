@@ -617,7 +617,9 @@ int kv8_read(const qmv_kv_desc* desc, const void* cache, const int32_t* slots, i
  * h * head_dim. Products are exact with fp32 sums (q is scaled per row by a
  * power of two into fp16: exact for fp16, and for bf16 down to 2^-27 of the
  * row's largest value; fp32 queries are rounded to 11 bits); probabilities are
- * rounded to fp16 for the product with V; sums and softmax statistics are fp32.
+ * rounded to fp16 for the product with V, above 32 rows per KV head together with
+ * their page's V scale, against the largest of the row's own; sums and softmax
+ * statistics are fp32.
  * The result is reproducible bit for bit.
  * max_new is the host's bound on the rows of one request. It chooses the
  * kernel's row tile; a request with more rows is still served in full.

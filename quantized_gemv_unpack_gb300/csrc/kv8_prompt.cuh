@@ -15,16 +15,16 @@
 // while the other's softmax runs, and the commit behind QK_t(j+1) also covers
 // PV_t(j): when a tile's softmax sees its next scores, its O may be rescaled.
 //
-// Rescaling is put off: a row's reference maximum moves only when the maximum has
-// grown by more than 2^7, and the pages' V scales (s_v) enter as p * s_v / s_ref in
-// the exponent, with s_ref moving only when a page's scale is over 128 times it; so
-// P stays below 2^14 in fp16 and the accumulator in tensor memory is read back a
-// few times per row and not once per step.
+// A page's V scale s_v enters in the exponent: with s a score and u = s + log2(s_v), P = 2^(u - M + 9) against a
+// reference M of the row's own largest u, so that each key's weight in P V is held to 2^-11 of itself or 2^-33 of the
+// largest weight that the row has, whatever other rows see. The softmax's sum has a reference m of its own among the
+// scores. Rescaling is put off: a reference moves, to a whole number, only when its maximum has grown by more than 6.5; so
+// P stays below 2^16 in fp16 and the accumulator in tensor memory is read back a few times per row and not once per step.
 //
 // What bounds it: per step and tile 2 * 128 * 128 * D multiply-adds, 1024 tensor
 // clocks for D = 128, against 128 exponentials per row thread (the exponential
 // unit) and 16 codes per conversion lane and register. Three chunks of up to 1500
-// tokens over up to 4096 keys (40 and 8 heads of 128): 201 us, 0.98 PFLOP/s, half of
+// tokens over up to 4096 keys (40 and 8 heads of 128): 204 us, 0.97 PFLOP/s, half of
 // the measured peak. A step takes about 3300 clocks for 2048 of products, because
 // each tile's chain of scores, maximum, exponentials and P is as long as that, and
 // tensor memory has no room for a second tile of scores. With cap and slopes 420 us
@@ -56,7 +56,10 @@ constexpr int kChunk = 4, kWhole = 6;
 // Items the roles may be apart. The converters and the products are three steps apart at most, and an item has a step; but a
 // softmax group sits out items of one row tile, and nothing of such an item waits for it: it gives back what it is past.
 constexpr int kItems = 8;
-constexpr float kSlack = 7.f;            // log2 of what a maximum or a V scale may grow before O is rescaled
+constexpr float kSlack = 6.5f, kLift = 9.f;   // what a maximum may pass its reference by; P is 2^9 at the reference: 2^15.5 at most
+// A page whose V scale is so far below the row's others that its P is 0 in fp16 anyway counts as 2^-60 of the reference, so that
+// its sum does not leave the range of fp32.
+constexpr float kLeast = -60.f;
 
 // ---- two fp32 operations in one instruction
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
@@ -172,7 +175,7 @@ struct Smem {
   alignas(1024) unsigned char k[2][D / 64][kStep * 128];
   alignas(1024) unsigned char v[2][kStep / 64][D * 128];
   alignas(8) uint64_t item_full[kItems], item_done[kItems], q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2][2], o_full[2];
-  float4 scale[4][2];   // of the step's two pages, see below
+  float2 scale[4][2];   // of the step's two pages: K scale (negative: no such page), log2 of the V scale
   int item[kItems];
   uint32_t tmem;
   int tiles_max[kWarps];
@@ -436,14 +439,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
       const int hi_all = __reduce_min_sync(0xFFFFFFFFu, hi), lo_all = __reduce_max_sync(0xFFFFFFFFu, lo);
       const float slope = MODS && a.slopes ? a.slopes[hq] * kLog2e : 0.f;
-      float m = -INFINITY, l = 0.f, s_ref = 0.f;
+      float m = -INFINITY, l = 0.f, M = -INFINITY;   // references of scores and of scores with the V scale; sum in units of 2^m
       if (in_use) {
         for (int j = 0; j < it.steps; ++j) {
           core::mbar_wait(&sm.s_full[tile], n_mine & 1, a.err);
           fence_after();
-          // per page: K scale (negative: no such page), log2 of r = V scale over its reference, 1 / r; and what O is off by
-          // since the reference moved, and the reference
-          const float4 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
+          const float2 sc0 = sm.scale[(n + j) & 3][0], sc1 = sm.scale[(n + j) & 3][1];
           const int key0 = (it.p0 + 2 * j) * kPage;
           float f0 = fmaxf(mult * sc0.x, 1e-37f), f1 = fmaxf(mult * sc1.x, 1e-37f);
           const bool cut = sc0.x < 0.f || sc1.x < 0.f || key0 < lo_all || key0 + kStep > hi_all;
@@ -501,36 +502,34 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               top[c] = fmaxf(top[c], fmaxf(__uint_as_float(x[32 * c + q]), __uint_as_float(x[32 * c + q + 1])));
             top[c] = fmaxf(top[c], __uint_as_float(x[32 * c + 31]));
           }
-          const float mx = fmaxf(fmaxf(top[0], top[1]) * f0, fmaxf(top[2], top[3]) * f1);
+          const float top0 = fmaxf(top[0], top[1]) * f0, top1 = fmaxf(top[2], top[3]) * f1;
 
-          // the reference of the maximum, and what O is off by after moving it
-          float fix = sc0.w;
-          s_ref = sc1.w;
-          if (mx > m + kSlack || m == -INFINITY) {
-            if (m != -INFINITY) {
-              const float down = ex2(m - mx);
-              fix *= down;
-              l *= down;
-            }
-            m = mx;
-          }
-          if (j > 0 && __any_sync(0xFFFFFFFFu, fix != 1.f)) {
-            // eight columns at a time: the scores fill the registers
+          // the references, and O after moving its own (a row that has seen no key yet has none: -infinity)
+          const float mx = fmaxf(top0, top1), mu = fmaxf(top0 + sc0.y, top1 + sc1.y);
+          if (__any_sync(0xFFFFFFFFu, mx > m + kSlack || mu > M + kSlack)) {
+            const float m_to = mx > m + kSlack ? ceilf(mx) : m, M_to = mu > M + kSlack ? ceilf(mu) : M;
+            if (m_to != m) l *= ex2(m - m_to);   // l is 0 until there is a reference
+            const float fix = M_to != M && M != -INFINITY ? ex2(M - M_to) : 1.f;
+            m = m_to;
+            M = M_to;
+            if (j > 0 && __any_sync(0xFFFFFFFFu, fix != 1.f)) {
+              // eight columns at a time: the scores fill the registers
 #pragma unroll 1
-            for (int c = 0; c < D / 8; ++c) {
-              uint32_t y[8];
-              tmem_ld8(o_at + 8 * c, y);
-              wait_ld();
+              for (int c = 0; c < D / 8; ++c) {
+                uint32_t y[8];
+                tmem_ld8(o_at + 8 * c, y);
+                wait_ld();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * fix);
-              tmem_st8(o_at + 8 * c, y);
+                for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(__uint_as_float(y[q]) * fix);
+                tmem_st8(o_at + 8 * c, y);
+              }
             }
           }
-          const float use = m == -INFINITY ? 0.f : m;
-          // p = exp2(score + log2 of the V scale over s_ref): sixteen-bit pairs to tensor memory, their sum to l
+          const float use = m == -INFINITY ? 0.f : m, use_u = M == -INFINITY ? 0.f : M;
+          // P = 2^(score + shift): sixteen-bit pairs to tensor memory, their sum to l
 #pragma unroll
           for (int page = 0; page < 2; ++page) {
-            const float f = page ? f1 : f0, shift = (page ? sc1.y : sc0.y) - use;
+            const float f = page ? f1 : f0, shift = fmaxf((page ? sc1.y : sc0.y) - use_u + kLift, kLeast - use);
             const uint64_t f2 = two(f, f), off = two(shift, shift);
             uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
 #pragma unroll
@@ -549,12 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
               }
               tmem_st16(s_at + 32 * page + 16 * c, p);
             }
-            float a0, a1;
-            split(add2(sum0, sum1), a0, a1);
-            l += (a0 + a1) * (page ? sc1.z : sc0.z);
             wait_st();
             fence_before();
             attend::mbar_arrive(&sm.p_full[tile][page]);   // the product with this page may begin
+            float a0, a1;
+            split(add2(sum0, sum1), a0, a1);
+            l = fmaf(a0 + a1, ex2(-shift - use), l);
           }
           ++n_mine;
         }
@@ -565,7 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int64_t at = (int64_t)(it.r.qs + tok) * a.ldo + (int64_t)hq * D;
         const bool part = SPLIT && it.parts > 1;
         const int64_t mine = (int64_t)(it.base * n_split + it.part) * 2 * kRows + tile * kRows + row;   // of a part's rows
-        const float f = part ? s_ref : l == 0.f ? 0.f : s_ref / l;
+        // from units of 2^(M - 9) to those of 2^m, in two factors that stay in range
+        const float half = l == 0.f ? 0.f : ex2(0.5f * (M - kLift - m)), rest = part || l == 0.f ? half : half / l;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t y[32];
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
             for (int q = 0; q < 4; ++q) {
               float v[8];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) v[x] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + x]) * f;
+              for (int x = 0; x < 8; ++x) v[x] = l == 0.f ? 0.f : __uint_as_float(y[8 * q + x]) * half * rest;
               if (part) kv8::store8(a.part_o + mine * D + 32 * c + 8 * q, v);
               else kv8::store8_as(a.out_type, a.out, at + 32 * c + 8 * q, v);
             }
@@ -682,22 +682,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         uint4 raw[2 * U];
         float2 sc[2];
         fetch(it, 0, 0, w, raw, std::integral_constant<int, T>(), sc);
-        float s_ref = 0.f;
         for (int j = 0; j < it.steps; ++j, ++n) {
           const int stage = n & 1;
           core::mbar_wait(&sm.k_empty[stage], ((n >> 1) & 1) ^ 1, a.err);
-          {
-            // the V scales' reference moves where a scale is over 128 times it, and O with it
-            const float sv = fmaxf(sc[0].y, sc[1].y);
-            float fix = 1.f;
-            if (sv > s_ref * 128.f) {
-              if (s_ref > 0.f) fix = s_ref / sv;
-              s_ref = sv;
-            }
-            if (w < 2) {
-              const float y = w ? sc[1].y : sc[0].y, r = y > 0.f ? __fdividef(y, s_ref) : 1.f;
-              sm.scale[n & 3][w] = make_float4(w ? sc[1].x : sc[0].x, __log2f(r), __fdividef(1.f, r), w ? s_ref : fix);
-            }
+          // a page of zeros has no scale: it counts as less than any
+          if (w < 2) {
+            const float2 s = w ? sc[1] : sc[0];
+            sm.scale[n & 3][w] = make_float2(s.x, s.y > 0.f ? log2f(s.y) : -150.f);
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e)

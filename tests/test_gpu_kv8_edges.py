@@ -256,3 +256,71 @@ def test_smallest_cap(env, new):
     c.q[0] = 0
     c.q[2, 1] = 0
     c.check(softcap=float(np.float32(1.2e-38)))
+
+
+# ----------------------------------------------------------------------------- attention: V scales of many sizes
+
+def _check_v_scales(c, slopes=None, window=0, **opt):
+    """Against float64 attention with a bound that knows what each key contributes: p s_v is held to 2^-11 of itself or 2^-33
+    of the row's largest p s_v, so |do| <= (2^-11 + 2 d + 2^-20) sum p |v| + n 2^-33 max(p s_v) top (see _Case.check for d)."""
+    kw = dict(window=window)
+    if slopes is not None:
+        kw["slopes"] = slopes
+    o, lse = c.run(**kw, **opt)
+    got = _f64(o)
+    from oracle import kv8
+    ref, want_lse, pv, _, n, sabs = kv8.attend(c.cache_ref, _f64(c.q), c.q_start, c.ctx, c.table, float(np.float32(c.D ** -0.5)), **kw)
+    x = _f64(c.q)
+    scale = float(np.float32(c.D ** -0.5))
+    G = c.Hq // c.H
+    most = np.zeros((len(x), c.Hq))
+    for b, L in enumerate(c.ctx):
+        t0, t1 = c.q_start[b], c.q_start[b + 1]
+        pages = c.table[b, :-(-L // 64)]
+        K = np.concatenate([c.cache_ref.page_values(p, 0) for p in pages], 1)[:, :L]
+        sv = np.concatenate([np.repeat(c.cache_ref.scales[p, :, 1].astype(np.float64)[:, None], 64, 1) for p in pages], 1)[:, :L]
+        key, pos = np.arange(L), (L - (t1 - t0) + np.arange(t1 - t0))[:, None]
+        ok = (key <= pos) & ((pos - key < window) if window else True)
+        for h in range(c.Hq):
+            s = scale * (x[t0:t1, h] @ K[h // G].T)
+            if slopes is not None:
+                s = s - slopes[h] * np.abs(pos - key)
+            p = np.where(ok, np.exp(s - want_lse[t0:t1, h][:, None]), 0.0)
+            most[t0:t1, h] = (p * sv[h // G]).max(1)
+    top = 127.0 if c.desc.type == 1 else 448.0
+    big = sabs + np.where(np.isfinite(want_lse), np.abs(want_lse), 0)
+    d = 2.0 ** -20 * big + 2.0 ** -21 + (2.0 ** -20 * np.max(slopes) * float(np.max(c.ctx)) if slopes is not None else 0)
+    # the log of a V scale joins the exponent: up to 2^-20 of its magnitude
+    ly = np.abs(np.log2(np.maximum(c.cache_ref.scales[c.table[c.table >= 0], :, 1], 1e-45))).max()
+    d = d + 2.0 ** -20 * ly
+    tol = (2.0 ** -11 + 2 * d + 2.0 ** -20)[..., None] * pv + (n * 2.0 ** -33 * most * top)[..., None]
+    bad = np.abs(got - ref) > tol + 1e-37
+    assert np.isfinite(got).all()
+    assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], ref[bad][:5], tol[bad][:5])
+    assert np.all(np.abs(_f64(lse) - want_lse) <= 2 * d + 2.0 ** -20 * (1 + np.abs(want_lse)))
+
+
+@pytest.mark.parametrize("factor", [1e-8, 1e3, 1e6, 1e8, 1e20, 1e30])
+@pytest.mark.parametrize("Hq,H,D,kind,new", [(2, 2, 64, 1, 200), (80, 80, 64, 2, 200), (4, 2, 128, 1, 170), (40, 40, 128, 2, 170), (5, 1, 64, 1, 2)])
+def test_a_page_that_a_row_does_not_see_leaves_it_alone(env, factor, Hq, H, D, kind, new):
+    """An early page whose V scale is far from the rest, out of most rows' windows or far down their distance bias."""
+    q, torch, dev = env
+    c = _Case(env, [64 + new], [new], Hq, H, D, kind, "bf16", seed=5, spread=0.0)
+    c.cache_ref.scales[c.table[0, 0], :, 1] *= np.float32(factor)
+    c.cache.copy_(torch.from_numpy(c.cache_ref.buf))
+    _check_v_scales(c, window=64)
+    _check_v_scales(c, slopes=[1.0 + h / 64 for h in range(Hq)])
+    _check_v_scales(c)
+
+
+def test_v_scales_from_the_smallest_to_the_largest(env):
+    """Every page its own size, rising and falling, with pages of zeros among them."""
+    q, torch, dev = env
+    for sizes in ([1e-37, 1e-30, 0.0, 1e-10, 1.0, 1e10, 1e30], [1e30, 1e10, 1.0, 0.0, 1e-10, 1e-30, 1e-37], [0.0] * 7, [1e-37] * 7):
+        for Hq, H, new in ((2, 2, 200), (80, 80, 100), (2, 2, 3)):
+            c = _Case(env, [420], [new], Hq, H, 64, 1, "bf16", seed=6, spread=0.0)
+            for i, s in enumerate(sizes):
+                c.cache_ref.scales[c.table[0, i], :, 1] = s
+            c.cache.copy_(torch.from_numpy(c.cache_ref.buf))
+            _check_v_scales(c, window=64)
+            _check_v_scales(c)
