@@ -73,6 +73,9 @@ struct Args {
 };
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// A row's reference lies 2^15 below its maximum, so that p reaches 2^15 in fp16 and is held down to 2^-40 of the largest: against
+// the maximum itself, keys below 2^-25 of it would leave the product with V but not the sum, however many they are.
+constexpr float kLift = 15.f;
 constexpr int kStreamRows = 128, kPartRows = 256;   // rows per block of the workspace: of its streams, in all
 
 template <int D, int N, int R>
@@ -832,7 +835,7 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const float mn = fmaxf(m[n][c], mx[c] * f[c]);
+              const float mn = fmaxf(m[n][c], fmaf(mx[c], f[c], -kLift));
               use[c] = mn == -INFINITY ? 0.f : mn;
               corr[n][c] = ex2(m[n][c] - use[c]);
               m[n][c] = mn;

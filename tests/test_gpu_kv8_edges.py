@@ -2,6 +2,8 @@
 
 The bounds are those of test_gpu_kv8.py unless a test derives its own.
 """
+import math
+
 import numpy as np
 import pytest
 
@@ -324,3 +326,46 @@ def test_v_scales_from_the_smallest_to_the_largest(env):
             c.cache.copy_(torch.from_numpy(c.cache_ref.buf))
             _check_v_scales(c, window=64)
             _check_v_scales(c)
+
+
+# ----------------------------------------------------------------------------- attention: probabilities far below the largest
+
+def _one_key_and_many(env, B, pages, new, H, D, kind, gap):
+    """Every request reads the same pages: key 0 scores gap * log 2 and has the value 0, all others score 0 and have the
+    value 1. Returns the call's arguments and the exact output of a row that sees n keys."""
+    q, torch, dev = env
+    d, cache = _fresh_cache(env, kind, pages, H, D, fill=128 if kind == 1 else 0)
+    ref = _host(cache, d)
+    one = 128 + 1 if kind == 1 else 0x38
+    ref.scales[:] = 1.0
+    for p in range(pages):
+        ref.codes[p, :, 1] = one
+    from oracle import kv8
+    ref.codes[0, :, 0, kv8.k_byte(0, 0, D)] = one
+    for at in range(D):
+        ref.codes[0, :, 1, kv8.v_byte(0, at)] = 128 if kind == 1 else 0
+    cache.copy_(torch.from_numpy(ref.buf))
+    x = torch.zeros((B * new, H, D), device=dev)
+    x[:, :, 0] = gap                      # an integer: exact in every type
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    ctx = pages * 64
+    out = torch.zeros((B * new, H, D), device=dev)
+    lse = torch.zeros((B * new, H), device=dev)
+    call = q.KvAttend(d, cache, x, out, i32([b * new for b in range(B + 1)]), i32([ctx] * B), i32([list(range(pages))] * B), math.log(2),
+                      max_new=new, lse=lse)
+    call.run()
+    n = np.tile(ctx - new + 1 + np.arange(new), B)
+    rest = (n - 1) * 2.0 ** -gap
+    return _f64(out), _f64(lse), (rest / (1 + rest))[:, None, None], (np.log1p(rest) + gap * math.log(2))[:, None], n[:, None, None]
+
+
+@pytest.mark.parametrize("kind", [1, 2])
+@pytest.mark.parametrize("B,new,H,D", [(1400, 1, 1, 64), (1300, 1, 1, 128), (700, 3, 2, 64), (700, 20, 1, 64), (80, 40, 1, 64), (80, 40, 1, 128),
+                                       (3, 200, 1, 64), (1, 40, 1, 128)])
+@pytest.mark.parametrize("gap", [20, 26, 28])
+def test_many_keys_far_below_the_largest(env, kind, B, new, H, D, gap):
+    """Thousands of keys of probability 2^-gap beside one: their sum is the output. A probability is held to 2^-11 of itself
+    or 2^-33 of the largest, each value is 1, the scores are exact: |do| <= (2^-11 + 2^-19) o + n 2^-33."""
+    out, lse, want, want_lse, n = _one_key_and_many(env, B, 64, new, H, D, kind, gap)
+    assert np.all(np.abs(out - want) <= (2.0 ** -11 + 2.0 ** -19) * want + n * 2.0 ** -33), (out.ravel()[:4], want.ravel()[:4])
+    assert np.all(np.abs(lse - want_lse) <= 2.0 ** -19 * want_lse)
