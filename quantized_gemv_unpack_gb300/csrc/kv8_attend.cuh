@@ -115,12 +115,15 @@ __device__ __forceinline__ int4 load_req4(const Args& a, int b) {
   const int s = min(max(q0, 0), a.T), e = min(max(q1, 0), a.T);
   return make_int4(s, max(e - s, 0), (int)min((int64_t)max(ctx, 0), (int64_t)a.max_pages * kPage), pfx);
 }
+// First key that a row at `pos` sees (0 or less: from the first on). A row before the first key sees the prefix alone, from its
+// beginning; its position is left out of the subtraction, which then stays in range for every window.
+__device__ __forceinline__ int first_key(const Args& a, int pos) { return a.window > 0 ? max(pos, 0) - a.window + 1 : 0; }
 // Pages [p0, p0 + n) that hold the keys seen by a row tile; p0 = -1, n = 1 where it sees none.
 __device__ __forceinline__ void tile_pages(const Args& a, const Req& r, int tile, int tile_rows, int& p0, int& n) {
   const int first = a.by_g(tile * tile_rows), last = a.by_g(min(r.rows, (tile + 1) * tile_rows) - 1);
   const int base = r.ctx - r.qlen;
   const int hi = min(max(base + last + 1, r.pfx), r.ctx);
-  const int lo = a.window > 0 ? max(0, base + first - a.window + 1) : 0;
+  const int lo = max(0, first_key(a, base + first));
   if (hi <= lo) {
     p0 = -1;
     n = 1;
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(Shape<D, N, R>::kThreads, 1) attend_kernel(con
           const int rr = min(row0 + 8 * n + 2 * t + c, cw.r.rows - 1), tok = a.by_g(rr);
           pos[n][c] = cw.r.ctx - cw.r.qlen + tok;
           hi[n][c] = min(max(pos[n][c] + 1, cw.r.pfx), cw.r.ctx);
-          lo[n][c] = a.window > 0 ? pos[n][c] - a.window + 1 : 0;
+          lo[n][c] = first_key(a, pos[n][c]);
           slope[n][c] = 0.f;
           if (MODS) {
             if (a.slopes) slope[n][c] = a.slopes[cw.h * a.G + rr - tok * a.G] * kLog2e;

@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (in_use) mult = query_row(real ? (int64_t)(it.r.qs + tok) * a.ldq + (int64_t)hq * D : (int64_t)-1);
       const int pos = it.r.ctx - it.r.qlen + tok;
       const int hi = min(max(pos + 1, it.r.pfx), it.r.ctx);
-      const int lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int lo = attend::first_key(a, pos);
       const int hi_all = __reduce_min_sync(0xFFFFFFFFu, hi), lo_all = __reduce_max_sync(0xFFFFFFFFu, lo);
       const float slope = MODS && a.slopes ? a.slopes[hq] * kLog2e : 0.f;
       float m = -INFINITY, l = 0.f, M = -INFINITY;   // references of scores and of scores with the V scale; sum in units of 2^m

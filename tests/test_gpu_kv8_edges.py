@@ -369,3 +369,14 @@ def test_many_keys_far_below_the_largest(env, kind, B, new, H, D, gap):
     out, lse, want, want_lse, n = _one_key_and_many(env, B, 64, new, H, D, kind, gap)
     assert np.all(np.abs(out - want) <= (2.0 ** -11 + 2.0 ** -19) * want + n * 2.0 ** -33), (out.ravel()[:4], want.ravel()[:4])
     assert np.all(np.abs(lse - want_lse) <= 2.0 ** -19 * want_lse)
+
+
+# ----------------------------------------------------------------------------- attention: the window
+
+@pytest.mark.parametrize("new", [[9, 4], [100, 90]])
+def test_largest_window_and_rows_before_the_first_key(env, new):
+    """Rows at negative positions see the prefix whatever the window; a window of 2^31 - 1 hides nothing."""
+    c = _Case(env, [5, 70], new, 60, 30, 64, seed=7)
+    want = c.check(prefix=[3, 20])
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 64):
+        assert (c.check(prefix=[3, 20], window=window) == want).all()
