@@ -626,8 +626,9 @@ int kv8_read(const qmv_kv_desc* desc, const void* cache, const int32_t* slots, i
  * A table entry outside the cache sets QMV_ERR_CORRUPT and its page is not
  * read: its keys count as unseen.
  * workspace: device, >= kv8_attend_workspace_size(desc) bytes, given to
- * kv8_attend_init once; every call leaves it ready for the next. Calls that
- * overlap on the GPU need one each. After QMV_ERR_TIMEOUT init it again.
+ * kv8_attend_init once (which clears it on its stream: a first call on another
+ * stream has to come after that); every call leaves it ready for the next. Calls
+ * that overlap on the GPU need one each. After QMV_ERR_TIMEOUT init it again.
  */
 typedef struct {
   const void* q;

@@ -572,7 +572,9 @@ class KvRead:
 
 
 def kv8_workspace(desc: qmv_kv_desc, device):
-    """A workspace for kv8_attend (uint8), ready for use. Calls that overlap on the GPU need one each."""
+    """A workspace for kv8_attend (uint8; 1 KB per SM and value of a head: 20 MB for heads of 128), ready for use on any
+    stream: the call waits until it is cleared, unless it is made during a graph capture, to which it then belongs. Calls
+    that overlap on the GPU need one each; layers that follow one another on a stream can share one."""
     import torch
     n = int(lib().kv8_attend_workspace_size(ctypes.byref(desc)))
     if n == 0:
@@ -580,6 +582,8 @@ def kv8_workspace(desc: qmv_kv_desc, device):
     ws = torch.empty(n, dtype=torch.uint8, device=device)
     with torch.cuda.device(ws.device):
         _check(lib().kv8_attend_init(ctypes.byref(desc), ws.data_ptr(), n, _stream(None)))
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
     return ws
 
 
@@ -613,13 +617,26 @@ class KvAttend:
         if prefix is not None:
             a.prefix = _ints("prefix", prefix, (B,), dev).data_ptr()
         self.workspace = kv8_workspace(desc, dev) if workspace is None else workspace
+        # a workspace made here: the streams that its memory is known to be used on
+        self._streams = {_stream(None)} if workspace is None else None
         a.workspace, a.ws_bytes = self.workspace.data_ptr(), self.workspace.numel() * self.workspace.element_size()
         self.keep = (desc, _cache(desc, cache), q, out, q_start, ctx, table, slopes, prefix, lse)
         self._call = lib().kv8_attend
         self._args = (ctypes.byref(desc), cache.data_ptr(), ctypes.byref(a))
 
     def run(self, stream=None):
-        _check(self._call(*self._args, _stream(stream)))
+        s = _stream(stream)
+        if self._streams is not None and s not in self._streams:
+            self._use(s)
+        _check(self._call(*self._args, s))
+
+    def _use(self, s):
+        """The caller does not see the workspace, so its memory is not given out again before stream s is done with it."""
+        import torch
+        if not torch.cuda.is_current_stream_capturing():   # a graph's memory lives as long as what it was captured from
+            self.workspace.record_stream(torch.cuda.ExternalStream(s, device=self.workspace.device))
+            self._streams.add(s)
+
 
 
 # ----------------------------------------------------------------------------- packed-weight files

@@ -380,3 +380,87 @@ def test_largest_window_and_rows_before_the_first_key(env, new):
     want = c.check(prefix=[3, 20])
     for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 64):
         assert (c.check(prefix=[3, 20], window=window) == want).all()
+
+
+# ----------------------------------------------------------------------------- attention: the workspace
+
+@pytest.mark.parametrize("new", [[5], [20], [150]])
+def test_workspace_made_on_another_stream(env, new):
+    """The object and its workspace are made on a stream with work ahead, the call runs on another: the workspace is ready."""
+    q, torch, dev = env
+    c = _Case(env, [9000], new, 4, 1, 64, seed=sum(new))
+    want, _ = c.run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    junk = torch.full_like(c.call.workspace, 0xFF)     # memory that the allocator gives out next, far from zero
+    del junk
+    c.call = None
+    o = torch.full_like(want, 7.0)
+    i32 = lambda v: torch.tensor(np.ascontiguousarray(v, dtype=np.int32), device=dev)  # noqa: E731
+    args = [c.desc, c.cache, c.q, o, i32(c.q_start), i32(c.ctx), i32(c.table), 64 ** -0.5]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)
+    call = q.KvAttend(*args, max_new=max(new))
+    call.run(side)
+    side.synchronize()
+    assert torch.equal(o, want)
+    torch.cuda._sleep(40_000_000)
+    ws = q.kv8_workspace(c.desc, dev)
+    o.fill_(7.0)
+    side.wait_stream(torch.cuda.current_stream())
+    q.KvAttend(*args, max_new=max(new), workspace=ws).run(side)
+    side.synchronize()
+    assert torch.equal(o, want) and int(ws[:16384].view(torch.int32).abs().sum()) == 0
+
+
+def test_workspace_outlives_its_object_on_another_stream(env):
+    """An object that is dropped while its call still waits on a side stream: its memory is not given to anyone before that."""
+    q, torch, dev = env
+    c = _Case(env, [9000], [5], 4, 1, 64, seed=2)
+    want, _ = c.run()
+    keep = c.call.keep
+    c.call = None
+    o = torch.full_like(want, 7.0)
+    i32 = lambda v: torch.tensor(np.ascontiguousarray(v, dtype=np.int32), device=dev)  # noqa: E731
+    args = [c.desc, c.cache, c.q, o, i32(c.q_start), i32(c.ctx), i32(c.table), 64 ** -0.5]
+    call = q.KvAttend(*args, max_new=5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    at, n = call.workspace.data_ptr(), call.workspace.numel()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)
+    call.run(side)
+    del call
+    other = torch.full((n,), 0xFF, dtype=torch.uint8, device=dev)
+    assert other.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and keep is not None
+
+
+def test_workspace_made_aside_used_on_the_default_stream_and_in_a_capture(env):
+    q, torch, dev = env
+    c = _Case(env, [3000], [5], 4, 1, 64, seed=2)
+    want, _ = c.run()
+    o = torch.full_like(want, 7.0)
+    i32 = lambda v: torch.tensor(np.ascontiguousarray(v, dtype=np.int32), device=dev)  # noqa: E731
+    args = [c.desc, c.cache, c.q, o, i32(c.q_start), i32(c.ctx), i32(c.table), 64 ** -0.5]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call = q.KvAttend(*args, max_new=5)
+    for _ in range(2):
+        call.run()
+        assert torch.equal(o, want)
+        o.fill_(7.0)
+    for inside in (False, True):
+        call = q.KvAttend(*args, max_new=5)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if inside:
+                call = q.KvAttend(*args, max_new=5)
+            call.run()
+        for _ in range(3):
+            o.fill_(7.0)
+            g.replay()
+            assert torch.equal(o, want)
+        del g
