@@ -616,6 +616,8 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
     if (g->q == g->q_out && (g->x_type != g->q_out_type || g->ldq != g->ldqo))
       return fail(QMV_ERR_ARG, "in place needs one type and one stride");
   }
+  const int64_t per_head = (int64_t)g->n_runs * desc->n_kv_heads;   // runs times heads: numbered in 31 bits
+  if (per_head > INT32_MAX / 2) return fail(QMV_ERR_UNSUPPORTED, "n_runs=%d of %d heads", g->n_runs, desc->n_kv_heads);
   if (g->n_tokens == 0) return QMV_OK;
   if (!cache || !g->k || !g->v || !g->slots || (g->n_runs > 0 && !g->runs) || (rope && !g->positions))
     return fail(QMV_ERR_ARG, "NULL cache, k, v, slots, runs or positions");
@@ -657,7 +659,7 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   // The heads of a block share the angles of its run's tokens: the fewest heads (a power of two, up to 8) with which all
   // blocks are resident at once. 8190 tokens of 40 and 8 heads of 128, rotation included: 49 us with 4 heads a block (the
   // rule's choice), 57, 53 and 63 with 1, 2 and 8; 512 tokens: 10.2 with 1, 12.2, 17.9 and 28 with 2, 4 and 8.
-  const int64_t per_head = (int64_t)g->n_runs * desc->n_kv_heads, resident = (int64_t)sms * (1024 / (4 * D));
+  const int64_t resident = (int64_t)sms * (1024 / (4 * D));
   a.head_group = 1;
   while (rope && a.head_group < 8 && per_head > a.head_group * resident) a.head_group *= 2;
   a.head_groups = (desc->n_kv_heads + a.head_group - 1) / a.head_group;
@@ -665,15 +667,8 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   if (g->q && few) {
     a.q_heads = g->n_q_heads > 16 ? 16 : g->n_q_heads;
     blocks += (int64_t)g->n_tokens * ((g->n_q_heads + a.q_heads - 1) / a.q_heads);
-  } else if (g->q) {
-    // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 49
-    // us, and 65 us as blocks of one launch, where the cache write's registers halve the rotation's loads in flight)
-    rc = rope_launch(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
-                     g->ldqo, 0, static_cast<cudaStream_t>(stream));
-    if (rc) return rc;
+    if (blocks > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "n_tokens=%d of %d query heads", g->n_tokens, g->n_q_heads);
   }
-  if (blocks == 0) return QMV_OK;
-  if (blocks > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "too many runs");
   const void* f = g->x_type == QMV_F32 ? append_kernel<float>(D, (int)desc->type, few)
                   : g->x_type == QMV_BF16 ? append_kernel<__nv_bfloat16>(D, (int)desc->type, few)
                                           : append_kernel<__half>(D, (int)desc->type, few);
@@ -682,6 +677,14 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   int per_sm = 0;
   rc = kernel_fit(f, threads, smem, &per_sm);
   if (rc) return rc;
+  if (g->q && !few) {
+    // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 49
+    // us, and 65 us as blocks of one launch, where the cache write's registers halve the rotation's loads in flight)
+    rc = rope_launch(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
+                     g->ldqo, 0, static_cast<cudaStream_t>(stream));
+    if (rc) return rc;
+  }
+  if (blocks == 0) return QMV_OK;
   void* args[] = {&a};
   cudaError_t e = launch_early(f, dim3((unsigned)blocks), threads, args, smem, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv8_append launch");

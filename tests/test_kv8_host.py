@@ -186,3 +186,14 @@ def test_binding_refuses_wrong_tensors(L):
         q.Rope(q.rope_desc(64, [1.0] * 32), k, slots[:2], k)
     with pytest.raises(ValueError):
         q.Rope(q.rope_desc(64, [1.0] * 32, axis=[1] * 32), k, slots, k)
+
+
+def test_append_refuses_more_runs_than_it_numbers(L):
+    """Runs times heads past 31 bits, before anything is launched (the rotation of q among it)."""
+    r = q.rope_desc(64, [1.0] * 32)
+    for H, n_runs in ((2, 2 ** 31 - 1), (1024, 2 ** 21), (8, 2 ** 28), (1, 2 ** 30)):
+        d = q.kv8_desc(q.QMV_KV_INT8, 4, H, 64)
+        for n_tokens in (1, 4):
+            a = _filled(q.kv8_append_args, **{**APPEND, "ldk": 64 * H, "ldv": 64 * H, "n_runs": n_runs, "n_tokens": n_tokens, "positions": 256, "ldp": 4,
+                                              "q": 512, "q_out": 1024, "n_q_heads": 4, "ldq": 256, "ldqo": 256, "q_out_type": q.QMV_BF16})
+            assert L.kv8_append(ctypes.byref(d), 256, ctypes.byref(r), ctypes.byref(a), None) == q.QMV_ERR_UNSUPPORTED, q.qmv_last_error()
