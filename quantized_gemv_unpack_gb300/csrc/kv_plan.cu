@@ -307,7 +307,8 @@ int kv_plan(const kv_plan_args* a, void* stream) {
   const int threads = most <= 256 ? 256 : kMaxPlanThreads;
   const size_t smem = (size_t)B * 5 * sizeof(int32_t);
   int per_sm = 0;
-  int rc = kernel_fit(reinterpret_cast<const void*>(kv_plan_kernel), threads, smem, &per_sm);
+  // asked for the most requests: the library keeps an answer per size asked for, and B differs from step to step
+  int rc = kernel_fit(reinterpret_cast<const void*>(kv_plan_kernel), threads, (size_t)QMV_KV_MAX_REQUESTS * 5 * sizeof(int32_t), &per_sm);
   if (rc) return rc;
   kv_plan_args copy = *a;
   int blocks = n_blocks;

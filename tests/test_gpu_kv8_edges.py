@@ -464,3 +464,15 @@ def test_workspace_made_aside_used_on_the_default_stream_and_in_a_capture(env):
             g.replay()
             assert torch.equal(o, want)
         del g
+
+
+def test_plan_of_every_request_count(env):
+    """The number of requests changes from call to call, down and up: each is planned, with the shared memory that it takes."""
+    from oracle import kv8
+    g = np.random.default_rng(4)
+    for B in [8000, 5, 3000, 2457, 2458, 1, 8191] + list(range(250, 260)):
+        lens, table, ring, head = _plan_state(g, B, 3, 2 * B + 9, 9, 64)
+        add = np.where(g.random(B) < 0.01, 2, 0).astype(np.int32)
+        T = int(add.sum())
+        want = kv8.plan(lens, add, table, ring, head, 9, T, _q(env).kv_max_runs(B, T))
+        _check_plan(_run_plan(env, lens, add, table, ring, head, 9, T), want)
