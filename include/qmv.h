@@ -476,15 +476,16 @@ int kv8_desc(int type, int64_t n_pages, int32_t n_kv_heads, int32_t head_dim, qm
  *
  * Request b has lens[b] tokens in the cache and brings add[b] new ones (their
  * rows of q, k and v lie at q_start[b].. in the order of requests; a negative
- * add means that the request leaves). With held = ceil(lens / 64) and after =
- * ceil((lens + add) / 64), in the order of requests:
- *   status 0 (served): its after - held new pages are taken from the ring's
+ * add means that the request leaves). Its row of the table holds held[b] pages,
+ * or ceil(lens / 64) where held is NULL. With after = ceil((lens + add) / 64), in
+ * the order of requests:
+ *   status 0 (served): its max(0, after - held) new pages are taken from the ring's
  *     head and entered in its row of the table; lens_out = ctx = lens + add.
  *   status 1 (no pages): it needs pages and the needs of all requests up to it
  *     exceed count; nothing of it changes, lens_out = lens, ctx = 0.
- *   status 2 (out of bounds): lens is negative, held or after is over
- *     max_pages, or its rows end past T; nothing of it changes, ctx = 0, and
- *     it needs nothing.
+ *   status 2 (out of bounds): lens is negative, held is below ceil(lens / 64),
+ *     held or after is over max_pages, or its rows end past T; nothing of it
+ *     changes, ctx = 0, and it needs nothing.
  *   status 3 (left): its held pages go to the ring's tail (free from the next
  *     step on), in the order of its row; lens_out = ctx = 0.
  * q_start[0..B] are the exclusive sums of max(add, 0), at most T. slots[t] and
@@ -492,7 +493,13 @@ int kv8_desc(int type, int64_t n_pages, int32_t n_kv_heads, int32_t head_dim, qm
  * to no served request. runs lists the runs of new tokens that share a page, as
  * (first token, count), in order; the rest of its max_runs entries are (0, 0).
  * max_runs has to be at least kv_max_runs(B, T).
- * lens_out may be lens, and ring_state_out may be ring_state. A call whose
+ * held_out is max(held, after) where served, 0 where left, else held.
+ * A request may be shortened between steps by lowering lens, as when drafts are
+ * rejected. Where that takes it over a page's end, the pages past its length
+ * stay in its row: held (with held_out, both or neither) keeps count of them,
+ * so that they serve the next tokens and go back when it leaves. Without held
+ * the next step would give it new ones in their place, and they would be lost.
+ * lens_out may be lens, held_out held, and ring_state_out ring_state. A call whose
  * outputs are separate may be repeated with the same inputs and gives the same
  * result. A ring_state that is out of range, or pages that come back to a ring
  * that cannot hold them, set QMV_ERR_CORRUPT in the device error word.
@@ -517,6 +524,8 @@ typedef struct {
   int32_t* slots;            /* [T] */
   int32_t* positions;        /* [T] */
   int32_t* runs;             /* [max_runs][2] */
+  const int32_t* held;       /* [B], nullable */
+  int32_t* held_out;         /* [B], where held is given */
 } kv_plan_args;
 
 int64_t kv_max_runs(int64_t n_requests, int64_t n_tokens);

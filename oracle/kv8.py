@@ -86,11 +86,13 @@ class Cache:
 
 # ----------------------------------------------------------------------------- plan
 
-def plan(lens, add, table, ring, head, count, T, max_runs):
-    """One step, request by request. Returns a dict of the outputs; table and ring are copies."""
+def plan(lens, add, table, ring, head, count, T, max_runs, held=None):
+    """One step, request by request. Returns a dict of the outputs; table and ring are copies. held: pages in each row (NULL:
+    those that the length fills)."""
+    counts = held
     B, cap, N = len(lens), table.shape[1], len(ring)
     table, ring = table.copy(), ring.copy()
-    out = {k: np.zeros(B, dtype=np.int64) for k in ("lens_out", "ctx", "status")}
+    out = {k: np.zeros(B, dtype=np.int64) for k in ("lens_out", "ctx", "status", "held_out")}
     q_start = np.zeros(B + 1, dtype=np.int64)
     slots, positions = np.full(T, -1), np.full(T, -1)
     runs = []
@@ -99,22 +101,25 @@ def plan(lens, add, table, ring, head, count, T, max_runs):
     for b in range(B):
         length, new = int(lens[b]), max(int(add[b]), 0)
         q_start[b] = min(at, T)
-        held, after = -(-length // PAGE), -(-(length + new) // PAGE)
+        full, after = -(-length // PAGE), -(-(length + new) // PAGE)
+        held = full if counts is None else int(counts[b])
         out["lens_out"][b] = length
-        if length < 0 or held > cap or after > cap or at + new > T:
+        out["held_out"][b] = held
+        if length < 0 or held < full or held > cap or after > cap or at + new > T:
             out["status"][b] = 2
         elif add[b] < 0:
             out["status"][b] = 3
-            out["lens_out"][b] = 0
+            out["lens_out"][b] = out["held_out"][b] = 0
             back += [int(p) for p in table[b, :held]]
         else:
-            needed += after - held
+            needed += max(after - held, 0)
             if after > held and needed > count:
                 out["status"][b] = 1
             else:
                 for i in range(held, after):
                     table[b, i] = ring[(head + taken) % N]
                     taken += 1
+                out["held_out"][b] = max(held, after)
                 out["lens_out"][b] = out["ctx"][b] = length + new
                 for i in range(new):
                     p = length + i

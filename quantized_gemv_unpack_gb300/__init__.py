@@ -78,7 +78,7 @@ class kv_plan_args(ctypes.Structure):
     _fields_ = [("n_requests", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("ld_table", ctypes.c_int64), ("max_runs", ctypes.c_int32)] + [
                     (n, ctypes.c_void_p) for n in ("lens", "add", "table", "ring", "ring_state", "ring_state_out", "lens_out",
-                                                   "ctx", "status", "q_start", "slots", "positions", "runs")]
+                                                   "ctx", "status", "q_start", "slots", "positions", "runs", "held", "held_out")]
 
 
 class kv8_append_args(ctypes.Structure):
@@ -442,9 +442,11 @@ class KvPlan:
     """kv_plan: block tables and slot maps of one step (see include/qmv.h). int32 device tensors lens, add [B],
     table [B][max_pages], ring [n_pages], ring_state [2] = (head, count); n_tokens is the number of new tokens' rows.
     run() fills slots, positions [n_tokens], runs [max_runs][2], q_start [B + 1], ctx, status [B], and lens_out and
-    ring_state_out, which may be given as lens and ring_state to advance the state in place."""
+    ring_state_out, which may be given as lens and ring_state to advance the state in place. A loop that takes tokens back
+    (lens lowered between steps) gives held [B], the pages in each row of the table, too: held_out, which may be held, is
+    then filled, and no page is lost."""
 
-    def __init__(self, lens, add, table, ring, ring_state, n_tokens: int, lens_out=None, ring_state_out=None):
+    def __init__(self, lens, add, table, ring, ring_state, n_tokens: int, lens_out=None, ring_state_out=None, held=None, held_out=None):
         import torch
         dev = lens.device
         B = lens.shape[0]
@@ -454,6 +456,10 @@ class KvPlan:
         self.ring_state = _ints("ring_state", ring_state, (2,), dev)
         self.lens_out = new(B) if lens_out is None else _ints("lens_out", lens_out, (B,), dev)
         self.ring_state_out = new(2) if ring_state_out is None else _ints("ring_state_out", ring_state_out, (2,), dev)
+        if held is None and held_out is not None:
+            raise ValueError("held_out needs held")
+        self.held = None if held is None else _ints("held", held, (B,), dev)
+        self.held_out = None if held is None else new(B) if held_out is None else _ints("held_out", held_out, (B,), dev)
         max_runs = kv_max_runs(B, n_tokens)
         self.ctx, self.status, self.q_start = new(B), new(B), new(B + 1)
         self.slots, self.positions, self.runs = new(n_tokens), new(n_tokens), new(max_runs, 2)
@@ -461,6 +467,8 @@ class KvPlan:
         for n in ("lens", "add", "table", "ring", "ring_state", "ring_state_out", "lens_out", "ctx", "status", "q_start",
                   "slots", "positions", "runs"):
             setattr(a, n, getattr(self, n).data_ptr())
+        if held is not None:
+            a.held, a.held_out = self.held.data_ptr(), self.held_out.data_ptr()
         self._call, self._args = lib().kv_plan, ctypes.byref(a)
 
     def run(self, stream=None):

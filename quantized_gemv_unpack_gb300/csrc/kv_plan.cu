@@ -27,10 +27,12 @@ constexpr int kPlanCluster = 8;   // blocks: the largest cluster that every devi
 struct Scratch {   // per request, in dynamic shared memory
   int32_t* start;  // first token (at most T)
   int32_t* len;    // tokens in the cache before the step
+  int32_t* held;   // pages in its row before the step
   int32_t* page;   // place of its first new page among the step's new pages
   int32_t* run;    // place of its first run, or of its first returned page
   int32_t* status;
 };
+constexpr int kScratchWords = sizeof(Scratch) / sizeof(int32_t*);
 
 // Sums stop at kMost: past any count of tokens or pages that a call can serve (2^30 tokens at most), so that a sum that has
 // stopped is over every limit. Two of them come to 2^31 + 2, which does not fit an int: they are added without sign.
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
   extern __shared__ int32_t plan_smem[];
   __shared__ int warp_sums[5][32];
   const int B = a.n_requests, T = a.n_tokens, N = a.n_pages;
-  const Scratch s{plan_smem, plan_smem + B, plan_smem + 2 * B, plan_smem + 3 * B, plan_smem + 4 * B};
+  const Scratch s{plan_smem, plan_smem + B, plan_smem + 2 * B, plan_smem + 3 * B, plan_smem + 4 * B, plan_smem + 5 * B};
   const int tid = threadIdx.x, nt = blockDim.x;
   const int block = blockIdx.x;
   const int per = (B + nt - 1) / nt;
@@ -104,13 +106,14 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
   for (int b = b0; b < b1; ++b) {
     const int len = a.lens[b], add = a.add[b];
     const int tok = min(max(add, 0), kMost);
-    const int held = (int)(((long long)len + 63) >> 6);
+    const int full = (int)(((long long)len + 63) >> 6), held = a.held ? a.held[b] : full;
     const long long after = ((long long)len + tok + 63) >> 6;
-    const bool bad = len < 0 || held > a.max_pages || after > a.max_pages || (unsigned)at + (unsigned)tok > (unsigned)T;
+    const bool bad = len < 0 || held < full || held > a.max_pages || after > a.max_pages || (unsigned)at + (unsigned)tok > (unsigned)T;
     s.start[b] = min(at, T);
     s.len[b] = len;
+    s.held[b] = held;
     s.status[b] = bad ? 2 : (add < 0 ? 3 : 0);
-    if (!bad && add > 0) need[0] = add_most(need[0], (int)after - held);
+    if (!bad && add > 0) need[0] = add_most(need[0], max((int)after - held, 0));
     at = add_most(at, tok);
   }
   // new pages: a request is short of pages where the needs up to its own exceed what is free
@@ -119,10 +122,10 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
   int sums3[3] = {0, 0, 0}, total3[3];   // runs, returned pages, pages taken
   for (int b = b0; b < b1; ++b) {
     const int len = s.len[b];
-    if (s.status[b] == 3) sums3[1] = add_most(sums3[1], (len + 63) >> 6);
+    if (s.status[b] == 3) sums3[1] = add_most(sums3[1], s.held[b]);
     if (s.status[b] != 0) continue;
     const int add = max(a.add[b], 0);   // served so far: at most T
-    const int held = (len + 63) >> 6, want = ((len + add + 63) >> 6) - held;
+    const int want = max(((len + add + 63) >> 6) - s.held[b], 0);
     s.page[b] = need_at;
     need_at = add_most(need_at, want);
     if (want > 0 && need_at > count) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
     const int len = s.len[b];
     if (s.status[b] == 3) {
       s.run[b] = back_at;
-      back_at = add_most(back_at, (len + 63) >> 6);
+      back_at = add_most(back_at, s.held[b]);
     } else if (s.status[b] == 0) {
       s.run[b] = run_at;
       const int add = max(a.add[b], 0);
@@ -166,6 +169,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
     const int after = len + (end - start);
     a.lens_out[b] = st == 0 ? after : (st == 3 ? 0 : len);
     a.ctx[b] = st == 0 ? after : 0;
+    if (a.held) a.held_out[b] = st == 0 ? max(s.held[b], (after + 63) >> 6) : (st == 3 ? 0 : s.held[b]);
   }
   if (gtid == 0) {
     const int kept = min(n_back, room);
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
     int b = 0;
     for (int step = 1 << (search - 1); step; step >>= 1)
       if (b + step < B && s.start[b + step] <= t0) b += step;
-    int start = s.start[b], end = b + 1 < B ? s.start[b + 1] : n_tokens, len = s.len[b], page_index = -1, page = 0;
+    int start = s.start[b], end = b + 1 < B ? s.start[b + 1] : n_tokens, len = s.len[b], held = s.held[b], page_index = -1, page = 0;
     bool served = s.status[b] == 0;
     int slot[4], pos[4];
 #pragma unroll
@@ -198,12 +202,13 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
         start = end;
         end = b + 1 < B ? s.start[b + 1] : n_tokens;
         len = s.len[b];
+        held = s.held[b];
         served = s.status[b] == 0;
         page_index = -1;
       }
       if (!served) continue;
       pos[u] = len + t - start;
-      const int held = (len + 63) >> 6, index = pos[u] >> 6;
+      const int index = pos[u] >> 6;
       const bool opens = (pos[u] & 63) == 0;
       if (index != page_index) {
         page_index = index;
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(kMaxPlanThreads) kv_plan_kernel(const __grid_c
       if (turn-- != 0) continue;
       turn = sharers - 1;
       const int b = first + __ffs(gone) - 1;
-      const int held = (s.len[b] + 63) >> 6, place = s.run[b], n = min(held, room - place);
+      const int held = s.held[b], place = s.run[b], n = min(held, room - place);
       const int32_t* row = a.table + (int64_t)b * a.ld_table;
 #pragma unroll 4
       for (int i = lane; i < n; i += 32) {
@@ -291,6 +296,9 @@ int kv_plan(const kv_plan_args* a, void* stream) {
     if (!p) return fail(QMV_ERR_ARG, "NULL pointer");
     if (reinterpret_cast<uintptr_t>(p) & 3u) return fail(QMV_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
   }
+  if ((a->held != nullptr) != (a->held_out != nullptr)) return fail(QMV_ERR_ARG, "held and held_out: both or neither");
+  if ((reinterpret_cast<uintptr_t>(a->held) | reinterpret_cast<uintptr_t>(a->held_out)) & 3u)
+    return fail(QMV_ERR_ALIGN, "int32 arrays must be 4-byte aligned");
   if (a->n_tokens > 0) {
     if (!a->slots || !a->positions || !a->runs) return fail(QMV_ERR_ARG, "NULL slots, positions or runs");
     if ((reinterpret_cast<uintptr_t>(a->slots) | reinterpret_cast<uintptr_t>(a->positions)) & 3u)
@@ -305,10 +313,10 @@ int kv_plan(const kv_plan_args* a, void* stream) {
   // one block while its threads see at most four requests or four tokens each: more blocks only add the cluster barrier
   const int n_blocks = most > 4 * kMaxPlanThreads ? kPlanCluster : 1;
   const int threads = most <= 256 ? 256 : kMaxPlanThreads;
-  const size_t smem = (size_t)B * 5 * sizeof(int32_t);
+  const size_t smem = (size_t)B * kScratchWords * sizeof(int32_t);
   int per_sm = 0;
   // asked for the most requests: the library keeps an answer per size asked for, and B differs from step to step
-  int rc = kernel_fit(reinterpret_cast<const void*>(kv_plan_kernel), threads, (size_t)QMV_KV_MAX_REQUESTS * 5 * sizeof(int32_t), &per_sm);
+  int rc = kernel_fit(reinterpret_cast<const void*>(kv_plan_kernel), threads, (size_t)QMV_KV_MAX_REQUESTS * kScratchWords * sizeof(int32_t), &per_sm);
   if (rc) return rc;
   kv_plan_args copy = *a;
   int blocks = n_blocks;

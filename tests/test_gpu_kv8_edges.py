@@ -476,3 +476,66 @@ def test_plan_of_every_request_count(env):
         T = int(add.sum())
         want = kv8.plan(lens, add, table, ring, head, 9, T, _q(env).kv_max_runs(B, T))
         _check_plan(_run_plan(env, lens, add, table, ring, head, 9, T), want)
+
+
+# ----------------------------------------------------------------------------- plan: requests that are shortened
+
+def _run_plan_held(env, lens, add, table, ring, head, count, T, held, in_place=False):
+    q, torch, dev = env
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)  # noqa: E731
+    l, st, h = t(lens), t([head, count]), t(held)
+    p = q.KvPlan(l, t(add), t(table), t(ring), st, T, lens_out=l if in_place else None, ring_state_out=st if in_place else None, held=h,
+                 held_out=h if in_place else None)
+    p.run()
+    torch.cuda.synchronize()
+    return p
+
+
+@pytest.mark.parametrize("B,max_len,new,free", [(1, 64, 1, 1), (3, 200, 5, 2), (64, 300, 90, 30), (257, 130, 3, 60), (2048, 500, 7, 300), (6, 300, 3000, 400)])
+def test_plan_with_held_pages_matches_oracle(env, B, max_len, new, free):
+    """Rows that hold more pages than their lengths fill, and counts that cannot be."""
+    from oracle import kv8
+    g = np.random.default_rng(B + new)
+    cap = (max_len + new + 63) // 64 + 1
+    N = B * (max_len // 64 + 1) + free + 5
+    lens, table, ring, head = _plan_state(g, B, cap, N, free, max_len)
+    held = -(-lens // 64)
+    lens = np.maximum(lens - g.integers(0, 150, B), 0).astype(np.int32)
+    add = g.integers(0, new + 1, B).astype(np.int32)
+    add[g.random(B) < 0.15] = -1
+    add[g.random(B) < 0.05] = cap * 64
+    held[g.random(B) < 0.03] = cap + 1
+    held[g.random(B) < 0.03] = -1
+    T = int(np.maximum(add, 0).sum())
+    want = kv8.plan(lens, add, table, ring, head, free, T, _q(env).kv_max_runs(B, T), held=held)
+    for in_place in (False, True):
+        p = _run_plan_held(env, lens, add, table, ring, head, free, T, held, in_place)
+        _check_plan(p, want)
+        assert p.held_out.tolist() == want["held_out"].tolist()
+
+
+def test_plan_loses_no_page_of_rejected_drafts(env):
+    """200 steps of drafts of which some are taken back, over page ends too: no page is owned twice, none is lost."""
+    q, torch, dev = env
+    from oracle import kv8
+    g = np.random.default_rng(9)
+    B, cap, N, T = 12, 8, 50, 300
+    lens, held, table = np.zeros(B, dtype=np.int32), np.zeros(B, dtype=np.int32), np.full((B, cap), -1, dtype=np.int32)
+    ring, head, count = np.arange(N, dtype=np.int32), 0, N
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).to(dev)  # noqa: E731
+    dl, dt, dr, ds, da, dh = t(lens), t(table), t(ring), t([head, count]), t(np.zeros(B)), t(held)
+    p = q.KvPlan(dl, da, dt, dr, ds, T, lens_out=dl, ring_state_out=ds, held=dh, held_out=dh)
+    for step in range(200):
+        add = np.where(g.random(B) < 0.1, -1, g.integers(0, 26, B)).astype(np.int32)
+        da.copy_(t(add))
+        want = kv8.plan(lens, add, table, ring, head, count, T, q.kv_max_runs(B, T), held=held)
+        p.run()
+        torch.cuda.synchronize()
+        _check_plan(p, want)
+        lens, held, table, ring = (want[k].astype(np.int32) for k in ("lens_out", "held_out", "table", "ring"))
+        assert p.held_out.tolist() == held.tolist()
+        head, count = (int(v) for v in want["ring_state_out"])
+        owned = [int(x) for b in range(B) for x in table[b, :held[b]]]
+        assert sorted(owned + [int(ring[(head + i) % N]) for i in range(count)]) == list(range(N))
+        lens = np.maximum(lens - np.where(g.random(B) < 0.5, g.integers(0, 100, B), 0), 0).astype(np.int32)   # rejected
+        dl.copy_(t(lens))

@@ -197,3 +197,16 @@ def test_append_refuses_more_runs_than_it_numbers(L):
             a = _filled(q.kv8_append_args, **{**APPEND, "ldk": 64 * H, "ldv": 64 * H, "n_runs": n_runs, "n_tokens": n_tokens, "positions": 256, "ldp": 4,
                                               "q": 512, "q_out": 1024, "n_q_heads": 4, "ldq": 256, "ldqo": 256, "q_out_type": q.QMV_BF16})
             assert L.kv8_append(ctypes.byref(d), 256, ctypes.byref(r), ctypes.byref(a), None) == q.QMV_ERR_UNSUPPORTED, q.qmv_last_error()
+
+
+def test_plan_held_refusals(L):
+    for change, status in [(dict(held=256), -1), (dict(held_out=256), -1), (dict(held=258, held_out=256), -2), (dict(held=256, held_out=257), -2)]:
+        a = _filled(q.kv_plan_args, **{**PLAN, **change})
+        assert L.kv_plan(ctypes.byref(a), None) == status, q.qmv_last_error()
+    import torch
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
+    q.KvPlan(i32(2), i32(2), i32(2, 4), i32(8), i32(2), 5, held=i32(2))
+    with pytest.raises(ValueError):
+        q.KvPlan(i32(2), i32(2), i32(2, 4), i32(8), i32(2), 5, held_out=i32(2))
+    with pytest.raises(ValueError):
+        q.KvPlan(i32(2), i32(2), i32(2, 4), i32(8), i32(2), 5, held=i32(3))

@@ -127,3 +127,18 @@ def test_append_keeps_the_least_scale():
         kv8.append(c, k, k, np.array([64, 65]), [[1, 1]])
         assert c.scales[1, 0].tolist() == [2.0 ** -125] * 2
         assert c.page_values(1, 1)[0, 1, 1] == 2.0 ** -125 * top and not c.page_values(1, 1)[0, :2, 2:].any()
+
+
+def test_plan_keeps_the_pages_of_a_shortened_request():
+    """Two requests of 130 tokens taken back to 60 and 64: their further pages stay in their rows, serve the next tokens and
+    go back with them."""
+    table = np.array([[5, 6, 7, -1], [1, 2, 3, -1]])
+    ring = np.array([9, 8, -1, -1, -1, -1])
+    p = kv8.plan(np.array([60, 64]), np.array([10, -1]), table, ring, 0, 2, 10, 3, held=[3, 3])
+    assert p["status"].tolist() == [0, 3] and p["held_out"].tolist() == [3, 0] and p["table"].tolist() == table.tolist()
+    assert p["slots"].tolist() == [5 * 64 + i for i in range(60, 64)] + [6 * 64 + i for i in range(6)]
+    assert p["ring_state_out"].tolist() == [0, 5] and p["ring"].tolist() == [9, 8, 1, 2, 3, -1]
+    p = kv8.plan(np.array([60, 64]), np.array([140, 1]), table, np.array([9, 8, -1, -1]), 0, 2, 141, 9, held=[3, 1])
+    assert p["status"].tolist() == [0, 0] and p["table"].tolist() == [[5, 6, 7, 9], [1, 8, 3, -1]] and p["held_out"].tolist() == [4, 2]
+    p = kv8.plan(np.array([60, 64]), np.array([1, 1]), table, ring, 0, 2, 2, 2, held=[0, 5])
+    assert p["status"].tolist() == [2, 2] and p["held_out"].tolist() == [0, 5]
