@@ -575,14 +575,18 @@ int rope_run(const qmv_rope* rope, const void* x, int x_type, int64_t n_tokens, 
  * the run's values and top = 127 (int8) or 448 (e4m3), the scale becomes
  * s' = max(s, a / top), or 2^-126 where that is smaller and not 0; where it
  * grows, the codes already in the page are rounded again from code * s * (1 / s');
- * the new codes are x * (1 / s'), rounded
- * to nearest even and held to +-top. All of it is fp32. An infinite value takes
- * the largest code and does not count for a; a NaN is stored as 0; either sets
- * QMV_ERR_CORRUPT in the device error word, and so does a run outside the
- * tokens, its page or the cache (nothing is written for that run).
+ * the new codes are x * (1 / s'), rounded to nearest even and held to +-top. All
+ * of it is fp32. An infinite value takes the largest code and does not count for
+ * a; a NaN is stored as 0; either sets QMV_ERR_CORRUPT in the device error word,
+ * and so does a run outside the tokens, its page or the cache (nothing is written
+ * for that run).
  * rope (nullable) rotates k by `positions` before it is stored and, where q is
  * given, q [n_tokens][ldq] (n_q_heads heads) to q_out [n_tokens][ldqo] of
  * q_out_type. Without rope q must be NULL.
+ * One kernel serves a call, chosen by the tokens per entry of runs. Where a step
+ * has single tokens of many requests and a long prompt chunk, two calls over the
+ * same arrays are faster, one with the runs of the single tokens (the first
+ * requests, a run each) and one with the rest of the list, q in one of them.
  */
 typedef struct {
   const void* k;
@@ -631,7 +635,10 @@ int kv8_read(const qmv_kv_desc* desc, const void* cache, const int32_t* slots, i
  * statistics are fp32.
  * The result is reproducible bit for bit.
  * max_new is the host's bound on the rows of one request. It chooses the
- * kernel's row tile; a request with more rows is still served in full.
+ * kernel and its row tile; a request with more rows is still served in full.
+ * Where a step has single tokens of many requests and a long prompt chunk, two
+ * calls are faster, each over its own requests (q_start, ctx, table and prefix
+ * from its first request on) with its own max_new; q, out and lse stay as they are.
  * A table entry outside the cache sets QMV_ERR_CORRUPT and its page is not
  * read: its keys count as unseen.
  * workspace: device, >= kv8_attend_workspace_size(desc) bytes, given to

@@ -599,7 +599,8 @@ class KvAttend:
     """kv8_attend: attention of q [tokens][q_heads][head_dim] over the cache into out (same shape), with a KvPlan's
     q_start [B + 1], ctx [B] and table [B][max_pages]. max_new bounds the new tokens of one request. slopes [q_heads]
     (fp32) and prefix [B] (int32) are device tensors; lse [tokens][q_heads] (fp32) is optional. Without a workspace
-    one is made; layers of one stream can share it (its `workspace`)."""
+    one is made (kv8_workspace); layers of one stream should share it (its `workspace`). A step that mixes single tokens and
+    a long prompt chunk is faster as two calls, over slices q_start[a:b + 1], ctx[a:b], table[a:b] with a max_new each."""
 
     def __init__(self, desc: qmv_kv_desc, cache, q, out, q_start, ctx, table, scale: float, max_new: int = 1,
                  softcap: float = 0.0, slopes=None, window: int = 0, prefix=None, lse=None, workspace=None):

@@ -17,10 +17,11 @@
 // and head, whose further blocks rotate the query heads, so that a layer's
 // rotation and cache write are one launch there.
 //
-// Measured (40 query and 8 KV heads of 128): 8190 prompt tokens, bf16 to e4m3, 20 us
-// behind the 31 of the rotation of q, 50 together; reading them back 15 us. Both
-// are bound by instructions and block-wide steps (issue 54 and 63 % busy, DRAM 15 %). A step of 64
-// tokens: 4.5 us, and 5.5 to read them back, launch and dependent loads.
+// Measured (40 query and 8 KV heads of 128): 8190 prompt tokens, bf16 to e4m3, 18 us
+// behind the 32 of the rotation of q, 50 together; reading them back 14 us. Neither
+// the write nor the read reaches a limit of the machine: block-wide steps and the
+// transposition of V leave issue 52 and 63 % busy, DRAM 18 and 13 %. A step of 64
+// tokens: 4.5 us, and 5.6 to read them back, launch and dependent loads.
 #include "kv8.cuh"
 
 #include <cstring>
@@ -654,11 +655,14 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   a.H = desc->n_kv_heads;
   a.err = err;
   const int D = desc->head_dim, sms = sm_count();
-  // runs of less than eight tokens on average go to the kernel of one warp per run and head
+  // Fewer than eight tokens per entry of the run list go to the kernel of one warp per run and head. A plan's list ends in
+  // empty entries (it has room for about two runs per request), so that its bound is 16 to 18 tokens per request. The choice is
+  // one for the call: 63 decode tokens beside a prompt chunk of 1000 (40 and 8 heads of 128, fp32) take 67 us so, a warp to a
+  // page, and 20 as two calls.
   const bool few = g->n_tokens < 8 * (int64_t)g->n_runs;
   // The heads of a block share the angles of its run's tokens: the fewest heads (a power of two, up to 8) with which all
-  // blocks are resident at once. 8190 tokens of 40 and 8 heads of 128, rotation included: 49 us with 4 heads a block (the
-  // rule's choice), 57, 53 and 63 with 1, 2 and 8; 512 tokens: 10.2 with 1, 12.2, 17.9 and 28 with 2, 4 and 8.
+  // blocks are resident at once. 8190 tokens of 40 and 8 heads of 128, rotation included: 50 us with 4 heads a block (the
+  // rule's choice), 59, 55 and 60 with 1, 2 and 8; 512 tokens: 11.6 with 1, 13.7, 19 and 30 with 2, 4 and 8.
   const int64_t resident = (int64_t)sms * (1024 / (4 * D));
   a.head_group = 1;
   while (rope && a.head_group < 8 && per_head > a.head_group * resident) a.head_group *= 2;
@@ -678,7 +682,7 @@ int kv8_append(const qmv_kv_desc* desc, void* cache, const qmv_rope* rope, const
   rc = kernel_fit(f, threads, smem, &per_sm);
   if (rc) return rc;
   if (g->q && !few) {
-    // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 49
+    // long runs: the query heads are rotated by a launch of their own (measured on 8190 tokens of 40 and 8 heads: 50
     // us, and 65 us as blocks of one launch, where the cache write's registers halve the rotation's loads in flight)
     rc = rope_launch(rope, g->q, g->x_type, g->n_tokens, g->n_q_heads, g->ldq, g->positions, g->ldp, g->q_out, g->q_out_type,
                      g->ldqo, 0, static_cast<cudaStream_t>(stream));

@@ -20,7 +20,7 @@
 // on timing.
 //
 // What bounds it: the cache's bytes where there are many (64 requests of up to
-// 16384 tokens, 1.16 GB: 184 us, 6.3 TB/s, 0.93 of the measured copy rate); for few
+// 16384 tokens, 1.16 GB: 184 us, 6.3 TB/s, 0.92 of the measured copy rate); for few
 // requests the launch and a chain of dependent loads (one token over 300 tokens 7.5 us, over
 // 1000 9.5), then the products of one page per stream at a time; with 25 rows the
 // latency of mma.sync at two warps per scheduler (5 tokens over 32771: 42 us).
@@ -38,7 +38,9 @@
 // accumulator to B fragment by one 8 x 8 transpose per eight tokens. Codes become
 // fp16 exactly: int8 as 1024 + byte by a byte permute and a subtraction, e4m3 by
 // the conversion instruction. q is scaled per row by a power of two into fp16, so
-// q . k is exact up to its fp32 sum. The page's K scale multiplies the scores, its
+// q . k is exact up to its fp32 sum for fp16 and, down to 2^-27 of a row's largest
+// value, bf16 queries (their 8 bits fit in 11); fp32 queries are rounded to 11 bits,
+// since a second product with what is left of them would double the scores' work. The page's K scale multiplies the scores, its
 // V scale the page's product with V: in fp32 both, after the sum over the page.
 #pragma once
 

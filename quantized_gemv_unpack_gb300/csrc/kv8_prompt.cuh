@@ -26,8 +26,9 @@
 // unit) and 16 codes per conversion lane and register. Three chunks of up to 1500
 // tokens over up to 4096 keys (40 and 8 heads of 128): 204 us, 0.97 PFLOP/s, half of
 // the measured peak. A step takes about 3300 clocks for 2048 of products, because
-// each tile's chain of scores, maximum, exponentials and P is as long as that, and
-// tensor memory has no room for a second tile of scores. With cap and slopes 420 us
+// each tile's chain of scores, maximum, exponentials and P is as long as that, and a
+// tile's next scores go where its scores and then P were, so they wait for PV. (P
+// leaves half of those columns free, room for the scores of half a step ahead.) With cap and slopes 420 us
 // (scores below half the cap; 550 where both sides of it meet: three special-function results per score in place of one).
 #pragma once
 

@@ -539,3 +539,61 @@ def test_plan_loses_no_page_of_rejected_drafts(env):
         assert sorted(owned + [int(ring[(head + i) % N]) for i in range(count)]) == list(range(N))
         lens = np.maximum(lens - np.where(g.random(B) < 0.5, g.integers(0, 100, B), 0), 0).astype(np.int32)   # rejected
         dl.copy_(t(lens))
+
+
+# ----------------------------------------------------------------------------- together
+
+def test_a_mixed_step_in_one_call_and_in_two(env):
+    """Single tokens of many requests beside a prompt chunk: the cache write and the attention as one call each, and as one for
+    the single tokens and one for the chunk over slices of the plan."""
+    q, torch, dev = env
+    H, Hq, D, n, chunk = 2, 10, 64, 19, 170
+    g = np.random.default_rng(1)
+    lens = g.integers(1, 300, n + 1)
+    T = n + chunk
+    i32 = lambda v: torch.tensor(np.asarray(v, dtype=np.int32), device=dev)  # noqa: E731
+    need = -(-lens // 64)
+    order = g.permutation(200)
+    table = np.full((n + 1, 9), -1)
+    at = 0
+    for b, m in enumerate(need):
+        table[b, :m] = order[at:at + m]
+        at += m
+    p = q.KvPlan(i32(lens), i32([1] * n + [chunk]), i32(table), i32(np.concatenate([order[at:], np.full(at, -1)])), i32([0, 200 - at]), T)
+    p.run()
+    assert not p.status.any()
+    gen = torch.Generator(device=dev).manual_seed(2)
+    x = torch.randn((T, Hq + 2 * H, D), generator=gen, device=dev)
+    rope = q.rope_desc(D, [100.0 ** (-i / 32) for i in range(32)])
+    d, base = _fresh_cache(env, 1, 200, H, D)
+    ref = _host(base, d)
+    ref.scales[:] = 0.02
+    ref.codes[:] = g.integers(1, 256, ref.codes.shape)
+    base.copy_(torch.from_numpy(ref.buf))
+
+    def append(cache, runs, with_q):
+        qo = torch.zeros((T, Hq, D), device=dev, dtype=torch.bfloat16)
+        kw = dict(q=x[:, :Hq], q_out=qo) if with_q else {}
+        q.KvAppend(d, cache, x[:, Hq:Hq + H], x[:, Hq + H:], p.slots, runs, rope=rope, positions=p.positions, **kw).run()
+        return qo
+
+    one, two = base.clone(), base.clone()
+    qo = append(one, p.runs, True)
+    append(two, p.runs[:n], False)
+    assert torch.equal(append(two, p.runs[n:], True), qo)
+    a, b = _host(one, d), _host(two, d)
+    full = np.concatenate([lens[:n] + 1, [lens[n] + chunk]])
+    for r in range(n + 1):
+        for i in range(-(-int(full[r]) // 64)):
+            page, fill = int(p.table[r, i]), min(64, int(full[r]) - 64 * i)
+            assert np.array_equal(a.scales[page], b.scales[page])
+            for w in (0, 1):
+                assert np.array_equal(a.page_codes(page, w)[:, :fill], b.page_codes(page, w)[:, :fill])
+    outs = [torch.zeros((T, Hq, D), device=dev) for _ in range(2)]
+    q.KvAttend(d, one, qo, outs[0], p.q_start, p.ctx, p.table, D ** -0.5, max_new=chunk).run()
+    q.KvAttend(d, one, qo, outs[1], p.q_start[:n + 1], p.ctx[:n], p.table[:n], D ** -0.5, max_new=1).run()
+    q.KvAttend(d, one, qo, outs[1], p.q_start[n:], p.ctx[n:], p.table[n:], D ** -0.5, max_new=chunk).run()
+    assert torch.equal(outs[0][n:], outs[1][n:])
+    # P in fp16 against references of different height: 2^-11 on either side
+    assert float((outs[0] - outs[1]).abs().max()) <= 2.0 ** -9 * float(outs[0].abs().max())
+    assert q.qmv_check_status() == 0
