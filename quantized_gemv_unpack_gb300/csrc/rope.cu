@@ -12,7 +12,7 @@
 //
 // Measured: 8192 tokens of 48 heads of 128, bf16, three axes: 34.9 us, 5.8 TB/s (0.85
 // of the measured copy rate); 4095 tokens of 16 heads of 64 in fp32: 7.5 us; one token 1.9 us in a
-// captured graph, 4.0 issued from the host. Two,
+// captured graph, 4.3 issued from the host. Two,
 // three or eight tokens per block and three loads in flight per thread were no faster.
 #include "kv8.cuh"
 
