@@ -671,6 +671,143 @@ int kv8_attend_init(const qmv_kv_desc* desc, void* workspace, size_t ws_bytes, v
 int kv8_attend(const qmv_kv_desc* desc, const void* cache, const kv8_attend_args* args, void* stream);
 
 /*
+ * Around the projections of a serving step that answers many requests with one
+ * packed model:
+ *
+ *   qmv_embed    first: the step's tokens as rows of the packed matrix
+ *   lora_plan    once per step: its tokens grouped by adapter
+ *   lora_run     beside projections, after them: each token's adapter added to y
+ *   logprob_run  last: log probabilities out of the LM head's y
+ *
+ * Tokens, adapters and places are int32 device arrays that need only their
+ * natural alignment.
+ */
+
+/*
+ * Embedding rows out of a packed matrix (a tied LM head, or a table of its own):
+ *   out[t][k] = scale * q[tokens[t]][k] * s[tokens[t]][k / 128],  k < K.
+ * desc: QMV_TERNARY2, QMV_INT4 or one of their byte-lookup layouts
+ * (QMV_ERR_UNSUPPORTED for the others). out: [n_tokens][ldo] of out_type
+ * (qmv_dtype), rows 16-byte aligned; q * s is exact, its product with scale is
+ * rounded to fp32 and then to out_type. The same token may appear any number of
+ * times. A negative token (padding) gives a row of zeros, one past N too, with
+ * QMV_ERR_CORRUPT in the device error word; a ternary code 11 gives 0 and sets it.
+ * n_tokens may be 0.
+ */
+int qmv_embed(const qmv_desc* desc, const void* packed, const int32_t* tokens, int64_t n_tokens, float scale,
+              void* out, int out_type, int64_t ldo, void* stream);
+
+/*
+ * Low-rank adapters of many requests beside a shared projection. An adapter a of
+ * a projection of K columns and N rows is a pair of factors of its rank r, kept
+ * rank row by rank row in two pools, A [pool_rows][lda] and B [pool_rows][ldb]
+ * (bf16; B's rank rows are the columns of the usual N x r factor):
+ * rows first .. first + r - 1 of both, with table[a] = (first, r). Adapters may
+ * be loaded and dropped in any order, and share rows.
+ *
+ * lora_plan groups a step's tokens by adapter, once for all layers. ids[t] is
+ * the adapter of token t, negative for none. order lists the tokens that have
+ * one, adapter by adapter, each adapter's in their order, then -1. tiles lists
+ * their tiles of at most lora_tile(n_tokens) tokens (16, or 64 from 1024 tokens
+ * on) as (adapter, first place in order, count, 0); the rest of the max_tiles
+ * entries are 0. An id of n_adapters or more counts as none and sets
+ * QMV_ERR_CORRUPT in the device error word. The result depends on ids alone.
+ */
+#define QMV_LORA_MAX_ADAPTERS 1024
+#define QMV_LORA_MAX_TOKENS 1048576
+#define QMV_LORA_MAX_RANK 128
+#define QMV_LORA_MAX_TASKS 8
+
+typedef struct {
+  int32_t n_tokens, n_adapters;
+  int32_t max_tiles;         /* at least lora_max_tiles(n_tokens, n_adapters) */
+  const int32_t* ids;        /* [n_tokens] */
+  int32_t* order;            /* [n_tokens] */
+  int32_t* tiles;            /* [max_tiles][4], 16-byte aligned */
+} lora_plan_args;
+
+int32_t lora_tile(int64_t n_tokens);
+int64_t lora_max_tiles(int64_t n_tokens, int64_t n_adapters);
+int lora_plan(const lora_plan_args* args, void* stream);
+
+/*
+ * For every token t of the plan, with a its adapter, and every task:
+ *   y[t][n] += scale[a] * sum_{j < r} B[first + j][n] * (sum_k A[first + j][k] x[t][k]),
+ * n < N. Rows of tokens without an adapter stay as they are. The tasks (1 to
+ * QMV_LORA_MAX_TASKS: q|k|v, gate|up) share x, the plan, the table and the
+ * scales, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
+ * and ldx multiples of 8; y: [n_tokens][ldy] of y_type, as the projection left
+ * it (rows of 32-byte alignment are fastest). n_tokens, n_adapters and max_tiles
+ * are the plan's. max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
+ * chooses the kernel; an adapter may have rank 0.
+ * Products are exact and sums fp32; the r values between the two products are
+ * rounded to 2^-25 of themselves for an fp32 y (three bf16 parts) and to 2^-17
+ * for the others, and y once. The result is reproducible bit for bit, and a
+ * token's does not depend on the other tokens (the order of its sums goes by
+ * lora_tile and max_rank alone).
+ * A tile, place or adapter outside its array, a rank over max_rank or rows
+ * outside the pool set QMV_ERR_CORRUPT in the device error word, and that tile
+ * (or place) is left out.
+ */
+typedef struct {
+  const void* a;             /* bf16 [pool_rows][lda] */
+  const void* b;             /* bf16 [pool_rows][ldb] */
+  void* y;                   /* [n_tokens][ldy] of y_type */
+  int64_t lda, ldb, ldy;     /* lda and ldb multiples of 8 */
+  int32_t N, y_type;
+} lora_task;
+
+typedef struct {
+  const void* x;             /* bf16 [n_tokens][ldx] */
+  int64_t ldx;
+  int32_t K, n_tokens, n_adapters, max_tiles;
+  int32_t pool_rows, max_rank;
+  const int32_t* order;      /* [n_tokens] */
+  const int32_t* tiles;      /* [max_tiles][4] */
+  const int32_t* table;      /* [n_adapters][2] */
+  const float* scale;        /* [n_adapters] */
+} lora_args;
+
+int lora_run(const lora_args* args, const lora_task* tasks, int n_tasks, void* stream);
+
+/*
+ * Log probabilities of rows of logits x [n_rows][ldx] (x_type, base 16-byte
+ * aligned, rows of any stride ldx >= V): with z = scale * x (scale an inverse
+ * temperature, positive), lse = ln sum_i e^z_i and p_i = e^(z_i - lse),
+ *   logprob[t]     = z[tokens[t]] - lse[t]
+ *   rank[t]        = how many values come before the token's own in the order below
+ *   entropy[t]     = - sum_i p_i ln p_i  (0 ln 0 = 0)
+ *   top_index[t][j], top_logprob[t][j]: the first `top` of the row in that order.
+ * Order: larger x first, equal ones by the lower index; -0 equals +0 and a NaN
+ * ranks as -inf. lse, entropy, logprob and rank are nullable (the last two want
+ * tokens), top may be 0. A negative token gives logprob 0 and rank -1, one past V
+ * too, with QMV_ERR_CORRUPT in the device error word. -inf is a value of
+ * probability 0 (a masked token); a row of nothing else has lse and log
+ * probabilities -inf and entropy 0. A NaN or +inf in a row makes its lse,
+ * entropy and log probabilities NaN; its order stands.
+ * Sums are fp32, taken against the row's largest value. The result is
+ * reproducible bit for bit.
+ */
+#define QMV_LOGPROB_MAX_V 16777216
+#define QMV_LOGPROB_MAX_TOP 32
+
+typedef struct {
+  const void* x;             /* [n_rows][ldx] */
+  int64_t ldx;
+  int32_t x_type, n_rows, V, top;
+  float scale;
+  const int32_t* tokens;     /* [n_rows], nullable */
+  float* logprob;            /* [n_rows], nullable */
+  int32_t* rank;             /* [n_rows], nullable */
+  float* lse;                /* [n_rows], nullable */
+  float* entropy;            /* [n_rows], nullable */
+  int32_t* top_index;        /* [n_rows][top] */
+  float* top_logprob;        /* [n_rows][top] */
+} logprob_args;
+
+int logprob_run(const logprob_args* args, void* stream);
+
+/*
  * Packed-weight files ("Ternary Bonsai 2", section 3.6: the packed indices,
  * scales and flags are exported as the file that inference loads). A file
  * holds named packed matrices of any format above, each with its qmv_desc and

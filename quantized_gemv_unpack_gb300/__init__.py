@@ -28,7 +28,9 @@ QMV_FLAG_TEST_WAIT_TIMEOUT = 0x100           # qmv_desc.flags, testing only: the
 QMV_KV_PAGE, QMV_KV_MAX_REQUESTS = 64, 8192  # tokens of a cache page; requests of a step
 QMV_ROPE_MAX_PAIRS, QMV_ROPE_MAX_AXES = 128, 4
 QMV_KV_INT8, QMV_KV_E4M3 = 1, 2              # code types of the KV cache
-QMV_F32, QMV_BF16, QMV_F16 = 1, 2, 3         # activation types of the rope_* and kv8_* calls
+QMV_F32, QMV_BF16, QMV_F16 = 1, 2, 3         # activation types of the rope_*, kv8_*, lora_*, logprob_* calls and qmv_embed
+QMV_LORA_MAX_ADAPTERS, QMV_LORA_MAX_TOKENS, QMV_LORA_MAX_RANK, QMV_LORA_MAX_TASKS = 1024, 1048576, 128, 8
+QMV_LOGPROB_MAX_V, QMV_LOGPROB_MAX_TOP = 16777216, 32
 
 # the exported C symbols (one per declaration in include/qmv.h)
 EXPORTS = ("qmv_pack_desc", "qmv_pack_ternary", "qmv_pack_int4", "qmv_unpack", "qmv_run_ternary",
@@ -36,6 +38,7 @@ EXPORTS = ("qmv_pack_desc", "qmv_pack_ternary", "qmv_pack_int4", "qmv_unpack", "
            "cass_speculate_step", "moe_workspace_size", "moe_qmv_run", "moe_qmv_run_static",
            "kv8_desc", "kv_max_runs", "kv_plan", "rope_desc", "rope_run", "kv8_append", "kv8_read",
            "kv8_attend_workspace_size", "kv8_attend_init", "kv8_attend",
+           "qmv_embed", "lora_tile", "lora_max_tiles", "lora_plan", "lora_run", "logprob_run",
            "qmv_file_write", "qmv_file_open", "qmv_file_count", "qmv_file_tensor", "qmv_file_find", "qmv_file_load",
            "qmv_file_read_host", "qmv_file_close", "qmv_crc32", "qmv_check_status", "qmv_last_error")
 
@@ -97,6 +100,28 @@ class kv8_attend_args(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+class lora_plan_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_tokens", "n_adapters", "max_tiles")] + [
+        (n, ctypes.c_void_p) for n in ("ids", "order", "tiles")]
+
+
+class lora_task(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("a", "b", "y")] + [(n, ctypes.c_int64) for n in ("lda", "ldb", "ldy")] + [
+        ("N", ctypes.c_int32), ("y_type", ctypes.c_int32)]
+
+
+class lora_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("K", "n_tokens", "n_adapters", "max_tiles", "pool_rows", "max_rank")] + [
+        (n, ctypes.c_void_p) for n in ("order", "tiles", "table", "scale")]
+
+
+class logprob_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("x_type", "n_rows", "V", "top")] + [("scale", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("tokens", "logprob", "rank", "lse", "entropy", "top_index", "top_logprob")]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -133,6 +158,12 @@ _SIGS = {
     "kv8_attend_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(qmv_kv_desc)]),
     "kv8_attend_init": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.c_size_t, _P]),
     "kv8_attend": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.POINTER(kv8_attend_args), _P]),
+    "qmv_embed": (_I32, [_DESC, _P, _P, _I64, ctypes.c_float, _P, _I32, _I64, _P]),
+    "lora_tile": (ctypes.c_int32, [_I64]),
+    "lora_max_tiles": (_I64, [_I64, _I64]),
+    "lora_plan": (_I32, [ctypes.POINTER(lora_plan_args), _P]),
+    "lora_run": (_I32, [ctypes.POINTER(lora_args), ctypes.POINTER(lora_task), _I32, _P]),
+    "logprob_run": (_I32, [ctypes.POINTER(logprob_args), _P]),
     "qmv_file_write": (_I32, [ctypes.c_char_p, _I32, ctypes.POINTER(ctypes.c_char_p), _DESC, ctypes.POINTER(_P)]),
     "qmv_file_open": (_I32, [ctypes.c_char_p, ctypes.POINTER(_P)]),
     "qmv_file_count": (_I32, [_P]),
@@ -646,6 +677,141 @@ class KvAttend:
             self.workspace.record_stream(torch.cuda.ExternalStream(s, device=self.workspace.device))
             self._streams.add(s)
 
+
+# ----------------------------------------------------------------------------- around the projections of a step
+
+def _matrix(name, t, rows, cols, device):
+    """(address, row stride) of a [rows][cols] tensor whose rows lie in one piece each (None: any extent)."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({rows}, {cols})")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must lie side by side (strides {t.stride()})")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {t.stride()})")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else (max(t.shape[1], t.stride(0)) + 7) // 8 * 8
+
+
+class Embed:
+    """qmv_embed: rows `tokens` [n] (int32) of a packed ternary or INT4 matrix, times scale, into out [n][K]."""
+
+    def __init__(self, desc: qmv_desc, packed, tokens, out, scale: float = 1.0):
+        import torch
+        dev = out.device
+        n = tokens.shape[0]
+        op, ldo = _matrix("out", out, n, desc.K, dev)
+        if packed.dtype != torch.uint8 or not packed.is_contiguous() or packed.numel() < desc.total_bytes or packed.device != dev:
+            raise ValueError(f"packed: a contiguous uint8 tensor of at least {desc.total_bytes} bytes on {dev} expected")
+        _ints("tokens", tokens, (n,), dev)
+        self.keep = (desc, packed, tokens, out)
+        self._call = lib().qmv_embed
+        self._args = _ready(self._call, ctypes.byref(desc), packed.data_ptr(), tokens.data_ptr(), n, scale, op, _dtype(out), ldo)
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
+
+def qmv_embed(desc: qmv_desc, packed, tokens, out, scale: float = 1.0, stream=None):
+    """One call of Embed(...).run()."""
+    Embed(desc, packed, tokens, out, scale).run(stream)
+
+
+def lora_tile(n_tokens: int) -> int:
+    return int(lib().lora_tile(n_tokens))
+
+
+def lora_max_tiles(n_tokens: int, n_adapters: int) -> int:
+    return int(lib().lora_max_tiles(n_tokens, n_adapters))
+
+
+class LoraPlan:
+    """lora_plan: a step's tokens grouped by adapter. ids [tokens] (int32): each token's adapter, negative for none. run()
+    fills order [tokens] and tiles [max_tiles][4], which the Lora calls of all layers of the step read."""
+
+    def __init__(self, ids, n_adapters: int):
+        import torch
+        dev = ids.device
+        T = ids.shape[0]
+        self.ids, self.n_adapters = _ints("ids", ids, (T,), dev), n_adapters
+        max_tiles = lora_max_tiles(T, n_adapters)
+        self.order = torch.empty(T, dtype=torch.int32, device=dev)
+        self.tiles = torch.empty((max_tiles, 4), dtype=torch.int32, device=dev)
+        a = self.args = lora_plan_args(T, n_adapters, max_tiles, ids.data_ptr(), self.order.data_ptr(), self.tiles.data_ptr())
+        self._call, self._args = lib().lora_plan, ctypes.byref(a)
+
+    def run(self, stream=None):
+        _check(self._call(self._args, _stream(stream)))
+
+
+class Lora:
+    """lora_run: each token's adapter added to the outputs of projections that share x [tokens][K] (bf16). table [adapters][2]
+    (int32): an adapter's first rank row and its rank; scale [adapters] (fp32). tasks: (a, b, y) per projection: the pools of
+    rank rows a [rows][K] and b [rows][N] (bf16), and y [tokens][N], to which the projection has written. max_rank bounds
+    the ranks in the table; a lower bound gives a leaner kernel. The plan's run() comes first, once per step."""
+
+    def __init__(self, plan: LoraPlan, table, scale, x, tasks, max_rank: int = QMV_LORA_MAX_RANK):
+        import torch
+        dev = x.device
+        T, A = plan.ids.shape[0], plan.n_adapters
+        if x.dtype != torch.bfloat16:
+            raise TypeError(f"x: bfloat16 expected, got {x.dtype}")
+        g = self.args = lora_args()
+        g.x, g.ldx = _matrix("x", x, T, None, dev)
+        g.K, g.n_tokens, g.n_adapters, g.max_rank = x.shape[1], T, A, max_rank
+        if plan.ids.device != dev:
+            raise ValueError(f"plan: on {plan.ids.device}, expected {dev}")
+        if scale.dtype != torch.float32 or tuple(scale.shape) != (A,) or not scale.is_contiguous() or scale.device != dev:
+            raise ValueError(f"scale: a contiguous float32 tensor of shape ({A},) on {dev} expected")
+        g.order, g.tiles, g.max_tiles = plan.order.data_ptr(), plan.tiles.data_ptr(), plan.tiles.shape[0]
+        g.table, g.scale = _ints("table", table, (A, 2), dev).data_ptr(), scale.data_ptr()
+        tasks = [tuple(t) for t in tasks]
+        if not tasks:
+            raise ValueError("no tasks")
+        g.pool_rows = rows = tasks[0][0].shape[0]
+        self.tasks = (lora_task * len(tasks))()
+        for i, (a, b, y) in enumerate(tasks):
+            if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+                raise TypeError(f"task {i}: a and b must be bfloat16")
+            k = self.tasks[i]
+            k.a, k.lda = _matrix(f"task {i}: a", a, rows, x.shape[1], dev)
+            k.b, k.ldb = _matrix(f"task {i}: b", b, rows, None, dev)
+            k.y, k.ldy = _matrix(f"task {i}: y", y, T, b.shape[1], dev)
+            k.N, k.y_type = b.shape[1], _dtype(y)
+        self.keep = (plan, table, scale, x, tasks)
+        self._call, self._args = lib().lora_run, (ctypes.byref(g), self.tasks, len(tasks))
+
+    def run(self, stream=None):
+        _check(self._call(*self._args, _stream(stream)))
+
+
+class LogProb:
+    """logprob_run: log probabilities of logits [rows][V] (fp32, bf16 or fp16), times scale. run() fills lse and entropy
+    [rows], with tokens [rows] (int32) logprob and rank [rows], with top (up to 32) top_index and top_logprob [rows][top]."""
+
+    def __init__(self, logits, tokens=None, top: int = 0, scale: float = 1.0):
+        import torch
+        dev = logits.device
+        T, V = logits.shape
+        a = self.args = logprob_args()
+        a.x, a.ldx = _matrix("logits", logits, None, None, dev)
+        a.x_type, a.n_rows, a.V, a.top, a.scale = _dtype(logits), T, V, top, scale
+        new = lambda kind, *shape: torch.empty(shape, dtype=kind, device=dev)  # noqa: E731
+        self.lse, self.entropy = new(torch.float32, T), new(torch.float32, T)
+        self.logprob = self.rank = self.top_index = self.top_logprob = None
+        if tokens is not None:
+            a.tokens = _ints("tokens", tokens, (T,), dev).data_ptr()
+            self.logprob, self.rank = new(torch.float32, T), new(torch.int32, T)
+        if top > 0:
+            self.top_index, self.top_logprob = new(torch.int32, T, top), new(torch.float32, T, top)
+        for n in ("lse", "entropy", "logprob", "rank", "top_index", "top_logprob"):
+            if getattr(self, n) is not None:
+                setattr(a, n, getattr(self, n).data_ptr())
+        self.keep = (logits, tokens)
+        self._call, self._args = lib().logprob_run, ctypes.byref(a)
+
+    def run(self, stream=None):
+        _check(self._call(self._args, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- packed-weight files
