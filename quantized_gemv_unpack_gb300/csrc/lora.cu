@@ -164,13 +164,14 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
 constexpr int kCluster = 8;    // blocks of a tile: the largest cluster that every device of this kind schedules
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
+constexpr int kHalfSm = 112 * 1024;   // shared memory of a block of which two fit an SM
 
 struct Task {
   const __nv_bfloat16* a;
   const __nv_bfloat16* b;
   void* y;
   int64_t lda, ldb, ldy;
-  int32_t N, y_type;
+  int32_t N;
   int32_t wide;                // rows of y are 32-byte aligned
 };
 
@@ -182,7 +183,7 @@ struct RunArgs {
   const float* scale;
   int* err;
   int64_t ldx;
-  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks;
+  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks, n_stages, cluster, tile, window;
   Task t[QMV_LORA_MAX_TASKS];
 };
 
@@ -209,7 +210,17 @@ __device__ __forceinline__ float4 ld_remote(uint32_t p) {
 __device__ __forceinline__ void st_remote(uint32_t p, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ uint4 ld_once(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
+// Sixteen bytes from memory to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint32_t to, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest n groups of this thread's copies are there.
+__device__ __forceinline__ void copies_wait(int n) {
+  if (n <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -224,12 +235,14 @@ __device__ __forceinline__ uint32_t split(float& x, float& y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ float2 unpack2(int type, uint32_t w) {
-  if (type == QMV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+template <int Y>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (Y == QMV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-__device__ __forceinline__ uint32_t pack2(int type, float x, float y) {
-  if (type == QMV_BF16) {
+template <int Y>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (Y == QMV_BF16) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
   }
@@ -237,49 +250,72 @@ __device__ __forceinline__ uint32_t pack2(int type, float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight consecutive values of a row of y, as they lie in memory: 32 bytes (fp32, one 256-bit access) or 16.
-__device__ __forceinline__ void ld_row(int type, const void* p, uint32_t (&w)[8]) {
-  if (type == QMV_F32) {
+// A lane's consecutive values of a row of y, `words` 32-bit words: 4 or 8.
+template <int WORDS>
+__device__ __forceinline__ void ld_shared(const unsigned char* p, uint32_t (&w)[WORDS]) {
+#pragma unroll
+  for (int i = 0; i < WORDS; i += 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p + 4 * i);
+    w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+  }
+}
+// BL columns of a row of B.
+__device__ __forceinline__ void ld_columns(const unsigned char* p, uint32_t (&w)[2]) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  w[0] = u.x, w[1] = u.y;
+}
+__device__ __forceinline__ void ld_columns(const unsigned char* p, uint32_t (&w)[4]) { ld_shared(p, w); }
+template <int WORDS>
+__device__ __forceinline__ void ld_global(const void* p, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 8) {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p)
-                 : "memory");
+                 : "l"(p));
   } else {
-    const uint4 v = *static_cast<const uint4*>(p);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    const uint4 u = *static_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
 }
-// w += s * v, to memory. v: the sums of the eight columns, block by block (column c is block c % 4, half c / 4).
-template <int HI>
-__device__ __forceinline__ void add_row(int type, void* p, float s, const float (&acc)[4][4], uint32_t (&w)[8]) {
-  if (type == QMV_F32) {
-#pragma unroll
-    for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(fmaf(s, acc[c & 3][2 * HI + (c >> 2)], __uint_as_float(w[c])));
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+template <int WORDS>
+__device__ __forceinline__ void st_global(void* p, const uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 8)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
                  : "memory");
-  } else {
-    uint32_t o[4];
+  else
+    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The sum of column c of the 2 * BLOCKS that a lane has of row HI (g or g + 8): block c % BLOCKS, half c / BLOCKS.
+template <int HI, int BLOCKS>
+__device__ __forceinline__ float column(const float (&d)[BLOCKS][4], int c) {
+  return d[c % BLOCKS][2 * HI + c / BLOCKS];
+}
+// y += s * d over a lane's columns, whose values are w.
+template <int Y, int HI, int BLOCKS, int WORDS>
+__device__ __forceinline__ void add_row(void* p, float s, const float (&d)[BLOCKS][4], uint32_t (&w)[WORDS]) {
+  if constexpr (Y == QMV_F32) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = 2 * i;
-      const float2 v = unpack2(type, w[i]);
-      o[i] = pack2(type, fmaf(s, acc[c & 3][2 * HI + (c >> 2)], v.x), fmaf(s, acc[(c + 1) & 3][2 * HI + ((c + 1) >> 2)], v.y));
+    for (int c = 0; c < WORDS; ++c) w[c] = __float_as_uint(fmaf(s, column<HI>(d, c), __uint_as_float(w[c])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      const float2 v = unpack2<Y>(w[i]);
+      w[i] = pack2<Y>(fmaf(s, column<HI>(d, 2 * i), v.x), fmaf(s, column<HI>(d, 2 * i + 1), v.y));
     }
-    *static_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
   }
+  st_global(p, w);
 }
-// The same value by value, up to column n of the row.
-template <int HI>
-__device__ __forceinline__ void add_row_part(int type, void* p, int n, float s, const float (&acc)[4][4]) {
+// The same value by value, up to column n of them.
+template <int Y, int HI, int BLOCKS>
+__device__ __forceinline__ void add_row_part(void* p, int n, float s, const float (&d)[BLOCKS][4]) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
+  for (int c = 0; c < 2 * BLOCKS; ++c) {
     if (c >= n) break;
-    const float v = acc[c & 3][2 * HI + (c >> 2)];
-    if (type == QMV_F32) {
+    const float v = column<HI>(d, c);
+    if constexpr (Y == QMV_F32) {
       float* q = static_cast<float*>(p) + c;
       *q = fmaf(s, v, *q);
-    } else if (type == QMV_BF16) {
+    } else if constexpr (Y == QMV_BF16) {
       __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + c;
       *q = __float2bfloat16_rn(fmaf(s, v, __bfloat162float(*q)));
     } else {
@@ -289,36 +325,51 @@ __device__ __forceinline__ void add_row_part(int type, void* p, int n, float s, 
   }
 }
 
-// MT 16-token blocks per tile, NB blocks of eight rank rows (the call's largest rank).
-template <int MT, int NB>
+// MT 16-token blocks per tile, NB blocks of eight rank rows (the call's largest rank), y in fp32 or in 16 bits.
+template <int MT, int NB, int Y>
 struct Shape {
+  static constexpr bool F32 = Y == QMV_F32;
+  static constexpr int kBlocks = MT > 1 && !F32 ? 8 : 4;      // n8 blocks of a warp in a stage of the second product
+  static constexpr int kParts3 = F32 ? 3 : 2;                 // bf16 parts of the values between the products
   static constexpr int kSteps = NB / 2;                       // k16 steps of the second product
   static constexpr int kShare = kLoraWarps / MT;              // warps that share a 16-token block
   static constexpr int kHalves = NB > 8 ? 2 : 1;              // in the first product a warp has at most 64 rank rows
   static constexpr int kParts = kShare / kHalves;             // and a share of the columns of x
   static constexpr int kWords = MT * kSteps * 2 * 32;         // 16-byte words of the tile's r values, in the order of the fragments
-  static constexpr int kSums = kParts > 2 ? kParts : 2;       // room for the warps' sums, then for the three parts of their total
-  static constexpr size_t kSmem = (size_t)(kSums + 1) * kWords * 16 + 16 * MT * sizeof(int);
+  static constexpr int kCols1 = 32 * kParts, kCols2 = 8 * kBlocks * kShare;   // columns of a stage of either product
+  static constexpr int kRowB = kCols2 * 2 + 16;               // bytes of a row of B in a stage: 16 more keep a warp's reads apart
+  static constexpr int kRowsB = 8 * NB;
+  static constexpr bool kStageY = MT > 1;                     // y goes through the stages too (few tokens: through registers)
+  static constexpr int kRowY = kCols2 * (F32 ? 4 : 2) + 16;
+  static constexpr int kFixed = kWords * 16 * (2 + kParts3) / 2 + 16 * MT * (int)sizeof(int);
+  // pieces of 16 bytes: threads side by side take a row's, then the next row's
+  static constexpr int kPer1 = kCols1 / 8, kPer2 = kCols2 / 8, kRows1 = kLoraThreads / kPer1, kRows2 = kLoraThreads / kPer2;
+  static constexpr int kTurnsX = 16 * MT / kRows1, kTurnsA = (8 * NB + kRows1 - 1) / kRows1, kTurnsB = (8 * NB + kRows2 - 1) / kRows2,
+                       kTurnsY = 16 * MT / kRows2;
+  static constexpr int kFirst = (16 * MT + 8 * NB) * kCols1 * 2, kSecond = kRowsB * kRowB + (kStageY ? 16 * MT * kRowY : 0),
+                       kSums = (MT == 1 ? kParts : kParts - 1) * kWords * 16;
+  static constexpr int kStage = kFirst > kSecond ? (kFirst > kSums ? kFirst : kSums) : (kSecond > kSums ? kSecond : kSums);
 };
-constexpr int kAhead = 2;                                     // k16 steps of B in flight
 
-template <int MT, int NB>
+template <int MT, int NB, int Y>
 __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(const __grid_constant__ RunArgs a) {
-  using S = Shape<MT, NB>;
-  constexpr int KS = S::kSteps, W = S::kWords, RB = NB / S::kHalves;
-  extern __shared__ uint4 lora_smem[];
-  float4* sums = reinterpret_cast<float4*>(lora_smem);        // [kParts][W]: the warps' sums
-  uint4* frag = lora_smem;                                    // [MT][KS][3][32], after them: the three parts of the finished values
-  float4* mine = sums + S::kSums * W;                        // [W]: this block's sums, which the cluster reads
-  int* token = reinterpret_cast<int*>(mine + W);              // [16 * MT]
+  using S = Shape<MT, NB, Y>;
+  constexpr int KS = S::kSteps, W = S::kWords, RB = NB / S::kHalves, BL = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2;
+  constexpr bool F32 = S::F32;
+  extern __shared__ __align__(16) unsigned char lora_smem[];
+  float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
+  uint4* frag = reinterpret_cast<uint4*>(mine + W);           // [MT][KS][P3][32]: the parts of the finished values
+  int* token = reinterpret_cast<int*>(frag + W * P3 / 2);      // [16 * MT]
+  unsigned char* stages = lora_smem + S::kFixed;              // [n_stages][stage_bytes]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int mb = warp % MT, share = warp / MT;                // this warp's 16-token block, its share of columns
   const int half = share % S::kHalves, part = share / S::kHalves;
-  const int rank = (int)cluster_rank();
-  const int clusters = gridDim.x / kCluster;
+  const int rank = (int)cluster_rank(), C = a.cluster;
+  const int clusters = gridDim.x / C, n_stages = a.n_stages;
+  const uint32_t stages_at = (uint32_t)__cvta_generic_to_shared(stages);
   follow_previous();
   bool reading = false;                                       // other blocks may still read `mine`
-  for (int unit = blockIdx.x / kCluster; unit < a.max_tiles * a.n_tasks; unit += clusters) {
+  for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
     const Task& t = a.t[unit / a.max_tiles];
     const int4 tile = a.tiles[unit % a.max_tiles];
     if (tile.z == 0) continue;
@@ -336,7 +387,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
     }
     if (r == 0) continue;
     const int count = tile.z;
-    __syncthreads();                                          // the unit before this one is done with token and frag
+    __syncthreads();                                          // the unit before this one is done with token, frag and the stages
     if (tid < 16 * MT) {
       int k = -1;
       if (tid < count) {
@@ -352,65 +403,162 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
     const bool mine_used = mb * 16 < count;                   // false: this warp's tokens are none
     const int tok0 = token[mb * 16 + g], tok1 = token[mb * 16 + g + 8];
 
-    // ---- first product, over this block's share of K
+    // this block's columns of both products, and the stages that they take
+    const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 8 * BL - 1) / (C * 8 * BL) * (8 * BL);
+    const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
+    const int n1 = k_hi > k_lo ? (k_hi - k_lo + S::kCols1 - 1) / S::kCols1 : 0, n2 = n_hi > n_lo ? (n_hi - n_lo + S::kCols2 - 1) / S::kCols2 : 0;
+
+    // this thread's pieces of the stages: rows of x and A, then rows of B and y
+    const int c1 = tid % S::kPer1, r1 = tid / S::kPer1, c2 = tid % S::kPer2, r2 = tid / S::kPer2;
+    const uint32_t to1 = (r1 * S::kPer1 + (S::kPer1 > 4 ? c1 ^ ((r1 & 1) << 2) : c1)) * 16, to2 = r2 * S::kRowB + c2 * 16;
+    int k_next = k_lo + 8 * c1, n_next = n_lo + 8 * c2;
+    const __nv_bfloat16* px[S::kTurnsX];
+#pragma unroll
+    for (int i = 0; i < S::kTurnsX; ++i) {
+      const int tok = token[r1 + i * S::kRows1];
+      px[i] = tok < 0 ? nullptr : a.x + (int64_t)tok * a.ldx + k_next;
+    }
+    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + k_next;
+    const __nv_bfloat16* pb = t.b + (int64_t)(row0 + r2) * t.ldb + n_next;
+    const char* py[S::kStageY ? S::kTurnsY : 1];
+    if constexpr (S::kStageY) {
+#pragma unroll
+      for (int i = 0; i < S::kTurnsY; ++i) {
+        const int tok = token[r2 + i * S::kRows2];
+        py[i] = tok < 0 || !t.wide ? nullptr : static_cast<const char*>(t.y) + ((int64_t)tok * t.ldy + n_next) * size;
+      }
+    }
+    const int64_t step_a = S::kRows1 * t.lda, step_b = S::kRows2 * t.ldb;
+    int to_begin = 0, slot_in = 0, slot_out = 0;              // the next stage to begin, its place; the place of the next to read
+    // Begins the copies of a stage. Rows past the rank and tokens that are none are not copied: their readers take 0.
+    const auto load = [&]() {
+      const uint32_t at = stages_at + slot_in * S::kStage;
+      if (to_begin < n1) {
+        if (k_next < k_hi) {
+#pragma unroll
+          for (int i = 0; i < S::kTurnsX; ++i)
+            if (px[i]) copy16(at + to1 + i * (S::kRows1 * S::kPer1 * 16), px[i] + (k_next - k_lo - 8 * c1));
+          const __nv_bfloat16* p = pa + (k_next - k_lo - 8 * c1);
+#pragma unroll
+          for (int i = 0; i < S::kTurnsA; ++i, p += step_a) {
+            if (r1 + i * S::kRows1 >= r) break;
+            copy16(at + to1 + (16 * MT + i * S::kRows1) * (S::kPer1 * 16), p);
+          }
+        }
+        k_next += S::kCols1;
+      } else if (to_begin < n1 + n2) {
+        if (n_next < n_hi) {
+          const int off = n_next - n_lo - 8 * c2;
+          const __nv_bfloat16* p = pb + off;
+          if (n_next + 8 <= t.N) {
+#pragma unroll
+            for (int i = 0; i < S::kTurnsB; ++i, p += step_b) {
+              if (r2 + i * S::kRows2 >= r) break;
+              copy16(at + to2 + i * (S::kRows2 * S::kRowB), p);
+            }
+            if constexpr (S::kStageY) {
+              const uint32_t to = at + S::kRowsB * S::kRowB + r2 * S::kRowY + 8 * c2 * size;
+#pragma unroll
+              for (int i = 0; i < S::kTurnsY; ++i)
+                if (py[i]) {
+                  copy16(to + i * S::kRows2 * S::kRowY, py[i] + off * size);
+                  if constexpr (F32) copy16(to + i * S::kRows2 * S::kRowY + 16, py[i] + off * size + 16);
+                }
+            }
+          } else {                                            // the rows' last values, one by one
+            for (int i = 0; i < S::kTurnsB; ++i, p += step_b) {
+              if (r2 + i * S::kRows2 >= r) break;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
+              uint16_t* d = reinterpret_cast<uint16_t*>(stages + slot_in * S::kStage + to2 + i * (S::kRows2 * S::kRowB));
+              for (int c = 0; c < 8; ++c) d[c] = n_next + c < t.N ? v[c] : (uint16_t)0;
+            }
+          }
+        }
+        n_next += S::kCols2;
+      }
+      copies_end();
+      ++to_begin;
+      if (++slot_in == n_stages) slot_in = 0;
+    };
+    for (int q = 0; q < n_stages - 1; ++q) load();
+
+    // ---- first product
     float acc[RB][4];
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     const int j0 = half * 8 * RB;                             // this warp's first rank row
-    if (mine_used && j0 < r) {
-      const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
-      const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
-      const __nv_bfloat16* pa = t.a + (int64_t)(row0 + j0 + g) * t.lda;
-      const int64_t step = 8 * t.lda;
-      for (int k0 = (rank * S::kParts + part) * 32; k0 < a.K; k0 += kCluster * S::kParts * 32) {
-        const int k = k0 + 8 * t4;
-        const bool in = k < a.K;
-        uint4 p = make_uint4(0, 0, 0, 0), q = p, w[RB];
-        if (in && tok0 >= 0) p = ld_once(x0 + k);
-        if (in && tok1 >= 0) q = ld_once(x1 + k);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (in && j0 + 8 * i + g < r) w[i] = ld_once(pa + i * step + k);
-        }
+    for (int q = 0; q < n1; ++q) {
+      copies_wait(n_stages - 2);
+      __syncthreads();                                        // stage q is there, and q - 1 has been read
+      load();
+      // this warp's 32 columns; columns past K were not copied
+      const int left = k_hi - (k_lo + q * S::kCols1 + part * 32);
+      if (mine_used && j0 < r && left > 0) {
+        const int piece = part * 4 + t4;
+        const unsigned char* st = stages + slot_out * S::kStage + g * (S::kPer1 * 16) + (S::kPer1 > 4 ? piece ^ ((g & 1) << 2) : piece) * 16;
+        const bool in = 8 * t4 < left;
+        uint4 p = make_uint4(0, 0, 0, 0), o = p;
+        if (in && tok0 >= 0) p = *reinterpret_cast<const uint4*>(st + (mb * 16) * (S::kPer1 * 16));
+        if (in && tok1 >= 0) o = *reinterpret_cast<const uint4*>(st + (mb * 16 + 8) * (S::kPer1 * 16));
 #pragma unroll
         for (int i = 0; i < RB; ++i) {
           if (j0 + 8 * i >= r) break;
-          mma(acc[i], p.x, q.x, p.y, q.y, w[i].x, w[i].y);
-          mma(acc[i], p.z, q.z, p.w, q.w, w[i].z, w[i].w);
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (in && j0 + 8 * i + g < r) w = *reinterpret_cast<const uint4*>(st + (16 * MT + j0 + 8 * i) * (S::kPer1 * 16));
+          mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
+          mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
         }
       }
+      if (++slot_out == n_stages) slot_out = 0;
     }
-    float4* to = sums + ((part * MT + mb) * S::kHalves + half) * RB * 32 + lane;
+    // the sums of the block's warps, by way of the stage that comes free
+    __syncthreads();
+    float4* sums = reinterpret_cast<float4*>(stages + slot_in * S::kStage);
+    const int own = (mb * S::kHalves + half) * RB * 32 + lane;
+    if (MT == 1 || part > 0) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i) to[i * 32] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      for (int i = 0; i < RB; ++i) sums[(MT == 1 ? part : part - 1) * W + own + i * 32] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    }
     __syncthreads();
     if (reading) cluster_wait();
-    for (int i = tid; i < W; i += kLoraThreads) {
-      float4 v = sums[i];
+    if constexpr (MT == 1) {
+      for (int i = tid; i < W; i += kLoraThreads) {
+        float4 v = sums[i];
 #pragma unroll
-      for (int p = 1; p < S::kParts; ++p) {
-        const float4 o = sums[p * W + i];
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        for (int p = 1; p < S::kParts; ++p) {
+          const float4 o = sums[p * W + i];
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        mine[i] = v;
       }
-      mine[i] = v;
+    } else if (part == 0) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+#pragma unroll
+        for (int p = 1; p < S::kParts; ++p) {
+          const float4 o = sums[(p - 1) * W + own + i * 32];
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        mine[own + i * 32] = v;
+      }
     }
     cluster_arrive();
     cluster_wait();
 
     // ---- the cluster's sums: item i is a lane's eight values of one k16 step
-    const auto finish = [&](int i, uint4 (&f)[3]) {
+    const auto finish = [&](int i, uint4 (&f)[P3]) {
       const int at = (i / 32) * 64 + i % 32;
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-#pragma unroll
-      for (int c = 0; c < kCluster; ++c) {
+#pragma unroll 8
+      for (int c = 0; c < C; ++c) {
         const uint32_t p = remote(mine + at, c);
-        const float4 o = ld_remote(p), q = ld_remote(p + 32 * 16);
+        const float4 o = ld_remote(p), w = ld_remote(p + 32 * 16);
         u.x += o.x, u.y += o.y, u.z += o.z, u.w += o.w;
-        v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
       }
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
+      for (int k = 0; k < P3; ++k) {
         f[k].x = split(u.x, u.y);
         f[k].y = split(u.z, u.w);
         f[k].z = split(v.x, v.y);
@@ -420,108 +568,417 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
     if constexpr (MT == 1) {
       // few values: every block takes all of them
       for (int i = tid; i < W / 2; i += kLoraThreads) {
-        uint4 f[3];
+        uint4 f[P3];
         finish(i, f);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) frag[((i / 32) * 3 + k) * 32 + i % 32] = f[k];
+        for (int k = 0; k < P3; ++k) frag[((i / 32) * P3 + k) * 32 + i % 32] = f[k];
       }
       cluster_arrive();
       reading = true;
-      __syncthreads();
     } else {
-      // each block finishes an eighth and hands it to all
-      for (int i = rank * (W / 16) + tid; i < (rank + 1) * (W / 16); i += kLoraThreads) {
-        uint4 f[3];
+      // each block finishes its share and hands it to all
+      for (int i = rank * (W / 2 / C) + tid; i < (rank + 1) * (W / 2 / C); i += kLoraThreads) {
+        uint4 f[P3];
         finish(i, f);
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int c = 0; c < kCluster; ++c)
-#pragma unroll
-          for (int k = 0; k < 3; ++k) st_remote(remote(frag + ((i / 32) * 3 + k) * 32 + i % 32, c), f[k]);
+          for (int k = 0; k < P3; ++k) st_remote(remote(frag + ((i / 32) * P3 + k) * 32 + i % 32, c), f[k]);
       }
       cluster_arrive();
       cluster_wait();
     }
-    if (!mine_used) continue;
 
-    // ---- second product, over this block's share of N: 32 columns at a time
-    const int type = t.y_type, size = type == QMV_F32 ? 4 : 2;
-    const bool third = type == QMV_F32;
+    // ---- second product, 8 * BL columns of a stage per warp
     char* y0 = static_cast<char*>(t.y) + (int64_t)(tok0 < 0 ? 0 : tok0) * t.ldy * size;
     char* y1 = static_cast<char*>(t.y) + (int64_t)(tok1 < 0 ? 0 : tok1) * t.ldy * size;
-    const uint4* h = frag + mb * KS * 96 + lane;
-    for (int n0 = (rank * S::kShare + share) * 32; n0 < t.N; n0 += kCluster * S::kShare * 32) {
-      const int n = n0 + 8 * t4, col = n0 + 4 * g;            // first column of this lane's sums, and of its loads of B
-      const bool whole = t.wide && n + 8 <= t.N;
-      uint32_t v0[8], v1[8];
-      if (whole && tok0 >= 0) ld_row(type, y0 + (int64_t)n * size, v0);
-      if (whole && tok1 >= 0) ld_row(type, y1 + (int64_t)n * size, v1);
-      float d[4][4];
+    const uint4* h = frag + mb * (KS * P3 * 32) + lane;
+    constexpr int LC = 2 * BL, WORDS = LC * size / 4;         // columns of a lane, and their words
+    uint32_t v0[WORDS], v1[WORDS];                            // few tokens: this stage's values of y
+    const auto ahead = [&](int n0) {
+      const int n = n0 + LC * t4;
+      if (t.wide && n0 < n_hi && n + LC <= t.N) {
+        if (tok0 >= 0) ld_global(y0 + (int64_t)n * size, v0);
+        if (tok1 >= 0) ld_global(y1 + (int64_t)n * size, v1);
+      }
+    };
+    if constexpr (!S::kStageY) ahead(n_lo + share * (8 * BL));
+    for (int q = 0; q < n2; ++q) {
+      copies_wait(n_stages - 2);
+      __syncthreads();                                        // the stage is there, and the one before it (or the sums) has been read
+      load();
+      const unsigned char* st = stages + slot_out * S::kStage;
+      if (++slot_out == n_stages) slot_out = 0;
+      const int n0 = n_lo + q * S::kCols2 + share * (8 * BL);
+      if (!mine_used || n0 >= n_hi) continue;
+      float d[BL][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-      const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
+      for (int i = 0; i < BL; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+      const unsigned char* sb = st + 2 * t4 * S::kRowB + (share * (8 * BL) + BL * g) * 2;
 #pragma unroll
-      for (int s0 = 0; s0 < KS; s0 += kAhead) {
-        if (16 * s0 >= r) break;
-        uint2 w[kAhead][4];
+      for (int s = 0; s < KS; ++s) {
+        if (16 * s >= r) break;
+        uint32_t b[BL][2];
+        const bool full = 16 * s + 16 <= r;
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e)
+        for (int i = 0; i < 2; ++i) {
+          const int j = 16 * s + 8 * i;
+          uint32_t u[BL / 2], v[BL / 2];                      // rows j + 2 t4 and the next of BL columns
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int off = 16 * (s0 + e) + (i & 1) + 8 * (i >> 1);
-            w[e][i] = make_uint2(0, 0);
-            if (s0 + e < KS && off + 2 * t4 < r && col < t.N) {
-              const __nv_bfloat16* p = pb + (int64_t)off * t.ldb;
-              if (col + 4 <= t.N) {
-                w[e][i] = __ldg(reinterpret_cast<const uint2*>(p));
-              } else {
-                const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
-                w[e][i].x = q[0] | (col + 1 < t.N ? (uint32_t)q[1] << 16 : 0u);
-                w[e][i].y = col + 2 < t.N ? q[2] : 0u;
-              }
-            }
-          }
+          for (int c = 0; c < BL / 2; ++c) u[c] = v[c] = 0u;
+          if (full || j + 2 * t4 < r) ld_columns(sb + j * S::kRowB, u);
+          if (full || j + 2 * t4 + 1 < r) ld_columns(sb + (j + 1) * S::kRowB, v);
 #pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-          if (s0 + e >= KS || 16 * (s0 + e) >= r) break;
-          uint32_t b[4][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            b[0][i] = __byte_perm(w[e][2 * i].x, w[e][2 * i + 1].x, 0x5410);
-            b[1][i] = __byte_perm(w[e][2 * i].x, w[e][2 * i + 1].x, 0x7632);
-            b[2][i] = __byte_perm(w[e][2 * i].y, w[e][2 * i + 1].y, 0x5410);
-            b[3][i] = __byte_perm(w[e][2 * i].y, w[e][2 * i + 1].y, 0x7632);
-          }
-          if (third) {
-            const uint4 f = h[(s0 + e) * 96 + 64];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
-          }
-#pragma unroll
-          for (int k = 1; k >= 0; --k) {
-            const uint4 f = h[(s0 + e) * 96 + 32 * k];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
+          for (int c = 0; c < BL / 2; ++c) {
+            b[2 * c][i] = __byte_perm(u[c], v[c], 0x5410);
+            b[2 * c + 1][i] = __byte_perm(u[c], v[c], 0x7632);
           }
         }
+#pragma unroll
+        for (int k = P3 - 1; k >= 0; --k) {
+          const uint4 f = h[(s * P3 + k) * 32];
+#pragma unroll
+          for (int i = 0; i < BL; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
+        }
       }
-      if (whole) {
-        if (tok0 >= 0) add_row<0>(type, y0 + (int64_t)n * size, scale, d, v0);
-        if (tok1 >= 0) add_row<1>(type, y1 + (int64_t)n * size, scale, d, v1);
+      const int n = n0 + LC * t4;                             // first column of this lane's sums
+      if (t.wide && n + LC <= t.N) {
+        const unsigned char* sy = st + S::kRowsB * S::kRowB + (mb * 16 + g) * S::kRowY + (share * (8 * BL) + LC * t4) * size;
+        if (tok0 >= 0) {
+          if constexpr (S::kStageY) ld_shared(sy, v0);
+          add_row<Y, 0>(y0 + (int64_t)n * size, scale, d, v0);
+        }
+        if (tok1 >= 0) {
+          if constexpr (S::kStageY) ld_shared(sy + 8 * S::kRowY, v1);
+          add_row<Y, 1>(y1 + (int64_t)n * size, scale, d, v1);
+        }
       } else {
-        if (tok0 >= 0) add_row_part<0>(type, y0 + (int64_t)n * size, t.N - n, scale, d);
-        if (tok1 >= 0) add_row_part<1>(type, y1 + (int64_t)n * size, t.N - n, scale, d);
+        if (tok0 >= 0) add_row_part<Y, 0>(y0 + (int64_t)n * size, t.N - n, scale, d);
+        if (tok1 >= 0) add_row_part<Y, 1>(y1 + (int64_t)n * size, t.N - n, scale, d);
       }
+      if constexpr (!S::kStageY) ahead(n0 + S::kCols2);
     }
   }
   if (reading) cluster_wait();
 }
 
-template <int MT>
-const void* run_kernel(int max_rank, size_t* smem) {
-  if (max_rank <= 16) return *smem = Shape<MT, 2>::kSmem, reinterpret_cast<const void*>(lora_kernel<MT, 2>);
-  if (max_rank <= 32) return *smem = Shape<MT, 4>::kSmem, reinterpret_cast<const void*>(lora_kernel<MT, 4>);
-  if (max_rank <= 64) return *smem = Shape<MT, 8>::kSmem, reinterpret_cast<const void*>(lora_kernel<MT, 8>);
-  return *smem = Shape<MT, 16>::kSmem, reinterpret_cast<const void*>(lora_kernel<MT, 16>);
+// ---- many tokens
+//
+// A cluster takes up to 128 tokens of one adapter (a window of the plan's tiles, run by run). In the first product a warp
+// owns 16 tokens and takes A from shared memory, so its sums need no other warp's. In the second it owns 32 columns: their
+// values of B stay in its registers while the tokens pass by, without a barrier. x and y come through a ring of asynchronous
+// copies, in which each lane finds what it has asked for itself: registers as the targets of loads that far ahead were slower
+// (a wait for one of them waits for all: 470 us for 8190 tokens).
+constexpr int kLongBlocks = 8;                                // 16-token blocks of a window: one per warp
+constexpr int kLongTokens = 16 * kLongBlocks;
+
+template <int NB, int Y>
+struct Long {
+  static constexpr bool F32 = Y == QMV_F32;
+  static constexpr int kSteps = NB / 2, kParts3 = F32 ? 3 : 2;
+  static constexpr int kWords = kLongBlocks * kSteps * 64;    // 16-byte words of the window's fp32 values
+  static constexpr int kFrag = kLongBlocks * kSteps * kParts3 * 32;
+  static constexpr int kCols = 128;                           // columns of A at a time, two of them in shared memory
+  static constexpr int kChunk = 8 * NB * kCols * 2;
+  static constexpr int kRing = 8192;                          // bytes of a warp's ring
+  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kAheadY = kRing / kBlockY;
+  static constexpr int kAheadX = kRing / 1024;                // k32 steps of 16 tokens
+  static constexpr int kFirst = kWords * 16 > kLoraWarps * kRing ? kWords * 16 : kLoraWarps * kRing;
+  static constexpr int kSmem = kFirst + (2 * kChunk > kFrag * 16 ? 2 * kChunk : kFrag * 16) + kLongTokens * (int)sizeof(int64_t);
+};
+
+template <int NB, int Y>
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel(const __grid_constant__ RunArgs a) {
+  using S = Long<NB, Y>;
+  constexpr bool F32 = S::F32;
+  constexpr int KS = S::kSteps, P3 = S::kParts3, size = F32 ? 4 : 2, WORDS = F32 ? 8 : 4, AY = S::kAheadY;
+  extern __shared__ __align__(16) unsigned char lora_smem[];
+  float4* mine = reinterpret_cast<float4*>(lora_smem);        // this block's sums, which the cluster reads; before and after them the rings
+  unsigned char* chunks = lora_smem + S::kFirst;         // two of A
+  uint4* frag = reinterpret_cast<uint4*>(chunks);             // after them: [blocks][KS][P3][32], the parts of the finished values
+  int64_t* row_y = reinterpret_cast<int64_t*>(lora_smem + S::kSmem) - kLongTokens;   // bytes to each token's row of y; negative: none
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int rank = (int)cluster_rank(), C = a.cluster, clusters = gridDim.x / C;
+  const uint32_t chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
+  constexpr int PER = S::kCols / 8, ROWS = kLoraThreads / PER, TURNS = 8 * NB / ROWS;   // 16-byte pieces of a row of A; rows at a time
+  const int c1 = tid % PER, r1 = tid / PER;
+  unsigned char* ring = lora_smem + warp * S::kRing + lane * 16;   // this lane's 16 bytes of each 512
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const uint32_t to_a = (r1 * PER + (c1 ^ ((r1 & 1) << 2))) * 16;
+  const int windows = (a.max_tiles + a.window - 1) / a.window;
+  follow_previous();
+  for (int unit = blockIdx.x / C; unit < windows * a.n_tasks; unit += clusters) {
+    const Task& t = a.t[unit / windows];
+    const int base = unit % windows * a.window, tiles = min(a.window, a.max_tiles - base);
+    for (int j = 0; j < tiles;) {
+      const int4 tile = a.tiles[base + j++];
+      if (tile.z == 0) break;
+      const auto fits = [&](const int4& v) {
+        return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
+      };
+      int row0 = 0, r = 0;
+      float scale = 0.f;
+      const bool good = fits(tile);
+      if (good) {
+        row0 = a.table[2 * tile.x];
+        r = a.table[2 * tile.x + 1];
+        scale = a.scale[tile.x];
+      }
+      if (!good || row0 < 0 || r < 0 || r > 8 * NB || row0 > a.pool_rows - r) {
+        if (rank == 0 && tid == 0) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+        continue;
+      }
+      if (r == 0) continue;
+      int count = tile.z;
+      for (; j < tiles; ++j) {                                // the adapter's next tiles
+        const int4 v = a.tiles[base + j];
+        if (!fits(v) || v.x != tile.x || v.y != tile.y + count || count + v.z > kLongTokens) break;
+        count += v.z;
+      }
+      __syncthreads();                                        // the run before this one is done with token and frag
+      const auto token_at = [&](int i) {                      // of this run; -1 past its end, and for a place outside
+        const int k = i < count ? a.order[tile.y + i] : -1;
+        return k < a.n_tokens ? k : -1;
+      };
+      const int tok0 = token_at(warp * 16 + g), tok1 = token_at(warp * 16 + g + 8);
+      if (tid < kLongTokens) {
+        int k = -1;
+        if (tid < count) {
+          k = a.order[tile.y + tid];
+          if (k < 0 || k >= a.n_tokens) {
+            k = -1;
+            atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+          }
+        }
+        row_y[tid] = k < 0 ? -1 : (int64_t)k * t.ldy * size;
+      }
+      const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 32 - 1) / (C * 32) * 32;
+      const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
+
+      // ---- first product, over this block's share of K
+      const int chunk_count = k_hi > k_lo ? (k_hi - k_lo + S::kCols - 1) / S::kCols : 0;
+      const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + k_lo + 8 * c1;
+      const int64_t step_a = ROWS * t.lda;
+      const auto load = [&](int q) {
+        if (q < chunk_count && k_lo + q * S::kCols + 8 * c1 < k_hi) {
+          const __nv_bfloat16* p = pa + q * S::kCols;
+          const uint32_t to = chunks_at + (q & 1) * S::kChunk + to_a;
+#pragma unroll
+          for (int i = 0; i < TURNS; ++i, p += step_a) {
+            if (r1 + i * ROWS >= r) break;
+            copy16(to + i * (ROWS * PER * 16), p);
+          }
+        }
+        copies_end();
+      };
+      load(0);
+      __syncthreads();
+      const bool used = warp * 16 < count;
+      const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
+      const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
+      // the ring's groups are those of the chunks of A too: one of each for a chunk, then one for each step
+      constexpr int AX = S::kAheadX, STEPS = S::kCols / 32;
+      int k_ahead = k_lo + 8 * t4, slot_in = 0, slot = 0;
+      const auto ahead = [&]() {
+        if (used && k_ahead < k_hi) {
+          if (tok0 >= 0) copy16(ring_at + slot_in * 1024, x0 + k_ahead);
+          if (tok1 >= 0) copy16(ring_at + slot_in * 1024 + 512, x1 + k_ahead);
+        }
+        copies_end();
+        k_ahead += 32;
+        slot_in = slot_in + 1 == AX ? 0 : slot_in + 1;
+      };
+      for (int i = 0; i < AX - 1; ++i) ahead();
+      float acc[NB][4];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+      for (int q = 0; q < chunk_count; ++q) {
+        // chunk q was asked for before the latest STEPS (the first: AX - 1) steps of x
+        asm volatile("cp.async.wait_group %0;" ::"n"(STEPS < AX - 1 ? STEPS : AX - 1) : "memory");
+        __syncthreads();                                      // chunk q is there, and q - 1 has been read
+        load(q + 1);
+        const unsigned char* st = chunks + (q & 1) * S::kChunk + g * (PER * 16);
+#pragma unroll
+        for (int e = 0; e < STEPS; ++e) {
+          ahead();
+          // since step e: AX - 1 more steps, and a chunk of A
+          asm volatile("cp.async.wait_group %0;" ::"n"(AX - 1) : "memory");
+          const int k = k_lo + q * S::kCols + 32 * e + 8 * t4;
+          uint4 p = make_uint4(0, 0, 0, 0), o = p;
+          if (k < k_hi && tok0 >= 0) p = *reinterpret_cast<const uint4*>(ring + slot * 1024);
+          if (k < k_hi && tok1 >= 0) o = *reinterpret_cast<const uint4*>(ring + slot * 1024 + 512);
+          slot = slot + 1 == AX ? 0 : slot + 1;
+          if (used && k - 8 * t4 < k_hi) {
+            const unsigned char* sa = st + (((e * 4 + t4) ^ ((g & 1) << 2)) * 16);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+              if (8 * i >= r) break;
+              uint4 w = make_uint4(0, 0, 0, 0);
+              if (8 * i + g < r && k < k_hi) w = *reinterpret_cast<const uint4*>(sa + i * (8 * PER * 16));
+              mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
+              mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
+            }
+          }
+        }
+      }
+      __syncthreads();                                        // the rings have been read: their place is that of the sums
+      if (used) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) mine[(warp * NB + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      }
+      cluster_arrive();
+      cluster_wait();
+
+      // ---- the cluster's sums: each block finishes its share of a lane's eight values of one k16 step, and hands it to all
+      const int items = (count + 15) / 16 * KS * 32, item_share = (items + C - 1) / C;
+      for (int i = rank * item_share + tid; i < min(items, (rank + 1) * item_share); i += kLoraThreads) {
+        const int at = (i / 32) * 64 + i % 32;
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 8
+        for (int c = 0; c < C; ++c) {
+          const uint32_t m = remote(mine + at, c);
+          const float4 e = ld_remote(m), f = ld_remote(m + 32 * 16);
+          u.x += e.x, u.y += e.y, u.z += e.z, u.w += e.w;
+          v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+        }
+#pragma unroll
+        for (int k = 0; k < P3; ++k) {
+          uint4 f;
+          f.x = split(u.x, u.y);
+          f.y = split(u.z, u.w);
+          f.z = split(v.x, v.y);
+          f.w = split(v.z, v.w);
+          for (int c = 0; c < C; ++c) st_remote(remote(frag + ((i / 32) * P3 + k) * 32 + i % 32, c), f);
+        }
+      }
+      cluster_arrive();
+      cluster_wait();
+
+      // ---- second product, over this block's share of N
+      const int blocks = (count + 15) / 16;
+      char* y = static_cast<char*>(t.y);
+      int n_in = n_lo + warp * 32, m_in = 0;                  // the next block of y to ask for
+      slot_in = slot = 0;
+      const auto ahead_y = [&]() {
+        const int n = n_in + 8 * t4;
+        if (t.wide && n_in < n_hi && n + 8 <= t.N) {
+          const int64_t ta = row_y[m_in * 16 + g], tb = row_y[m_in * 16 + g + 8];
+          const uint32_t to = ring_at + slot_in * S::kBlockY;
+          const char* q = y + (int64_t)n * size;
+          if (ta >= 0) {
+            copy16(to, q + ta);
+            if constexpr (F32) copy16(to + 512, q + ta + 16);
+          }
+          if (tb >= 0) {
+            copy16(to + S::kBlockY / 2, q + tb);
+            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, q + tb + 16);
+          }
+        }
+        copies_end();
+        if (++m_in == blocks) m_in = 0, n_in += kLoraWarps * 32;
+        slot_in = slot_in + 1 == AY ? 0 : slot_in + 1;
+      };
+      for (int i = 0; i < AY - 2; ++i) ahead_y();
+#pragma unroll 1
+      for (int n0 = n_lo + warp * 32; n0 < n_hi; n0 += kLoraWarps * 32) {
+        const int n = n0 + 8 * t4, col = n0 + 4 * g;          // first column of this lane's sums, and of its loads of B
+        const bool whole = t.wide && n + 8 <= t.N;
+        uint32_t b[KS][4][2];
+        const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int off = 16 * s + (i & 1) + 8 * (i >> 1);
+            w[i] = make_uint2(0, 0);
+            if (off + 2 * t4 < r && col < t.N) {
+              const __nv_bfloat16* q = pb + (int64_t)off * t.ldb;
+              if (col + 4 <= t.N) {
+                w[i] = __ldg(reinterpret_cast<const uint2*>(q));
+              } else {
+                const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
+                w[i].x = e[0] | (col + 1 < t.N ? (uint32_t)e[1] << 16 : 0u);
+                w[i].y = col + 2 < t.N ? e[2] : 0u;
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            b[s][0][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x5410);
+            b[s][1][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x7632);
+            b[s][2][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x5410);
+            b[s][3][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x7632);
+          }
+        }
+        const auto finish_block = [&](int m, const float (&d)[4][4]) {
+          const int64_t ta = row_y[m * 16 + g], tb = row_y[m * 16 + g + 8];
+          const unsigned char* sy = ring + slot * S::kBlockY;
+          slot = slot + 1 == AY ? 0 : slot + 1;
+          uint32_t v[WORDS];
+          const auto row = [&](const unsigned char* q) {
+            const uint4 u = *reinterpret_cast<const uint4*>(q);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+            if constexpr (F32) {
+              const uint4 w = *reinterpret_cast<const uint4*>(q + 512);
+              v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
+            }
+          };
+          char* q = y + (int64_t)n * size;
+          if (whole) {
+            if (ta >= 0) row(sy), add_row<Y, 0>(q + ta, scale, d, v);
+            if (tb >= 0) row(sy + S::kBlockY / 2), add_row<Y, 1>(q + tb, scale, d, v);
+          } else {
+            if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
+            if (tb >= 0) add_row_part<Y, 1>(q + tb, t.N - n, scale, d);
+          }
+        };
+        // two blocks at a time: twice the products that wait for no other
+#pragma unroll 1
+        for (int m = 0; m < blocks; m += 2) {
+          const bool two = m + 1 < blocks;
+          ahead_y();
+          if (two) ahead_y();
+          float d[2][4][4];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) d[i / 16][i / 4 % 4][i % 4] = 0.f;
+          const uint4* h = frag + m * (KS * P3 * 32) + lane;
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if (16 * s >= r) break;
+#pragma unroll
+            for (int k = P3 - 1; k >= 0; --k) {
+              const uint4 e = h[(s * P3 + k) * 32], f = h[(KS * P3 + s * P3 + k) * 32];   // past the last block: of no use
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                mma(d[0][i], e.x, e.y, e.z, e.w, b[s][i][0], b[s][i][1]);
+                mma(d[1][i], f.x, f.y, f.z, f.w, b[s][i][0], b[s][i][1]);
+              }
+            }
+          }
+          // since this block's copies: AY - 1 more groups (AY - 2 after a last block without a second: one more has to be there)
+          asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
+          finish_block(m, d[0]);
+          if (two) finish_block(m + 1, d[1]);
+        }
+      }
+      copies_wait(0);
+    }
+  }
+}
+
+// A kernel and its shared memory: what a block has beside the stages, and a stage's bytes.
+struct Choice {
+  const void* kernel;
+  int fixed, stage;
+};
+template <int NB, int Y>
+Choice choice_of(bool many) {
+  if (many) return {reinterpret_cast<const void*>(lora_long_kernel<NB, Y>), Long<NB, Y>::kSmem, 0};
+  return {reinterpret_cast<const void*>(lora_kernel<1, NB, Y>), Shape<1, NB, Y>::kFixed, Shape<1, NB, Y>::kStage};
+}
+template <int Y>
+Choice choose(int max_rank, bool many) {
+  return max_rank <= 16 ? choice_of<2, Y>(many) : max_rank <= 32 ? choice_of<4, Y>(many) : max_rank <= 64 ? choice_of<8, Y>(many) : choice_of<16, Y>(many);
 }
 
 }  // namespace
@@ -599,29 +1056,40 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
     const lora_task& k = tasks[i];
     const int ys = kv8::dtype_size(k.y_type);
     if (!ys) return fail(QMV_ERR_ARG, "task %d: y_type=%d", i, k.y_type);
+    if (k.y_type != tasks[0].y_type) return fail(QMV_ERR_ARG, "task %d: y_type=%d beside %d: one type for a call", i, k.y_type, tasks[0].y_type);
     if (k.N < 1 || k.lda < g->K || k.ldb < k.N || k.ldy < k.N)
       return fail(QMV_ERR_ARG, "task %d: N=%d lda=%lld ldb=%lld ldy=%lld", i, k.N, (long long)k.lda, (long long)k.ldb, (long long)k.ldy);
+    if (k.N > (1 << 26)) return fail(QMV_ERR_UNSUPPORTED, "task %d: N=%d over 2^26", i, k.N);
     if (k.lda % 8 || k.ldb % 8) return fail(QMV_ERR_ALIGN, "task %d: rows of a and b must be 16-byte aligned", i);
     if (g->n_tokens > 0) {
       if (!k.a || !k.b || !k.y) return fail(QMV_ERR_ARG, "task %d: NULL a, b or y", i);
       if (!aligned16(k.a) || !aligned16(k.b) || !aligned16(k.y)) return fail(QMV_ERR_ALIGN, "task %d: a, b and y must be 16-byte aligned", i);
     }
-    a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, k.y_type,
-              (int32_t)(k.ldy * ys % 32 == 0 && (reinterpret_cast<uintptr_t>(k.y) & 31u) == 0)};
+    a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, (int32_t)(k.ldy * ys % 32 == 0 && (reinterpret_cast<uintptr_t>(k.y) & 31u) == 0)};
   }
   if (g->n_tokens == 0) return QMV_OK;
   if ((int64_t)g->max_tiles * n_tasks > INT32_MAX / 2) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d tasks", g->max_tiles, n_tasks);
   a.err = device_error_word();
   if (!a.err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
-  size_t smem = 0;
-  const void* f = lora_tile(g->n_tokens) == kSmallTile ? run_kernel<kSmallTile / 16>(g->max_rank, &smem) : run_kernel<kLargeTile / 16>(g->max_rank, &smem);
+  a.tile = lora_tile(g->n_tokens);
+  a.window = 2;
+  const bool many = a.tile == kLargeTile;
+  const int type = tasks[0].y_type;
+  const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank, many) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank, many) : choose<QMV_F16>(g->max_rank, many);
+  a.cluster = kCluster;
+  // as many stages as two blocks of an SM leave room for, up to four; two at least (ranks past 64: one block)
+  a.n_stages = 2;
+  while (a.n_stages < 4 && c.fixed + (a.n_stages + 1) * c.stage <= kHalfSm) ++a.n_stages;
+  const size_t smem = c.fixed + (size_t)a.n_stages * c.stage;
   int per_sm = 0;
-  int rc = kernel_fit(f, kLoraThreads, smem, &per_sm);
+  int rc = kernel_fit(c.kernel, kLoraThreads, smem, &per_sm);
   if (rc) return rc;
-  const int64_t units = (int64_t)g->max_tiles * n_tasks, resident = (int64_t)sm_count() * per_sm / kCluster;
-  const int clusters = (int)(units < resident ? units : resident);
+  const int64_t units = (int64_t)(many ? (g->max_tiles + a.window - 1) / a.window : g->max_tiles) * n_tasks, resident = (int64_t)sm_count() * per_sm / a.cluster;
+  // a cluster for every unit, up to eight rounds of them: the device hands them out as others end (units differ by rank and N).
+  // Past that they take several each, so that a list with many empty tiles costs few launches of blocks.
+  const int clusters = (int)(units < 8 * resident ? units : 8 * resident);
   void* args[] = {&a};
-  cudaError_t e = kv8::launch_early(f, dim3((unsigned)(clusters * kCluster)), kLoraThreads, args, smem, static_cast<cudaStream_t>(stream), kCluster);
+  cudaError_t e = kv8::launch_early(c.kernel, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, smem, static_cast<cudaStream_t>(stream), a.cluster);
   if (e != cudaSuccess) return cuda_fail(e, "lora_run launch");
   return QMV_OK;
 }
