@@ -3,24 +3,31 @@
 //
 // One pass over a row: a thread keeps the largest value M it has seen, and with
 // d_i = (x_i - M) scale log2 e the sums S = sum 2^d_i and U = sum 2^d_i d_i, which
-// give lse = scale M + ln S and the entropy ln S - ln 2 U / S. The difference comes
-// before the product: it overflows only to a power of 0, and a row of the type's
-// lowest value is an ordinary row. Partial results of threads, warps and blocks
-// join by S = sum S_p 2^D_p, U = sum (U_p + D_p S_p) 2^D_p, D_p their M less the
-// largest.
+// give lse = scale M + ln S and the entropy ln S - ln 2 U / S. Partial results of
+// threads, warps and blocks join by S = sum S_p 2^D_p, U = sum (U_p + D_p S_p) 2^D_p,
+// D_p their M less the largest. d is one fused multiply-add from the rounded product
+// M scale log2 e (what the rounding took is put back into ln S); where M is so large that
+// the product could overflow (a row masked by its type's lowest value), the difference
+// comes first.
 //
 // The top k (k <= 32) are kept by each warp as a sorted list, an entry per lane,
 // of 64-bit keys: the value in an order-preserving 32-bit form, then the index's
 // complement, so that no two keys are equal, ties go to the lowest index and
 // the result does not depend on the order in which candidates arrive. A vector of
-// loaded values whose largest does not reach the warp's k-th value (or that of
-// any warp of the block) costs one vote; others push what passes into a buffer in
-// shared memory, which goes into the list 32 at a time by a bitonic sort and
-// merge. The first loads' lane maxima give a first threshold (the k-th largest of
-// 32 of them is below k values), so that few pass from the start.
+// loaded values whose largest is below the threshold, of which the block knows that k
+// values reach it, costs one vote; what passes is put into the list, one by one where
+// few lanes have some, else 32 at a time by a bitonic sort and merge. The threshold is the largest of
+// any warp's k-th value and of the least of all warps' j-th (j times warps >= k), which
+// is near the block's own k-th; the first one comes from the lanes' maxima of the first loads.
+// At the end what reaches the threshold, few more than k keys, is sorted by one warp.
 //
-// Bound by memory: a row is read once. Few rows are cut over a cluster of up to
-// eight blocks that join in distributed shared memory.
+// A token's rank is counted where a thread's values reach it: in 16 bits two values per
+// instruction, against the token's value or, before its place, the one below it.
+//
+// Bound by memory: a row is read once, through a ring of asynchronous copies in
+// which a thread finds what it has asked for itself; in 16 bits the exponentials (16 per
+// clock and SM) take three quarters of the time that the loads do. Few rows are cut over
+// a cluster of up to eight blocks that join in distributed shared memory.
 #include "kv8.cuh"
 
 #include <type_traits>
@@ -30,8 +37,7 @@ namespace {
 
 using kv8::follow_previous;
 
-constexpr int kRowThreads = 256;
-constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kManyThreads = 256, kFewThreads = 512;
 constexpr int kMaxCluster = 8;   // the largest cluster that every device of this kind schedules
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -62,20 +68,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return y;
 }
 
-// m: the largest value; s = sum 2^d and u = sum 2^d d with d = (value - m) * scale2.
+// m: the largest value; s = sum 2^d and u = sum 2^d d with d the distance of a value from m.
 struct Sums {
   float m, s, u;
 };
-__device__ __forceinline__ Sums join(const Sums& a, const Sums& b, float scale2) {
-  if (b.s == 0.f) return a;
-  if (a.s == 0.f) return b;
-  Sums r;
-  r.m = fmaxf(a.m, b.m);
-  const float da = (a.m - r.m) * scale2, db = (b.m - r.m) * scale2, fa = exp2_fast(da), fb = exp2_fast(db);
-  // a part whose factor is 0 leaves nothing (or its NaN): -inf * 0 would be NaN
-  r.s = a.s * fa + b.s * fb;
-  r.u = (fa == 0.f ? a.s * 0.f : (a.u + da * a.s) * fa) + (fb == 0.f ? b.s * 0.f : (b.u + db * b.s) * fb);
-  return r;
+
+// What a kernel knows of the scale: values up to `most` keep clear of overflow, and so does what lies `gap` or more below them.
+struct Scale {
+  float scale2, most;
+  __device__ __forceinline__ bool plain(float m) const { return fabsf(m) <= most; }
+  // distance in powers of 2 between what two sums were taken against: the rounded products, or the values
+  __device__ __forceinline__ float between(float v, float m) const {
+    return plain(m) ? __fsub_rn(__fmul_rn(v, scale2), __fmul_rn(m, scale2)) : (v - m) * scale2;
+  }
+};
+
+// The sum of the lanes' parts, in every lane.
+__device__ __forceinline__ Sums join(Sums t, const Scale& k) {
+  float m = t.m;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  if (t.s != 0.f) {
+    const float d = k.between(t.m, m), f = exp2_fast(d);
+    // a part whose factor is 0 leaves nothing (or its NaN): -inf * 0 would be NaN
+    t.u = f == 0.f ? t.s * 0.f : (t.u + d * t.s) * f;
+    t.s *= f;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    t.s += __shfl_xor_sync(0xFFFFFFFFu, t.s, d);
+    t.u += __shfl_xor_sync(0xFFFFFFFFu, t.u, d);
+  }
+  return {m, t.s, t.u};
 }
 
 // Pairs of fp32 in one instruction each.
@@ -89,11 +113,6 @@ __device__ __forceinline__ void parts(Pair p, float& x, float& y) { asm("mov.b64
 __device__ __forceinline__ Pair add2(Pair a, Pair b) {
   Pair d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
@@ -136,63 +155,129 @@ __device__ __forceinline__ Key join_lists(Key a, Key b, int lane) {
   return merge_down(a > r ? a : r, lane);
 }
 
-template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / sizeof(T);
-};
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f<__half>(__half x) { return __half2float(x); }
-
-template <typename T>
-__device__ __forceinline__ void unpack(uint4 w, float (&v)[Vec<T>::kN]) {
-  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-  if constexpr (sizeof(T) == 4) {
+// Lanes' values, largest first.
+__device__ __forceinline__ uint32_t sort_down32(uint32_t k, int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
-  } else {
+  for (int n = 2; n <= 32; n *= 2)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        v[2 * i] = __uint_as_float(r[i] << 16);
-        v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-      } else {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-      }
+    for (int j = n / 2; j; j >>= 1) {
+      const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
+      k = ((lane & j) == 0) == ((lane & n) == 0 || n == 32) ? max(k, o) : min(k, o);
     }
-  }
+  return k;
 }
 
-constexpr int kAhead = 4;         // vectors in flight per thread
-constexpr int kBuffer = 32 * 8;   // candidates of one vector of a warp, at most
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
+// Sixteen bytes of a row. least: a value that is taken in the place of -inf, so far below `most` that its power is 0.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static constexpr float kMost = 1e28f;
+  static __device__ __forceinline__ void values(const uint4& w, float (&v)[4]) {
+    v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+  static __device__ __forceinline__ void lift(uint4&) {}     // done on the distances
+  using Bound = float;
+  static __device__ __forceinline__ Bound bound(float x) { return x; }
+  static __device__ __forceinline__ Bound below(float x) {    // the value before x, which is neither 0 nor -inf
+    return __uint_as_float(__float_as_uint(x) + (x > 0.f ? -1 : 1));
+  }
+  static __device__ __forceinline__ int over(const uint4& w, Bound b) {
+    return (__uint_as_float(w.x) > b) + (__uint_as_float(w.y) > b) + (__uint_as_float(w.z) > b) + (__uint_as_float(w.w) > b);
+  }
+  static __device__ __forceinline__ void put(uint4& w, int i, float x) {
+    const uint32_t b = __float_as_uint(x);
+    if (i == 0) w.x = b; else if (i == 1) w.y = b; else if (i == 2) w.z = b; else w.w = b;
+  }
+};
+template <typename T, typename T2>
+struct Vec16 {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ T2 two(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
+  static __device__ __forceinline__ float largest(const uint4& w) {
+    const T2 m = __hmax2(__hmax2(two(w.x), two(w.y)), __hmax2(two(w.z), two(w.w)));
+    return fmaxf(to_f(m.x), to_f(m.y));
+  }
+  using Bound = T2;
+  static __device__ __forceinline__ Bound bound(float x) { return T2(T(x), T(x)); }
+  static __device__ __forceinline__ Bound below(float x) {
+    T h = T(x);
+    *reinterpret_cast<uint16_t*>(&h) += x > 0.f ? -1 : 1;
+    return T2(h, h);
+  }
+  static __device__ __forceinline__ int over(const uint4& w, Bound b) {
+    const T2 n = __hadd2(__hadd2(__hgt2(two(w.x), b), __hgt2(two(w.y), b)), __hadd2(__hgt2(two(w.z), b), __hgt2(two(w.w), b)));
+    return (int)(to_f(n.x) + to_f(n.y));
+  }
+  static __device__ __forceinline__ void put(uint4& w, int i, float x) {
+    const T h = T(x);
+    const uint32_t b = (uint32_t)*reinterpret_cast<const uint16_t*>(&h) << (16 * (i & 1)), keep = (i & 1) ? 0xFFFFu : 0xFFFF0000u;
+    if (i < 2) w.x = (w.x & keep) | b; else if (i < 4) w.y = (w.y & keep) | b; else if (i < 6) w.z = (w.z & keep) | b; else w.w = (w.w & keep) | b;
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {
+  static constexpr float kMost = 1e28f;
+  static __device__ __forceinline__ void values(const uint4& w, float (&v)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(r[i] << 16), v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+  }
+  static __device__ __forceinline__ uint32_t lift1(uint32_t w) {   // to -1e30 at least
+    uint32_t y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w), "r"(0xF149F149u));
+    return y;
+  }
+  static __device__ __forceinline__ void lift(uint4& w) { w = make_uint4(lift1(w.x), lift1(w.y), lift1(w.z), lift1(w.w)); }
+};
+template <>
+struct Vec<__half> : Vec16<__half, __half2> {
+  static constexpr float kMost = 60000.f;
+  static __device__ __forceinline__ void values(const uint4& w, float (&v)[8]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[i]));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint32_t lift1(uint32_t w) {   // to -65504 at least
+    uint32_t y;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(w), "r"(0xFBFFFBFFu));
+    return y;
+  }
+  static __device__ __forceinline__ void lift(uint4& w) { w = make_uint4(lift1(w.x), lift1(w.y), lift1(w.z), lift1(w.w)); }
+};
+
+constexpr int kAhead = 4, kGroups = 2;   // vectors of a thread at a time, and such groups on their way
+
+template <int WARPS>
 struct TopShared {
-  Key list[kRowWarps][32];
-  Key buffer[kRowWarps][kBuffer + 32];
-  int count[kRowWarps];
-  unsigned least;                 // the largest k-th value (order_of) that a warp of the block has seen
+  Key pool[WARPS * 32];
+  Key list[WARPS][32];
+  int pooled;
+  unsigned least;                 // k values of the block reach it (order_of)
+  unsigned jth[WARPS];            // j values of the warp reach it
 };
 
-template <bool TOP>
-struct Shared {
-  Sums sums[kRowWarps];
-  int ahead[kRowWarps];
-  Sums block_sums;
-  int block_ahead;
-};
-
-// A warp's list takes the buffer's keys, the last 32 of `n`.
-__device__ __forceinline__ Key take(Key list, const Key* buffer, int n, int lane) {
+// A warp's list takes the last 32 of n keys.
+__device__ __forceinline__ Key take(Key list, const Key* keys, int n, int lane) {
   const int i = n - 32 + lane;
-  Key k = i >= 0 ? buffer[i] : 0;
+  const Key k = i >= 0 ? keys[i] : 0;
   return join_lists(list, sort_down(k, lane), lane);
+}
+// It takes one key, the same in all lanes.
+__device__ __forceinline__ Key insert(Key list, Key k, int lane) {
+  const Key up = __shfl_up_sync(0xFFFFFFFFu, list, 1);
+  return list > k ? list : lane == 0 || up > k ? k : up;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -220,221 +305,307 @@ __device__ __forceinline__ Key ld_remote64(uint32_t p) {
   return v;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kRowThreads, 4) logprob_kernel(const __grid_constant__ Args a) {
-  constexpr int N = Vec<T>::kN;
-  __shared__ Shared<TOP> sh;
-  extern __shared__ __align__(16) unsigned char top_smem[];
-  TopShared& ts = *reinterpret_cast<TopShared*>(top_smem);   // there where TOP
+__device__ __forceinline__ void copy16(uint32_t to, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <typename T, bool TOP, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const __grid_constant__ Args a) {
+  using V = Vec<T>;
+  constexpr int N = V::kN, WARPS = THREADS / 32, kStep = THREADS * N * kAhead;
+  __shared__ Sums sums[WARPS];
+  __shared__ int aheads[WARPS];
+  __shared__ Sums block_sums;
+  __shared__ int block_ahead;
+  extern __shared__ __align__(16) unsigned char row_smem[];
+  TopShared<WARPS>& ts = *reinterpret_cast<TopShared<WARPS>*>(row_smem + kGroups * kAhead * THREADS * 16);   // there where TOP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.cluster, part = C > 1 ? (int)cluster_rank() : 0;
   const int64_t row = blockIdx.x / C;
   if constexpr (TOP) {
-    if (lane == 0) ts.count[warp] = 0;
-    if (tid == 0) ts.least = 0;
+    if (tid == 0) ts.pooled = 0, ts.least = 0;
+    __syncthreads();
   }
   follow_previous();
-  if constexpr (TOP) __syncthreads();
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   // vectors lie on 16-byte boundaries: position 0 is at or before the row's first value
   const int skew = (int)((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
   const T* base = x - skew;
   const int end = a.V + skew;                               // positions skew .. end - 1 are the row
   const int lo = part * a.piece, hi = min(end, lo + a.piece);
+  const uint4* ring = reinterpret_cast<const uint4*>(row_smem) + tid;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const auto ask = [&](int g0, int place) {                 // the block's group at position g0
+    const T* p = base + g0 + tid * N;
+    const uint32_t to = ring_at + place * (kAhead * THREADS * 16);
+    if (g0 >= skew && g0 + kStep <= hi) {
+#pragma unroll
+      for (int v = 0; v < kAhead; ++v) copy16(to + v * (THREADS * 16), p + v * (THREADS * N));
+    } else {
+#pragma unroll
+      for (int v = 0; v < kAhead; ++v) {
+        const int at = g0 + (v * THREADS + tid) * N;
+        if (at >= skew && at + N <= hi) copy16(to + v * (THREADS * 16), p + v * (THREADS * N));
+      }
+    }
+    copies_end();
+  };
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) ask(lo + i * kStep, i);
   int token = -1;
   if (a.tokens) token = a.tokens[row];
   if (token >= a.V) {
     if (part == 0 && tid == 0) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
     token = -1;
   }
-  float given = 0.f;
+  float given = INFINITY;                                   // no token: nothing to count
   if (token >= 0) given = fmaxf(to_f(x[token]), -INFINITY);  // NaN ranks as -inf
-  const int given_at = token + skew;
+  const int given_at = min(hi, token + skew);               // positions before it come first among equals
+  // given is an ordinary value: one below it exists, and compares as such
+  const bool counted = fabsf(given) > 1e-4f && given > -INFINITY;
+  const typename V::Bound at_given = V::bound(given), under_given = V::below(given);
+  const Scale scale{a.scale2, a.scale2 >= 0.05f && a.scale2 <= 1e6f ? V::kMost : -1.f};
   Sums t{-INFINITY, 0.f, 0.f};
   int ahead = 0;
   Key list = 0, least = 0;                                  // the warp's list and its k-th key
   float floor = -INFINITY;                                  // values below it are in no list
-  bool first = true;
-  for (int p0 = lo + tid * N; p0 - tid * N < hi; p0 += kRowThreads * N * kAhead) {
-    uint4 raw[kAhead];
+  int place = 0;
+  for (int g0 = lo; g0 < hi; g0 += kStep) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
+    const bool inside = g0 >= skew && g0 + kStep <= hi;
+    uint4 w[kAhead];
+    float vmax[kAhead];
 #pragma unroll
     for (int v = 0; v < kAhead; ++v) {
-      const int p = p0 + v * kRowThreads * N;
-      raw[v] = make_uint4(0, 0, 0, 0);
-      if (p >= skew && p + N <= hi) raw[v] = __ldcs(reinterpret_cast<const uint4*>(base + p));
-    }
-    float z[kAhead][N], vmax[kAhead];
+      w[v] = ring[(place * kAhead + v) * THREADS];
+      const int p = g0 + (v * THREADS + tid) * N;
+      if (!inside && (p < skew || p + N > hi)) {            // the row's ends, value by value; -inf where there is none
 #pragma unroll
-    for (int v = 0; v < kAhead; ++v) {
-      const int p = p0 + v * kRowThreads * N;
-      unpack<T>(raw[v], z[v]);
-      if (p < skew || p + N > hi) {                         // the row's ends, value by value; -inf where there is none
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[v][i] = p + i >= skew && p + i < hi ? to_f(base[p + i]) : -INFINITY;
+        for (int i = 0; i < N; ++i) V::put(w[v], i, p + i >= skew && p + i < hi ? to_f(base[p + i]) : -INFINITY);
       }
-      vmax[v] = z[v][0];
-#pragma unroll
-      for (int i = 1; i < N; ++i) vmax[v] = fmaxf(vmax[v], z[v][i]);
-      vmax[v] = fmaxf(vmax[v], -INFINITY);
+      vmax[v] = fmaxf(V::largest(w[v]), -INFINITY);
     }
-    float m = vmax[0];
-#pragma unroll
-    for (int v = 1; v < kAhead; ++v) m = fmaxf(m, vmax[v]);
+    ask(g0 + kGroups * kStep, place);
+    place = place + 1 == kGroups ? 0 : place + 1;
+    const float m = fmaxf(fmaxf(vmax[0], vmax[1]), fmaxf(vmax[2], vmax[3]));
     if (m > t.m) {
-      if (t.s > 0.f) {
-        const float d = (t.m - m) * a.scale2, f = exp2_fast(d);
-        t.u = f == 0.f ? 0.f : (t.u + d * t.s) * f;
+      if (t.s != 0.f) {
+        const float d = scale.between(t.m, m), f = exp2_fast(d);
+        t.u = f == 0.f ? t.s * 0.f : (t.u + d * t.s) * f;
         t.s *= f;
       }
       t.m = m;
     }
-    const float ref = t.m == -INFINITY ? 0.f : -t.m;
-    const Pair ref2 = pair(ref, ref), scale2 = pair(a.scale2, a.scale2);
     Pair s2 = 0, u2 = 0;
+    if (scale.plain(t.m)) {
+      const float r = -__fmul_rn(t.m, a.scale2);
+      const Pair ref2 = pair(r, r), scale2 = pair(a.scale2, a.scale2);
 #pragma unroll
-    for (int v = 0; v < kAhead; ++v)
+      for (int v = 0; v < kAhead; ++v) {
+        uint4 y = w[v];
+        V::lift(y);
+        float z[N];
+        V::values(y, z);
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        float d0, d1;
-        parts(mul2(add2(pair(z[v][i], z[v][i + 1]), ref2), scale2), d0, d1);
-        // -256: its power is 0, and so is the product
-        d0 = max_nan(d0, -256.f);
-        d1 = max_nan(d1, -256.f);
-        const Pair e = pair(exp2_fast(d0), exp2_fast(d1));
-        s2 = add2(s2, e);
-        u2 = fma2(e, pair(d0, d1), u2);
+        for (int i = 0; i < N; i += 2) {
+          Pair d2 = fma2(pair(z[i], z[i + 1]), scale2, ref2);
+          float d0, d1;
+          parts(d2, d0, d1);
+          if constexpr (N == 4) {                           // -256: its power is 0, and so is the product
+            d0 = max_nan(d0, -256.f);
+            d1 = max_nan(d1, -256.f);
+            d2 = pair(d0, d1);
+          }
+          const Pair e = pair(exp2_fast(d0), exp2_fast(d1));
+          s2 = add2(s2, e);
+          u2 = fma2(e, d2, u2);
+        }
       }
+    } else {
+      const float r = t.m == -INFINITY ? 0.f : -t.m;
+#pragma unroll
+      for (int v = 0; v < kAhead; ++v) {
+        float z[N];
+        V::values(w[v], z);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const float d0 = max_nan((z[i] + r) * a.scale2, -256.f), d1 = max_nan((z[i + 1] + r) * a.scale2, -256.f);
+          const Pair e = pair(exp2_fast(d0), exp2_fast(d1));
+          s2 = add2(s2, e);
+          u2 = fma2(e, pair(d0, d1), u2);
+        }
+      }
+    }
     float s0, s1, u0, u1;
     parts(s2, s0, s1);
     parts(u2, u0, u1);
     t.s += s0 + s1;
     t.u += u0 + u1;
-    if (token >= 0 && m >= given) {
+    if (m >= given) {
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
-        const int p = p0 + v * kRowThreads * N;
-        if (vmax[v] < given) continue;
+        const int p = g0 + (v * THREADS + tid) * N;
+        const bool before = p + N <= given_at;
+        if (counted && (before || p >= given_at)) {
+          ahead += V::over(w[v], before ? under_given : at_given);
+        } else if (vmax[v] >= given) {
+          float z[N];
+          V::values(w[v], z);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float y = fmaxf(z[v][i], -INFINITY);
-          const bool before = p + i >= skew && p + i < min(given_at, hi);   // of this block's, and with a lower index
-          ahead += (y > given) || (y == given && before);
+          for (int i = 0; i < N; ++i) {
+            const float y = fmaxf(z[i], -INFINITY);
+            ahead += (y > given) || (y == given && p + i >= skew && p + i < given_at);
+          }
         }
       }
     }
     if constexpr (TOP) {
-      if (first) {
-        // k lanes have seen a value of at least the k-th largest of the lanes' maxima
-        const Key s = sort_down((Key)order_of(m) << 32, lane);
-        const unsigned o = (unsigned)(__shfl_sync(0xFFFFFFFFu, s, a.top - 1) >> 32);
-        if (lane == 0) atomicMax(&ts.least, o);
-        floor = value_of(o);
-        first = false;
+      const int j = (a.top + WARPS - 1) / WARPS;
+      if (g0 == lo) {
+        // as many lanes of the warp have seen a value of at least their k-th, or j-th, largest
+        const uint32_t o = sort_down32(order_of(m), lane);
+        if (lane == a.top - 1) atomicMax(&ts.least, o);
+        if (lane == j - 1) ts.jth[warp] = o;
+        __syncthreads();
       }
-      floor = fmaxf(floor, value_of(max(order_of(-INFINITY), *(volatile unsigned*)&ts.least)));
+      const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, ((volatile unsigned*)ts.jth)[lane % WARPS]);
+      floor = fmaxf(floor, value_of(max(low, *(volatile unsigned*)&ts.least)));
+      bool changed = false;
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
-        const int p = p0 + v * kRowThreads * N;
         if (!__any_sync(0xFFFFFFFFu, vmax[v] >= floor)) continue;
+        const int p = g0 + (v * THREADS + tid) * N;
+        float z[N];
+        V::values(w[v], z);
+        uint32_t passes = 0;                                // this lane's values that are candidates
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (fmaxf(z[v][i], -INFINITY) >= floor && p + i >= skew && p + i < hi) {
-            const Key k = key_of(z[v][i], p + i - skew);
-            if (k > least) ts.buffer[warp][atomicAdd(&ts.count[warp], 1)] = k;
+        for (int i = 0; i < N; ++i)
+          if (fmaxf(z[i], -INFINITY) >= floor && (inside || (p + i >= skew && p + i < hi))) passes |= 1u << i;
+        while (uint32_t lanes = __ballot_sync(0xFFFFFFFFu, passes != 0)) {
+          const int i = __ffs(passes) - 1;
+          float y = z[0];
+#pragma unroll
+          for (int c = 1; c < N; ++c) y = i == c ? z[c] : y;
+          Key k = passes ? key_of(y, p + i - skew) : 0;
+          passes &= passes - 1;
+          if (k <= least) k = 0;
+          lanes = __ballot_sync(0xFFFFFFFFu, k != 0);
+          if (!lanes) continue;
+          if (__popc(lanes) <= 8) {
+            for (; lanes; lanes &= lanes - 1) list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(lanes) - 1), lane);
+          } else {
+            list = join_lists(list, sort_down(k, lane), lane);
           }
-        }
-        __syncwarp();
-        int n = *(volatile int*)&ts.count[warp];
-        if (n >= 32) {
-          for (; n >= 32; n -= 32) list = take(list, ts.buffer[warp], n, lane);
-          __syncwarp();
-          if (lane == 0) ts.count[warp] = n;
           least = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
-          if (least) {
-            floor = fmaxf(floor, value_of((unsigned)(least >> 32)));
-            if (lane == 0) atomicMax(&ts.least, (unsigned)(least >> 32));
-          }
-          __syncwarp();
+          changed = true;
+        }
+      }
+      if (changed) {
+        const uint32_t now = (uint32_t)(__shfl_sync(0xFFFFFFFFu, list, j - 1) >> 32), kth = (uint32_t)(least >> 32);
+        if (kth) floor = fmaxf(floor, value_of(kth));
+        if (lane == 0) {
+          if (now > ts.jth[warp]) ((volatile unsigned*)ts.jth)[warp] = now;
+          if (kth) atomicMax(&ts.least, kth);
         }
       }
     }
   }
 
   // the block's results
-  if constexpr (TOP) {
-    __syncwarp();
-    list = take(list, ts.buffer[warp], *(volatile int*)&ts.count[warp], lane);   // fewer than 32 are left
-    ts.list[warp][lane] = list;
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    const Sums o{__shfl_xor_sync(0xFFFFFFFFu, t.m, d), __shfl_xor_sync(0xFFFFFFFFu, t.s, d), __shfl_xor_sync(0xFFFFFFFFu, t.u, d)};
-    t = join(t, o, a.scale2);
-    ahead += __shfl_xor_sync(0xFFFFFFFFu, ahead, d);
-  }
+  t = join(t, scale);
+  ahead = __reduce_add_sync(0xFFFFFFFFu, ahead);
   if (lane == 0) {
-    sh.sums[warp] = t;
-    sh.ahead[warp] = ahead;
+    sums[warp] = t;
+    aheads[warp] = ahead;
   }
   __syncthreads();
   if constexpr (TOP) {
-    for (int d = kRowWarps / 2; d; d >>= 1) {
-      if (warp < d) ts.list[warp][lane] = join_lists(ts.list[warp][lane], ts.list[warp + d][lane], lane);
-      __syncthreads();
-    }
+    // what reaches the threshold, in one place
+    const uint32_t low = lo < hi ? __reduce_min_sync(0xFFFFFFFFu, ts.jth[lane % WARPS]) : 0;
+    if (list && list >= (Key)max(low, ts.least) << 32) ts.pool[atomicAdd(&ts.pooled, 1)] = list;
+    __syncthreads();
   }
   if (warp == 0) {
-    t = sh.sums[0];
-    ahead = sh.ahead[0];
-#pragma unroll
-    for (int w = 1; w < kRowWarps; ++w) {
-      t = join(t, sh.sums[w], a.scale2);
-      ahead += sh.ahead[w];
+    t = join(lane < WARPS ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, scale);
+    ahead = __reduce_add_sync(0xFFFFFFFFu, lane < WARPS ? aheads[lane] : 0);
+    if constexpr (TOP) {
+      list = 0;
+      int n = ts.pooled;
+      do {
+        list = take(list, ts.pool, n, lane);
+        n -= 32;
+      } while (n > 0);
     }
-    if constexpr (TOP) list = ts.list[0][lane];
   }
   if (C > 1) {
-    if (tid == 0) {
-      sh.block_sums = t;
-      sh.block_ahead = ahead;
+    if (warp == 0) {
+      if (lane == 0) {
+        block_sums = t;
+        block_ahead = ahead;
+      }
+      if constexpr (TOP) ts.list[0][lane] = list;
     }
     cluster_sync();
-    if (part == 0 && warp == 0) {
-      for (int c = 1; c < C; ++c) {
-        const uint32_t p = remote(&sh.block_sums, c);
-        const Sums o{__uint_as_float(ld_remote32(p)), __uint_as_float(ld_remote32(p + 4)), __uint_as_float(ld_remote32(p + 8))};
-        t = join(t, o, a.scale2);
-        ahead += (int)ld_remote32(remote(&sh.block_ahead, c));
-        if constexpr (TOP) list = join_lists(list, ld_remote64(remote(&ts.list[0][lane], c)), lane);
+    if (part == 0) {
+      if (warp == 0) {
+        Sums o{-INFINITY, 0.f, 0.f};
+        int n = 0;
+        if (lane < C) {
+          const uint32_t p = remote(&block_sums, lane);
+          o = {__uint_as_float(ld_remote32(p)), __uint_as_float(ld_remote32(p + 4)), __uint_as_float(ld_remote32(p + 8))};
+          n = (int)ld_remote32(remote(&block_ahead, lane));
+        }
+        t = join(o, scale);
+        ahead = __reduce_add_sync(0xFFFFFFFFu, n);
+      }
+      if constexpr (TOP) {
+        if (warp > 0 && warp < C) ts.list[warp][lane] = ld_remote64(remote(&ts.list[0][lane], warp));
+        __syncthreads();
+        for (int d = C / 2; d; d >>= 1) {
+          if (warp < d) ts.list[warp][lane] = join_lists(ts.list[warp][lane], ts.list[warp + d][lane], lane);
+          __syncthreads();
+        }
+        if (warp == 0) list = ts.list[0][lane];
       }
     }
     cluster_sync();                                         // the other blocks' memory has been read
   }
   if (part != 0 || warp != 0) return;
   const float log2_s = log2f(t.s);
+  // the sum against the value itself: what the product's rounding took is put back
+  const float ln_s = (log2_s - (scale.plain(t.m) ? fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)) : 0.f)) * kLn2;
   const bool none = t.s == 0.f;                             // every value is -inf
   const auto log_p = [&](float v) {
     if (none) return -INFINITY;
-    return v == -INFINITY ? (log2_s == log2_s ? -INFINITY : log2_s) : fmaf(v - t.m, a.scale, -log2_s * kLn2);
+    return v == -INFINITY ? (ln_s == ln_s ? -INFINITY : ln_s) : fmaf(v - t.m, a.scale, -ln_s);
   };
   if (lane == 0) {
-    if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(t.m, a.scale, log2_s * kLn2);
+    if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(t.m, a.scale, ln_s);
     if (a.entropy) a.entropy[row] = none ? 0.f : (log2_s - t.u / t.s) * kLn2;
-    if (a.logprob) a.logprob[row] = token < 0 ? 0.f : log_p(to_f(x[token]));
+    if (a.logprob) a.logprob[row] = token < 0 ? 0.f : log_p(given);
     if (a.rank) a.rank[row] = token < 0 ? -1 : ahead;
   }
   if constexpr (TOP) {
     if (lane < a.top && list != 0) {                        // top <= V: every one of these lanes has a key
-      const int i = (int)~(uint32_t)list;
-      a.top_index[row * a.top + lane] = i;
-      a.top_logprob[row * a.top + lane] = log_p(to_f(x[i]));
+      a.top_index[row * a.top + lane] = (int)~(uint32_t)list;
+      a.top_logprob[row * a.top + lane] = log_p(value_of((uint32_t)(list >> 32)));
     }
   }
 }
 
+struct Choice {
+  const void* kernel;
+  size_t smem;
+};
+template <typename T, int THREADS>
+Choice choice_of(bool top) {
+  return {top ? reinterpret_cast<const void*>(logprob_kernel<T, true, THREADS>) : reinterpret_cast<const void*>(logprob_kernel<T, false, THREADS>),
+          kGroups * kAhead * THREADS * 16 + (top ? sizeof(TopShared<THREADS / 32>) : 0)};
+}
 template <typename T>
-const void* kernel_of(bool top) {
-  return top ? reinterpret_cast<const void*>(logprob_kernel<T, true>) : reinterpret_cast<const void*>(logprob_kernel<T, false>);
+Choice choose(bool top, bool few) {
+  return few ? choice_of<T, kFewThreads>(top) : choice_of<T, kManyThreads>(top);
 }
 
 }  // namespace
@@ -481,15 +652,19 @@ int logprob_run(const logprob_args* g, void* stream) {
   a.scale2 = g->scale * kLog2E;
   const int N = 16 / xs;
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && (int64_t)g->n_rows * a.cluster < 2 * sm_count() && g->V / (2 * a.cluster) >= kRowThreads * N) a.cluster *= 2;
+  while (a.cluster < kMaxCluster && (int64_t)g->n_rows * a.cluster < 2 * sm_count() && g->V / (2 * a.cluster) >= kManyThreads * N) a.cluster *= 2;
+  const bool few = (int64_t)g->n_rows * a.cluster <= sm_count();   // a block per SM: twice the threads, all of a row's loads at once
   // positions of a row and of the skew before it, in vectors
   const int64_t vectors = (g->V + 2 * (int64_t)N - 2) / N;
   a.piece = (int32_t)((vectors + a.cluster - 1) / a.cluster * N);
   if ((int64_t)g->n_rows * a.cluster > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "n_rows=%d", g->n_rows);
   const bool top = g->top > 0;
-  const void* f = g->x_type == QMV_F32 ? kernel_of<float>(top) : g->x_type == QMV_BF16 ? kernel_of<__nv_bfloat16>(top) : kernel_of<__half>(top);
+  const Choice c = g->x_type == QMV_F32 ? choose<float>(top, few) : g->x_type == QMV_BF16 ? choose<__nv_bfloat16>(top, few) : choose<__half>(top, few);
+  int per_sm = 0;
+  int rc = kernel_fit(c.kernel, few ? kFewThreads : kManyThreads, c.smem, &per_sm);
+  if (rc) return rc;
   void* args[] = {&a};
-  cudaError_t e = kv8::launch_early(f, dim3((unsigned)(g->n_rows * a.cluster)), kRowThreads, args, top ? sizeof(TopShared) : 0,
+  cudaError_t e = kv8::launch_early(c.kernel, dim3((unsigned)(g->n_rows * a.cluster)), few ? kFewThreads : kManyThreads, args, c.smem,
                                     static_cast<cudaStream_t>(stream), a.cluster);
   if (e != cudaSuccess) return cuda_fail(e, "logprob_run launch");
   return QMV_OK;
