@@ -19,7 +19,7 @@
 // few lanes have some, else 32 at a time by a bitonic sort and merge. The threshold is the largest of
 // any warp's k-th value and of the least of all warps' j-th (j times warps >= k), which
 // is near the block's own k-th; the first one comes from the lanes' maxima of the first loads.
-// At the end what reaches the threshold, few more than k keys, is sorted by one warp.
+// Lists join two by two, each in an exchange and a bitonic merge.
 //
 // A token's rank is counted where a thread's values reach it: in 16 bits two values per
 // instruction, against the token's value or, before its place, the one below it.
@@ -193,6 +193,9 @@ struct Vec<float> {
   static __device__ __forceinline__ int over(const uint4& w, Bound b) {
     return (__uint_as_float(w.x) > b) + (__uint_as_float(w.y) > b) + (__uint_as_float(w.z) > b) + (__uint_as_float(w.w) > b);
   }
+  static __device__ __forceinline__ float value(const uint4& w, int i) {
+    return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+  }
   static __device__ __forceinline__ void put(uint4& w, int i, float x) {
     const uint32_t b = __float_as_uint(x);
     if (i == 0) w.x = b; else if (i == 1) w.y = b; else if (i == 2) w.z = b; else w.w = b;
@@ -216,6 +219,10 @@ struct Vec16 {
   static __device__ __forceinline__ int over(const uint4& w, Bound b) {
     const T2 n = __hadd2(__hadd2(__hgt2(two(w.x), b), __hgt2(two(w.y), b)), __hadd2(__hgt2(two(w.z), b), __hgt2(two(w.w), b)));
     return (int)(to_f(n.x) + to_f(n.y));
+  }
+  static __device__ __forceinline__ float value(const uint4& w, int i) {
+    const T2 h = two(i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w);
+    return to_f(i & 1 ? h.y : h.x);
   }
   static __device__ __forceinline__ void put(uint4& w, int i, float x) {
     const T h = T(x);
@@ -261,20 +268,13 @@ constexpr int kAhead = 4, kGroups = 2;   // vectors of a thread at a time, and s
 
 template <int WARPS>
 struct TopShared {
-  Key pool[WARPS * 32];
   Key list[WARPS][32];
-  int pooled;
+  Key lists[kMaxCluster][32];     // of the cluster's blocks, in its first
   unsigned least;                 // k values of the block reach it (order_of)
   unsigned jth[WARPS];            // j values of the warp reach it
 };
 
-// A warp's list takes the last 32 of n keys.
-__device__ __forceinline__ Key take(Key list, const Key* keys, int n, int lane) {
-  const int i = n - 32 + lane;
-  const Key k = i >= 0 ? keys[i] : 0;
-  return join_lists(list, sort_down(k, lane), lane);
-}
-// It takes one key, the same in all lanes.
+// A list takes one key, the same in all lanes.
 __device__ __forceinline__ Key insert(Key list, Key k, int lane) {
   const Key up = __shfl_up_sync(0xFFFFFFFFu, list, 1);
   return list > k ? list : lane == 0 || up > k ? k : up;
@@ -285,25 +285,21 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_arrive() {
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ uint32_t ld_remote32(uint32_t p) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ Key ld_remote64(uint32_t p) {
-  Key v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(p) : "memory");
-  return v;
-}
+__device__ __forceinline__ void st_remote32(uint32_t p, uint32_t v) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
+__device__ __forceinline__ void st_remote64(uint32_t p, Key v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(p), "l"(v) : "memory"); }
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* p) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
@@ -316,17 +312,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   constexpr int N = V::kN, WARPS = THREADS / 32, kStep = THREADS * N * kAhead;
   __shared__ Sums sums[WARPS];
   __shared__ int aheads[WARPS];
-  __shared__ Sums block_sums;
-  __shared__ int block_ahead;
+  __shared__ Sums all_sums[kMaxCluster];                    // of the cluster's blocks, in its first
+  __shared__ int all_ahead[kMaxCluster];
+  __shared__ Sums total;
+  __shared__ int total_ahead;
   extern __shared__ __align__(16) unsigned char row_smem[];
   TopShared<WARPS>& ts = *reinterpret_cast<TopShared<WARPS>*>(row_smem + kGroups * kAhead * THREADS * 16);   // there where TOP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = a.cluster, part = C > 1 ? (int)cluster_rank() : 0;
   const int64_t row = blockIdx.x / C;
   if constexpr (TOP) {
-    if (tid == 0) ts.pooled = 0, ts.least = 0;
+    if (tid == 0) ts.least = 0;
     __syncthreads();
   }
+  if (C > 1) cluster_arrive();                              // waited for before the first access to another block's memory
   follow_previous();
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   // vectors lie on 16-byte boundaries: position 0 is at or before the row's first value
@@ -362,8 +361,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   float given = INFINITY;                                   // no token: nothing to count
   if (token >= 0) given = fmaxf(to_f(x[token]), -INFINITY);  // NaN ranks as -inf
   const int given_at = min(hi, token + skew);               // positions before it come first among equals
-  // given is an ordinary value: one below it exists, and compares as such
-  const bool counted = fabsf(given) > 1e-4f && given > -INFINITY;
+  // given is -inf, which all values before its place precede, or an ordinary value, with one below it that compares as such
+  const bool lowest = given == -INFINITY, counted = fabsf(given) > 1e-4f;
   const typename V::Bound at_given = V::bound(given), under_given = V::below(given);
   const Scale scale{a.scale2, a.scale2 >= 0.05f && a.scale2 <= 1e6f ? V::kMost : -1.f};
   Sums t{-INFINITY, 0.f, 0.f};
@@ -398,8 +397,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       t.m = m;
     }
     Pair s2 = 0, u2 = 0;
-    if (scale.plain(t.m)) {
-      const float r = -__fmul_rn(t.m, a.scale2);
+    if (scale.plain(t.m) || (scale.most > 0.f && t.m == -INFINITY)) {
+      const float r = t.m == -INFINITY ? 0.f : -__fmul_rn(t.m, a.scale2);
       const Pair ref2 = pair(r, r), scale2 = pair(a.scale2, a.scale2);
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
@@ -447,8 +446,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       for (int v = 0; v < kAhead; ++v) {
         const int p = g0 + (v * THREADS + tid) * N;
         const bool before = p + N <= given_at;
-        if (counted && (before || p >= given_at)) {
-          ahead += V::over(w[v], before ? under_given : at_given);
+        if (counted && p >= skew && (before || p >= given_at)) {
+          ahead += before && lowest ? N : V::over(w[v], before ? under_given : at_given);
         } else if (vmax[v] >= given) {
           float z[N];
           V::values(w[v], z);
@@ -471,35 +470,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       }
       const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, ((volatile unsigned*)ts.jth)[lane % WARPS]);
       floor = fmaxf(floor, value_of(max(low, *(volatile unsigned*)&ts.least)));
-      bool changed = false;
+      uint32_t passes = 0;                                  // this lane's values that are candidates
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
         if (!__any_sync(0xFFFFFFFFu, vmax[v] >= floor)) continue;
         const int p = g0 + (v * THREADS + tid) * N;
         float z[N];
         V::values(w[v], z);
-        uint32_t passes = 0;                                // this lane's values that are candidates
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (fmaxf(z[i], -INFINITY) >= floor && (inside || (p + i >= skew && p + i < hi))) passes |= 1u << i;
-        while (uint32_t lanes = __ballot_sync(0xFFFFFFFFu, passes != 0)) {
-          const int i = __ffs(passes) - 1;
-          float y = z[0];
-#pragma unroll
-          for (int c = 1; c < N; ++c) y = i == c ? z[c] : y;
-          Key k = passes ? key_of(y, p + i - skew) : 0;
-          passes &= passes - 1;
-          if (k <= least) k = 0;
-          lanes = __ballot_sync(0xFFFFFFFFu, k != 0);
-          if (!lanes) continue;
-          if (__popc(lanes) <= 8) {
-            for (; lanes; lanes &= lanes - 1) list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(lanes) - 1), lane);
-          } else {
-            list = join_lists(list, sort_down(k, lane), lane);
-          }
-          least = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
-          changed = true;
+          if (fmaxf(z[i], -INFINITY) >= floor && (inside || (p + i >= skew && p + i < hi))) passes |= 1u << (v * N + i);
+      }
+      bool changed = false;
+      while (uint32_t lanes = __ballot_sync(0xFFFFFFFFu, passes != 0)) {
+        const int i = __ffs(passes) - 1, v = i / N;
+        const uint4 y = v == 0 ? w[0] : v == 1 ? w[1] : v == 2 ? w[2] : w[3];
+        Key k = passes ? key_of(V::value(y, i % N), g0 + (v * THREADS + tid) * N + i % N - skew) : 0;
+        passes &= passes - 1;
+        if (k <= least) k = 0;
+        lanes = __ballot_sync(0xFFFFFFFFu, k != 0);
+        if (!lanes) continue;
+        if (__popc(lanes) <= 8) {
+          for (; lanes; lanes &= lanes - 1) list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(lanes) - 1), lane);
+        } else {
+          list = join_lists(list, sort_down(k, lane), lane);
         }
+        least = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
+        changed = true;
       }
       if (changed) {
         const uint32_t now = (uint32_t)(__shfl_sync(0xFFFFFFFFu, list, j - 1) >> 32), kth = (uint32_t)(least >> 32);
@@ -519,59 +516,52 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
     sums[warp] = t;
     aheads[warp] = ahead;
   }
-  __syncthreads();
-  if constexpr (TOP) {
-    // what reaches the threshold, in one place
-    const uint32_t low = lo < hi ? __reduce_min_sync(0xFFFFFFFFu, ts.jth[lane % WARPS]) : 0;
-    if (list && list >= (Key)max(low, ts.least) << 32) ts.pool[atomicAdd(&ts.pooled, 1)] = list;
-    __syncthreads();
-  }
-  if (warp == 0) {
-    t = join(lane < WARPS ? sums[lane] : Sums{-INFINITY, 0.f, 0.f}, scale);
-    ahead = __reduce_add_sync(0xFFFFFFFFu, lane < WARPS ? aheads[lane] : 0);
+  // Joins n (a power of two) sums, counts and lists into the last warp's t and ahead, and warp 0's list.
+  const auto join_all = [&](const Sums* s, const int* c, Key (*l)[32], int n) {
+    if (warp == WARPS - 1) {
+      t = join(lane < n ? s[lane] : Sums{-INFINITY, 0.f, 0.f}, scale);
+      ahead = __reduce_add_sync(0xFFFFFFFFu, lane < n ? c[lane] : 0);
+    }
     if constexpr (TOP) {
-      list = 0;
-      int n = ts.pooled;
-      do {
-        list = take(list, ts.pool, n, lane);
-        n -= 32;
-      } while (n > 0);
+      for (int d = n / 2; d; d >>= 1) {
+        if (warp < d) {
+          list = join_lists(l[warp][lane], l[warp + d][lane], lane);
+          l[warp][lane] = list;
+        }
+        if (d > 1) __syncthreads();
+      }
     }
-  }
+  };
+  if constexpr (TOP) ts.list[warp][lane] = list;
+  __syncthreads();
+  Key (*own)[32] = nullptr, (*others)[32] = nullptr;
+  if constexpr (TOP) own = ts.list, others = ts.lists;
+  join_all(sums, aheads, own, WARPS);
   if (C > 1) {
-    if (warp == 0) {
-      if (lane == 0) {
-        block_sums = t;
-        block_ahead = ahead;
-      }
-      if constexpr (TOP) ts.list[0][lane] = list;
+    cluster_wait();
+    if (warp == WARPS - 1 && lane == 0) {
+      const uint32_t p = remote(&all_sums[part], 0);
+      st_remote32(p, __float_as_uint(t.m));
+      st_remote32(p + 4, __float_as_uint(t.s));
+      st_remote32(p + 8, __float_as_uint(t.u));
+      st_remote32(remote(&all_ahead[part], 0), (uint32_t)ahead);
     }
-    cluster_sync();
-    if (part == 0) {
-      if (warp == 0) {
-        Sums o{-INFINITY, 0.f, 0.f};
-        int n = 0;
-        if (lane < C) {
-          const uint32_t p = remote(&block_sums, lane);
-          o = {__uint_as_float(ld_remote32(p)), __uint_as_float(ld_remote32(p + 4)), __uint_as_float(ld_remote32(p + 8))};
-          n = (int)ld_remote32(remote(&block_ahead, lane));
-        }
-        t = join(o, scale);
-        ahead = __reduce_add_sync(0xFFFFFFFFu, n);
-      }
-      if constexpr (TOP) {
-        if (warp > 0 && warp < C) ts.list[warp][lane] = ld_remote64(remote(&ts.list[0][lane], warp));
-        __syncthreads();
-        for (int d = C / 2; d; d >>= 1) {
-          if (warp < d) ts.list[warp][lane] = join_lists(ts.list[warp][lane], ts.list[warp + d][lane], lane);
-          __syncthreads();
-        }
-        if (warp == 0) list = ts.list[0][lane];
-      }
+    if constexpr (TOP) {
+      if (warp == 0) st_remote64(remote(&ts.lists[part][lane], 0), list);
     }
-    cluster_sync();                                         // the other blocks' memory has been read
+    cluster_arrive();
+    if (part != 0) return;
+    cluster_wait();
+    join_all(all_sums, all_ahead, others, C);
   }
-  if (part != 0 || warp != 0) return;
+  if (warp == WARPS - 1 && lane == 0) {
+    total = t;
+    total_ahead = ahead;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  t = total;
+  ahead = total_ahead;
   const float log2_s = log2f(t.s);
   // the sum against the value itself: what the product's rounding took is put back
   const float ln_s = (log2_s - (scale.plain(t.m) ? fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)) : 0.f)) * kLn2;
