@@ -164,7 +164,6 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
 constexpr int kCluster = 8;    // blocks of a tile: the largest cluster that every device of this kind schedules
 constexpr int kLoraThreads = 256;
 constexpr int kLoraWarps = kLoraThreads / 32;
-constexpr int kHalfSm = 112 * 1024;   // shared memory of a block of which two fit an SM
 
 struct Task {
   const __nv_bfloat16* a;
@@ -183,7 +182,7 @@ struct RunArgs {
   const float* scale;
   int* err;
   int64_t ldx;
-  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks, n_stages, cluster, tile, window;
+  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks, cluster, tile, window;
   Task t[QMV_LORA_MAX_TASKS];
 };
 
@@ -214,13 +213,11 @@ __device__ __forceinline__ void st_remote(uint32_t p, uint4 v) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* p) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
 }
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the latest n groups of this thread's copies are there.
-__device__ __forceinline__ void copies_wait(int n) {
-  if (n <= 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
-  else asm volatile("cp.async.wait_group 2;" ::: "memory");
+__device__ __forceinline__ void copy8(uint32_t to, const void* p) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
 }
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }   // all of this thread's
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -250,30 +247,13 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A lane's consecutive values of a row of y, `words` 32-bit words: 4 or 8.
+// A lane's consecutive values of a row of y: one piece of 16 bytes, or two that lie 512 bytes apart.
 template <int WORDS>
-__device__ __forceinline__ void ld_shared(const unsigned char* p, uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ void ld_pieces(const unsigned char* p, uint32_t (&w)[WORDS]) {
 #pragma unroll
   for (int i = 0; i < WORDS; i += 4) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p + 4 * i);
+    const uint4 u = *reinterpret_cast<const uint4*>(p + 128 * i);
     w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
-  }
-}
-// BL columns of a row of B.
-__device__ __forceinline__ void ld_columns(const unsigned char* p, uint32_t (&w)[2]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  w[0] = u.x, w[1] = u.y;
-}
-__device__ __forceinline__ void ld_columns(const unsigned char* p, uint32_t (&w)[4]) { ld_shared(p, w); }
-template <int WORDS>
-__device__ __forceinline__ void ld_global(const void* p, uint32_t (&w)[WORDS]) {
-  if constexpr (WORDS == 8) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
-  } else {
-    const uint4 u = *static_cast<const uint4*>(p);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   }
 }
 template <int WORDS>
@@ -325,55 +305,51 @@ __device__ __forceinline__ void add_row_part(void* p, int n, float s, const floa
   }
 }
 
-// MT 16-token blocks per tile, NB blocks of eight rank rows (the call's largest rank), y in fp32 or in 16 bits.
-template <int MT, int NB, int Y>
-struct Shape {
+// ---- few tokens of an adapter
+//
+// A cluster takes a tile of up to 16 tokens. Each warp streams through its own ring of asynchronous copies: k32 steps of x and
+// A, then 32-column steps of B and y, of which the first are on their way while the sums of the first product meet. A lane
+// copies just what its fragments need, so a step needs no barrier. NB blocks of eight rank rows (the call's largest rank).
+template <int NB, int Y>
+struct Short {
   static constexpr bool F32 = Y == QMV_F32;
-  static constexpr int kBlocks = MT > 1 && !F32 ? 8 : 4;      // n8 blocks of a warp in a stage of the second product
   static constexpr int kParts3 = F32 ? 3 : 2;                 // bf16 parts of the values between the products
   static constexpr int kSteps = NB / 2;                       // k16 steps of the second product
-  static constexpr int kShare = kLoraWarps / MT;              // warps that share a 16-token block
   static constexpr int kHalves = NB > 8 ? 2 : 1;              // in the first product a warp has at most 64 rank rows
-  static constexpr int kParts = kShare / kHalves;             // and a share of the columns of x
-  static constexpr int kWords = MT * kSteps * 2 * 32;         // 16-byte words of the tile's r values, in the order of the fragments
-  static constexpr int kCols1 = 32 * kParts, kCols2 = 8 * kBlocks * kShare;   // columns of a stage of either product
-  static constexpr int kRowB = kCols2 * 2 + 16;               // bytes of a row of B in a stage: 16 more keep a warp's reads apart
-  static constexpr int kRowsB = 8 * NB;
-  static constexpr bool kStageY = MT > 1;                     // y goes through the stages too (few tokens: through registers)
-  static constexpr int kRowY = kCols2 * (F32 ? 4 : 2) + 16;
-  static constexpr int kFixed = kWords * 16 * (2 + kParts3) / 2 + 16 * MT * (int)sizeof(int);
-  // pieces of 16 bytes: threads side by side take a row's, then the next row's
-  static constexpr int kPer1 = kCols1 / 8, kPer2 = kCols2 / 8, kRows1 = kLoraThreads / kPer1, kRows2 = kLoraThreads / kPer2;
-  static constexpr int kTurnsX = 16 * MT / kRows1, kTurnsA = (8 * NB + kRows1 - 1) / kRows1, kTurnsB = (8 * NB + kRows2 - 1) / kRows2,
-                       kTurnsY = 16 * MT / kRows2;
-  static constexpr int kFirst = (16 * MT + 8 * NB) * kCols1 * 2, kSecond = kRowsB * kRowB + (kStageY ? 16 * MT * kRowY : 0),
-                       kSums = (MT == 1 ? kParts : kParts - 1) * kWords * 16;
-  static constexpr int kStage = kFirst > kSecond ? (kFirst > kSums ? kFirst : kSums) : (kSecond > kSums ? kSecond : kSums);
+  static constexpr int kParts = kLoraWarps / kHalves;         // and a share of the columns of x
+  static constexpr int kBlocks = NB / kHalves;
+  static constexpr int kWords = kSteps * 64;                  // 16-byte words of the tile's r values, in the order of the fragments
+  static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps * 1024, kSecond = kB + (F32 ? 2048 : 1024);
+  static constexpr int kSlot = kFirst > kSecond ? kFirst : kSecond;
+  static constexpr int kDepth = NB == 2 ? 4 : NB == 4 ? 3 : 2;
+  static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + (16 + kLoraWarps) * (int)sizeof(int);
+  static constexpr int kSmem = kFixed + kLoraWarps * kDepth * kSlot;
 };
 
-template <int MT, int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(const __grid_constant__ RunArgs a) {
-  using S = Shape<MT, NB, Y>;
-  constexpr int KS = S::kSteps, W = S::kWords, RB = NB / S::kHalves, BL = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2;
+template <int NB, int Y>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __grid_constant__ RunArgs a) {
+  using S = Short<NB, Y>;
+  constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth;
   constexpr bool F32 = S::F32;
   extern __shared__ __align__(16) unsigned char lora_smem[];
   float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
-  uint4* frag = reinterpret_cast<uint4*>(mine + W);           // [MT][KS][P3][32]: the parts of the finished values
-  int* token = reinterpret_cast<int*>(frag + W * P3 / 2);      // [16 * MT]
-  unsigned char* stages = lora_smem + S::kFixed;              // [n_stages][stage_bytes]
+  uint4* frag = reinterpret_cast<uint4*>(mine + W);           // [KS][P3][32]: the parts of the finished values
+  int* token = reinterpret_cast<int*>(frag + KS * P3 * 32);   // [16]
+  int* sums_in = token + 16;                                  // [kLoraWarps]: the slot in which a warp left its sums
+  unsigned char* rings = lora_smem + S::kFixed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  const int mb = warp % MT, share = warp / MT;                // this warp's 16-token block, its share of columns
-  const int half = share % S::kHalves, part = share / S::kHalves;
-  const int rank = (int)cluster_rank(), C = a.cluster;
-  const int clusters = gridDim.x / C, n_stages = a.n_stages;
-  const uint32_t stages_at = (uint32_t)__cvta_generic_to_shared(stages);
+  const int half = warp % S::kHalves, part = warp / S::kHalves;
+  const int rank = (int)cluster_rank(), C = a.cluster, clusters = gridDim.x / C;
+  unsigned char* ring = rings + warp * (D * S::kSlot);
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  const int j0 = half * 8 * RB;                               // this warp's first rank row in the first product
   follow_previous();
   bool reading = false;                                       // other blocks may still read `mine`
   for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
     const Task& t = a.t[unit / a.max_tiles];
     const int4 tile = a.tiles[unit % a.max_tiles];
     if (tile.z == 0) continue;
-    const bool fits = tile.x >= 0 && tile.x < a.n_adapters && tile.y >= 0 && tile.z > 0 && tile.z <= 16 * MT && tile.y <= a.n_tokens - tile.z;
+    const bool fits = tile.x >= 0 && tile.x < a.n_adapters && tile.y >= 0 && tile.z > 0 && tile.z <= 16 && tile.y <= a.n_tokens - tile.z;
     int row0 = 0, r = 0;
     float scale = 0.f;
     if (fits) {
@@ -386,11 +362,10 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
       continue;
     }
     if (r == 0) continue;
-    const int count = tile.z;
-    __syncthreads();                                          // the unit before this one is done with token, frag and the stages
-    if (tid < 16 * MT) {
+    __syncthreads();                                          // the unit before this one is done with token and frag
+    if (tid < 16) {
       int k = -1;
-      if (tid < count) {
+      if (tid < tile.z) {
         k = a.order[tile.y + tid];
         if (k < 0 || k >= a.n_tokens) {
           k = -1;
@@ -400,154 +375,117 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
       token[tid] = k;
     }
     __syncthreads();
-    const bool mine_used = mb * 16 < count;                   // false: this warp's tokens are none
-    const int tok0 = token[mb * 16 + g], tok1 = token[mb * 16 + g + 8];
+    const int tok0 = token[g], tok1 = token[g + 8];
+    const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
+    const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
+    char* y0 = static_cast<char*>(t.y) + (int64_t)(tok0 < 0 ? 0 : tok0) * t.ldy * size;
+    char* y1 = static_cast<char*>(t.y) + (int64_t)(tok1 < 0 ? 0 : tok1) * t.ldy * size;
 
-    // this block's columns of both products, and the stages that they take
-    const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 8 * BL - 1) / (C * 8 * BL) * (8 * BL);
+    // this block's columns of both products, and this warp's steps of them
+    const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 32 - 1) / (C * 32) * 32;
     const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
-    const int n1 = k_hi > k_lo ? (k_hi - k_lo + S::kCols1 - 1) / S::kCols1 : 0, n2 = n_hi > n_lo ? (n_hi - n_lo + S::kCols2 - 1) / S::kCols2 : 0;
-
-    // this thread's pieces of the stages: rows of x and A, then rows of B and y
-    const int c1 = tid % S::kPer1, r1 = tid / S::kPer1, c2 = tid % S::kPer2, r2 = tid / S::kPer2;
-    const uint32_t to1 = (r1 * S::kPer1 + (S::kPer1 > 4 ? c1 ^ ((r1 & 1) << 2) : c1)) * 16, to2 = r2 * S::kRowB + c2 * 16;
-    int k_next = k_lo + 8 * c1, n_next = n_lo + 8 * c2;
-    const __nv_bfloat16* px[S::kTurnsX];
+    int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, slot_in = 0, slot = 0;
+    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + j0 + g) * t.lda + 8 * t4;
+    const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + 4 * g;
+    const int64_t step_a = 8 * t.lda;
+    const auto ask = [&]() {
+      const uint32_t to = ring_at + slot_in * S::kSlot + lane * 16;
+      if (k_next < k_hi) {
+        const int k = k_next + 8 * t4;
+        if (k < k_hi) {
+          if (tok0 >= 0) copy16(to, x0 + k);
+          if (tok1 >= 0) copy16(to + 512, x1 + k);
+          const __nv_bfloat16* p = pa + k_next;
 #pragma unroll
-    for (int i = 0; i < S::kTurnsX; ++i) {
-      const int tok = token[r1 + i * S::kRows1];
-      px[i] = tok < 0 ? nullptr : a.x + (int64_t)tok * a.ldx + k_next;
-    }
-    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + k_next;
-    const __nv_bfloat16* pb = t.b + (int64_t)(row0 + r2) * t.ldb + n_next;
-    const char* py[S::kStageY ? S::kTurnsY : 1];
-    if constexpr (S::kStageY) {
+          for (int i = 0; i < RB; ++i, p += step_a)
+            if (j0 + 8 * i + g < r) copy16(to + 1024 + i * 512, p);
+        }
+        k_next += S::kParts * 32;
+      } else if (n_next < n_hi) {
+        const int col = n_next + 4 * g, n = n_next + 8 * t4;
+        if (col < t.N) {
+          const __nv_bfloat16* p = pb + n_next;
+          const uint32_t at = ring_at + slot_in * S::kSlot + lane * 8;
 #pragma unroll
-      for (int i = 0; i < S::kTurnsY; ++i) {
-        const int tok = token[r2 + i * S::kRows2];
-        py[i] = tok < 0 || !t.wide ? nullptr : static_cast<const char*>(t.y) + ((int64_t)tok * t.ldy + n_next) * size;
-      }
-    }
-    const int64_t step_a = S::kRows1 * t.lda, step_b = S::kRows2 * t.ldb;
-    int to_begin = 0, slot_in = 0, slot_out = 0;              // the next stage to begin, its place; the place of the next to read
-    // Begins the copies of a stage. Rows past the rank and tokens that are none are not copied: their readers take 0.
-    const auto load = [&]() {
-      const uint32_t at = stages_at + slot_in * S::kStage;
-      if (to_begin < n1) {
-        if (k_next < k_hi) {
+          for (int s = 0; s < KS; ++s)
 #pragma unroll
-          for (int i = 0; i < S::kTurnsX; ++i)
-            if (px[i]) copy16(at + to1 + i * (S::kRows1 * S::kPer1 * 16), px[i] + (k_next - k_lo - 8 * c1));
-          const __nv_bfloat16* p = pa + (k_next - k_lo - 8 * c1);
-#pragma unroll
-          for (int i = 0; i < S::kTurnsA; ++i, p += step_a) {
-            if (r1 + i * S::kRows1 >= r) break;
-            copy16(at + to1 + (16 * MT + i * S::kRows1) * (S::kPer1 * 16), p);
+            for (int i = 0; i < 4; ++i) {
+              const int off = 16 * s + (i & 1) + 8 * (i >> 1);
+              if (off + 2 * t4 >= r) continue;
+              const __nv_bfloat16* q = p + off * t.ldb;
+              if (col + 4 <= t.N) {
+                copy8(at + (4 * s + i) * 256, q);
+              } else {                                        // the row's last values, one by one
+                const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
+                uint16_t* d = reinterpret_cast<uint16_t*>(ring + slot_in * S::kSlot + lane * 8 + (4 * s + i) * 256);
+                for (int c = 0; c < 4; ++c) d[c] = col + c < t.N ? e[c] : (uint16_t)0;
+              }
+            }
+        }
+        if (t.wide && n + 8 <= t.N) {
+          if (tok0 >= 0) {
+            copy16(to + S::kB, y0 + (int64_t)n * size);
+            if constexpr (F32) copy16(to + S::kB + 512, y0 + (int64_t)n * size + 16);
+          }
+          if (tok1 >= 0) {
+            copy16(to + S::kB + 256 * size, y1 + (int64_t)n * size);
+            if constexpr (F32) copy16(to + S::kB + 256 * size + 512, y1 + (int64_t)n * size + 16);
           }
         }
-        k_next += S::kCols1;
-      } else if (to_begin < n1 + n2) {
-        if (n_next < n_hi) {
-          const int off = n_next - n_lo - 8 * c2;
-          const __nv_bfloat16* p = pb + off;
-          if (n_next + 8 <= t.N) {
-#pragma unroll
-            for (int i = 0; i < S::kTurnsB; ++i, p += step_b) {
-              if (r2 + i * S::kRows2 >= r) break;
-              copy16(at + to2 + i * (S::kRows2 * S::kRowB), p);
-            }
-            if constexpr (S::kStageY) {
-              const uint32_t to = at + S::kRowsB * S::kRowB + r2 * S::kRowY + 8 * c2 * size;
-#pragma unroll
-              for (int i = 0; i < S::kTurnsY; ++i)
-                if (py[i]) {
-                  copy16(to + i * S::kRows2 * S::kRowY, py[i] + off * size);
-                  if constexpr (F32) copy16(to + i * S::kRows2 * S::kRowY + 16, py[i] + off * size + 16);
-                }
-            }
-          } else {                                            // the rows' last values, one by one
-            for (int i = 0; i < S::kTurnsB; ++i, p += step_b) {
-              if (r2 + i * S::kRows2 >= r) break;
-              const uint16_t* v = reinterpret_cast<const uint16_t*>(p);
-              uint16_t* d = reinterpret_cast<uint16_t*>(stages + slot_in * S::kStage + to2 + i * (S::kRows2 * S::kRowB));
-              for (int c = 0; c < 8; ++c) d[c] = n_next + c < t.N ? v[c] : (uint16_t)0;
-            }
-          }
-        }
-        n_next += S::kCols2;
+        n_next += kLoraWarps * 32;
       }
       copies_end();
-      ++to_begin;
-      if (++slot_in == n_stages) slot_in = 0;
+      slot_in = slot_in + 1 == D ? 0 : slot_in + 1;
     };
-    for (int q = 0; q < n_stages - 1; ++q) load();
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) ask();
 
-    // ---- first product
+    // ---- first product, over this block's share of K
     float acc[RB][4];
 #pragma unroll
     for (int i = 0; i < RB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    const int j0 = half * 8 * RB;                             // this warp's first rank row
-    for (int q = 0; q < n1; ++q) {
-      copies_wait(n_stages - 2);
-      __syncthreads();                                        // stage q is there, and q - 1 has been read
-      load();
-      // this warp's 32 columns; columns past K were not copied
-      const int left = k_hi - (k_lo + q * S::kCols1 + part * 32);
-      if (mine_used && j0 < r && left > 0) {
-        const int piece = part * 4 + t4;
-        const unsigned char* st = stages + slot_out * S::kStage + g * (S::kPer1 * 16) + (S::kPer1 > 4 ? piece ^ ((g & 1) << 2) : piece) * 16;
-        const bool in = 8 * t4 < left;
-        uint4 p = make_uint4(0, 0, 0, 0), o = p;
-        if (in && tok0 >= 0) p = *reinterpret_cast<const uint4*>(st + (mb * 16) * (S::kPer1 * 16));
-        if (in && tok1 >= 0) o = *reinterpret_cast<const uint4*>(st + (mb * 16 + 8) * (S::kPer1 * 16));
+    for (int k0 = k_lo + part * 32; k0 < k_hi; k0 += S::kParts * 32) {
+      ask();
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const unsigned char* st = ring + slot * S::kSlot + lane * 16;
+      slot = slot + 1 == D ? 0 : slot + 1;
+      const bool in = k0 + 8 * t4 < k_hi;
+      uint4 p = make_uint4(0, 0, 0, 0), o = p;
+      if (in && tok0 >= 0) p = *reinterpret_cast<const uint4*>(st);
+      if (in && tok1 >= 0) o = *reinterpret_cast<const uint4*>(st + 512);
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-          if (j0 + 8 * i >= r) break;
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (in && j0 + 8 * i + g < r) w = *reinterpret_cast<const uint4*>(st + (16 * MT + j0 + 8 * i) * (S::kPer1 * 16));
-          mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
-          mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
-        }
+      for (int i = 0; i < RB; ++i) {
+        if (j0 + 8 * i >= r) break;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (in && j0 + 8 * i + g < r) w = *reinterpret_cast<const uint4*>(st + 1024 + i * 512);
+        mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
+        mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
       }
-      if (++slot_out == n_stages) slot_out = 0;
     }
-    // the sums of the block's warps, by way of the stage that comes free
-    __syncthreads();
-    float4* sums = reinterpret_cast<float4*>(stages + slot_in * S::kStage);
-    const int own = (mb * S::kHalves + half) * RB * 32 + lane;
-    if (MT == 1 || part > 0) {
+    // the sums of the block's warps, each by way of its ring's free slot
+    {
+      float4* to = reinterpret_cast<float4*>(ring + slot_in * S::kSlot) + lane;
 #pragma unroll
-      for (int i = 0; i < RB; ++i) sums[(MT == 1 ? part : part - 1) * W + own + i * 32] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      for (int i = 0; i < RB; ++i) to[i * 32] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      if (lane == 0) sums_in[warp] = slot_in * S::kSlot;
     }
     __syncthreads();
     if (reading) cluster_wait();
-    if constexpr (MT == 1) {
-      for (int i = tid; i < W; i += kLoraThreads) {
-        float4 v = sums[i];
+    for (int i = tid; i < W; i += kLoraThreads) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int p = 1; p < S::kParts; ++p) {
-          const float4 o = sums[p * W + i];
-          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
-        mine[i] = v;
+      for (int p = 0; p < S::kParts; ++p) {
+        const int w = p * S::kHalves + i / 32 / RB;
+        const float4 o = reinterpret_cast<const float4*>(rings + w * (D * S::kSlot) + sums_in[w])[i % (32 * RB)];
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
       }
-    } else if (part == 0) {
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        float4 v = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-#pragma unroll
-        for (int p = 1; p < S::kParts; ++p) {
-          const float4 o = sums[(p - 1) * W + own + i * 32];
-          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
-        mine[own + i * 32] = v;
-      }
+      mine[i] = v;
     }
     cluster_arrive();
     cluster_wait();
 
-    // ---- the cluster's sums: item i is a lane's eight values of one k16 step
-    const auto finish = [&](int i, uint4 (&f)[P3]) {
+    // ---- the cluster's sums, in every block: item i is a lane's eight values of one k16 step
+    for (int i = tid; i < W / 2; i += kLoraThreads) {
       const int at = (i / 32) * 64 + i % 32;
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
 #pragma unroll 8
@@ -559,104 +497,63 @@ __global__ void __launch_bounds__(kLoraThreads, NB <= 4 ? 3 : 2) lora_kernel(con
       }
 #pragma unroll
       for (int k = 0; k < P3; ++k) {
-        f[k].x = split(u.x, u.y);
-        f[k].y = split(u.z, u.w);
-        f[k].z = split(v.x, v.y);
-        f[k].w = split(v.z, v.w);
+        uint4 f;
+        f.x = split(u.x, u.y);
+        f.y = split(u.z, u.w);
+        f.z = split(v.x, v.y);
+        f.w = split(v.z, v.w);
+        frag[((i / 32) * P3 + k) * 32 + i % 32] = f;
       }
-    };
-    if constexpr (MT == 1) {
-      // few values: every block takes all of them
-      for (int i = tid; i < W / 2; i += kLoraThreads) {
-        uint4 f[P3];
-        finish(i, f);
-#pragma unroll
-        for (int k = 0; k < P3; ++k) frag[((i / 32) * P3 + k) * 32 + i % 32] = f[k];
-      }
-      cluster_arrive();
-      reading = true;
-    } else {
-      // each block finishes its share and hands it to all
-      for (int i = rank * (W / 2 / C) + tid; i < (rank + 1) * (W / 2 / C); i += kLoraThreads) {
-        uint4 f[P3];
-        finish(i, f);
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int k = 0; k < P3; ++k) st_remote(remote(frag + ((i / 32) * P3 + k) * 32 + i % 32, c), f[k]);
-      }
-      cluster_arrive();
-      cluster_wait();
     }
+    cluster_arrive();
+    reading = true;
+    __syncthreads();
 
-    // ---- second product, 8 * BL columns of a stage per warp
-    char* y0 = static_cast<char*>(t.y) + (int64_t)(tok0 < 0 ? 0 : tok0) * t.ldy * size;
-    char* y1 = static_cast<char*>(t.y) + (int64_t)(tok1 < 0 ? 0 : tok1) * t.ldy * size;
-    const uint4* h = frag + mb * (KS * P3 * 32) + lane;
-    constexpr int LC = 2 * BL, WORDS = LC * size / 4;         // columns of a lane, and their words
-    uint32_t v0[WORDS], v1[WORDS];                            // few tokens: this stage's values of y
-    const auto ahead = [&](int n0) {
-      const int n = n0 + LC * t4;
-      if (t.wide && n0 < n_hi && n + LC <= t.N) {
-        if (tok0 >= 0) ld_global(y0 + (int64_t)n * size, v0);
-        if (tok1 >= 0) ld_global(y1 + (int64_t)n * size, v1);
-      }
-    };
-    if constexpr (!S::kStageY) ahead(n_lo + share * (8 * BL));
-    for (int q = 0; q < n2; ++q) {
-      copies_wait(n_stages - 2);
-      __syncthreads();                                        // the stage is there, and the one before it (or the sums) has been read
-      load();
-      const unsigned char* st = stages + slot_out * S::kStage;
-      if (++slot_out == n_stages) slot_out = 0;
-      const int n0 = n_lo + q * S::kCols2 + share * (8 * BL);
-      if (!mine_used || n0 >= n_hi) continue;
-      float d[BL][4];
+    // ---- second product, over this block's share of N
+    const uint4* h = frag + lane;
+    for (int n0 = n_lo + warp * 32; n0 < n_hi; n0 += kLoraWarps * 32) {
+      ask();
+      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+      const unsigned char* st = ring + slot * S::kSlot;
+      slot = slot + 1 == D ? 0 : slot + 1;
+      const int n = n0 + 8 * t4;                              // first column of this lane's sums
+      float d[4][4];
 #pragma unroll
-      for (int i = 0; i < BL; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-      const unsigned char* sb = st + 2 * t4 * S::kRowB + (share * (8 * BL) + BL * g) * 2;
+      for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         if (16 * s >= r) break;
-        uint32_t b[BL][2];
+        uint32_t b[4][2];
         const bool full = 16 * s + 16 <= r;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int j = 16 * s + 8 * i;
-          uint32_t u[BL / 2], v[BL / 2];                      // rows j + 2 t4 and the next of BL columns
-#pragma unroll
-          for (int c = 0; c < BL / 2; ++c) u[c] = v[c] = 0u;
-          if (full || j + 2 * t4 < r) ld_columns(sb + j * S::kRowB, u);
-          if (full || j + 2 * t4 + 1 < r) ld_columns(sb + (j + 1) * S::kRowB, v);
-#pragma unroll
-          for (int c = 0; c < BL / 2; ++c) {
-            b[2 * c][i] = __byte_perm(u[c], v[c], 0x5410);
-            b[2 * c + 1][i] = __byte_perm(u[c], v[c], 0x7632);
-          }
+          const int j = 16 * s + 8 * i + 2 * t4;
+          uint2 u = make_uint2(0, 0), v = u;
+          if (full || j < r) u = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * s + 2 * i) * 256);
+          if (full || j + 1 < r) v = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * s + 2 * i + 1) * 256);
+          b[0][i] = __byte_perm(u.x, v.x, 0x5410);
+          b[1][i] = __byte_perm(u.x, v.x, 0x7632);
+          b[2][i] = __byte_perm(u.y, v.y, 0x5410);
+          b[3][i] = __byte_perm(u.y, v.y, 0x7632);
         }
 #pragma unroll
         for (int k = P3 - 1; k >= 0; --k) {
           const uint4 f = h[(s * P3 + k) * 32];
 #pragma unroll
-          for (int i = 0; i < BL; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
+          for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
         }
       }
-      const int n = n0 + LC * t4;                             // first column of this lane's sums
-      if (t.wide && n + LC <= t.N) {
-        const unsigned char* sy = st + S::kRowsB * S::kRowB + (mb * 16 + g) * S::kRowY + (share * (8 * BL) + LC * t4) * size;
-        if (tok0 >= 0) {
-          if constexpr (S::kStageY) ld_shared(sy, v0);
-          add_row<Y, 0>(y0 + (int64_t)n * size, scale, d, v0);
-        }
-        if (tok1 >= 0) {
-          if constexpr (S::kStageY) ld_shared(sy + 8 * S::kRowY, v1);
-          add_row<Y, 1>(y1 + (int64_t)n * size, scale, d, v1);
-        }
+      if (t.wide && n + 8 <= t.N) {
+        uint32_t v[WORDS];
+        const unsigned char* sy = st + S::kB + lane * 16;
+        if (tok0 >= 0) ld_pieces(sy, v), add_row<Y, 0>(y0 + (int64_t)n * size, scale, d, v);
+        if (tok1 >= 0) ld_pieces(sy + 256 * size, v), add_row<Y, 1>(y1 + (int64_t)n * size, scale, d, v);
       } else {
         if (tok0 >= 0) add_row_part<Y, 0>(y0 + (int64_t)n * size, t.N - n, scale, d);
         if (tok1 >= 0) add_row_part<Y, 1>(y1 + (int64_t)n * size, t.N - n, scale, d);
       }
-      if constexpr (!S::kStageY) ahead(n0 + S::kCols2);
     }
+    copies_wait();
   }
   if (reading) cluster_wait();
 }
@@ -915,18 +812,10 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel
           const unsigned char* sy = ring + slot * S::kBlockY;
           slot = slot + 1 == AY ? 0 : slot + 1;
           uint32_t v[WORDS];
-          const auto row = [&](const unsigned char* q) {
-            const uint4 u = *reinterpret_cast<const uint4*>(q);
-            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-            if constexpr (F32) {
-              const uint4 w = *reinterpret_cast<const uint4*>(q + 512);
-              v[4] = w.x, v[5] = w.y, v[6] = w.z, v[7] = w.w;
-            }
-          };
           char* q = y + (int64_t)n * size;
           if (whole) {
-            if (ta >= 0) row(sy), add_row<Y, 0>(q + ta, scale, d, v);
-            if (tb >= 0) row(sy + S::kBlockY / 2), add_row<Y, 1>(q + tb, scale, d, v);
+            if (ta >= 0) ld_pieces(sy, v), add_row<Y, 0>(q + ta, scale, d, v);
+            if (tb >= 0) ld_pieces(sy + S::kBlockY / 2, v), add_row<Y, 1>(q + tb, scale, d, v);
           } else {
             if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
             if (tb >= 0) add_row_part<Y, 1>(q + tb, t.N - n, scale, d);
@@ -961,20 +850,20 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel
           if (two) finish_block(m + 1, d[1]);
         }
       }
-      copies_wait(0);
+      copies_wait();
     }
   }
 }
 
-// A kernel and its shared memory: what a block has beside the stages, and a stage's bytes.
+// A kernel and its shared memory.
 struct Choice {
   const void* kernel;
-  int fixed, stage;
+  int smem;
 };
 template <int NB, int Y>
 Choice choice_of(bool many) {
-  if (many) return {reinterpret_cast<const void*>(lora_long_kernel<NB, Y>), Long<NB, Y>::kSmem, 0};
-  return {reinterpret_cast<const void*>(lora_kernel<1, NB, Y>), Shape<1, NB, Y>::kFixed, Shape<1, NB, Y>::kStage};
+  if (many) return {reinterpret_cast<const void*>(lora_long_kernel<NB, Y>), Long<NB, Y>::kSmem};
+  return {reinterpret_cast<const void*>(lora_short_kernel<NB, Y>), Short<NB, Y>::kSmem};
 }
 template <int Y>
 Choice choose(int max_rank, bool many) {
@@ -1077,10 +966,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   const int type = tasks[0].y_type;
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank, many) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank, many) : choose<QMV_F16>(g->max_rank, many);
   a.cluster = kCluster;
-  // as many stages as two blocks of an SM leave room for, up to four; two at least (ranks past 64: one block)
-  a.n_stages = 2;
-  while (a.n_stages < 4 && c.fixed + (a.n_stages + 1) * c.stage <= kHalfSm) ++a.n_stages;
-  const size_t smem = c.fixed + (size_t)a.n_stages * c.stage;
+  const size_t smem = c.smem;
   int per_sm = 0;
   int rc = kernel_fit(c.kernel, kLoraThreads, smem, &per_sm);
   if (rc) return rc;
