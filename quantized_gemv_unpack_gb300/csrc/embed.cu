@@ -139,7 +139,7 @@ const void* of_format(int format, int type) {
          : format == QMV_INT4 ? of_type<QMV_INT4, U>(type) : of_type<QMV_INT4_LUT, U>(type);
 }
 
-constexpr int kMany = 4;
+constexpr int kMany = 8;   // 8190 tokens of 5120 columns, INT4 to bf16: 23.8, 20.0 and 19.3 us with 2, 4 and 8
 
 }  // namespace
 }  // namespace qmv

@@ -37,8 +37,11 @@ constexpr int kSmallTile = 16, kLargeTile = 64;
 // A stable counting sort by one block. Each warp takes a range of the tokens and
 // counts them per adapter, 32 at a time (lanes of one adapter find each other by
 // a match, the first of them adds); sums over the warps, then over the adapters,
-// give each warp its place per adapter, and a second pass hands the places out.
-constexpr int kPlanAhead = 8;   // loads in flight per lane
+// give each warp its place per adapter. What a token finds in its warp's counter is
+// its place among the warp's, kept in a register where a lane has at most 16 tokens,
+// else found again in a second pass.
+// Measured: 64 tokens of 48 adapters 3.0 us, 16384 tokens of 512 adapters 7.9 us.
+constexpr int kPlanAhead = 16;   // tokens of a lane whose loads are in flight at once
 
 __device__ __forceinline__ int scan_add(int v, int lane) {
 #pragma unroll
@@ -72,8 +75,8 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
   const int lo = min(T, warp * chunk), hi = min(T, lo + chunk);
   int32_t* mine = hist + warp * A;
   bool bad = false;
-  for (int t0 = lo; t0 < hi; t0 += 32 * kPlanAhead) {
-    int id[kPlanAhead];
+  // The warp's tokens from t0 on, 16 to a lane: each one's adapter and its place among the warp's tokens of it, or -1.
+  const auto count = [&](int t0, int (&id)[kPlanAhead], int (&at)[kPlanAhead]) {
 #pragma unroll
     for (int u = 0; u < kPlanAhead; ++u) {
       const int t = t0 + 32 * u + lane;
@@ -83,11 +86,20 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
     for (int u = 0; u < kPlanAhead; ++u) {
       if (t0 + 32 * u >= hi) break;
       bad |= id[u] >= A;
-      const int k = id[u] < A ? id[u] : -1;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-      if (k >= 0 && lane == __ffs(same) - 1) mine[k] += __popc(same);
+      if (id[u] >= A) id[u] = -1;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, id[u]);
+      if (id[u] >= 0) at[u] = mine[id[u]] + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (id[u] >= 0 && lane == __ffs(same) - 1) mine[id[u]] += __popc(same);
       __syncwarp();
     }
+  };
+  int id[kPlanAhead], at[kPlanAhead];
+  const bool once = chunk <= 32 * kPlanAhead;
+  if (once) {
+    count(lo, id, at);
+  } else {
+    for (int t0 = lo; t0 < hi; t0 += 32 * kPlanAhead) count(t0, id, at);
   }
   if (bad) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
   __syncthreads();
@@ -97,21 +109,24 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
     const int k = a0 + tid;
     int n = 0;
     if (k < A)
-      for (int w = 0; w < warps; ++w) {
-        const int c = hist[w * A + k];
-        hist[w * A + k] = n;
-        n += c;
+      for (int w = 0; w < warps; w += 8) {                    // warps is a multiple of eight
+        int c[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) c[u] = hist[(w + u) * A + k];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          hist[(w + u) * A + k] = n;
+          n += c[u];
+        }
       }
     const int tiles = (n + a.tile - 1) / a.tile;
     const int sn = scan_add(n, lane), st = scan_add(tiles, lane);
     if (lane == 31) sums[warp] = make_int2(sn, st);
     __syncthreads();
-    int2 before = base, all = base;
-    for (int w = 0; w < warps; ++w) {
-      const int2 s = sums[w];
-      if (w < warp) before.x += s.x, before.y += s.y;
-      all.x += s.x, all.y += s.y;
-    }
+    const int2 of = lane < warps ? sums[lane] : make_int2(0, 0);
+    const int before_x = scan_add(of.x, lane), before_y = scan_add(of.y, lane);   // up to and with each warp's
+    const int2 before = make_int2(base.x + __shfl_sync(0xFFFFFFFFu, before_x - of.x, warp), base.y + __shfl_sync(0xFFFFFFFFu, before_y - of.y, warp));
+    const int2 all = make_int2(base.x + __shfl_sync(0xFFFFFFFFu, before_x, 31), base.y + __shfl_sync(0xFFFFFFFFu, before_y, 31));
     if (k < A) {
       first[k] = before.x + sn - n;
       tile0[k] = before.y + st - tiles;
@@ -125,21 +140,11 @@ __global__ void __launch_bounds__(1024) lora_plan_kernel(const PlanArgs a) {
   }
   __syncthreads();
   for (int t0 = lo; t0 < hi; t0 += 32 * kPlanAhead) {
-    int id[kPlanAhead];
-#pragma unroll
-    for (int u = 0; u < kPlanAhead; ++u) {
-      const int t = t0 + 32 * u + lane;
-      id[u] = t < hi ? a.ids[t] : -1;
-    }
+    if (!once) count(t0, id, at);                             // from the counters that the sums have left
 #pragma unroll
     for (int u = 0; u < kPlanAhead; ++u) {
       if (t0 + 32 * u >= hi) break;
-      const int k = id[u] < A ? id[u] : -1;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, k);
-      if (k >= 0) a.order[first[k] + mine[k] + __popc(same & ((1u << lane) - 1))] = t0 + 32 * u + lane;
-      __syncwarp();
-      if (k >= 0 && lane == __ffs(same) - 1) mine[k] += __popc(same);
-      __syncwarp();
+      if (id[u] >= 0) a.order[first[id[u]] + at[u] + (once ? mine[id[u]] : 0)] = t0 + 32 * u + lane;
     }
   }
   for (int t = base.x + tid; t < T; t += threads) a.order[t] = -1;
@@ -322,7 +327,7 @@ struct Short {
   static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps * 1024, kSecond = kB + (F32 ? 2048 : 1024);
   static constexpr int kSlot = kFirst > kSecond ? kFirst : kSecond;
   static constexpr int kDepth = NB == 2 ? 4 : NB == 4 ? 3 : 2;
-  static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + (16 + kLoraWarps) * (int)sizeof(int);
+  static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + kLoraWarps * (int)sizeof(int);
   static constexpr int kSmem = kFixed + kLoraWarps * kDepth * kSlot;
 };
 
@@ -334,8 +339,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   extern __shared__ __align__(16) unsigned char lora_smem[];
   float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
   uint4* frag = reinterpret_cast<uint4*>(mine + W);           // [KS][P3][32]: the parts of the finished values
-  int* token = reinterpret_cast<int*>(frag + KS * P3 * 32);   // [16]
-  int* sums_in = token + 16;                                  // [kLoraWarps]: the slot in which a warp left its sums
+  int* sums_in = reinterpret_cast<int*>(frag + KS * P3 * 32); // [kLoraWarps]: the slot in which a warp left its sums
   unsigned char* rings = lora_smem + S::kFixed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int half = warp % S::kHalves, part = warp / S::kHalves;
@@ -350,9 +354,11 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     const int4 tile = a.tiles[unit % a.max_tiles];
     if (tile.z == 0) continue;
     const bool fits = tile.x >= 0 && tile.x < a.n_adapters && tile.y >= 0 && tile.z > 0 && tile.z <= 16 && tile.y <= a.n_tokens - tile.z;
-    int row0 = 0, r = 0;
+    int row0 = 0, r = 0, tok0 = -1, tok1 = -1;                // this lane's tokens: rows g and g + 8 of the tile
     float scale = 0.f;
     if (fits) {
+      if (g < tile.z) tok0 = a.order[tile.y + g];
+      if (g + 8 < tile.z) tok1 = a.order[tile.y + g + 8];
       row0 = a.table[2 * tile.x];
       r = a.table[2 * tile.x + 1];
       scale = a.scale[tile.x];
@@ -362,20 +368,12 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       continue;
     }
     if (r == 0) continue;
-    __syncthreads();                                          // the unit before this one is done with token and frag
-    if (tid < 16) {
-      int k = -1;
-      if (tid < tile.z) {
-        k = a.order[tile.y + tid];
-        if (k < 0 || k >= a.n_tokens) {
-          k = -1;
-          atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
-        }
-      }
-      token[tid] = k;
+    if ((g < tile.z && (tok0 < 0 || tok0 >= a.n_tokens)) || (g + 8 < tile.z && (tok1 < 0 || tok1 >= a.n_tokens))) {
+      atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+      if (tok0 >= a.n_tokens) tok0 = -1;
+      if (tok1 >= a.n_tokens) tok1 = -1;
     }
-    __syncthreads();
-    const int tok0 = token[g], tok1 = token[g + 8];
+    __syncthreads();                                          // the unit before this one is done with frag
     const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
     const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
     char* y0 = static_cast<char*>(t.y) + (int64_t)(tok0 < 0 ? 0 : tok0) * t.ldy * size;
@@ -965,12 +963,17 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   const bool many = a.tile == kLargeTile;
   const int type = tasks[0].y_type;
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank, many) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank, many) : choose<QMV_F16>(g->max_rank, many);
-  a.cluster = kCluster;
   const size_t smem = c.smem;
   int per_sm = 0;
   int rc = kernel_fit(c.kernel, kLoraThreads, smem, &per_sm);
   if (rc) return rc;
-  const int64_t units = (int64_t)(many ? (g->max_tiles + a.window - 1) / a.window : g->max_tiles) * n_tasks, resident = (int64_t)sm_count() * per_sm / a.cluster;
+  const int64_t units = (int64_t)(many ? (g->max_tiles + a.window - 1) / a.window : g->max_tiles) * n_tasks, blocks = (int64_t)sm_count() * per_sm;
+  // Few units are cut into eight blocks each; more of them into four or two, as long as all make no more than two rounds, since a
+  // unit has two meetings of its cluster whatever its size. 64 tokens of 48 adapters, q|k|v: 46.0, 30.6 and 35.4 us with 8, 4 and 2;
+  // 80 tokens of 12 adapters, gate|up: 14.7, 16.6 and 27.8. Windows of many tokens: eight (282 us, 328 with 4, 428 with 2).
+  a.cluster = kCluster;
+  while (!many && a.cluster > 2 && units * a.cluster > 2 * blocks + blocks / 8) a.cluster /= 2;
+  const int64_t resident = blocks / a.cluster;
   // a cluster for every unit, up to eight rounds of them: the device hands them out as others end (units differ by rank and N).
   // Past that they take several each, so that a list with many empty tiles costs few launches of blocks.
   const int clusters = (int)(units < 8 * resident ? units : 8 * resident);
