@@ -735,7 +735,7 @@ int lora_plan(const lora_plan_args* args, void* stream);
  *   y[t][n] += scale[a] * sum_{j < r} B[first + j][n] * (sum_k A[first + j][k] x[t][k]),
  * n < N. Rows of tokens without an adapter stay as they are. The tasks (1 to
  * QMV_LORA_MAX_TASKS: q|k|v, gate|up) share x, the plan, the table and the
- * scales, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
+ * scales, have one y_type, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
  * and ldx multiples of 8; y: [n_tokens][ldy] of y_type, as the projection left
  * it (rows of 32-byte alignment are fastest). n_tokens, n_adapters and max_tiles
  * are the plan's. max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
@@ -748,6 +748,9 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * A tile, place or adapter outside its array, a rank over max_rank or rows
  * outside the pool set QMV_ERR_CORRUPT in the device error word, and that tile
  * (or place) is left out.
+ * workspace: device, 16-byte aligned, lora_workspace_size(n_tokens, n_adapters,
+ * max_rank, n_tasks) bytes, which is 0 where the call needs none (few tokens per
+ * adapter). It needs no clearing; calls that overlap on the GPU need one each.
  */
 typedef struct {
   const void* a;             /* bf16 [pool_rows][lda] */
@@ -766,8 +769,11 @@ typedef struct {
   const int32_t* tiles;      /* [max_tiles][4] */
   const int32_t* table;      /* [n_adapters][2] */
   const float* scale;        /* [n_adapters] */
+  void* workspace;           /* nullable where its size is 0 */
+  size_t ws_bytes;
 } lora_args;
 
+size_t lora_workspace_size(int64_t n_tokens, int64_t n_adapters, int32_t max_rank, int32_t n_tasks);
 int lora_run(const lora_args* args, const lora_task* tasks, int n_tasks, void* stream);
 
 /*

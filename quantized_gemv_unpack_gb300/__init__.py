@@ -38,7 +38,7 @@ EXPORTS = ("qmv_pack_desc", "qmv_pack_ternary", "qmv_pack_int4", "qmv_unpack", "
            "cass_speculate_step", "moe_workspace_size", "moe_qmv_run", "moe_qmv_run_static",
            "kv8_desc", "kv_max_runs", "kv_plan", "rope_desc", "rope_run", "kv8_append", "kv8_read",
            "kv8_attend_workspace_size", "kv8_attend_init", "kv8_attend",
-           "qmv_embed", "lora_tile", "lora_max_tiles", "lora_plan", "lora_run", "logprob_run",
+           "qmv_embed", "lora_tile", "lora_max_tiles", "lora_plan", "lora_workspace_size", "lora_run", "logprob_run",
            "qmv_file_write", "qmv_file_open", "qmv_file_count", "qmv_file_tensor", "qmv_file_find", "qmv_file_load",
            "qmv_file_read_host", "qmv_file_close", "qmv_crc32", "qmv_check_status", "qmv_last_error")
 
@@ -113,7 +113,7 @@ class lora_task(ctypes.Structure):
 class lora_args(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("K", "n_tokens", "n_adapters", "max_tiles", "pool_rows", "max_rank")] + [
-        (n, ctypes.c_void_p) for n in ("order", "tiles", "table", "scale")]
+        (n, ctypes.c_void_p) for n in ("order", "tiles", "table", "scale", "workspace")] + [("ws_bytes", ctypes.c_size_t)]
 
 
 class logprob_args(ctypes.Structure):
@@ -162,6 +162,7 @@ _SIGS = {
     "lora_tile": (ctypes.c_int32, [_I64]),
     "lora_max_tiles": (_I64, [_I64, _I64]),
     "lora_plan": (_I32, [ctypes.POINTER(lora_plan_args), _P]),
+    "lora_workspace_size": (ctypes.c_size_t, [_I64, _I64, ctypes.c_int32, ctypes.c_int32]),
     "lora_run": (_I32, [ctypes.POINTER(lora_args), ctypes.POINTER(lora_task), _I32, _P]),
     "logprob_run": (_I32, [ctypes.POINTER(logprob_args), _P]),
     "qmv_file_write": (_I32, [ctypes.c_char_p, _I32, ctypes.POINTER(ctypes.c_char_p), _DESC, ctypes.POINTER(_P)]),
@@ -230,6 +231,14 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _use_on(workspace, s, streams):
+    """The caller does not see a workspace that a class has made, so its memory is not given out again before stream s is done with it."""
+    import torch
+    if not torch.cuda.is_current_stream_capturing():   # a graph's memory lives as long as what it was captured from
+        workspace.record_stream(torch.cuda.ExternalStream(s, device=workspace.device))
+        streams.add(s)
 
 
 def _ready(f, first, *rest):
@@ -725,6 +734,10 @@ def lora_max_tiles(n_tokens: int, n_adapters: int) -> int:
     return int(lib().lora_max_tiles(n_tokens, n_adapters))
 
 
+def lora_workspace_size(n_tokens: int, n_adapters: int, max_rank: int, n_tasks: int) -> int:
+    return int(lib().lora_workspace_size(n_tokens, n_adapters, max_rank, n_tasks))
+
+
 class LoraPlan:
     """lora_plan: a step's tokens grouped by adapter. ids [tokens] (int32): each token's adapter, negative for none. run()
     fills order [tokens] and tiles [max_tiles][4], which the Lora calls of all layers of the step read."""
@@ -748,9 +761,11 @@ class Lora:
     """lora_run: each token's adapter added to the outputs of projections that share x [tokens][K] (bf16). table [adapters][2]
     (int32): an adapter's first rank row and its rank; scale [adapters] (fp32). tasks: (a, b, y) per projection: the pools of
     rank rows a [rows][K] and b [rows][N] (bf16), and y [tokens][N], to which the projection has written. max_rank bounds
-    the ranks in the table; a lower bound gives a leaner kernel. The plan's run() comes first, once per step."""
+    the ranks in the table; a lower bound gives a leaner kernel. The plan's run() comes first, once per step. Calls of many
+    tokens need a workspace of lora_workspace_size bytes: one is made where none is given; layers of one stream should share it
+    (its `workspace`)."""
 
-    def __init__(self, plan: LoraPlan, table, scale, x, tasks, max_rank: int = QMV_LORA_MAX_RANK):
+    def __init__(self, plan: LoraPlan, table, scale, x, tasks, max_rank: int = QMV_LORA_MAX_RANK, workspace=None):
         import torch
         dev = x.device
         T, A = plan.ids.shape[0], plan.n_adapters
@@ -778,11 +793,21 @@ class Lora:
             k.b, k.ldb = _matrix(f"task {i}: b", b, rows, None, dev)
             k.y, k.ldy = _matrix(f"task {i}: y", y, T, b.shape[1], dev)
             k.N, k.y_type = b.shape[1], _dtype(y)
+        need = lora_workspace_size(T, A, max_rank, len(tasks))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if self.workspace.device != dev or not self.workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous tensor on {dev} expected")
+        # a workspace made here: the streams that its memory is known to be used on
+        self._streams = {_stream(None)} if workspace is None and need else None
+        g.workspace, g.ws_bytes = self.workspace.data_ptr(), self.workspace.numel() * self.workspace.element_size()
         self.keep = (plan, table, scale, x, tasks)
         self._call, self._args = lib().lora_run, (ctypes.byref(g), self.tasks, len(tasks))
 
     def run(self, stream=None):
-        _check(self._call(*self._args, _stream(stream)))
+        s = _stream(stream)
+        if self._streams is not None and s not in self._streams:
+            _use_on(self.workspace, s, self._streams)
+        _check(self._call(*self._args, s))
 
 
 class LogProb:

@@ -187,7 +187,8 @@ struct RunArgs {
   const float* scale;
   int* err;
   int64_t ldx;
-  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks, cluster, tile, window;
+  int32_t K, n_tokens, n_adapters, pool_rows, max_tiles, n_tasks, cluster, tile, window, window2, slices;
+  uint4* values;               // many tokens: what lies between the products, as the second one takes it
   Task t[QMV_LORA_MAX_TASKS];
 };
 
@@ -210,9 +211,6 @@ __device__ __forceinline__ float4 ld_remote(uint32_t p) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
   return v;
-}
-__device__ __forceinline__ void st_remote(uint32_t p, uint4 v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 // Sixteen bytes from memory to shared memory, asynchronously.
 __device__ __forceinline__ void copy16(uint32_t to, const void* p) {
@@ -556,206 +554,255 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   if (reading) cluster_wait();
 }
 
-// ---- many tokens
+// ---- many tokens of an adapter
 //
-// A cluster takes up to 128 tokens of one adapter (a window of the plan's tiles, run by run). In the first product a warp
-// owns 16 tokens and takes A from shared memory, so its sums need no other warp's. In the second it owns 32 columns: their
-// values of B stay in its registers while the tokens pass by, without a barrier. x and y come through a ring of asynchronous
-// copies, in which each lane finds what it has asked for itself: registers as the targets of loads that far ahead were slower
-// (a wait for one of them waits for all: 470 us for 8190 tokens).
-constexpr int kLongBlocks = 8;                                // 16-token blocks of a window: one per warp
-constexpr int kLongTokens = 16 * kLongBlocks;
+// Two kernels, with the values between them in the caller's workspace as the fragments of the second: one cluster's meeting
+// per run of tokens would leave the memory idle for a third of the time (in one kernel: 282 us for 8190 tokens).
+//
+// lora_first_kernel: a cluster takes a run of up to 128 tokens of one adapter and one projection, each block an eighth of K.
+// A warp owns 16 tokens, whose x it copies for itself; A's columns are shared, 64 at a time, four groups in flight. The
+// blocks' sums meet in distributed shared memory.
+//
+// lora_second_kernel: a block takes 256 columns and a window of tokens. A warp owns 32 columns: their values of B stay in its
+// registers while the tokens pass by; y comes through a ring in which each lane finds what it has asked for itself (registers
+// as the targets of loads that far ahead were slower: a wait for one of them waits for all).
+constexpr int kRunBlocks = 8;                                 // 16-token blocks of a run of the first kernel: one per warp
+constexpr int kMostBlocks = 16;                               // of a window of the second
 
 template <int NB, int Y>
-struct Long {
+struct Many {
   static constexpr bool F32 = Y == QMV_F32;
   static constexpr int kSteps = NB / 2, kParts3 = F32 ? 3 : 2;
-  static constexpr int kWords = kLongBlocks * kSteps * 64;    // 16-byte words of the window's fp32 values
-  static constexpr int kFrag = kLongBlocks * kSteps * kParts3 * 32;
-  static constexpr int kCols = 128;                           // columns of A at a time, two of them in shared memory
-  static constexpr int kChunk = 8 * NB * kCols * 2;
-  static constexpr int kRing = 8192;                          // bytes of a warp's ring
-  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kAheadY = kRing / kBlockY;
-  static constexpr int kAheadX = kRing / 1024;                // k32 steps of 16 tokens
-  static constexpr int kFirst = kWords * 16 > kLoraWarps * kRing ? kWords * 16 : kLoraWarps * kRing;
-  static constexpr int kSmem = kFirst + (2 * kChunk > kFrag * 16 ? 2 * kChunk : kFrag * 16) + kLongTokens * (int)sizeof(int64_t);
+  static constexpr int kBlockWords = kSteps * kParts3 * 32;   // 16-byte words of a 16-token block's finished values
+  // first kernel
+  static constexpr int kWords = kRunBlocks * kSteps * 64;     // 16-byte words of the run's fp32 values
+  static constexpr int kCols = 64, kGroups = 4, kChunk = 8 * NB * kCols * 2, kRing = kGroups * 2048;
+  static constexpr int kSmem1 = kWords * 16 > kLoraWarps * kRing + kGroups * kChunk ? kWords * 16 : kLoraWarps * kRing + kGroups * kChunk;
+  // second kernel
+  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kAheadY = 8192 / kBlockY;
+  static constexpr int kChunkBlocks = kBlockWords * 16 * 8 > 36 * 1024 ? 2 : 4, kChunkH = kChunkBlocks * kBlockWords * 16;
+  static constexpr int kSmem2 = kLoraWarps * 8192 + 2 * kChunkH + 16 * kMostBlocks * (int)sizeof(int64_t);
 };
 
+// Whether tile v continues the run of tile u before it.
+__device__ __forceinline__ bool fits(const RunArgs& a, const int4& v) {
+  return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
+}
+__device__ __forceinline__ bool follows(const RunArgs& a, const int4& u, const int4& v) {
+  return fits(a, u) && fits(a, v) && u.x == v.x && u.z == a.tile && u.y + u.z == v.y;
+}
+
 template <int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel(const __grid_constant__ RunArgs a) {
-  using S = Long<NB, Y>;
-  constexpr bool F32 = S::F32;
-  constexpr int KS = S::kSteps, P3 = S::kParts3, size = F32 ? 4 : 2, WORDS = F32 ? 8 : 4, AY = S::kAheadY;
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_first_kernel(const __grid_constant__ RunArgs a) {
+  using S = Many<NB, Y>;
+  constexpr int KS = S::kSteps, P3 = S::kParts3, G = S::kGroups;
   extern __shared__ __align__(16) unsigned char lora_smem[];
-  float4* mine = reinterpret_cast<float4*>(lora_smem);        // this block's sums, which the cluster reads; before and after them the rings
-  unsigned char* chunks = lora_smem + S::kFirst;         // two of A
-  uint4* frag = reinterpret_cast<uint4*>(chunks);             // after them: [blocks][KS][P3][32], the parts of the finished values
-  int64_t* row_y = reinterpret_cast<int64_t*>(lora_smem + S::kSmem) - kLongTokens;   // bytes to each token's row of y; negative: none
+  float4* mine = reinterpret_cast<float4*>(lora_smem);        // after the columns: this block's sums, which the cluster reads
+  unsigned char* chunks = lora_smem + kLoraWarps * S::kRing;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int rank = (int)cluster_rank(), C = a.cluster, clusters = gridDim.x / C;
-  const uint32_t chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
-  constexpr int PER = S::kCols / 8, ROWS = kLoraThreads / PER, TURNS = 8 * NB / ROWS;   // 16-byte pieces of a row of A; rows at a time
+  unsigned char* ring = lora_smem + warp * S::kRing + lane * 16;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring), chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
+  constexpr int PER = S::kCols / 8, ROWS = kLoraThreads / PER, TURNS = (8 * NB + ROWS - 1) / ROWS;   // 16-byte pieces of a row of A; rows at a time
   const int c1 = tid % PER, r1 = tid / PER;
-  unsigned char* ring = lora_smem + warp * S::kRing + lane * 16;   // this lane's 16 bytes of each 512
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
-  const uint32_t to_a = (r1 * PER + (c1 ^ ((r1 & 1) << 2))) * 16;
-  const int windows = (a.max_tiles + a.window - 1) / a.window;
+  const uint32_t to_a = chunks_at + (r1 * PER + (c1 ^ ((r1 & 1) << 2))) * 16;
   follow_previous();
-  for (int unit = blockIdx.x / C; unit < windows * a.n_tasks; unit += clusters) {
-    const Task& t = a.t[unit / windows];
-    const int base = unit % windows * a.window, tiles = min(a.window, a.max_tiles - base);
-    for (int j = 0; j < tiles;) {
-      const int4 tile = a.tiles[base + j++];
-      if (tile.z == 0) break;
-      const auto fits = [&](const int4& v) {
-        return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
-      };
-      int row0 = 0, r = 0;
-      float scale = 0.f;
-      const bool good = fits(tile);
-      if (good) {
-        row0 = a.table[2 * tile.x];
-        r = a.table[2 * tile.x + 1];
-        scale = a.scale[tile.x];
-      }
-      if (!good || row0 < 0 || r < 0 || r > 8 * NB || row0 > a.pool_rows - r) {
-        if (rank == 0 && tid == 0) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
-        continue;
-      }
-      if (r == 0) continue;
-      int count = tile.z;
-      for (; j < tiles; ++j) {                                // the adapter's next tiles
-        const int4 v = a.tiles[base + j];
-        if (!fits(v) || v.x != tile.x || v.y != tile.y + count || count + v.z > kLongTokens) break;
-        count += v.z;
-      }
-      __syncthreads();                                        // the run before this one is done with token and frag
-      const auto token_at = [&](int i) {                      // of this run; -1 past its end, and for a place outside
-        const int k = i < count ? a.order[tile.y + i] : -1;
-        return k < a.n_tokens ? k : -1;
-      };
-      const int tok0 = token_at(warp * 16 + g), tok1 = token_at(warp * 16 + g + 8);
-      if (tid < kLongTokens) {
-        int k = -1;
-        if (tid < count) {
-          k = a.order[tile.y + tid];
-          if (k < 0 || k >= a.n_tokens) {
-            k = -1;
-            atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
-          }
-        }
-        row_y[tid] = k < 0 ? -1 : (int64_t)k * t.ldy * size;
-      }
-      const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 32 - 1) / (C * 32) * 32;
-      const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
-
-      // ---- first product, over this block's share of K
-      const int chunk_count = k_hi > k_lo ? (k_hi - k_lo + S::kCols - 1) / S::kCols : 0;
-      const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + k_lo + 8 * c1;
-      const int64_t step_a = ROWS * t.lda;
-      const auto load = [&](int q) {
-        if (q < chunk_count && k_lo + q * S::kCols + 8 * c1 < k_hi) {
-          const __nv_bfloat16* p = pa + q * S::kCols;
-          const uint32_t to = chunks_at + (q & 1) * S::kChunk + to_a;
+  for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
+    const Task& t = a.t[unit / a.max_tiles];
+    const int first = unit % a.max_tiles;
+    const int4 tile = a.tiles[first];
+    if (tile.z == 0) continue;
+    if (first % a.window && follows(a, a.tiles[first - 1], tile)) continue;   // another unit's
+    int row0 = 0, r = 0;
+    float scale = 1.f;                                        // 16-bit y: part of these values; fp32: of the second product's sums
+    const bool good = fits(a, tile);
+    if (good) {
+      row0 = a.table[2 * tile.x];
+      r = a.table[2 * tile.x + 1];
+      if constexpr (!S::F32) scale = a.scale[tile.x];
+    }
+    if (!good || row0 < 0 || r < 0 || r > 8 * NB || row0 > a.pool_rows - r) {
+      if (rank == 0 && tid == 0) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+      continue;
+    }
+    if (r == 0) continue;
+    int count = tile.z;
+    for (int4 last = tile; (first + (count - 1) / a.tile + 1) % a.window && first + (count - 1) / a.tile + 1 < a.max_tiles;) {
+      const int4 v = a.tiles[first + (count - 1) / a.tile + 1];
+      if (!follows(a, last, v)) break;
+      count += v.z;
+      last = v;
+    }
+    const auto token_at = [&](int i) {                        // of this run; -1 past its end, and for a place outside
+      const int k = i < count ? a.order[tile.y + i] : -1;
+      if (i < count && (k < 0 || k >= a.n_tokens)) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+      return k < a.n_tokens ? k : -1;
+    };
+    const int tok0 = token_at(warp * 16 + g), tok1 = token_at(warp * 16 + g + 8);
+    const bool used = warp * 16 < count;
+    const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx + 8 * t4;
+    const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx + 8 * t4;
+    const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share);
+    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + 8 * c1;
+    const int64_t step_a = ROWS * t.lda;
+    int k_next = k_lo, slot_in = 0, slot = 0;
+    const auto ask = [&]() {
+      if (k_next < k_hi) {
+        if (k_next + 8 * c1 < k_hi) {
+          const __nv_bfloat16* p = pa + k_next;
 #pragma unroll
           for (int i = 0; i < TURNS; ++i, p += step_a) {
             if (r1 + i * ROWS >= r) break;
-            copy16(to + i * (ROWS * PER * 16), p);
+            copy16(to_a + slot_in * S::kChunk + i * (ROWS * PER * 16), p);
           }
         }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int k = k_next + 32 * e;
+          if (k + 8 * t4 < k_hi) {
+            if (tok0 >= 0) copy16(ring_at + slot_in * 2048 + e * 1024, x0 + k);
+            if (tok1 >= 0) copy16(ring_at + slot_in * 2048 + e * 1024 + 512, x1 + k);
+          }
+        }
+        k_next += S::kCols;
+      }
+      copies_end();
+      slot_in = slot_in + 1 == G ? 0 : slot_in + 1;
+    };
+    // what no copy reaches is 0: rows past the rank up to a block of eight, tokens that are none
+    for (int i = tid; i < G * 8 * PER; i += kLoraThreads) {
+      const int j = r / 8 * 8 + i / PER % 8;
+      if (r % 8 && j >= r) *reinterpret_cast<uint4*>(chunks + i / (8 * PER) * S::kChunk + (j * PER + i % PER) * 16) = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      if (tok0 < 0) *reinterpret_cast<uint4*>(ring + i * 1024) = make_uint4(0, 0, 0, 0);
+      if (tok1 < 0) *reinterpret_cast<uint4*>(ring + i * 1024 + 512) = make_uint4(0, 0, 0, 0);
+    }
+    for (int i = 0; i < G - 1; ++i) ask();
+    float acc[NB][4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int k0 = k_lo; k0 < k_hi; k0 += S::kCols) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(G - 2) : "memory");
+      __syncthreads();                                        // these columns are there, and those before them have been read
+      ask();
+      if (used) {
+        const unsigned char* st = chunks + slot * S::kChunk + g * (PER * 16);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const unsigned char* sa = st + (((e * 4 + t4) ^ ((g & 1) << 2)) * 16);
+          uint4 p = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024), o = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024 + 512);
+          const bool in = k0 + 32 * e + 8 * t4 < k_hi;
+          if (k0 + S::kCols > k_hi && !in) p = o = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            if (8 * i >= r) break;
+            uint4 w = *reinterpret_cast<const uint4*>(sa + i * (8 * PER * 16));
+            if (k0 + S::kCols > k_hi && !in) w = make_uint4(0, 0, 0, 0);   // the last columns: what lies past them was not copied
+            mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
+            mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
+          }
+        }
+      }
+      slot = slot + 1 == G ? 0 : slot + 1;
+    }
+    __syncthreads();                                          // all columns have been read: their place is that of the sums
+    if (used) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i) mine[(warp * NB + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    }
+    cluster_arrive();
+    cluster_wait();
+    // the cluster's sums, a share in each block: an item is a lane's eight values of one k16 step
+    const int blocks = (count + 15) / 16, items = blocks * KS * 32, share = (items + C - 1) / C;
+    uint4* to = a.values + ((int64_t)(unit / a.max_tiles) * a.max_tiles + first) * (a.tile / 16) * S::kBlockWords;
+    for (int i = rank * share + tid; i < min(items, (rank + 1) * share); i += kLoraThreads) {
+      const int at = (i / 32) * 64 + i % 32;
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 8
+      for (int c = 0; c < C; ++c) {
+        const uint32_t m = remote(mine + at, c);
+        const float4 e = ld_remote(m), f = ld_remote(m + 32 * 16);
+        u.x += e.x, u.y += e.y, u.z += e.z, u.w += e.w;
+        v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
+      }
+      if constexpr (!S::F32) {
+        u.x *= scale, u.y *= scale, u.z *= scale, u.w *= scale;
+        v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+      }
+#pragma unroll
+      for (int k = 0; k < P3; ++k) {
+        uint4 f;
+        f.x = split(u.x, u.y);
+        f.y = split(u.z, u.w);
+        f.z = split(v.x, v.y);
+        f.w = split(v.z, v.w);
+        to[((i / 32) * P3 + k) * 32 + i % 32] = f;
+      }
+    }
+    cluster_arrive();
+    cluster_wait();                                           // the blocks' sums have been read
+  }
+}
+
+template <int NB, int Y>
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_second_kernel(const __grid_constant__ RunArgs a) {
+  using S = Many<NB, Y>;
+  constexpr int KS = S::kSteps, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, AY = S::kAheadY, CB = S::kChunkBlocks;
+  constexpr bool F32 = S::F32;
+  extern __shared__ __align__(16) unsigned char lora_smem[];
+  unsigned char* chunks = lora_smem + kLoraWarps * 8192;      // two of finished values, each of kChunkBlocks 16-token blocks
+  int64_t* row_y = reinterpret_cast<int64_t*>(chunks + 2 * S::kChunkH);   // bytes to each token's row of y; negative: none
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  unsigned char* ring = lora_smem + warp * 8192 + lane * 16;
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring), chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
+  const int windows = (a.max_tiles + a.window2 - 1) / a.window2;
+  follow_previous();
+  for (int unit = blockIdx.x; unit < windows * a.slices; unit += gridDim.x) {
+    int slice = unit % a.slices, task = 0;
+    while (slice >= (a.t[task].N + 255) / 256) slice -= (a.t[task++].N + 255) / 256;
+    const Task& t = a.t[task];
+    const int base = unit / a.slices * a.window2, tiles = min(a.window2, a.max_tiles - base);
+    const int n0 = slice * 256 + warp * 32, n = n0 + 8 * t4, col = n0 + 4 * g;   // this warp's columns; the first of this lane's sums, and of its loads of B
+    const bool whole = t.wide && n + 8 <= t.N;
+    char* y = static_cast<char*>(t.y);
+    for (int j = 0; j < tiles;) {
+      const int first = base + j++;
+      const int4 tile = a.tiles[first];
+      if (tile.z == 0) break;
+      if (!fits(a, tile)) continue;                           // reported by the first kernel, as is a bad adapter
+      const int row0 = a.table[2 * tile.x], r = a.table[2 * tile.x + 1];
+      float scale = 1.f;                                      // 16-bit y: the finished values have it
+      if constexpr (F32) scale = a.scale[tile.x];
+      if (row0 < 0 || r <= 0 || r > 8 * NB || row0 > a.pool_rows - r) continue;
+      int count = tile.z;
+      for (int4 last = tile; j < tiles; ++j) {                // the adapter's next tiles
+        const int4 v = a.tiles[base + j];
+        if (!follows(a, last, v)) break;
+        count += v.z;
+        last = v;
+      }
+      __syncthreads();                                        // the run before this one is done with row_y and the chunks
+      if (tid < count) {
+        const int k = a.order[tile.y + tid];
+        row_y[tid] = k < 0 || k >= a.n_tokens ? -1 : (int64_t)k * t.ldy * size;
+      } else if (tid < (count + 15) / 16 * 16) {
+        row_y[tid] = -1;
+      }
+      const int blocks = (count + 15) / 16;
+      const uint4* values = a.values + ((int64_t)task * a.max_tiles + first) * (a.tile / 16) * S::kBlockWords;
+      const auto load = [&](int c) {                          // chunk c of the finished values
+        const int words = min(CB, blocks - c * CB) * S::kBlockWords;
+        for (int i = tid; i < words; i += kLoraThreads)
+          copy16(chunks_at + (c & 1) * S::kChunkH + i * 16, values + (int64_t)c * CB * S::kBlockWords + i);
         copies_end();
       };
       load(0);
       __syncthreads();
-      const bool used = warp * 16 < count;
-      const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
-      const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
-      // the ring's groups are those of the chunks of A too: one of each for a chunk, then one for each step
-      constexpr int AX = S::kAheadX, STEPS = S::kCols / 32;
-      int k_ahead = k_lo + 8 * t4, slot_in = 0, slot = 0;
-      const auto ahead = [&]() {
-        if (used && k_ahead < k_hi) {
-          if (tok0 >= 0) copy16(ring_at + slot_in * 1024, x0 + k_ahead);
-          if (tok1 >= 0) copy16(ring_at + slot_in * 1024 + 512, x1 + k_ahead);
-        }
-        copies_end();
-        k_ahead += 32;
-        slot_in = slot_in + 1 == AX ? 0 : slot_in + 1;
-      };
-      for (int i = 0; i < AX - 1; ++i) ahead();
-      float acc[NB][4];
-#pragma unroll
-      for (int i = 0; i < NB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-      for (int q = 0; q < chunk_count; ++q) {
-        // chunk q was asked for before the latest STEPS (the first: AX - 1) steps of x
-        asm volatile("cp.async.wait_group %0;" ::"n"(STEPS < AX - 1 ? STEPS : AX - 1) : "memory");
-        __syncthreads();                                      // chunk q is there, and q - 1 has been read
-        load(q + 1);
-        const unsigned char* st = chunks + (q & 1) * S::kChunk + g * (PER * 16);
-#pragma unroll
-        for (int e = 0; e < STEPS; ++e) {
-          ahead();
-          // since step e: AX - 1 more steps, and a chunk of A
-          asm volatile("cp.async.wait_group %0;" ::"n"(AX - 1) : "memory");
-          const int k = k_lo + q * S::kCols + 32 * e + 8 * t4;
-          uint4 p = make_uint4(0, 0, 0, 0), o = p;
-          if (k < k_hi && tok0 >= 0) p = *reinterpret_cast<const uint4*>(ring + slot * 1024);
-          if (k < k_hi && tok1 >= 0) o = *reinterpret_cast<const uint4*>(ring + slot * 1024 + 512);
-          slot = slot + 1 == AX ? 0 : slot + 1;
-          if (used && k - 8 * t4 < k_hi) {
-            const unsigned char* sa = st + (((e * 4 + t4) ^ ((g & 1) << 2)) * 16);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              if (8 * i >= r) break;
-              uint4 w = make_uint4(0, 0, 0, 0);
-              if (8 * i + g < r && k < k_hi) w = *reinterpret_cast<const uint4*>(sa + i * (8 * PER * 16));
-              mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
-              mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
-            }
-          }
-        }
-      }
-      __syncthreads();                                        // the rings have been read: their place is that of the sums
-      if (used) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) mine[(warp * NB + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      }
-      cluster_arrive();
-      cluster_wait();
-
-      // ---- the cluster's sums: each block finishes its share of a lane's eight values of one k16 step, and hands it to all
-      const int items = (count + 15) / 16 * KS * 32, item_share = (items + C - 1) / C;
-      for (int i = rank * item_share + tid; i < min(items, (rank + 1) * item_share); i += kLoraThreads) {
-        const int at = (i / 32) * 64 + i % 32;
-        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-#pragma unroll 8
-        for (int c = 0; c < C; ++c) {
-          const uint32_t m = remote(mine + at, c);
-          const float4 e = ld_remote(m), f = ld_remote(m + 32 * 16);
-          u.x += e.x, u.y += e.y, u.z += e.z, u.w += e.w;
-          v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
-        }
-#pragma unroll
-        for (int k = 0; k < P3; ++k) {
-          uint4 f;
-          f.x = split(u.x, u.y);
-          f.y = split(u.z, u.w);
-          f.z = split(v.x, v.y);
-          f.w = split(v.z, v.w);
-          for (int c = 0; c < C; ++c) st_remote(remote(frag + ((i / 32) * P3 + k) * 32 + i % 32, c), f);
-        }
-      }
-      cluster_arrive();
-      cluster_wait();
-
-      // ---- second product, over this block's share of N
-      const int blocks = (count + 15) / 16;
-      char* y = static_cast<char*>(t.y);
-      int n_in = n_lo + warp * 32, m_in = 0;                  // the next block of y to ask for
-      slot_in = slot = 0;
-      const auto ahead_y = [&]() {
-        const int n = n_in + 8 * t4;
-        if (t.wide && n_in < n_hi && n + 8 <= t.N) {
+      int m_in = 0, slot_in = 0, slot = 0;                    // the next block of y to ask for
+      const auto ask = [&]() {
+        if (whole && m_in < blocks) {
           const int64_t ta = row_y[m_in * 16 + g], tb = row_y[m_in * 16 + g + 8];
           const uint32_t to = ring_at + slot_in * S::kBlockY;
           const char* q = y + (int64_t)n * size;
@@ -769,72 +816,105 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel
           }
         }
         copies_end();
-        if (++m_in == blocks) m_in = 0, n_in += kLoraWarps * 32;
+        ++m_in;
         slot_in = slot_in + 1 == AY ? 0 : slot_in + 1;
       };
-      for (int i = 0; i < AY - 2; ++i) ahead_y();
-#pragma unroll 1
-      for (int n0 = n_lo + warp * 32; n0 < n_hi; n0 += kLoraWarps * 32) {
-        const int n = n0 + 8 * t4, col = n0 + 4 * g;          // first column of this lane's sums, and of its loads of B
-        const bool whole = t.wide && n + 8 <= t.N;
-        uint32_t b[KS][4][2];
-        const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
+      for (int i = 0; i < AY - 2; ++i) ask();
+      uint32_t b[KS][4][2];
+      const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          uint2 w[4];
+      for (int s = 0; s < KS; ++s) {
+        uint2 w[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int off = 16 * s + (i & 1) + 8 * (i >> 1);
-            w[i] = make_uint2(0, 0);
-            if (off + 2 * t4 < r && col < t.N) {
-              const __nv_bfloat16* q = pb + (int64_t)off * t.ldb;
-              if (col + 4 <= t.N) {
-                w[i] = __ldg(reinterpret_cast<const uint2*>(q));
-              } else {
-                const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
-                w[i].x = e[0] | (col + 1 < t.N ? (uint32_t)e[1] << 16 : 0u);
-                w[i].y = col + 2 < t.N ? e[2] : 0u;
-              }
+        for (int i = 0; i < 4; ++i) {
+          const int off = 16 * s + (i & 1) + 8 * (i >> 1);
+          w[i] = make_uint2(0, 0);
+          if (off + 2 * t4 < r && col < t.N) {
+            const __nv_bfloat16* q = pb + (int64_t)off * t.ldb;
+            if (col + 4 <= t.N) {
+              w[i] = __ldg(reinterpret_cast<const uint2*>(q));
+            } else {
+              const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
+              w[i].x = e[0] | (col + 1 < t.N ? (uint32_t)e[1] << 16 : 0u);
+              w[i].y = col + 2 < t.N ? e[2] : 0u;
             }
           }
+        }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            b[s][0][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x5410);
-            b[s][1][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x7632);
-            b[s][2][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x5410);
-            b[s][3][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x7632);
+        for (int i = 0; i < 2; ++i) {
+          b[s][0][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x5410);
+          b[s][1][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x7632);
+          b[s][2][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x5410);
+          b[s][3][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x7632);
+        }
+      }
+      // Block m's values of y: fp32 ones are added in the end (one rounding), 16-bit ones are what the products are added to.
+      const auto begin = [&](int m, float (&d)[4][4], uint32_t (&v)[2][WORDS]) {
+        const unsigned char* sy = ring + slot * S::kBlockY;
+        slot = slot + 1 == AY ? 0 : slot + 1;
+        ld_pieces(sy, v[0]);
+        ld_pieces(sy + S::kBlockY / 2, v[1]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i / 4][i % 4] = 0.f;
+        if constexpr (!F32) {
+          if (whole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 f = unpack2<Y>(v[i / 4][i % 4]);
+              const int c = 2 * (i % 4), hi = 2 * (i / 4);
+              d[c % 4][hi + c / 4] = f.x;
+              d[(c + 1) % 4][hi + (c + 1) / 4] = f.y;
+            }
           }
         }
-        const auto finish_block = [&](int m, const float (&d)[4][4]) {
-          const int64_t ta = row_y[m * 16 + g], tb = row_y[m * 16 + g + 8];
-          const unsigned char* sy = ring + slot * S::kBlockY;
-          slot = slot + 1 == AY ? 0 : slot + 1;
-          uint32_t v[WORDS];
-          char* q = y + (int64_t)n * size;
-          if (whole) {
-            if (ta >= 0) ld_pieces(sy, v), add_row<Y, 0>(q + ta, scale, d, v);
-            if (tb >= 0) ld_pieces(sy + S::kBlockY / 2, v), add_row<Y, 1>(q + tb, scale, d, v);
+      };
+      const auto finish = [&](int m, const float (&d)[4][4], uint32_t (&v)[2][WORDS]) {
+        const int64_t ta = row_y[m * 16 + g], tb = row_y[m * 16 + g + 8];
+        char* q = y + (int64_t)n * size;
+        if (whole) {
+          if constexpr (F32) {
+            if (ta >= 0) add_row<Y, 0>(q + ta, scale, d, v[0]);
+            if (tb >= 0) add_row<Y, 1>(q + tb, scale, d, v[1]);
           } else {
-            if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
-            if (tb >= 0) add_row_part<Y, 1>(q + tb, t.N - n, scale, d);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = 2 * (i % 4), hi = 2 * (i / 4);
+              v[i / 4][i % 4] = pack2<Y>(d[c % 4][hi + c / 4], d[(c + 1) % 4][hi + (c + 1) / 4]);
+            }
+            if (ta >= 0) st_global(q + ta, v[0]);
+            if (tb >= 0) st_global(q + tb, v[1]);
           }
-        };
+        } else {
+          if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
+          if (tb >= 0) add_row_part<Y, 1>(q + tb, t.N - n, scale, d);
+        }
+      };
+      for (int c = 0; c * CB < blocks; ++c) {
+        // since chunk c: the prologue's AY - 2 groups of y, or the CB of the chunk before this one
+        if (c == 0) asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
+        else asm volatile("cp.async.wait_group %0;" ::"n"(CB) : "memory");
+        __syncthreads();                                      // chunk c is there, and c - 1 has been read
+        if ((c + 1) * CB < blocks) load(c + 1);
+        else copies_end();
         // two blocks at a time: twice the products that wait for no other
 #pragma unroll 1
-        for (int m = 0; m < blocks; m += 2) {
+        for (int m = c * CB; m < min(blocks, (c + 1) * CB); m += 2) {
           const bool two = m + 1 < blocks;
-          ahead_y();
-          if (two) ahead_y();
+          ask();
+          if (two) ask();
+          // since these blocks' copies: AY - 2 groups of y, and of the finished values one or more
+          asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
           float d[2][4][4];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) d[i / 16][i / 4 % 4][i % 4] = 0.f;
-          const uint4* h = frag + m * (KS * P3 * 32) + lane;
+          uint32_t v[2][2][WORDS];
+          begin(m, d[0], v[0]);
+          if (two) begin(m + 1, d[1], v[1]);
+          const uint4* h = reinterpret_cast<const uint4*>(chunks + (c & 1) * S::kChunkH) + (m - c * CB) * S::kBlockWords + lane;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             if (16 * s >= r) break;
 #pragma unroll
             for (int k = P3 - 1; k >= 0; --k) {
-              const uint4 e = h[(s * P3 + k) * 32], f = h[(KS * P3 + s * P3 + k) * 32];   // past the last block: of no use
+              const uint4 e = h[(s * P3 + k) * 32], f = h[S::kBlockWords + (s * P3 + k) * 32];   // past the last block: of no use
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 mma(d[0][i], e.x, e.y, e.z, e.w, b[s][i][0], b[s][i][1]);
@@ -842,10 +922,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel
               }
             }
           }
-          // since this block's copies: AY - 1 more groups (AY - 2 after a last block without a second: one more has to be there)
-          asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
-          finish_block(m, d[0]);
-          if (two) finish_block(m + 1, d[1]);
+          finish(m, d[0], v[0]);
+          if (two) finish(m + 1, d[1], v[1]);
         }
       }
       copies_wait();
@@ -853,20 +931,25 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_long_kernel
   }
 }
 
-// A kernel and its shared memory.
+// The kernels of a call and their shared memory.
 struct Choice {
-  const void* kernel;
-  int smem;
+  const void* few;
+  const void* first;
+  const void* second;
+  int few_smem, first_smem, second_smem, block_words;
 };
 template <int NB, int Y>
-Choice choice_of(bool many) {
-  if (many) return {reinterpret_cast<const void*>(lora_long_kernel<NB, Y>), Long<NB, Y>::kSmem};
-  return {reinterpret_cast<const void*>(lora_short_kernel<NB, Y>), Short<NB, Y>::kSmem};
+Choice choice_of() {
+  return {reinterpret_cast<const void*>(lora_short_kernel<NB, Y>), reinterpret_cast<const void*>(lora_first_kernel<NB, Y>),
+          reinterpret_cast<const void*>(lora_second_kernel<NB, Y>), Short<NB, Y>::kSmem, Many<NB, Y>::kSmem1, Many<NB, Y>::kSmem2, Many<NB, Y>::kBlockWords};
 }
 template <int Y>
-Choice choose(int max_rank, bool many) {
-  return max_rank <= 16 ? choice_of<2, Y>(many) : max_rank <= 32 ? choice_of<4, Y>(many) : max_rank <= 64 ? choice_of<8, Y>(many) : choice_of<16, Y>(many);
+Choice choose(int max_rank) {
+  return max_rank <= 16 ? choice_of<2, Y>() : max_rank <= 32 ? choice_of<4, Y>() : max_rank <= 64 ? choice_of<8, Y>() : choice_of<16, Y>();
 }
+
+// Whether a call is one of many tokens per adapter, by the tokens that an adapter has on average.
+bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1024; }
 
 }  // namespace
 }  // namespace qmv
@@ -880,6 +963,12 @@ int32_t lora_tile(int64_t n_tokens) { return n_tokens < 1024 ? kSmallTile : kLar
 int64_t lora_max_tiles(int64_t n_tokens, int64_t n_adapters) {
   if (n_tokens <= 0 || n_adapters <= 0) return 0;
   return n_tokens / lora_tile(n_tokens) + (n_tokens < n_adapters ? n_tokens : n_adapters);
+}
+
+size_t lora_workspace_size(int64_t n_tokens, int64_t n_adapters, int32_t max_rank, int32_t n_tasks) {
+  if (n_tokens <= 0 || n_adapters <= 0 || max_rank <= 0 || max_rank > kMaxRank || n_tasks <= 0 || !many_tokens(n_tokens, n_adapters)) return 0;
+  const int64_t steps = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : max_rank <= 64 ? 4 : 8;   // of 16 rank rows, as the kernels are made
+  return (size_t)(lora_max_tiles(n_tokens, n_adapters) * (lora_tile(n_tokens) / 16) * n_tasks * steps * 3 * 512);
 }
 
 int lora_plan(const lora_plan_args* g, void* stream) {
@@ -955,31 +1044,52 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
     a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, (int32_t)(k.ldy * ys % 32 == 0 && (reinterpret_cast<uintptr_t>(k.y) & 31u) == 0)};
   }
   if (g->n_tokens == 0) return QMV_OK;
-  if ((int64_t)g->max_tiles * n_tasks > INT32_MAX / 2) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d tasks", g->max_tiles, n_tasks);
+  if ((int64_t)g->max_tiles * n_tasks > INT32_MAX / 64) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d tasks", g->max_tiles, n_tasks);
+  const size_t need = lora_workspace_size(g->n_tokens, g->n_adapters, g->max_rank, n_tasks);
+  if (need && (!g->workspace || g->ws_bytes < need)) return fail(QMV_ERR_ARG, "workspace of %zu bytes, lora_workspace_size is %zu", g->ws_bytes, need);
+  if (need && !aligned16(g->workspace)) return fail(QMV_ERR_ALIGN, "workspace must be 16-byte aligned");
   a.err = device_error_word();
   if (!a.err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
   a.tile = lora_tile(g->n_tokens);
-  a.window = 2;
-  const bool many = a.tile == kLargeTile;
-  const int type = tasks[0].y_type;
-  const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank, many) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank, many) : choose<QMV_F16>(g->max_rank, many);
-  const size_t smem = c.smem;
-  int per_sm = 0;
-  int rc = kernel_fit(c.kernel, kLoraThreads, smem, &per_sm);
-  if (rc) return rc;
-  const int64_t units = (int64_t)(many ? (g->max_tiles + a.window - 1) / a.window : g->max_tiles) * n_tasks, blocks = (int64_t)sm_count() * per_sm;
-  // Few units are cut into eight blocks each; more of them into four or two, as long as all make no more than two rounds, since a
-  // unit has two meetings of its cluster whatever its size. 64 tokens of 48 adapters, q|k|v: 46.0, 30.6 and 35.4 us with 8, 4 and 2;
-  // 80 tokens of 12 adapters, gate|up: 14.7, 16.6 and 27.8. Windows of many tokens: eight (282 us, 328 with 4, 428 with 2).
-  a.cluster = kCluster;
-  while (!many && a.cluster > 2 && units * a.cluster > 2 * blocks + blocks / 8) a.cluster /= 2;
-  const int64_t resident = blocks / a.cluster;
-  // a cluster for every unit, up to eight rounds of them: the device hands them out as others end (units differ by rank and N).
-  // Past that they take several each, so that a list with many empty tiles costs few launches of blocks.
-  const int clusters = (int)(units < 8 * resident ? units : 8 * resident);
+  const int type = tasks[0].y_type, cluster = kCluster;
+  const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank) : choose<QMV_F16>(g->max_rank);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* args[] = {&a};
-  cudaError_t e = kv8::launch_early(c.kernel, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, smem, static_cast<cudaStream_t>(stream), a.cluster);
-  if (e != cudaSuccess) return cuda_fail(e, "lora_run launch");
+  const int64_t units = (int64_t)g->max_tiles * n_tasks;
+  int per_sm = 0;
+  // Clusters and blocks are one for every unit, up to eight rounds of them: the device hands them out as others end (units differ
+  // by rank and N). Past that they take several each, so that a list with many empty tiles costs few launches of blocks.
+  if (!many_tokens(g->n_tokens, g->n_adapters)) {
+    int rc = kernel_fit(c.few, kLoraThreads, c.few_smem, &per_sm);
+    if (rc) return rc;
+    // Few units are cut into eight blocks each; more of them into four or two, as long as all make no more than two rounds, since a
+    // unit has two meetings of its cluster whatever its size. 64 tokens of 48 adapters, q|k|v: 46.0, 30.6 and 35.4 us with 8, 4 and 2;
+    // 80 tokens of 12 adapters, gate|up: 14.7, 16.6 and 27.8.
+    const int64_t blocks = (int64_t)sm_count() * per_sm;
+    a.cluster = cluster;
+    while (a.cluster > 2 && units * a.cluster > 2 * blocks + blocks / 8) a.cluster /= 2;
+    const int64_t most = 8 * blocks / a.cluster, clusters = units < most ? units : most;
+    cudaError_t e = kv8::launch_early(c.few, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.few_smem, s, a.cluster);
+    if (e != cudaSuccess) return cuda_fail(e, "lora_run launch");
+    return QMV_OK;
+  }
+  a.values = static_cast<uint4*>(g->workspace);
+  a.cluster = cluster;
+  a.window = kRunBlocks * 16 / a.tile;
+  a.window2 = kMostBlocks * 16 / a.tile;
+  a.slices = 0;
+  for (int i = 0; i < n_tasks; ++i) a.slices += (tasks[i].N + 255) / 256;
+  int rc = kernel_fit(c.first, kLoraThreads, c.first_smem, &per_sm);
+  if (rc) return rc;
+  const int64_t most = 8 * (int64_t)sm_count() * per_sm / cluster, clusters = units < most ? units : most;
+  rc = kernel_fit(c.second, kLoraThreads, c.second_smem, &per_sm);
+  if (rc) return rc;
+  const int64_t pieces = (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices, most2 = 64 * (int64_t)sm_count() * per_sm;
+  if (pieces > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d slices of columns", g->max_tiles, a.slices);
+  cudaError_t e = kv8::launch_early(c.first, dim3((unsigned)(clusters * cluster)), kLoraThreads, args, c.first_smem, s, cluster);
+  if (e != cudaSuccess) return cuda_fail(e, "lora_run launch (first product)");
+  e = kv8::launch_early(c.second, dim3((unsigned)(pieces < most2 ? pieces : most2)), kLoraThreads, args, c.second_smem, s);
+  if (e != cudaSuccess) return cuda_fail(e, "lora_run launch (second product)");
   return QMV_OK;
 }
 

@@ -75,7 +75,7 @@ def test_lora_plan_refusals(L):
 def test_lora_run_refusals(L):
     def call(n_tasks=2, task=None, at=1, **kw):
         a = dict(x=256, ldx=512, K=512, n_tokens=100, n_adapters=5, max_tiles=11, pool_rows=64, max_rank=16, order=256, tiles=256, table=256,
-                 scale=256) | kw
+                 scale=256, workspace=None, ws_bytes=0) | kw
         tasks = (q.lora_task * max(n_tasks, 1))()
         for i in range(n_tasks):
             k = dict(a=256, b=256, y=256, lda=512, ldb=64, ldy=60, N=60, y_type=q.QMV_F32) | ((task or {}) if i == at else {})
@@ -95,6 +95,14 @@ def test_lora_run_refusals(L):
                          (dict(y_type=0), -1), (dict(y_type=4), -1)]:
         _err(call(task=task), status, "task 1")
     assert call(n_tokens=0, max_tiles=0) == q.QMV_OK
+    # many tokens want a workspace; one type for a call's tasks
+    many = dict(n_tokens=4000, max_tiles=q.lora_max_tiles(4000, 5))
+    need = q.lora_workspace_size(4000, 5, 16, 2)
+    assert need > 0 and q.lora_workspace_size(100, 5, 16, 2) == 0 == q.lora_workspace_size(4000, 5, 129, 2)
+    assert q.lora_workspace_size(4000, 5, 128, 1) > q.lora_workspace_size(4000, 5, 64, 1)
+    for kw, status in [(dict(), -1), (dict(workspace=256, ws_bytes=need - 1), -1), (dict(workspace=264, ws_bytes=need), -2)]:
+        _err(call(**many, **kw), status, "workspace")
+    _err(call(task=dict(y_type=q.QMV_BF16)), -1, "task 1")
 
 
 def test_logprob_refusals(L):
