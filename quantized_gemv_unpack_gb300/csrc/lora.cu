@@ -576,12 +576,12 @@ struct Many {
   static constexpr int kBlockWords = kSteps * kParts3 * 32;   // 16-byte words of a 16-token block's finished values
   // first kernel
   static constexpr int kWords = kRunBlocks * kSteps * 64;     // 16-byte words of the run's fp32 values
-  static constexpr int kCols = 64, kGroups = 4, kChunk = 8 * NB * kCols * 2, kRing = kGroups * 2048;
+  static constexpr int kCols = 64, kGroups = 3, kChunk = 8 * NB * kCols * 2, kRing = kGroups * 2048;
   static constexpr int kSmem1 = kWords * 16 > kLoraWarps * kRing + kGroups * kChunk ? kWords * 16 : kLoraWarps * kRing + kGroups * kChunk;
   // second kernel
-  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kAheadY = 8192 / kBlockY;
+  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kRingY = F32 ? 8192 : 4096, kAheadY = kRingY / kBlockY;
   static constexpr int kChunkBlocks = kBlockWords * 16 * 8 > 36 * 1024 ? 2 : 4, kChunkH = kChunkBlocks * kBlockWords * 16;
-  static constexpr int kSmem2 = kLoraWarps * 8192 + 2 * kChunkH + 16 * kMostBlocks * (int)sizeof(int64_t);
+  static constexpr int kSmem2 = kLoraWarps * kRingY + 2 * kChunkH + 16 * kMostBlocks * (int)sizeof(int64_t);
 };
 
 // Whether tile v continues the run of tile u before it.
@@ -593,7 +593,7 @@ __device__ __forceinline__ bool follows(const RunArgs& a, const int4& u, const i
 }
 
 template <int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_first_kernel(const __grid_constant__ RunArgs a) {
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_first_kernel(const __grid_constant__ RunArgs a) {
   using S = Many<NB, Y>;
   constexpr int KS = S::kSteps, P3 = S::kParts3, G = S::kGroups;
   extern __shared__ __align__(16) unsigned char lora_smem[];
@@ -747,15 +747,15 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_first_kerne
 }
 
 template <int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_second_kernel(const __grid_constant__ RunArgs a) {
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kernel(const __grid_constant__ RunArgs a) {
   using S = Many<NB, Y>;
   constexpr int KS = S::kSteps, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, AY = S::kAheadY, CB = S::kChunkBlocks;
   constexpr bool F32 = S::F32;
   extern __shared__ __align__(16) unsigned char lora_smem[];
-  unsigned char* chunks = lora_smem + kLoraWarps * 8192;      // two of finished values, each of kChunkBlocks 16-token blocks
+  unsigned char* chunks = lora_smem + kLoraWarps * S::kRingY;      // two of finished values, each of kChunkBlocks 16-token blocks
   int64_t* row_y = reinterpret_cast<int64_t*>(chunks + 2 * S::kChunkH);   // bytes to each token's row of y; negative: none
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  unsigned char* ring = lora_smem + warp * 8192 + lane * 16;
+  unsigned char* ring = lora_smem + warp * S::kRingY + lane * 16;
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring), chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
   const int windows = (a.max_tiles + a.window2 - 1) / a.window2;
   follow_previous();
@@ -819,7 +819,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_second_kern
         ++m_in;
         slot_in = slot_in + 1 == AY ? 0 : slot_in + 1;
       };
-      for (int i = 0; i < AY - 2; ++i) ask();
+      for (int i = 0; i < AY - 1; ++i) ask();
       uint32_t b[KS][4][2];
       const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
 #pragma unroll
@@ -890,40 +890,32 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 2) lora_second_kern
         }
       };
       for (int c = 0; c * CB < blocks; ++c) {
-        // since chunk c: the prologue's AY - 2 groups of y, or the CB of the chunk before this one
-        if (c == 0) asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
+        // since chunk c: the prologue's AY - 1 groups of y, or the CB of the chunk before this one
+        if (c == 0) asm volatile("cp.async.wait_group %0;" ::"n"(AY - 1) : "memory");
         else asm volatile("cp.async.wait_group %0;" ::"n"(CB) : "memory");
         __syncthreads();                                      // chunk c is there, and c - 1 has been read
         if ((c + 1) * CB < blocks) load(c + 1);
         else copies_end();
-        // two blocks at a time: twice the products that wait for no other
 #pragma unroll 1
-        for (int m = c * CB; m < min(blocks, (c + 1) * CB); m += 2) {
-          const bool two = m + 1 < blocks;
+        for (int m = c * CB; m < min(blocks, (c + 1) * CB); ++m) {
           ask();
-          if (two) ask();
-          // since these blocks' copies: AY - 2 groups of y, and of the finished values one or more
-          asm volatile("cp.async.wait_group %0;" ::"n"(AY - 2) : "memory");
-          float d[2][4][4];
-          uint32_t v[2][2][WORDS];
-          begin(m, d[0], v[0]);
-          if (two) begin(m + 1, d[1], v[1]);
+          // since this block's copies: AY - 1 groups of y, and of the finished values one or more
+          asm volatile("cp.async.wait_group %0;" ::"n"(AY - 1) : "memory");
+          float d[4][4];
+          uint32_t v[2][WORDS];
+          begin(m, d, v);
           const uint4* h = reinterpret_cast<const uint4*>(chunks + (c & 1) * S::kChunkH) + (m - c * CB) * S::kBlockWords + lane;
 #pragma unroll
           for (int s = 0; s < KS; ++s) {
             if (16 * s >= r) break;
 #pragma unroll
             for (int k = P3 - 1; k >= 0; --k) {
-              const uint4 e = h[(s * P3 + k) * 32], f = h[S::kBlockWords + (s * P3 + k) * 32];   // past the last block: of no use
+              const uint4 f = h[(s * P3 + k) * 32];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                mma(d[0][i], e.x, e.y, e.z, e.w, b[s][i][0], b[s][i][1]);
-                mma(d[1][i], f.x, f.y, f.z, f.w, b[s][i][0], b[s][i][1]);
-              }
+              for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[s][i][0], b[s][i][1]);
             }
           }
-          finish(m, d[0], v[0]);
-          if (two) finish(m + 1, d[1], v[1]);
+          finish(m, d, v);
         }
       }
       copies_wait();
