@@ -21,6 +21,8 @@
 // The r values in between are fp32 sums, handed to the second product as two
 // bf16 parts (value and remainder: 2^-18 of each), so that an fp32 y keeps its
 // precision.
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace qmv {
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
 // registers while the tokens pass by; y comes through a ring in which each lane finds what it has asked for itself (registers
 // as the targets of loads that far ahead were slower: a wait for one of them waits for all).
 constexpr int kRunBlocks = 8;                                 // 16-token blocks of a run of the first kernel: one per warp
-constexpr int kMostBlocks = 16;                               // of a window of the second
+constexpr int kMostBlocks = 64;                               // of a window of the second
 
 template <int NB, int Y>
 struct Many {
@@ -687,23 +689,29 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_first_kerne
       asm volatile("cp.async.wait_group %0;" ::"n"(G - 2) : "memory");
       __syncthreads();                                        // these columns are there, and those before them have been read
       ask();
-      if (used) {
+      // PLAIN: all columns and (but for zeros) all rank rows are there
+      const auto multiply = [&](auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
         const unsigned char* st = chunks + slot * S::kChunk + g * (PER * 16);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const unsigned char* sa = st + (((e * 4 + t4) ^ ((g & 1) << 2)) * 16);
           uint4 p = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024), o = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024 + 512);
-          const bool in = k0 + 32 * e + 8 * t4 < k_hi;
-          if (k0 + S::kCols > k_hi && !in) p = o = make_uint4(0, 0, 0, 0);
+          const bool in = PLAIN || k0 + 32 * e + 8 * t4 < k_hi;
+          if (!in) p = o = make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            if (8 * i >= r) break;
+            if (!PLAIN && 8 * i >= r) break;
             uint4 w = *reinterpret_cast<const uint4*>(sa + i * (8 * PER * 16));
-            if (k0 + S::kCols > k_hi && !in) w = make_uint4(0, 0, 0, 0);   // the last columns: what lies past them was not copied
+            if (!in) w = make_uint4(0, 0, 0, 0);              // what lies past the columns was not copied
             mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
             mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
           }
         }
+      };
+      if (used) {
+        if (k0 + S::kCols <= k_hi && r > 8 * (NB - 1)) multiply(std::true_type{});
+        else multiply(std::false_type{});
       }
       slot = slot + 1 == G ? 0 : slot + 1;
     }
@@ -784,13 +792,14 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kern
         last = v;
       }
       __syncthreads();                                        // the run before this one is done with row_y and the chunks
-      if (tid < count) {
-        const int k = a.order[tile.y + tid];
-        row_y[tid] = k < 0 || k >= a.n_tokens ? -1 : (int64_t)k * t.ldy * size;
-      } else if (tid < (count + 15) / 16 * 16) {
-        row_y[tid] = -1;
-      }
       const int blocks = (count + 15) / 16;
+      bool odd = false;
+      for (int i = tid; i < blocks * 16; i += kLoraThreads) {
+        const int k = i < count ? a.order[tile.y + i] : -1;
+        const bool there = k >= 0 && k < a.n_tokens;
+        row_y[i] = there ? (int64_t)k * t.ldy * size : -1;
+        odd |= i < count && !there;
+      }
       const uint4* values = a.values + ((int64_t)task * a.max_tiles + first) * (a.tile / 16) * S::kBlockWords;
       const auto load = [&](int c) {                          // chunk c of the finished values
         const int words = min(CB, blocks - c * CB) * S::kBlockWords;
@@ -799,20 +808,22 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kern
         copies_end();
       };
       load(0);
-      __syncthreads();
+      // 16-token blocks of this warp that need no look at what is there: all their columns, rank rows and tokens
+      odd = __syncthreads_or(odd);
+      const int plain_blocks = t.wide && n0 + 32 <= t.N && r > 16 * (KS - 1) && !odd ? count / 16 : 0;
       int m_in = 0, slot_in = 0, slot = 0;                    // the next block of y to ask for
+      const char* yq = y + (int64_t)n * size;
       const auto ask = [&]() {
-        if (whole && m_in < blocks) {
+        if (m_in < blocks) {
           const int64_t ta = row_y[m_in * 16 + g], tb = row_y[m_in * 16 + g + 8];
           const uint32_t to = ring_at + slot_in * S::kBlockY;
-          const char* q = y + (int64_t)n * size;
-          if (ta >= 0) {
-            copy16(to, q + ta);
-            if constexpr (F32) copy16(to + 512, q + ta + 16);
+          if (m_in < plain_blocks || (whole && ta >= 0)) {
+            copy16(to, yq + ta);
+            if constexpr (F32) copy16(to + 512, yq + ta + 16);
           }
-          if (tb >= 0) {
-            copy16(to + S::kBlockY / 2, q + tb);
-            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, q + tb + 16);
+          if (m_in < plain_blocks || (whole && tb >= 0)) {
+            copy16(to + S::kBlockY / 2, yq + tb);
+            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, yq + tb + 16);
           }
         }
         copies_end();
@@ -848,41 +859,50 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kern
           b[s][3][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x7632);
         }
       }
-      // Block m's values of y: fp32 ones are added in the end (one rounding), 16-bit ones are what the products are added to.
-      const auto begin = [&](int m, float (&d)[4][4], uint32_t (&v)[2][WORDS]) {
+      // Block m: fp32 values of y are added in the end (one rounding), 16-bit ones are what the products are added to.
+      const auto block = [&](auto plain, int m, const uint4* h) {
+        constexpr bool PLAIN = decltype(plain)::value;
+        const int64_t ta = row_y[m * 16 + g], tb = row_y[m * 16 + g + 8];
         const unsigned char* sy = ring + slot * S::kBlockY;
-        slot = slot + 1 == AY ? 0 : slot + 1;
+        uint32_t v[2][WORDS];
         ld_pieces(sy, v[0]);
         ld_pieces(sy + S::kBlockY / 2, v[1]);
+        float d[4][4];
+        if (F32 || !(PLAIN || whole)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) d[i / 4][i % 4] = 0.f;
-        if constexpr (!F32) {
-          if (whole) {
+          for (int i = 0; i < 16; ++i) d[i / 4][i % 4] = 0.f;
+        } else if constexpr (!F32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = unpack2<Y>(v[i / 4][i % 4]);
-              const int c = 2 * (i % 4), hi = 2 * (i / 4);
-              d[c % 4][hi + c / 4] = f.x;
-              d[(c + 1) % 4][hi + (c + 1) / 4] = f.y;
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float2 f = unpack2<Y>(v[i / 4][i % 4]);
+            const int c = 2 * (i % 4), hi = 2 * (i / 4);
+            d[c % 4][hi + c / 4] = f.x;
+            d[(c + 1) % 4][hi + (c + 1) / 4] = f.y;
           }
         }
-      };
-      const auto finish = [&](int m, const float (&d)[4][4], uint32_t (&v)[2][WORDS]) {
-        const int64_t ta = row_y[m * 16 + g], tb = row_y[m * 16 + g + 8];
-        char* q = y + (int64_t)n * size;
-        if (whole) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          if (!PLAIN && 16 * s >= r) break;
+#pragma unroll
+          for (int k = P3 - 1; k >= 0; --k) {
+            const uint4 f = h[(s * P3 + k) * 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[s][i][0], b[s][i][1]);
+          }
+        }
+        char* q = const_cast<char*>(yq);
+        if (PLAIN || whole) {
           if constexpr (F32) {
-            if (ta >= 0) add_row<Y, 0>(q + ta, scale, d, v[0]);
-            if (tb >= 0) add_row<Y, 1>(q + tb, scale, d, v[1]);
+            if (PLAIN || ta >= 0) add_row<Y, 0>(q + ta, scale, d, v[0]);
+            if (PLAIN || tb >= 0) add_row<Y, 1>(q + tb, scale, d, v[1]);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const int c = 2 * (i % 4), hi = 2 * (i / 4);
               v[i / 4][i % 4] = pack2<Y>(d[c % 4][hi + c / 4], d[(c + 1) % 4][hi + (c + 1) / 4]);
             }
-            if (ta >= 0) st_global(q + ta, v[0]);
-            if (tb >= 0) st_global(q + tb, v[1]);
+            if (PLAIN || ta >= 0) st_global(q + ta, v[0]);
+            if (PLAIN || tb >= 0) st_global(q + tb, v[1]);
           }
         } else {
           if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
@@ -901,21 +921,10 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kern
           ask();
           // since this block's copies: AY - 1 groups of y, and of the finished values one or more
           asm volatile("cp.async.wait_group %0;" ::"n"(AY - 1) : "memory");
-          float d[4][4];
-          uint32_t v[2][WORDS];
-          begin(m, d, v);
           const uint4* h = reinterpret_cast<const uint4*>(chunks + (c & 1) * S::kChunkH) + (m - c * CB) * S::kBlockWords + lane;
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            if (16 * s >= r) break;
-#pragma unroll
-            for (int k = P3 - 1; k >= 0; --k) {
-              const uint4 f = h[(s * P3 + k) * 32];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[s][i][0], b[s][i][1]);
-            }
-          }
-          finish(m, d, v);
+          if (m < plain_blocks) block(std::true_type{}, m, h);
+          else block(std::false_type{}, m, h);
+          slot = slot + 1 == AY ? 0 : slot + 1;
         }
       }
       copies_wait();
