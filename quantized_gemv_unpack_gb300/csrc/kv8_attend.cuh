@@ -46,6 +46,7 @@
 
 #include "gemv_core.cuh"
 #include "kv8.cuh"
+#include "tcgen05.cuh"
 
 namespace qmv {
 namespace attend {
@@ -277,11 +278,7 @@ __device__ __forceinline__ void load_pieces_as(int type, const void* base, const
   else load_pieces<float>(base, at, v);
 }
 // True in one lane of a warp, the same one each time.
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
-  return r != 0;
-}
+using umma::elected;
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(core::smem_addr(bar)) : "memory");
 }

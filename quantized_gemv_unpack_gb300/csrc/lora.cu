@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "kv8.cuh"
+#include "tcgen05.cuh"
 
 namespace qmv {
 namespace {
@@ -324,9 +325,9 @@ struct Short {
   static constexpr int kParts = kLoraWarps / kHalves;         // and a share of the columns of x
   static constexpr int kBlocks = NB / kHalves;
   static constexpr int kWords = kSteps * 64;                  // 16-byte words of the tile's r values, in the order of the fragments
-  static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps * 1024, kSecond = kB + (F32 ? 2048 : 1024);
+  static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps / kHalves * 1024, kSecond = kB + (F32 ? 2048 : 1024);
   static constexpr int kSlot = kFirst > kSecond ? kFirst : kSecond;
-  static constexpr int kDepth = NB == 2 ? 4 : NB == 4 ? 3 : 2;
+  static constexpr int kDepth = NB == 8 ? 2 : NB == 4 ? 3 : 4;   // two blocks per SM, one of ranks past 64
   static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + kLoraWarps * (int)sizeof(int);
   static constexpr int kSmem = kFixed + kLoraWarps * kDepth * kSlot;
 };
@@ -334,7 +335,7 @@ struct Short {
 template <int NB, int Y>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __grid_constant__ RunArgs a) {
   using S = Short<NB, Y>;
-  constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth;
+  constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth, KH = KS / S::kHalves;
   constexpr bool F32 = S::F32;
   extern __shared__ __align__(16) unsigned char lora_smem[];
   float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     // this block's columns of both products, and this warp's steps of them
     const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 32 - 1) / (C * 32) * 32;
     const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
-    int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, slot_in = 0, slot = 0;
+    int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, half_next = 0, slot_in = 0, slot = 0;
     const __nv_bfloat16* pa = t.a + (int64_t)(row0 + j0 + g) * t.lda + 8 * t4;
     const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + 4 * g;
     const int64_t step_a = 8 * t.lda;
@@ -402,14 +403,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       } else if (n_next < n_hi) {
         const int col = n_next + 4 * g, n = n_next + 8 * t4;
         if (col < t.N) {
-          const __nv_bfloat16* p = pb + n_next;
+          const __nv_bfloat16* p = pb + n_next + (int64_t)(16 * KH * half_next) * t.ldb;
           const uint32_t at = ring_at + slot_in * S::kSlot + lane * 8;
 #pragma unroll
-          for (int s = 0; s < KS; ++s)
+          for (int s = 0; s < KH; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int off = 16 * s + (i & 1) + 8 * (i >> 1);
-              if (off + 2 * t4 >= r) continue;
+              if (16 * KH * half_next + off + 2 * t4 >= r) continue;
               const __nv_bfloat16* q = p + off * t.ldb;
               if (col + 4 <= t.N) {
                 copy8(at + (4 * s + i) * 256, q);
@@ -420,7 +421,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
               }
             }
         }
-        if (t.wide && n + 8 <= t.N) {
+        const bool last = ++half_next == S::kHalves;          // y comes with the last rank rows
+        if (last) half_next = 0;
+        if (last && t.wide && n + 8 <= t.N) {
           if (tok0 >= 0) {
             copy16(to + S::kB, y0 + (int64_t)n * size);
             if constexpr (F32) copy16(to + S::kB + 512, y0 + (int64_t)n * size + 16);
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
             if constexpr (F32) copy16(to + S::kB + 256 * size + 512, y1 + (int64_t)n * size + 16);
           }
         }
-        n_next += kLoraWarps * 32;
+        if (last) n_next += kLoraWarps * 32;
       }
       copies_end();
       slot_in = slot_in + 1 == D ? 0 : slot_in + 1;
@@ -510,35 +513,40 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     // ---- second product, over this block's share of N
     const uint4* h = frag + lane;
     for (int n0 = n_lo + warp * 32; n0 < n_hi; n0 += kLoraWarps * 32) {
-      ask();
-      asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
-      const unsigned char* st = ring + slot * S::kSlot;
-      slot = slot + 1 == D ? 0 : slot + 1;
       const int n = n0 + 8 * t4;                              // first column of this lane's sums
       float d[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+      const unsigned char* st = ring;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        if (16 * s >= r) break;
-        uint32_t b[4][2];
-        const bool full = 16 * s + 16 <= r;
+      for (int hf = 0; hf < S::kHalves; ++hf) {
+        ask();
+        asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+        st = ring + slot * S::kSlot;
+        slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = 16 * s + 8 * i + 2 * t4;
-          uint2 u = make_uint2(0, 0), v = u;
-          if (full || j < r) u = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * s + 2 * i) * 256);
-          if (full || j + 1 < r) v = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * s + 2 * i + 1) * 256);
-          b[0][i] = __byte_perm(u.x, v.x, 0x5410);
-          b[1][i] = __byte_perm(u.x, v.x, 0x7632);
-          b[2][i] = __byte_perm(u.y, v.y, 0x5410);
-          b[3][i] = __byte_perm(u.y, v.y, 0x7632);
-        }
+        for (int e = 0; e < KH; ++e) {
+          const int s = hf * KH + e;
+          if (16 * s >= r) break;
+          uint32_t b[4][2];
+          const bool full = 16 * s + 16 <= r;
 #pragma unroll
-        for (int k = P3 - 1; k >= 0; --k) {
-          const uint4 f = h[(s * P3 + k) * 32];
+          for (int i = 0; i < 2; ++i) {
+            const int j = 16 * s + 8 * i + 2 * t4;
+            uint2 u = make_uint2(0, 0), v = u;
+            if (full || j < r) u = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * e + 2 * i) * 256);
+            if (full || j + 1 < r) v = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * e + 2 * i + 1) * 256);
+            b[0][i] = __byte_perm(u.x, v.x, 0x5410);
+            b[1][i] = __byte_perm(u.x, v.x, 0x7632);
+            b[2][i] = __byte_perm(u.y, v.y, 0x5410);
+            b[3][i] = __byte_perm(u.y, v.y, 0x7632);
+          }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
+          for (int k = P3 - 1; k >= 0; --k) {
+            const uint4 f = h[(s * P3 + k) * 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
+          }
         }
       }
       if (t.wide && n + 8 <= t.N) {
@@ -562,8 +570,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
 // per run of tokens would leave the memory idle for a third of the time (in one kernel: 282 us for 8190 tokens).
 //
 // lora_first_kernel: a cluster takes a run of up to 128 tokens of one adapter and one projection, each block an eighth of K.
-// A warp owns 16 tokens, whose x it copies for itself; A's columns are shared, 64 at a time, four groups in flight. The
-// blocks' sums meet in distributed shared memory.
+// The product is one of the fifth-generation tensor cores (the tokens' 128 rows of x by the rank rows of A, 64 columns at a
+// time, sums in tensor memory), so that the warps only copy; the blocks' sums meet in distributed shared memory.
 //
 // lora_second_kernel: a block takes 256 columns and a window of tokens. A warp owns 32 columns: their values of B stay in its
 // registers while the tokens pass by; y comes through a ring in which each lane finds what it has asked for itself (registers
@@ -577,9 +585,9 @@ struct Many {
   static constexpr int kSteps = NB / 2, kParts3 = F32 ? 3 : 2;
   static constexpr int kBlockWords = kSteps * kParts3 * 32;   // 16-byte words of a 16-token block's finished values
   // first kernel
-  static constexpr int kWords = kRunBlocks * kSteps * 64;     // 16-byte words of the run's fp32 values
-  static constexpr int kCols = 64, kGroups = 3, kChunk = 8 * NB * kCols * 2, kRing = kGroups * 2048;
-  static constexpr int kSmem1 = kWords * 16 > kLoraWarps * kRing + kGroups * kChunk ? kWords * 16 : kLoraWarps * kRing + kGroups * kChunk;
+  static constexpr int kColumns = NB <= 4 ? 32 : 8 * NB;      // of tensor memory: the run's sums
+  static constexpr int kCols = 64, kX = 16 * kRunBlocks * kCols * 2, kStage = kX + 8 * NB * kCols * 2, kStages = NB <= 4 ? 4 : 3;
+  static constexpr int kSmem1 = kStages * kStage + 1024;      // the stages on a boundary of 1024 bytes
   // second kernel
   static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kRingY = F32 ? 8192 : 4096, kAheadY = kRingY / kBlockY;
   static constexpr int kChunkBlocks = kBlockWords * 16 * 8 > 36 * 1024 ? 2 : 4, kChunkH = kChunkBlocks * kBlockWords * 16;
@@ -595,19 +603,31 @@ __device__ __forceinline__ bool follows(const RunArgs& a, const int4& u, const i
 }
 
 template <int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_first_kernel(const __grid_constant__ RunArgs a) {
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 2 : 3) lora_first_kernel(const __grid_constant__ RunArgs a) {
   using S = Many<NB, Y>;
-  constexpr int KS = S::kSteps, P3 = S::kParts3, G = S::kGroups;
+  constexpr int KS = S::kSteps, P3 = S::kParts3, G = S::kStages;
   extern __shared__ __align__(16) unsigned char lora_smem[];
-  float4* mine = reinterpret_cast<float4*>(lora_smem);        // after the columns: this block's sums, which the cluster reads
-  unsigned char* chunks = lora_smem + kLoraWarps * S::kRing;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  __shared__ __align__(8) uint64_t done[G];                   // a stage's products
+  __shared__ uint32_t tmem_at;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int rank = (int)cluster_rank(), C = a.cluster, clusters = gridDim.x / C;
-  unsigned char* ring = lora_smem + warp * S::kRing + lane * 16;
-  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring), chunks_at = (uint32_t)__cvta_generic_to_shared(chunks);
-  constexpr int PER = S::kCols / 8, ROWS = kLoraThreads / PER, TURNS = (8 * NB + ROWS - 1) / ROWS;   // 16-byte pieces of a row of A; rows at a time
-  const int c1 = tid % PER, r1 = tid / PER;
-  const uint32_t to_a = chunks_at + (r1 * PER + (c1 ^ ((r1 & 1) << 2))) * 16;
+  unsigned char* stages = lora_smem + (1024 - ((uint32_t)__cvta_generic_to_shared(lora_smem) & 1023)) % 1024;
+  const uint32_t stages_at = (uint32_t)__cvta_generic_to_shared(stages);
+  float4* mine = reinterpret_cast<float4*>(stages);           // after the columns: this block's sums, which the cluster reads
+  if (warp == 0) umma::tmem_alloc<S::kColumns>(&tmem_at);
+  if (tid == 0) {
+    for (int i = 0; i < G; ++i) core::mbar_init(&done[i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  umma::fence_before();
+  __syncthreads();
+  umma::fence_after();
+  const uint32_t tmem = tmem_at;
+  // this thread's 16-byte pieces of a stage: piece c of rows r1, r1 + 32, ..., in the order of the 128-byte swizzle
+  constexpr int ROWS = kLoraThreads / 8, TURNS_X = 16 * kRunBlocks / ROWS, TURNS_A = (8 * NB + ROWS - 1) / ROWS;
+  const int c1 = tid % 8, r1 = tid / 8;
+  const uint32_t to1 = r1 * 128 + (c1 ^ (r1 & 7)) * 16;
+  int begun = 0;                                              // stages of all units so far
   follow_previous();
   for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
     const Task& t = a.t[unit / a.max_tiles];
@@ -635,98 +655,102 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_first_kerne
       count += v.z;
       last = v;
     }
-    const auto token_at = [&](int i) {                        // of this run; -1 past its end, and for a place outside
-      const int k = i < count ? a.order[tile.y + i] : -1;
-      if (i < count && (k < 0 || k >= a.n_tokens)) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
-      return k < a.n_tokens ? k : -1;
-    };
-    const int tok0 = token_at(warp * 16 + g), tok1 = token_at(warp * 16 + g + 8);
-    const bool used = warp * 16 < count;
-    const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx + 8 * t4;
-    const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx + 8 * t4;
     const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share);
-    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + 8 * c1;
+    const int n_stages = k_hi > k_lo ? (k_hi - k_lo + S::kCols - 1) / S::kCols : 0, rows = (r + 15) / 16 * 16;
+    const __nv_bfloat16* px[TURNS_X];                         // nullptr: no token; its row of the product is of no use
+#pragma unroll
+    for (int i = 0; i < TURNS_X; ++i) {
+      const int at = r1 + i * ROWS, k = at < count ? a.order[tile.y + at] : -1;
+      if (at < count && (k < 0 || k >= a.n_tokens)) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
+      px[i] = k < 0 || k >= a.n_tokens ? nullptr : a.x + (int64_t)k * a.ldx + k_lo + 8 * c1;
+    }
+    const __nv_bfloat16* pa = t.a + (int64_t)(row0 + r1) * t.lda + k_lo + 8 * c1;
     const int64_t step_a = ROWS * t.lda;
-    int k_next = k_lo, slot_in = 0, slot = 0;
-    const auto ask = [&]() {
-      if (k_next < k_hi) {
-        if (k_next + 8 * c1 < k_hi) {
-          const __nv_bfloat16* p = pa + k_next;
+    // rank rows past the rank are 0: no copy reaches them
 #pragma unroll
-          for (int i = 0; i < TURNS; ++i, p += step_a) {
-            if (r1 + i * ROWS >= r) break;
-            copy16(to_a + slot_in * S::kChunk + i * (ROWS * PER * 16), p);
-          }
-        }
+    for (int i = 0; i < TURNS_A; ++i) {
+      const int j = r1 + i * ROWS;
+      if (j >= r && j < rows)
+        for (int g = 0; g < G; ++g) *reinterpret_cast<uint4*>(stages + g * S::kStage + S::kX + to1 + i * (ROWS * 128)) = make_uint4(0, 0, 0, 0);
+    }
+    const auto ask = [&](int q) {
+      if (q < n_stages) {
+        const int use = begun + q, slot = use % G, off = q * S::kCols;
+        if (q >= G) core::mbar_wait(&done[slot], (use / G - 1) & 1, a.err);   // the stage's products before these
+        const uint32_t to = stages_at + slot * S::kStage + to1;
+        if (k_lo + off + 8 * c1 < k_hi) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int k = k_next + 32 * e;
-          if (k + 8 * t4 < k_hi) {
-            if (tok0 >= 0) copy16(ring_at + slot_in * 2048 + e * 1024, x0 + k);
-            if (tok1 >= 0) copy16(ring_at + slot_in * 2048 + e * 1024 + 512, x1 + k);
-          }
+          for (int i = 0; i < TURNS_X; ++i)
+            if (px[i]) copy16(to + i * (ROWS * 128), px[i] + off);
+          const __nv_bfloat16* p = pa + off;
+#pragma unroll
+          for (int i = 0; i < TURNS_A; ++i, p += step_a)
+            if (r1 + i * ROWS < r) copy16(to + S::kX + i * (ROWS * 128), p);
+        } else {                                              // past the last column: 0 by 0
+          unsigned char* z = stages + slot * S::kStage + to1;
+#pragma unroll
+          for (int i = 0; i < TURNS_X; ++i) *reinterpret_cast<uint4*>(z + i * (ROWS * 128)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < TURNS_A; ++i)
+            if (r1 + i * ROWS < rows) *reinterpret_cast<uint4*>(z + S::kX + i * (ROWS * 128)) = make_uint4(0, 0, 0, 0);
         }
-        k_next += S::kCols;
       }
       copies_end();
-      slot_in = slot_in + 1 == G ? 0 : slot_in + 1;
     };
-    // what no copy reaches is 0: rows past the rank up to a block of eight, tokens that are none
-    for (int i = tid; i < G * 8 * PER; i += kLoraThreads) {
-      const int j = r / 8 * 8 + i / PER % 8;
-      if (r % 8 && j >= r) *reinterpret_cast<uint4*>(chunks + i / (8 * PER) * S::kChunk + (j * PER + i % PER) * 16) = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      if (tok0 < 0) *reinterpret_cast<uint4*>(ring + i * 1024) = make_uint4(0, 0, 0, 0);
-      if (tok1 < 0) *reinterpret_cast<uint4*>(ring + i * 1024 + 512) = make_uint4(0, 0, 0, 0);
-    }
-    for (int i = 0; i < G - 1; ++i) ask();
-    float acc[NB][4];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    for (int k0 = k_lo; k0 < k_hi; k0 += S::kCols) {
+    for (int q = 0; q < G - 1; ++q) ask(q);
+    const uint32_t shape = umma::mma_shape_bf16(rows);
+    for (int q = 0; q < n_stages; ++q) {
       asm volatile("cp.async.wait_group %0;" ::"n"(G - 2) : "memory");
-      __syncthreads();                                        // these columns are there, and those before them have been read
-      ask();
-      // PLAIN: all columns and (but for zeros) all rank rows are there
-      const auto multiply = [&](auto plain) {
-        constexpr bool PLAIN = decltype(plain)::value;
-        const unsigned char* st = chunks + slot * S::kChunk + g * (PER * 16);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();                                        // the stage is there
+      if (warp == 0) {
+        umma::fence_after();
+        if (umma::elected()) {
+          const uint32_t st = stages_at + (begun + q) % G * S::kStage;
+          const uint64_t xa = umma::operand(st), ab = umma::operand(st + S::kX);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const unsigned char* sa = st + (((e * 4 + t4) ^ ((g & 1) << 2)) * 16);
-          uint4 p = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024), o = *reinterpret_cast<const uint4*>(ring + slot * 2048 + e * 1024 + 512);
-          const bool in = PLAIN || k0 + 32 * e + 8 * t4 < k_hi;
-          if (!in) p = o = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            if (!PLAIN && 8 * i >= r) break;
-            uint4 w = *reinterpret_cast<const uint4*>(sa + i * (8 * PER * 16));
-            if (!in) w = make_uint4(0, 0, 0, 0);              // what lies past the columns was not copied
-            mma(acc[i], p.x, o.x, p.y, o.y, w.x, w.y);
-            mma(acc[i], p.z, o.z, p.w, o.w, w.z, w.w);
-          }
+          for (int e = 0; e < 4; ++e) umma::mma_ss(tmem, xa + 2 * e, ab + 2 * e, shape, q + e > 0);
+          umma::commit(&done[(begun + q) % G]);
         }
-      };
-      if (used) {
-        if (k0 + S::kCols <= k_hi && r > 8 * (NB - 1)) multiply(std::true_type{});
-        else multiply(std::false_type{});
+        __syncwarp();
       }
-      slot = slot + 1 == G ? 0 : slot + 1;
+      ask(q + G - 1);
     }
-    __syncthreads();                                          // all columns have been read: their place is that of the sums
-    if (used) {
+    const int blocks = (count + 15) / 16;
+    if (n_stages) {
+      const int use = begun + n_stages - 1;
+      core::mbar_wait(&done[use % G], (use / G) & 1, a.err);  // the last stage's products, and with them all
+    }
+    begun += n_stages;
+    umma::fence_after();
+    copies_wait();
+    // tensor memory has a token per lane; `mine` the order of the second product's fragments
+    {
+      const int row = warp % 4 * 32 + lane, b = row / 16, g = row % 8, high = row % 16 / 8;
+      for (int nb = warp / 4; nb < rows / 8; nb += 2) {
+        uint32_t v[8];
+        if (n_stages) {
+          umma::tmem_ld8(tmem + ((uint32_t)(warp % 4 * 32) << 16) + nb * 8, v);
+          umma::wait_ld();
+        } else {
 #pragma unroll
-      for (int i = 0; i < NB; ++i) mine[(warp * NB + i) * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+          for (int i = 0; i < 8; ++i) v[i] = 0;
+        }
+        if (b < blocks) {
+          float* to = reinterpret_cast<float*>(mine + (b * NB + nb) * 32 + g * 4) + 2 * high;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint2*>(to + 4 * i) = make_uint2(v[2 * i], v[2 * i + 1]);
+        }
+      }
     }
+    umma::fence_before();
     cluster_arrive();
     cluster_wait();
     // the cluster's sums, a share in each block: an item is a lane's eight values of one k16 step
-    const int blocks = (count + 15) / 16, items = blocks * KS * 32, share = (items + C - 1) / C;
+    const int steps = rows / 16, items = blocks * steps * 32, share = (items + C - 1) / C;
     uint4* to = a.values + ((int64_t)(unit / a.max_tiles) * a.max_tiles + first) * (a.tile / 16) * S::kBlockWords;
     for (int i = rank * share + tid; i < min(items, (rank + 1) * share); i += kLoraThreads) {
-      const int at = (i / 32) * 64 + i % 32;
+      const int b = i / 32 / steps, s = i / 32 % steps, at = (b * NB + 2 * s) * 32 + i % 32;
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
 #pragma unroll 8
       for (int c = 0; c < C; ++c) {
@@ -746,12 +770,14 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_first_kerne
         f.y = split(u.z, u.w);
         f.z = split(v.x, v.y);
         f.w = split(v.z, v.w);
-        to[((i / 32) * P3 + k) * 32 + i % 32] = f;
+        to[((b * KS + s) * P3 + k) * 32 + i % 32] = f;
       }
     }
     cluster_arrive();
     cluster_wait();                                           // the blocks' sums have been read
   }
+  __syncthreads();
+  if (warp == 0) umma::tmem_free<S::kColumns>(tmem);
 }
 
 template <int NB, int Y>
@@ -1075,19 +1101,20 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
     return QMV_OK;
   }
   a.values = static_cast<uint4*>(g->workspace);
-  a.cluster = cluster;
+  int rc = kernel_fit(c.first, kLoraThreads, c.first_smem, &per_sm);
+  if (rc) return rc;
+  // four blocks per run where that fills the device twice, else eight: 8190 tokens, gate|up: 189 us with 4, 199 with 8
+  a.cluster = units * cluster > 2 * (int64_t)sm_count() * per_sm ? cluster / 2 : cluster;
   a.window = kRunBlocks * 16 / a.tile;
   a.window2 = kMostBlocks * 16 / a.tile;
   a.slices = 0;
   for (int i = 0; i < n_tasks; ++i) a.slices += (tasks[i].N + 255) / 256;
-  int rc = kernel_fit(c.first, kLoraThreads, c.first_smem, &per_sm);
-  if (rc) return rc;
-  const int64_t most = 8 * (int64_t)sm_count() * per_sm / cluster, clusters = units < most ? units : most;
+  const int64_t most = 8 * (int64_t)sm_count() * per_sm / a.cluster, clusters = units < most ? units : most;
   rc = kernel_fit(c.second, kLoraThreads, c.second_smem, &per_sm);
   if (rc) return rc;
   const int64_t pieces = (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices, most2 = 64 * (int64_t)sm_count() * per_sm;
   if (pieces > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d slices of columns", g->max_tiles, a.slices);
-  cudaError_t e = kv8::launch_early(c.first, dim3((unsigned)(clusters * cluster)), kLoraThreads, args, c.first_smem, s, cluster);
+  cudaError_t e = kv8::launch_early(c.first, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.first_smem, s, a.cluster);
   if (e != cudaSuccess) return cuda_fail(e, "lora_run launch (first product)");
   e = kv8::launch_early(c.second, dim3((unsigned)(pieces < most2 ? pieces : most2)), kLoraThreads, args, c.second_smem, s);
   if (e != cudaSuccess) return cuda_fail(e, "lora_run launch (second product)");
