@@ -325,9 +325,10 @@ struct Short {
   static constexpr int kParts = kLoraWarps / kHalves;         // and a share of the columns of x
   static constexpr int kBlocks = NB / kHalves;
   static constexpr int kWords = kSteps * 64;                  // 16-byte words of the tile's r values, in the order of the fragments
-  static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps / kHalves * 1024, kSecond = kB + (F32 ? 2048 : 1024);
+  static constexpr int kPieces = NB > 8 ? 4 : 1;              // steps that 32 columns of B take, so that a slot is no larger than the first product needs
+  static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps / kPieces * 1024, kSecond = kB + (F32 ? 2048 : 1024);
   static constexpr int kSlot = kFirst > kSecond ? kFirst : kSecond;
-  static constexpr int kDepth = NB == 8 ? 2 : NB == 4 ? 3 : 4;   // two blocks per SM, one of ranks past 64
+  static constexpr int kDepth = NB == 2 ? 4 : NB == 4 ? 3 : 2;   // what two blocks of an SM have room for
   static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + kLoraWarps * (int)sizeof(int);
   static constexpr int kSmem = kFixed + kLoraWarps * kDepth * kSlot;
 };
@@ -335,7 +336,7 @@ struct Short {
 template <int NB, int Y>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __grid_constant__ RunArgs a) {
   using S = Short<NB, Y>;
-  constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth, KH = KS / S::kHalves;
+  constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth, KH = KS / S::kPieces;
   constexpr bool F32 = S::F32;
   extern __shared__ __align__(16) unsigned char lora_smem[];
   float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     // this block's columns of both products, and this warp's steps of them
     const int k_share = (a.K + C * 32 - 1) / (C * 32) * 32, n_share = (t.N + C * 32 - 1) / (C * 32) * 32;
     const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
-    int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, half_next = 0, slot_in = 0, slot = 0;
+    int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, piece_next = 0, slot_in = 0, slot = 0;
     const __nv_bfloat16* pa = t.a + (int64_t)(row0 + j0 + g) * t.lda + 8 * t4;
     const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + 4 * g;
     const int64_t step_a = 8 * t.lda;
@@ -403,14 +404,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       } else if (n_next < n_hi) {
         const int col = n_next + 4 * g, n = n_next + 8 * t4;
         if (col < t.N) {
-          const __nv_bfloat16* p = pb + n_next + (int64_t)(16 * KH * half_next) * t.ldb;
+          const __nv_bfloat16* p = pb + n_next + (int64_t)(16 * KH * piece_next) * t.ldb;
           const uint32_t at = ring_at + slot_in * S::kSlot + lane * 8;
 #pragma unroll
           for (int s = 0; s < KH; ++s)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int off = 16 * s + (i & 1) + 8 * (i >> 1);
-              if (16 * KH * half_next + off + 2 * t4 >= r) continue;
+              if (16 * KH * piece_next + off + 2 * t4 >= r) continue;
               const __nv_bfloat16* q = p + off * t.ldb;
               if (col + 4 <= t.N) {
                 copy8(at + (4 * s + i) * 256, q);
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
               }
             }
         }
-        const bool last = ++half_next == S::kHalves;          // y comes with the last rank rows
-        if (last) half_next = 0;
+        const bool last = ++piece_next == S::kPieces;         // y comes with the last rank rows
+        if (last) piece_next = 0;
         if (last && t.wide && n + 8 <= t.N) {
           if (tok0 >= 0) {
             copy16(to + S::kB, y0 + (int64_t)n * size);
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
       const unsigned char* st = ring;
 #pragma unroll
-      for (int hf = 0; hf < S::kHalves; ++hf) {
+      for (int hf = 0; hf < S::kPieces; ++hf) {
         ask();
         asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
         st = ring + slot * S::kSlot;
@@ -589,7 +590,7 @@ struct Many {
   static constexpr int kCols = 64, kX = 16 * kRunBlocks * kCols * 2, kStage = kX + 8 * NB * kCols * 2, kStages = NB <= 4 ? 4 : 3;
   static constexpr int kSmem1 = kStages * kStage + 1024;      // the stages on a boundary of 1024 bytes
   // second kernel
-  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kRingY = F32 ? 8192 : 4096, kAheadY = kRingY / kBlockY;
+  static constexpr int kBlockY = 16 * 32 * (F32 ? 4 : 2), kRingY = F32 && NB <= 8 ? 8192 : 4096, kAheadY = kRingY / kBlockY;
   static constexpr int kChunkBlocks = kBlockWords * 16 * 8 > 36 * 1024 ? 2 : 4, kChunkH = kChunkBlocks * kBlockWords * 16;
   static constexpr int kSmem2 = kLoraWarps * kRingY + 2 * kChunkH + 16 * kMostBlocks * (int)sizeof(int64_t);
 };
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 2 : 3) lora_first_kerne
 }
 
 template <int NB, int Y>
-__global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 1 : 3) lora_second_kernel(const __grid_constant__ RunArgs a) {
+__global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) lora_second_kernel(const __grid_constant__ RunArgs a) {
   using S = Many<NB, Y>;
   constexpr int KS = S::kSteps, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, AY = S::kAheadY, CB = S::kChunkBlocks;
   constexpr bool F32 = S::F32;
@@ -1106,12 +1107,14 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   // four blocks per run where that fills the device twice, else eight: 8190 tokens, gate|up: 189 us with 4, 199 with 8
   a.cluster = units * cluster > 2 * (int64_t)sm_count() * per_sm ? cluster / 2 : cluster;
   a.window = kRunBlocks * 16 / a.tile;
-  a.window2 = kMostBlocks * 16 / a.tile;
   a.slices = 0;
   for (int i = 0; i < n_tasks; ++i) a.slices += (tasks[i].N + 255) / 256;
   const int64_t most = 8 * (int64_t)sm_count() * per_sm / a.cluster, clusters = units < most ? units : most;
   rc = kernel_fit(c.second, kLoraThreads, c.second_smem, &per_sm);
   if (rc) return rc;
+  // the second kernel's windows: up to 1024 tokens, as long as there are four blocks of them for each that is resident
+  a.window2 = kMostBlocks * 16 / a.tile;
+  while (a.window2 > 1 && (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices < 4 * (int64_t)sm_count() * per_sm) a.window2 /= 2;
   const int64_t pieces = (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices, most2 = 64 * (int64_t)sm_count() * per_sm;
   if (pieces > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d slices of columns", g->max_tiles, a.slices);
   cudaError_t e = kv8::launch_early(c.first, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.first_smem, s, a.cluster);
