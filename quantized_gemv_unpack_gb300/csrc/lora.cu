@@ -219,9 +219,6 @@ __device__ __forceinline__ float4 ld_remote(uint32_t p) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* p) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
 }
-__device__ __forceinline__ void copy8(uint32_t to, const void* p) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(p) : "memory");
-}
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }   // all of this thread's
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -348,6 +345,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   const int rank = (int)cluster_rank(), C = a.cluster, clusters = gridDim.x / C;
   unsigned char* ring = rings + warp * (D * S::kSlot);
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  // B: eight rank rows of 64 bytes, the even ones and then the odd ones, each piece where neither its copy nor the reads of
+  // column 4 g of rows 2 t4 and 2 t4 + 1 meet another lane's bank
+  const int b_to = (g & 1) * 256 + ((g >> 1) ^ (g & 1)) * 64 + ((t4 ^ (g >> 2) * 2) * 16);
+  const int b_even = t4 * 64 + ((g >> 1) ^ (t4 >> 1) * 2) * 16 + (g & 1) * 8, b_odd = 256 + (b_even ^ 64);
   const int j0 = half * 8 * RB;                               // this warp's first rank row in the first product
   follow_previous();
   bool reading = false;                                       // other blocks may still read `mine`
@@ -386,7 +387,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     const int k_lo = rank * k_share, k_hi = min(a.K, k_lo + k_share), n_lo = rank * n_share, n_hi = min(t.N, n_lo + n_share);
     int k_next = k_lo + part * 32, n_next = n_lo + warp * 32, piece_next = 0, slot_in = 0, slot = 0;
     const __nv_bfloat16* pa = t.a + (int64_t)(row0 + j0 + g) * t.lda + 8 * t4;
-    const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + 4 * g;
+    const __nv_bfloat16* pb = t.b + (int64_t)(row0 + g) * t.ldb + 8 * t4;
+    const int64_t step_b = 8 * t.ldb;
     const int64_t step_a = 8 * t.lda;
     const auto ask = [&]() {
       const uint32_t to = ring_at + slot_in * S::kSlot + lane * 16;
@@ -402,25 +404,21 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
         }
         k_next += S::kParts * 32;
       } else if (n_next < n_hi) {
-        const int col = n_next + 4 * g, n = n_next + 8 * t4;
+        const int col = n_next + 8 * t4, n = col;
         if (col < t.N) {
           const __nv_bfloat16* p = pb + n_next + (int64_t)(16 * KH * piece_next) * t.ldb;
-          const uint32_t at = ring_at + slot_in * S::kSlot + lane * 8;
+          const uint32_t at = slot_in * S::kSlot + b_to;
 #pragma unroll
-          for (int s = 0; s < KH; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int off = 16 * s + (i & 1) + 8 * (i >> 1);
-              if (16 * KH * piece_next + off + 2 * t4 >= r) continue;
-              const __nv_bfloat16* q = p + off * t.ldb;
-              if (col + 4 <= t.N) {
-                copy8(at + (4 * s + i) * 256, q);
-              } else {                                        // the row's last values, one by one
-                const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
-                uint16_t* d = reinterpret_cast<uint16_t*>(ring + slot_in * S::kSlot + lane * 8 + (4 * s + i) * 256);
-                for (int c = 0; c < 4; ++c) d[c] = col + c < t.N ? e[c] : (uint16_t)0;
-              }
+          for (int i = 0; i < 2 * KH; ++i, p += step_b) {
+            if (16 * KH * piece_next + 8 * i + g >= r) continue;
+            if (col + 8 <= t.N) {
+              copy16(ring_at + at + i * 512, p);
+            } else {                                          // the row's last values, one by one
+              const uint16_t* e = reinterpret_cast<const uint16_t*>(p);
+              uint16_t* d = reinterpret_cast<uint16_t*>(ring + at + i * 512);
+              for (int c = 0; c < 8; ++c) d[c] = col + c < t.N ? e[c] : (uint16_t)0;
             }
+          }
         }
         const bool last = ++piece_next == S::kPieces;         // y comes with the last rank rows
         if (last) piece_next = 0;
@@ -521,8 +519,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       const unsigned char* st = ring;
 #pragma unroll
       for (int hf = 0; hf < S::kPieces; ++hf) {
+        __syncwarp();                                         // the slot that is asked for was other lanes' too
         ask();
         asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+        __syncwarp();
         st = ring + slot * S::kSlot;
         slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
@@ -535,8 +535,8 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
           for (int i = 0; i < 2; ++i) {
             const int j = 16 * s + 8 * i + 2 * t4;
             uint2 u = make_uint2(0, 0), v = u;
-            if (full || j < r) u = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * e + 2 * i) * 256);
-            if (full || j + 1 < r) v = *reinterpret_cast<const uint2*>(st + lane * 8 + (4 * e + 2 * i + 1) * 256);
+            if (full || j < r) u = *reinterpret_cast<const uint2*>(st + b_even + (2 * e + i) * 512);
+            if (full || j + 1 < r) v = *reinterpret_cast<const uint2*>(st + b_odd + (2 * e + i) * 512);
             b[0][i] = __byte_perm(u.x, v.x, 0x5410);
             b[1][i] = __byte_perm(u.x, v.x, 0x7632);
             b[2][i] = __byte_perm(u.y, v.y, 0x5410);
