@@ -976,8 +976,10 @@ Choice choose(int max_rank) {
   return max_rank <= 16 ? choice_of<2, Y>() : max_rank <= 32 ? choice_of<4, Y>() : max_rank <= 64 ? choice_of<8, Y>() : choice_of<16, Y>();
 }
 
-// Whether a call is one of many tokens per adapter, by the tokens that an adapter has on average.
-bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1024; }
+// Whether a call is one of many tokens per adapter: its tiles then have 64 tokens, and it takes the two kernels. With 16-token
+// tiles and with these, us: 1536 tokens of 5 adapters, rank 64, K 5120, q|k|v 61 and 52, gate|up 157 and 120; of 60 adapters, rank
+// 16, N 5120 28 and 36; of 200 adapters, rank 64 67 and 108; 1000 tokens of one adapter, rank 64, gate|up 90 and 98.
+bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1024 && n_tokens >= 64 * n_adapters; }
 
 }  // namespace
 }  // namespace qmv
@@ -986,17 +988,17 @@ using namespace qmv;
 
 extern "C" {
 
-int32_t lora_tile(int64_t n_tokens) { return n_tokens < 1024 ? kSmallTile : kLargeTile; }
+int32_t lora_tile(int64_t n_tokens, int64_t n_adapters) { return many_tokens(n_tokens, n_adapters) ? kLargeTile : kSmallTile; }
 
 int64_t lora_max_tiles(int64_t n_tokens, int64_t n_adapters) {
   if (n_tokens <= 0 || n_adapters <= 0) return 0;
-  return n_tokens / lora_tile(n_tokens) + (n_tokens < n_adapters ? n_tokens : n_adapters);
+  return n_tokens / lora_tile(n_tokens, n_adapters) + (n_tokens < n_adapters ? n_tokens : n_adapters);
 }
 
 size_t lora_workspace_size(int64_t n_tokens, int64_t n_adapters, int32_t max_rank, int32_t n_tasks) {
   if (n_tokens <= 0 || n_adapters <= 0 || max_rank <= 0 || max_rank > kMaxRank || n_tasks <= 0 || !many_tokens(n_tokens, n_adapters)) return 0;
   const int64_t steps = max_rank <= 16 ? 1 : max_rank <= 32 ? 2 : max_rank <= 64 ? 4 : 8;   // of 16 rank rows, as the kernels are made
-  return (size_t)(lora_max_tiles(n_tokens, n_adapters) * (lora_tile(n_tokens) / 16) * n_tasks * steps * 3 * 512);
+  return (size_t)(lora_max_tiles(n_tokens, n_adapters) * (kLargeTile / 16) * n_tasks * steps * 3 * 512);
 }
 
 int lora_plan(const lora_plan_args* g, void* stream) {
@@ -1011,7 +1013,7 @@ int lora_plan(const lora_plan_args* g, void* stream) {
   if (g->max_tiles == 0) return QMV_OK;
   int* err = device_error_word();
   if (!err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
-  PlanArgs a{g->ids, g->order, reinterpret_cast<int4*>(g->tiles), err, g->n_tokens, g->n_adapters, lora_tile(g->n_tokens), g->max_tiles};
+  PlanArgs a{g->ids, g->order, reinterpret_cast<int4*>(g->tiles), err, g->n_tokens, g->n_adapters, lora_tile(g->n_tokens, g->n_adapters), g->max_tiles};
   const void* f = reinterpret_cast<const void*>(lora_plan_kernel);
   // a warp for every 128 tokens, up to 32: fewer counters to clear and to sum where there are few
   const int warps = g->n_tokens >= 4096 ? 32 : g->n_tokens >= 512 ? 16 : 8;
@@ -1078,7 +1080,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (need && !aligned16(g->workspace)) return fail(QMV_ERR_ALIGN, "workspace must be 16-byte aligned");
   a.err = device_error_word();
   if (!a.err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
-  a.tile = lora_tile(g->n_tokens);
+  a.tile = lora_tile(g->n_tokens, g->n_adapters);
   const int type = tasks[0].y_type, cluster = kCluster;
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank) : choose<QMV_F16>(g->max_rank);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
