@@ -586,3 +586,154 @@ def test_streams_by_argument(env):
     call.run(s.cuda_stream)
     s.synchronize()
     assert abs(float(call.lse[0]) - float(torch.logsumexp(out[0].double(), 0))) < 1e-5
+
+
+# ----------------------------------------------------------------------------- sizes, workspaces and graphs
+
+def test_rows_past_32_bits(env):
+    """Rows whose offsets, in values and in bytes, are past 2^32."""
+    from oracle import int4, step
+    q, torch, dev = env
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    far = lambda rows, cols, ld, dt: torch.empty((rows - 1) * ld + cols, dtype=dt, device=dev).as_strided((rows, cols), (ld, 1))  # noqa: E731
+    g = np.random.default_rng(4)
+    # an embedding table of 4.5 GB whose last 16 rows, one group of the layout, are those of a small one; far rows of the result
+    n, K = 2 ** 21 + 16, 4096
+    small, packed, codes, s16 = _packed(env, "int4", 16, K, 3)
+    d = q.qmv_pack_desc(q.QMV_INT4, n, K)
+    big = torch.zeros(d.total_bytes, dtype=torch.uint8, device=dev)
+    for i in (0, 1):
+        of = lambda e: slice(e.off[i] + e.bytes[i] - small.bytes[i], e.off[i] + e.bytes[i])  # noqa: E731
+        big[of(d)] = packed[of(small)]
+    out = far(5, K, 2 ** 30 + 8, torch.float32)
+    q.qmv_embed(d, big, i32([n - 1, 0, n - 16, n - 7, n - 2]), out, 1.0)
+    w = torch.from_numpy(int4.dequant(codes, s16.view(np.uint16))).float().to(dev)
+    assert torch.equal(out[[0, 2, 3, 4]], w[[15, 0, 9, 14]]) and not bool(out[1].any())
+    del big, out
+    # adapters of one tile and of many: rows of x, A, B and y
+    for T, ld in ((3, 2 ** 31 + 8), (1030, 2 ** 23)):
+        x, y = far(T, 64, ld, torch.bfloat16), far(T, 72, ld, torch.bfloat16)
+        a, b = far(3, 64, 2 ** 31 + 8, torch.bfloat16), far(3, 72, 2 ** 31 + 8, torch.bfloat16)
+        for t in (x, y, a, b):
+            t.copy_(torch.from_numpy(g.standard_normal(tuple(t.shape))))
+        was, ids = _f64(y), np.zeros(T, dtype=int)
+        q.Lora(_plan(env, ids, 1), i32([[0, 3]]), torch.ones(1, device=dev), x, [(a, b, y)], max_rank=3).run()
+        want, s1, s2 = step.lora(was, _f64(x), ids, [(0, 3)], [1.0], _f64(a), _f64(b))
+        assert np.all(np.abs(_f64(y) - want) <= 2.0 ** -16 * (s1 + s2) + (HALF["bf16"] + 2.0 ** -20) * np.abs(want))
+        del x, y, a, b
+    torch.cuda.empty_cache()
+    # logits: an odd stride
+    x = far(3, 1000, 2 ** 31 + 5, torch.bfloat16)
+    x.copy_(torch.from_numpy(g.standard_normal((3, 1000)) * 3))
+    call = q.LogProb(x, i32([5, 999, 0]), top=3)
+    call.run()
+    for t in range(3):
+        lp, rank, lse, h, idx, vals = step.logprob(_f64(x[t]), 1.0, (5, 999, 0)[t], 3)
+        assert int(call.rank[t]) == rank and call.top_index[t].tolist() == idx
+        assert abs(float(call.lse[t]) - lse) <= 1e-5 and abs(float(call.logprob[t]) - lp) <= 1e-5 and abs(float(call.entropy[t]) - h) <= 1e-4
+    assert q.qmv_check_status() == 0
+    del x
+    torch.cuda.empty_cache()
+
+
+def test_no_tokens(env):
+    q, torch, dev = env
+    empty = lambda *s, dt=torch.float32: torch.empty(s, dtype=dt, device=dev)  # noqa: E731
+    d, packed, codes, s16 = _packed(env, "int4", 16, 128, 3)
+    ids = empty(0, dt=torch.int32)
+    q.qmv_embed(d, packed, ids, empty(0, 128), 1.0)
+    plan = q.LoraPlan(ids, 4)
+    plan.run()
+    a, b = empty(4, 64, dt=torch.bfloat16), empty(4, 8, dt=torch.bfloat16)
+    q.Lora(plan, torch.zeros((4, 2), dtype=torch.int32, device=dev), empty(4), empty(0, 64, dt=torch.bfloat16), [(a, b, empty(0, 8))]).run()
+    q.LogProb(empty(0, 50), ids, top=3).run()
+    torch.cuda.synchronize()
+    assert q.qmv_check_status() == 0
+
+
+def test_lora_long_runs_of_an_adapter(env):
+    """Many tokens: runs and windows that end inside the list, adapters that end inside a run, and rows without an adapter."""
+    g = np.random.default_rng(11)
+    for T, A, K, Ns, kind, rank in [(9000, 1, 40, [40], "f32", 5), (5000, 3, 104, [264, 16], "bf16", 33), (2500, 7, 72, [33], "f16", 100), (1537, 2, 2048, [300], "f32", 64)]:
+        ids = np.sort(g.integers(-1, A, T))
+        ids[g.integers(0, T, 9)] = -1
+        _lora_case(env, ids, np.maximum(g.integers(0, rank + 1, A), np.arange(A) == 0), K, Ns, kind, T, max_rank=rank, magnitude=0.1)
+
+
+class _Prompt:
+    """Two layers' adapters of a prompt chunk, on one workspace, with the step's plan."""
+
+    def __init__(self, env, T=1500, seed=0):
+        q, torch, dev = env
+        self.env, self.T, self.A = env, T, 6
+        g = torch.Generator(device=dev).manual_seed(seed)
+        new = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+        self.ids = torch.zeros(T, dtype=torch.int32, device=dev)
+        self.table = torch.tensor([[0, 16], [16, 7], [23, 1], [24, 0], [30, 12], [4, 16]], dtype=torch.int32, device=dev)
+        self.scale = torch.tensor([1.0, -0.5, 2.0, 1.0, 0.25, 1.5], device=dev)
+        self.x, self.a, self.b = new(T, 256), [new(48, 256), new(48, 200)], [new(48, 200), new(48, 264)]
+        self.y0 = [torch.randn((T, n), generator=g, device=dev) for n in (200, 264)]
+        self.y = [torch.empty_like(y) for y in self.y0]
+        self.mid = torch.empty((T, 200), dtype=torch.bfloat16, device=dev)
+        self.plan = q.LoraPlan(self.ids, self.A)
+        first = q.Lora(self.plan, self.table, self.scale, self.x, [(self.a[0], self.b[0], self.y[0])], max_rank=16)
+        assert first.workspace.numel() > 0
+        self.calls = [first, q.Lora(self.plan, self.table, self.scale, self.mid, [(self.a[1], self.b[1], self.y[1])], max_rank=16, workspace=first.workspace)]
+
+    def run(self):
+        for y, y0 in zip(self.y, self.y0):
+            y.copy_(y0)
+        self.plan.run()
+        self.calls[0].run()
+        self.mid.copy_(self.y[0])
+        self.calls[1].run()
+
+    def check(self):
+        from oracle import step
+        for x, a, b, y, y0 in zip((self.x, self.mid), self.a, self.b, self.y, self.y0):
+            want, s1, s2 = step.lora(_f64(y0), _f64(x), self.ids.tolist(), self.table.tolist(), self.scale.double().tolist(), _f64(a), _f64(b))
+            # K / 16 matrix products with 16 additions inside and 16 joins, then 26, each within 2^-23; y's rounding
+            assert np.all(np.abs(_f64(y) - want) <= (x.shape[1] / 16 + 32) * 2.0 ** -23 * s1 + 42 * 2.0 ** -23 * s2 + 2.0 ** -22 * np.abs(want) + 1e-30)
+
+    def fill(self, seed):
+        torch = self.env[1]
+        self.ids.copy_(torch.randint(-1, self.A, (self.T,), generator=torch.Generator().manual_seed(seed)))
+
+
+def test_lora_many_tokens_in_graphs_and_on_streams(env):
+    """A chunk's calls captured twice over one workspace, replayed on other ids, and run eagerly on streams of their own."""
+    q, torch, dev = env
+    s = _Prompt(env)
+    s.fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        s.run()
+    torch.cuda.synchronize()
+    s.check()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for gr in graphs:
+        with torch.cuda.graph(gr):
+            s.run()
+    for seed in (1, 2):
+        s.fill(seed)
+        graphs[seed % 2].replay()
+        graphs[(seed + 1) % 2].replay()
+        torch.cuda.synchronize()
+        s.check()
+        got = [y.clone() for y in s.y]
+        s.run()
+        assert all(torch.equal(a, b) for a, b in zip(got, s.y))
+    other = _Prompt(env, seed=7)
+    other.fill(3)
+    two = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            s.run()
+        with torch.cuda.stream(two):
+            other.run()
+    torch.cuda.synchronize()
+    s.check()
+    other.check()
+    assert q.qmv_check_status() == 0
