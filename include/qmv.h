@@ -737,7 +737,7 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * QMV_LORA_MAX_TASKS: q|k|v, gate|up) share x, the plan, the table and the
  * scales, have one y_type, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
  * and ldx multiples of 8; y: [n_tokens][ldy] of y_type, as the projection left
- * it (rows of 32-byte alignment are fastest). n_tokens, n_adapters and max_tiles
+ * it (rows of 16-byte alignment are fastest). n_tokens, n_adapters and max_tiles
  * are the plan's. max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
  * chooses the kernel; an adapter may have rank 0.
  * Products are exact and sums fp32; the r values between the two products are

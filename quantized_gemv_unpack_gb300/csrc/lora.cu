@@ -179,7 +179,7 @@ struct Task {
   void* y;
   int64_t lda, ldb, ldy;
   int32_t N;
-  int32_t wide;                // rows of y are 32-byte aligned
+  int32_t wide;                // rows of y are 16-byte aligned
 };
 
 struct RunArgs {
@@ -250,7 +250,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// A lane's consecutive values of a row of y: one piece of 16 bytes, or two that lie 512 bytes apart.
+// A lane's values of a row of y: one piece of 16 bytes, or two: 512 bytes apart in a ring, 64 in y.
 template <int WORDS>
 __device__ __forceinline__ void ld_pieces(const unsigned char* p, uint32_t (&w)[WORDS]) {
 #pragma unroll
@@ -260,14 +260,16 @@ __device__ __forceinline__ void ld_pieces(const unsigned char* p, uint32_t (&w)[
   }
 }
 template <int WORDS>
-__device__ __forceinline__ void st_global(void* p, const uint32_t (&w)[WORDS]) {
-  if constexpr (WORDS == 8)
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
-                 "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  else
-    *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void st_pieces(char* p, const uint32_t (&w)[WORDS]) {
+#pragma unroll
+  for (int i = 0; i < WORDS; i += 4) *reinterpret_cast<uint4*>(p + 16 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
 }
+// Where a lane's columns of 32 lie: eight consecutive ones in 16 bits, else four and, 16 columns on, four more, so that each access
+// of a warp has whole sectors; and, per column of an n8 block of the products, the first of its four.
+template <int Y>
+__device__ __forceinline__ int own_column(int t4) { return Y == QMV_F32 ? 4 * t4 : 8 * t4; }
+template <int Y>
+__device__ __forceinline__ int block_column(int g) { return Y == QMV_F32 ? 16 * (g & 1) + 4 * (g >> 1) : 4 * g; }
 // The sum of column c of the 2 * BLOCKS that a lane has of row HI (g or g + 8): block c % BLOCKS, half c / BLOCKS.
 template <int HI, int BLOCKS>
 __device__ __forceinline__ float column(const float (&d)[BLOCKS][4], int c) {
@@ -275,7 +277,7 @@ __device__ __forceinline__ float column(const float (&d)[BLOCKS][4], int c) {
 }
 // y += s * d over a lane's columns, whose values are w.
 template <int Y, int HI, int BLOCKS, int WORDS>
-__device__ __forceinline__ void add_row(void* p, float s, const float (&d)[BLOCKS][4], uint32_t (&w)[WORDS]) {
+__device__ __forceinline__ void add_row(char* p, float s, const float (&d)[BLOCKS][4], uint32_t (&w)[WORDS]) {
   if constexpr (Y == QMV_F32) {
 #pragma unroll
     for (int c = 0; c < WORDS; ++c) w[c] = __float_as_uint(fmaf(s, column<HI>(d, c), __uint_as_float(w[c])));
@@ -286,17 +288,18 @@ __device__ __forceinline__ void add_row(void* p, float s, const float (&d)[BLOCK
       w[i] = pack2<Y>(fmaf(s, column<HI>(d, 2 * i), v.x), fmaf(s, column<HI>(d, 2 * i + 1), v.y));
     }
   }
-  st_global(p, w);
+  st_pieces(p, w);
 }
-// The same value by value, up to column n of them.
+// The same value by value, up to column n from the first of them on.
 template <int Y, int HI, int BLOCKS>
 __device__ __forceinline__ void add_row_part(void* p, int n, float s, const float (&d)[BLOCKS][4]) {
 #pragma unroll
   for (int c = 0; c < 2 * BLOCKS; ++c) {
-    if (c >= n) break;
+    const int at = Y == QMV_F32 ? c % 4 + c / 4 * 16 : c;
+    if (at >= n) break;
     const float v = column<HI>(d, c);
     if constexpr (Y == QMV_F32) {
-      float* q = static_cast<float*>(p) + c;
+      float* q = static_cast<float*>(p) + at;
       *q = fmaf(s, v, *q);
     } else if constexpr (Y == QMV_BF16) {
       __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + c;
@@ -346,9 +349,11 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   unsigned char* ring = rings + warp * (D * S::kSlot);
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   // B: eight rank rows of 64 bytes, the even ones and then the odd ones, each piece where neither its copy nor the reads of
-  // column 4 g of rows 2 t4 and 2 t4 + 1 meet another lane's bank
-  const int b_to = (g & 1) * 256 + ((g >> 1) ^ (g & 1)) * 64 + ((t4 ^ (g >> 2) * 2) * 16);
-  const int b_even = t4 * 64 + ((g >> 1) ^ (t4 >> 1) * 2) * 16 + (g & 1) * 8, b_odd = 256 + (b_even ^ 64);
+  // the lane's four columns of rows 2 t4 and 2 t4 + 1 meet another lane's bank
+  constexpr int kTurn = F32 ? 1 : 2;
+  const int b_col = block_column<Y>(g);
+  const int b_to = (g & 1) * 256 + ((g >> 1) ^ (g & 1)) * 64 + ((t4 ^ (g >> 2) * kTurn) * 16);
+  const int b_even = t4 * 64 + ((b_col >> 3) ^ (t4 >> 1) * kTurn) * 16 + (b_col & 4) * 2, b_odd = 256 + (b_even ^ 64);
   const int j0 = half * 8 * RB;                               // this warp's first rank row in the first product
   follow_previous();
   bool reading = false;                                       // other blocks may still read `mine`
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
         }
         k_next += S::kParts * 32;
       } else if (n_next < n_hi) {
-        const int col = n_next + 8 * t4, n = col;
+        const int col = n_next + 8 * t4, n = n_next + own_column<Y>(t4);
         if (col < t.N) {
           const __nv_bfloat16* p = pb + n_next + (int64_t)(16 * KH * piece_next) * t.ldb;
           const uint32_t at = slot_in * S::kSlot + b_to;
@@ -422,14 +427,14 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
         }
         const bool last = ++piece_next == S::kPieces;         // y comes with the last rank rows
         if (last) piece_next = 0;
-        if (last && t.wide && n + 8 <= t.N) {
+        if (last && t.wide && (F32 ? n_next + 32 : n + 8) <= t.N) {
           if (tok0 >= 0) {
             copy16(to + S::kB, y0 + (int64_t)n * size);
-            if constexpr (F32) copy16(to + S::kB + 512, y0 + (int64_t)n * size + 16);
+            if constexpr (F32) copy16(to + S::kB + 512, y0 + (int64_t)n * size + 64);
           }
           if (tok1 >= 0) {
             copy16(to + S::kB + 256 * size, y1 + (int64_t)n * size);
-            if constexpr (F32) copy16(to + S::kB + 256 * size + 512, y1 + (int64_t)n * size + 16);
+            if constexpr (F32) copy16(to + S::kB + 256 * size + 512, y1 + (int64_t)n * size + 64);
           }
         }
         if (last) n_next += kLoraWarps * 32;
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     // ---- second product, over this block's share of N
     const uint4* h = frag + lane;
     for (int n0 = n_lo + warp * 32; n0 < n_hi; n0 += kLoraWarps * 32) {
-      const int n = n0 + 8 * t4;                              // first column of this lane's sums
+      const int n = n0 + own_column<Y>(t4);                   // first column of this lane's sums
       float d[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
           }
         }
       }
-      if (t.wide && n + 8 <= t.N) {
+      if (t.wide && (F32 ? n0 + 32 : n + 8) <= t.N) {
         uint32_t v[WORDS];
         const unsigned char* sy = st + S::kB + lane * 16;
         if (tok0 >= 0) ld_pieces(sy, v), add_row<Y, 0>(y0 + (int64_t)n * size, scale, d, v);
@@ -799,8 +804,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
     while (slice >= (a.t[task].N + 255) / 256) slice -= (a.t[task++].N + 255) / 256;
     const Task& t = a.t[task];
     const int base = unit / a.slices * a.window2, tiles = min(a.window2, a.max_tiles - base);
-    const int n0 = slice * 256 + warp * 32, n = n0 + 8 * t4, col = n0 + 4 * g;   // this warp's columns; the first of this lane's sums, and of its loads of B
-    const bool whole = t.wide && n + 8 <= t.N;
+    const int n0 = slice * 256 + warp * 32, n = n0 + own_column<Y>(t4), col = n0 + block_column<Y>(g);   // this warp's columns; the first of this lane's sums, and of its loads of B
+    const bool whole = t.wide && (F32 ? n0 + 32 : n + 8) <= t.N;
     char* y = static_cast<char*>(t.y);
     for (int j = 0; j < tiles;) {
       const int first = base + j++;
@@ -846,11 +851,11 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
           const uint32_t to = ring_at + slot_in * S::kBlockY;
           if (m_in < plain_blocks || (whole && ta >= 0)) {
             copy16(to, yq + ta);
-            if constexpr (F32) copy16(to + 512, yq + ta + 16);
+            if constexpr (F32) copy16(to + 512, yq + ta + 64);
           }
           if (m_in < plain_blocks || (whole && tb >= 0)) {
             copy16(to + S::kBlockY / 2, yq + tb);
-            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, yq + tb + 16);
+            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, yq + tb + 64);
           }
         }
         copies_end();
@@ -928,8 +933,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
               const int c = 2 * (i % 4), hi = 2 * (i / 4);
               v[i / 4][i % 4] = pack2<Y>(d[c % 4][hi + c / 4], d[(c + 1) % 4][hi + (c + 1) / 4]);
             }
-            if (PLAIN || ta >= 0) st_global(q + ta, v[0]);
-            if (PLAIN || tb >= 0) st_global(q + tb, v[1]);
+            if (PLAIN || ta >= 0) st_pieces(q + ta, v[0]);
+            if (PLAIN || tb >= 0) st_pieces(q + tb, v[1]);
           }
         } else {
           if (ta >= 0) add_row_part<Y, 0>(q + ta, t.N - n, scale, d);
@@ -1071,7 +1076,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
       if (!k.a || !k.b || !k.y) return fail(QMV_ERR_ARG, "task %d: NULL a, b or y", i);
       if (!aligned16(k.a) || !aligned16(k.b) || !aligned16(k.y)) return fail(QMV_ERR_ALIGN, "task %d: a, b and y must be 16-byte aligned", i);
     }
-    a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, (int32_t)(k.ldy * ys % 32 == 0 && (reinterpret_cast<uintptr_t>(k.y) & 31u) == 0)};
+    a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, (int32_t)(k.ldy * ys % 16 == 0)};
   }
   if (g->n_tokens == 0) return QMV_OK;
   if ((int64_t)g->max_tiles * n_tasks > INT32_MAX / 64) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d tasks", g->max_tiles, n_tasks);
