@@ -210,6 +210,13 @@ __device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   return r;
 }
+__device__ __forceinline__ float4 sum(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+__device__ __forceinline__ void st_remote(uint32_t p, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_remote(uint32_t p, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ float4 ld_remote(uint32_t p) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
@@ -329,6 +336,10 @@ struct Short {
   static constexpr int kFirst = (kBlocks + 2) * 512, kB = kSteps / kPieces * 1024, kSecond = kB + (F32 ? 2048 : 1024);
   static constexpr int kSlot = kFirst > kSecond ? kFirst : kSecond;
   static constexpr int kDepth = NB == 2 ? 4 : NB == 4 ? 3 : 2;   // what two blocks of an SM have room for
+  // Whether the blocks of a cluster share the work on its sums (two exchanges) or each reads all of them (one). us: 256 tokens of 4
+  // adapters, rank 128, K = N = 4096 16.8 and 20.3; 1000 tokens of rank 64, K = N = 5120 27.7 and 29.8; 1023 tokens of 8 adapters, rank
+  // 32, q|k|v 28.2 and 27.2; one token of rank 16, K = N = 4096 5.0 and 4.8.
+  static constexpr bool kShared = NB > 4;
   static constexpr int kFixed = kWords * 16 + kSteps * kParts3 * 512 + kLoraWarps * (int)sizeof(int);
   static constexpr int kSmem = kFixed + kLoraWarps * kDepth * kSlot;
 };
@@ -339,7 +350,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   constexpr int KS = S::kSteps, W = S::kWords, RB = S::kBlocks, P3 = S::kParts3, size = Y == QMV_F32 ? 4 : 2, WORDS = 2 * size, D = S::kDepth, KH = KS / S::kPieces;
   constexpr bool F32 = S::F32;
   extern __shared__ __align__(16) unsigned char lora_smem[];
-  float4* mine = reinterpret_cast<float4*>(lora_smem);        // [W]: this block's sums, which the cluster reads
+  float4* mine = reinterpret_cast<float4*>(lora_smem);        // kShared: [C][2][W / 2 / C], the blocks' sums of this block's items; else [W], its own sums
   uint4* frag = reinterpret_cast<uint4*>(mine + W);           // [KS][P3][32]: the parts of the finished values
   int* sums_in = reinterpret_cast<int*>(frag + KS * P3 * 32); // [kLoraWarps]: the slot in which a warp left its sums
   unsigned char* rings = lora_smem + S::kFixed;
@@ -355,8 +366,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   const int b_to = (g & 1) * 256 + ((g >> 1) ^ (g & 1)) * 64 + ((t4 ^ (g >> 2) * kTurn) * 16);
   const int b_even = t4 * 64 + ((b_col >> 3) ^ (t4 >> 1) * kTurn) * 16 + (b_col & 4) * 2, b_odd = 256 + (b_even ^ 64);
   const int j0 = half * 8 * RB;                               // this warp's first rank row in the first product
+  if constexpr (S::kShared) cluster_arrive();
   follow_previous();
-  bool reading = false;                                       // other blocks may still read `mine`
+  bool waiting = S::kShared;                                  // for the cluster: to have begun, or to have read `mine`
   for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
     const Task& t = a.t[unit / a.max_tiles];
     const int4 tile = a.tiles[unit % a.max_tiles];
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       if (tok0 >= a.n_tokens) tok0 = -1;
       if (tok1 >= a.n_tokens) tok1 = -1;
     }
-    __syncthreads();                                          // the unit before this one is done with frag
+    __syncthreads();                                          // the unit before this one is done with frag and the rings
     const __nv_bfloat16* x0 = a.x + (int64_t)(tok0 < 0 ? 0 : tok0) * a.ldx;
     const __nv_bfloat16* x1 = a.x + (int64_t)(tok1 < 0 ? 0 : tok1) * a.ldx;
     char* y0 = static_cast<char*>(t.y) + (int64_t)(tok0 < 0 ? 0 : tok0) * t.ldy * size;
@@ -475,44 +487,73 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       if (lane == 0) sums_in[warp] = slot_in * S::kSlot;
     }
     __syncthreads();
-    if (reading) cluster_wait();
-    for (int i = tid; i < W; i += kLoraThreads) {
+    if (waiting) cluster_wait();
+    // The cluster's sums, of which every block needs all. An item is a lane's eight values of one k16 step, two words.
+    const auto of_warps = [&](int i) {                        // this block's sum of word i
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int p = 0; p < S::kParts; ++p) {
         const int w = p * S::kHalves + i / 32 / RB;
-        const float4 o = reinterpret_cast<const float4*>(rings + w * (D * S::kSlot) + sums_in[w])[i % (32 * RB)];
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        v = sum(v, reinterpret_cast<const float4*>(rings + w * (D * S::kSlot) + sums_in[w])[i % (32 * RB)]);
       }
-      mine[i] = v;
-    }
-    cluster_arrive();
-    cluster_wait();
-
-    // ---- the cluster's sums, in every block: item i is a lane's eight values of one k16 step
-    for (int i = tid; i < W / 2; i += kLoraThreads) {
-      const int at = (i / 32) * 64 + i % 32;
-      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-#pragma unroll 8
-      for (int c = 0; c < C; ++c) {
-        const uint32_t p = remote(mine + at, c);
-        const float4 o = ld_remote(p), w = ld_remote(p + 32 * 16);
-        u.x += o.x, u.y += o.y, u.z += o.z, u.w += o.w;
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
-      }
+      return v;
+    };
+    const auto parts_of = [&](float4 u, float4 v, uint4 (&f)[P3]) {
 #pragma unroll
       for (int k = 0; k < P3; ++k) {
-        uint4 f;
-        f.x = split(u.x, u.y);
-        f.y = split(u.z, u.w);
-        f.z = split(v.x, v.y);
-        f.w = split(v.z, v.w);
-        frag[((i / 32) * P3 + k) * 32 + i % 32] = f;
+        f[k].x = split(u.x, u.y);
+        f[k].y = split(u.z, u.w);
+        f[k].z = split(v.x, v.y);
+        f[k].w = split(v.z, v.w);
       }
+    };
+    constexpr int ITEMS = W / 2;
+    if constexpr (S::kShared) {
+      // each block finishes a share of the items: it gets their words from every block, and sends the parts to every block
+      const int per = ITEMS / C;
+      for (int i = tid; i < W; i += kLoraThreads) {
+        if (8 * (i / 32) >= r) break;
+        const int item = i / 64 * 32 + i % 32;
+        st_remote(remote(mine + (rank * 2 + (i / 32 & 1)) * per + item % per, item / per), of_warps(i));
+      }
+      cluster_arrive();
+      cluster_wait();
+      const int at = tid % per, item = rank * per + at, j = item / 32 * 16;
+      if (tid < ITEMS && j < r) {
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+        for (int c = 0; c < C; ++c) u = sum(u, mine[2 * c * per + at]);
+        if (j + 8 < r)
+          for (int c = 0; c < C; ++c) v = sum(v, mine[(2 * c + 1) * per + at]);
+        uint4 f[P3];
+        parts_of(u, v, f);
+#pragma unroll
+        for (int k = 0; k < P3; ++k) st_remote(remote(frag + (item / 32 * P3 + k) * 32 + item % 32, tid / per), f[k]);
+      }
+      cluster_arrive();
+      cluster_wait();
+      waiting = false;
+    } else {
+      for (int i = tid; i < W; i += kLoraThreads) mine[i] = of_warps(i);
+      cluster_arrive();
+      cluster_wait();
+      for (int i = tid; i < ITEMS; i += kLoraThreads) {
+        const int at = i / 32 * 64 + i % 32;
+        float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 8
+        for (int c = 0; c < C; ++c) {
+          const uint32_t p = remote(mine + at, c);
+          u = sum(u, ld_remote(p));
+          v = sum(v, ld_remote(p + 32 * 16));
+        }
+        uint4 f[P3];
+        parts_of(u, v, f);
+#pragma unroll
+        for (int k = 0; k < P3; ++k) frag[(i / 32 * P3 + k) * 32 + i % 32] = f[k];
+      }
+      cluster_arrive();
+      waiting = true;
+      __syncthreads();
     }
-    cluster_arrive();
-    reading = true;
-    __syncthreads();
 
     // ---- second product, over this block's share of N
     const uint4* h = frag + lane;
@@ -567,7 +608,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
     }
     copies_wait();
   }
-  if (reading) cluster_wait();
+  if (waiting) cluster_wait();
 }
 
 // ---- many tokens of an adapter
