@@ -1127,7 +1127,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   a.err = device_error_word();
   if (!a.err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
   a.tile = lora_tile(g->n_tokens, g->n_adapters);
-  const int type = tasks[0].y_type, cluster = kCluster;
+  const int type = tasks[0].y_type;
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank) : choose<QMV_F16>(g->max_rank);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* args[] = {&a};
@@ -1138,12 +1138,12 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (!many_tokens(g->n_tokens, g->n_adapters)) {
     int rc = kernel_fit(c.few, kLoraThreads, c.few_smem, &per_sm);
     if (rc) return rc;
-    // Few units are cut into eight blocks each; more of them into four or two, as long as all make no more than two rounds, since a
-    // unit has two meetings of its cluster whatever its size. 64 tokens of 48 adapters, q|k|v: 46.0, 30.6 and 35.4 us with 8, 4 and 2;
-    // 80 tokens of 12 adapters, gate|up: 14.7, 16.6 and 27.8.
+    // Few units are cut into eight blocks each, as long as all are resident at once; more of them into four, up to two rounds, or
+    // two, since a unit has two meetings of its cluster whatever its size. us with 8, 4 and 2: 80 tokens of 12 adapters, rank 16,
+    // gate|up 11.9, 12.7, 20.1; 512 of 8, rank 64, gate|up 57, 41, 48; 64 of 48, rank 64, q|k|v 33.0, 24.4, 27.7; 1000 of one, rank 64,
+    // gate|up 89, 79, 73; 1023 of 8, rank 32, q|k|v 51, 33, 27.
     const int64_t blocks = (int64_t)sm_count() * per_sm;
-    a.cluster = cluster;
-    while (a.cluster > 2 && units * a.cluster > 2 * blocks + blocks / 8) a.cluster /= 2;
+    a.cluster = units * kCluster <= blocks + blocks / 4 ? kCluster : units * 4 <= 2 * blocks + blocks / 8 ? 4 : 2;
     const int64_t most = 8 * blocks / a.cluster, clusters = units < most ? units : most;
     cudaError_t e = kv8::launch_early(c.few, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.few_smem, s, a.cluster);
     if (e != cudaSuccess) return cuda_fail(e, "lora_run launch");
@@ -1153,7 +1153,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   int rc = kernel_fit(c.first, kLoraThreads, c.first_smem, &per_sm);
   if (rc) return rc;
   // four blocks per run where that fills the device twice, else eight: 8190 tokens, gate|up: 189 us with 4, 199 with 8
-  a.cluster = units * cluster > 2 * (int64_t)sm_count() * per_sm ? cluster / 2 : cluster;
+  a.cluster = units * kCluster > 2 * (int64_t)sm_count() * per_sm ? kCluster / 2 : kCluster;
   a.window = kRunBlocks * 16 / a.tile;
   a.slices = 0;
   for (int i = 0; i < n_tasks; ++i) a.slices += (tasks[i].N + 255) / 256;
