@@ -890,13 +890,11 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
         if (m_in < blocks) {
           const int64_t ta = row_y[m_in * 16 + g], tb = row_y[m_in * 16 + g + 8];
           const uint32_t to = ring_at + slot_in * S::kBlockY;
-          if (m_in < plain_blocks || (whole && ta >= 0)) {
-            copy16(to, yq + ta);
-            if constexpr (F32) copy16(to + 512, yq + ta + 64);
-          }
-          if (m_in < plain_blocks || (whole && tb >= 0)) {
-            copy16(to + S::kBlockY / 2, yq + tb);
-            if constexpr (F32) copy16(to + S::kBlockY / 2 + 512, yq + tb + 64);
+          const bool plain = m_in < plain_blocks;
+#pragma unroll
+          for (int i = 0; i < size / 2; ++i) {
+            if (plain || (whole && ta >= 0)) copy16(to + i * 512, yq + ta + i * 64);
+            if (plain || (whole && tb >= 0)) copy16(to + S::kBlockY / 2 + i * 512, yq + tb + i * 64);
           }
         }
         copies_end();
@@ -906,6 +904,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
       for (int i = 0; i < AY - 1; ++i) ask();
       uint32_t b[KS][4][2];
       const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
+      const int cols = t.N - col;                             // from this lane's first on
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         uint2 w[4];
@@ -913,14 +912,14 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
         for (int i = 0; i < 4; ++i) {
           const int off = 16 * s + (i & 1) + 8 * (i >> 1);
           w[i] = make_uint2(0, 0);
-          if (off + 2 * t4 < r && col < t.N) {
+          if (off + 2 * t4 < r && cols > 0) {
             const __nv_bfloat16* q = pb + (int64_t)off * t.ldb;
-            if (col + 4 <= t.N) {
+            if (cols >= 4) {
               w[i] = __ldg(reinterpret_cast<const uint2*>(q));
             } else {
               const uint16_t* e = reinterpret_cast<const uint16_t*>(q);
-              w[i].x = e[0] | (col + 1 < t.N ? (uint32_t)e[1] << 16 : 0u);
-              w[i].y = col + 2 < t.N ? e[2] : 0u;
+              w[i].x = e[0] | (cols > 1 ? (uint32_t)e[1] << 16 : 0u);
+              w[i].y = cols > 2 ? e[2] : 0u;
             }
           }
         }
