@@ -741,7 +741,7 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * are the plan's. max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
  * chooses the kernel; an adapter may have rank 0.
  * Products are exact and sums fp32; the r values between the two products are
- * rounded to 2^-25 of themselves for an fp32 y (three bf16 parts) and to 2^-17
+ * rounded to 2^-27 of themselves for an fp32 y (three bf16 parts) and to 2^-18
  * for the others, and y once. The result is reproducible bit for bit. A token's
  * does not depend on the values, the adapters or the places of the others, but
  * the sizes of the call (n_tokens, n_adapters, max_tiles, max_rank, the tasks)

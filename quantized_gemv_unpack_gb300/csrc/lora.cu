@@ -2,25 +2,27 @@
 // grouping of tokens by adapter (lora_plan) and
 //   y[t] += s_a * B_a^T (A_a x[t]),  a the adapter of token t        (lora_run).
 //
-// lora_run is bound by memory: a token's products cost 2 r (K + N) operations
-// for K + 2 N moved values, and a single token's adapter is read once. One launch
-// does both products, so that their r values in between never leave the chip: a
-// cluster of eight blocks takes a tile of tokens of one adapter and one
-// projection; each block forms the first product over an eighth of K, the
-// partial sums meet through distributed shared memory, and each block takes an
-// eighth of N in the second. Warp-level products (mma.sync m16n8k16, bf16 with
-// fp32 sums) are far from their limit here (11 GFLOP against 0.9 GB for the
-// largest measured call), and they take both operands as they lie in memory:
-// * first product: a lane's 16 bytes of a row of x and of a row of A are eight
-//   consecutive k. A contraction may take its index in any order, so these are
-//   the lane's pairs of two k16 steps: no shuffle and no shared memory.
-// * second product: a lane's 16 bytes of a row of B are eight consecutive n of
-//   one rank row; two rows zipped by byte permutes are the pairs of eight n8
-//   blocks, whose column m is n0 + 8 m + block. So a lane's sums are sixteen
-//   consecutive columns of y: whole 32-byte sectors in and out.
-// The r values in between are fp32 sums, handed to the second product as two
-// bf16 parts (value and remainder: 2^-18 of each), so that an fp32 y keeps its
-// precision.
+// What a call has to move: x once, y in and out, the rank rows of the adapters in use; 2 r (K + N) operations per token and
+// projection beside it. With few tokens per adapter the rank rows are most of it, with many y is. Both products run on what
+// lies in memory as it is:
+// * few tokens (lora_short_kernel): one launch. A cluster of blocks takes a tile of up to 16 tokens of one adapter and one
+//   projection, each block a share of K in the first product and of N in the second; the sums between them meet in
+//   distributed shared memory and never leave the chip. mma.sync m16n8k16, bf16 with fp32 sums.
+// * many tokens (lora_first_kernel, lora_second_kernel): two launches with the finished values between them in the caller's
+//   workspace. The first product is one of the fifth-generation tensor cores, 128 tokens by the rank; the second, whose y in and
+//   out is the call's bulk, is mma.sync with B in registers and y through rings of asynchronous copies.
+// In the mma.sync products operands are whole pieces of rows:
+// * first product: a lane's 16 bytes of a row of x and of a row of A are eight consecutive k. A contraction may take its
+//   index in any order, so these are the lane's pairs of two k16 steps: no shuffle.
+// * second product: a lane's 8 bytes of a row of B are four consecutive n of one rank row; two rows zipped by byte permutes
+//   are the pairs of four n8 blocks, so that a lane's sums are two runs of four columns of y (fp32), or one of eight (16 bits).
+// The r values between the products are fp32 sums, handed on as bf16 parts, each the rounding of what the ones before it have
+// left: three for an fp32 y (2^-27 of the value is lost at most, less than an fp32 sum's own rounding), two for a 16-bit y
+// (2^-18, where y itself is rounded to 2^-9 or 2^-12). One part would put 2^-9 of the adapter's whole product on y.
+//
+// Measured, us per call in a stream of calls (bytes that have to be moved, at their rate): one token of rank 16, K = N = 4096 4.6;
+// 64 tokens of 48 adapters of ranks up to 64, K 5120, q|k|v 26 (75 MB, 2.9 TB/s); 80 of 12, rank 16, gate|up 12.1 (33 MB, 2.8 TB/s);
+// 1023 of 24, ranks up to 128, K 13824, N 5120 53 (137 MB, 2.6 TB/s); 8190 of 5, rank 64, gate|up, bf16 189 (918 MB, 4.9 TB/s).
 #include <type_traits>
 
 #include "kv8.cuh"
@@ -321,8 +323,11 @@ __device__ __forceinline__ void add_row_part(void* p, int n, float s, const floa
 // ---- few tokens of an adapter
 //
 // A cluster takes a tile of up to 16 tokens. Each warp streams through its own ring of asynchronous copies: k32 steps of x and
-// A, then 32-column steps of B and y, of which the first are on their way while the sums of the first product meet. A lane
-// copies just what its fragments need, so a step needs no barrier. NB blocks of eight rank rows (the call's largest rank).
+// A, then 32-column steps of B and y, of which the first are on their way while the sums of the first product meet. A warp
+// copies just what its own fragments need, so a step needs no barrier of the block (B in pieces of 16 bytes, which a lane
+// shares with others of its warp: 64 tokens of 48 adapters 26 us, with 8-byte pieces of its own 30).
+// Bound by a unit's chain: its tile, table and tokens (1.1 us), the first loads, the meeting (2.5 us) and the steps, two or
+// three of which a warp has in flight; beyond 16 tokens per adapter also by L2, from which every tile reads its rank rows again. NB blocks of eight rank rows (the call's largest rank).
 template <int NB, int Y>
 struct Short {
   static constexpr bool F32 = Y == QMV_F32;
@@ -616,13 +621,17 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
 // Two kernels, with the values between them in the caller's workspace as the fragments of the second: one cluster's meeting
 // per run of tokens would leave the memory idle for a third of the time (in one kernel: 282 us for 8190 tokens).
 //
-// lora_first_kernel: a cluster takes a run of up to 128 tokens of one adapter and one projection, each block an eighth of K.
+// lora_first_kernel: a cluster takes a run of up to 128 tokens of one adapter and one projection, each block a share of K.
 // The product is one of the fifth-generation tensor cores (the tokens' 128 rows of x by the rank rows of A, 64 columns at a
 // time, sums in tensor memory), so that the warps only copy; the blocks' sums meet in distributed shared memory.
 //
 // lora_second_kernel: a block takes 256 columns and a window of tokens. A warp owns 32 columns: their values of B stay in its
 // registers while the tokens pass by; y comes through a ring in which each lane finds what it has asked for itself (registers
-// as the targets of loads that far ahead were slower: a wait for one of them waits for all).
+// as the targets of loads that far ahead were slower: a wait for one of them waits for all). On the tensor cores of the first
+// product it was slower (8190 tokens, gate|up: 252 us with a thread per token, 283 with the sums turned in shared memory, 189 so):
+// two groups of 32 columns per warp halve the reads of the values, but leave two blocks per SM for three (237).
+// Of those 189 us the first kernel takes 40 (L2: x for each projection, A for each run), the second the rest: L1's data path is 69 %
+// busy (the values for each warp, y in and out), the tensor cores 52 %, memory 58 %.
 constexpr int kRunBlocks = 8;                                 // 16-token blocks of a run of the first kernel: one per warp
 constexpr int kMostBlocks = 64;                               // of a window of the second
 
