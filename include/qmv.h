@@ -708,9 +708,9 @@ int qmv_embed(const qmv_desc* desc, const void* packed, const int32_t* tokens, i
  * lora_plan groups a step's tokens by adapter, once for all layers. ids[t] is
  * the adapter of token t, negative for none. order lists the tokens that have
  * one, adapter by adapter, each adapter's in their order, then -1. tiles lists
- * their tiles of at most lora_tile(n_tokens, n_adapters) tokens (16, or 64 where
- * there are at least 1024 tokens and 64 per adapter) as (adapter, first place in
- * order, count, 0); the rest of the max_tiles entries are 0. An id of n_adapters or more counts as none and sets
+ * their tiles of at most lora_tile(n_tokens) tokens (16, or 64 from 1024 tokens
+ * on) as (adapter, first place in order, count, 0); the rest of the max_tiles
+ * entries are 0. An id of n_adapters or more counts as none and sets
  * QMV_ERR_CORRUPT in the device error word. The result depends on ids alone.
  */
 #define QMV_LORA_MAX_ADAPTERS 1024
@@ -726,7 +726,7 @@ typedef struct {
   int32_t* tiles;            /* [max_tiles][4], 16-byte aligned */
 } lora_plan_args;
 
-int32_t lora_tile(int64_t n_tokens, int64_t n_adapters);
+int32_t lora_tile(int64_t n_tokens);
 int64_t lora_max_tiles(int64_t n_tokens, int64_t n_adapters);
 int lora_plan(const lora_plan_args* args, void* stream);
 
@@ -750,8 +750,8 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * outside the pool set QMV_ERR_CORRUPT in the device error word, and that tile
  * (or place) is left out.
  * workspace: device, 16-byte aligned, lora_workspace_size(n_tokens, n_adapters,
- * max_rank, n_tasks) bytes, which is 0 where the call needs none (where
- * lora_tile is 16). It needs no clearing; calls that overlap on the GPU need one each.
+ * max_rank, n_tasks) bytes, which is 0 where the call needs none (below
+ * 1024 tokens, or 64 per adapter). It needs no clearing; calls that overlap on the GPU need one each.
  */
 typedef struct {
   const void* a;             /* bf16 [pool_rows][lda] */

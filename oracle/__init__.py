@@ -20,6 +20,8 @@ division, round-half-even), written from the pages' definitions:
 * ``moe``       - top-k routing, softmax over the selected experts, SwiGLU
                   experts and the weighted combine ("Nemotron 3.5 Bolt",
                   expert top-K routing section).
+* ``step``      - embedding rows out of a packed matrix, low-rank adapters
+                  beside a projection, log probabilities of logits.
 * ``layout``    - the packed byte layout of each format, written from its
                   specification (section offsets, bit positions).
 

@@ -159,7 +159,7 @@ _SIGS = {
     "kv8_attend_init": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.c_size_t, _P]),
     "kv8_attend": (_I32, [ctypes.POINTER(qmv_kv_desc), _P, ctypes.POINTER(kv8_attend_args), _P]),
     "qmv_embed": (_I32, [_DESC, _P, _P, _I64, ctypes.c_float, _P, _I32, _I64, _P]),
-    "lora_tile": (ctypes.c_int32, [_I64, _I64]),
+    "lora_tile": (ctypes.c_int32, [_I64]),
     "lora_max_tiles": (_I64, [_I64, _I64]),
     "lora_plan": (_I32, [ctypes.POINTER(lora_plan_args), _P]),
     "lora_workspace_size": (ctypes.c_size_t, [_I64, _I64, ctypes.c_int32, ctypes.c_int32]),
@@ -726,8 +726,8 @@ def qmv_embed(desc: qmv_desc, packed, tokens, out, scale: float = 1.0, stream=No
     Embed(desc, packed, tokens, out, scale).run(stream)
 
 
-def lora_tile(n_tokens: int, n_adapters: int) -> int:
-    return int(lib().lora_tile(n_tokens, n_adapters))
+def lora_tile(n_tokens: int) -> int:
+    return int(lib().lora_tile(n_tokens))
 
 
 def lora_max_tiles(n_tokens: int, n_adapters: int) -> int:

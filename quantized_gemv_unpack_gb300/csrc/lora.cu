@@ -197,6 +197,9 @@ struct RunArgs {
   Task t[QMV_LORA_MAX_TASKS];
 };
 
+__device__ __forceinline__ bool tile_fits(const RunArgs& a, const int4& v) {
+  return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -322,7 +325,7 @@ __device__ __forceinline__ void add_row_part(void* p, int n, float s, const floa
 
 // ---- few tokens of an adapter
 //
-// A cluster takes a tile of up to 16 tokens. Each warp streams through its own ring of asynchronous copies: k32 steps of x and
+// A cluster takes up to 16 tokens of a tile. Each warp streams through its own ring of asynchronous copies: k32 steps of x and
 // A, then 32-column steps of B and y, of which the first are on their way while the sums of the first product meet. A warp
 // copies just what its own fragments need, so a step needs no barrier of the block (B in pieces of 16 bytes, which a lane
 // shares with others of its warp: 64 tokens of 48 adapters 26 us, with 8-byte pieces of its own 30).
@@ -374,11 +377,16 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
   if constexpr (S::kShared) cluster_arrive();
   follow_previous();
   bool waiting = S::kShared;                                  // for the cluster: to have begun, or to have read `mine`
-  for (int unit = blockIdx.x / C; unit < a.max_tiles * a.n_tasks; unit += clusters) {
-    const Task& t = a.t[unit / a.max_tiles];
-    const int4 tile = a.tiles[unit % a.max_tiles];
+  const int sixteens = a.tile / 16, units = a.max_tiles * sixteens;   // of a projection: a unit takes 16 tokens of a tile
+  for (int unit = blockIdx.x / C; unit < units * a.n_tasks; unit += clusters) {
+    const Task& t = a.t[unit / units];
+    int4 tile = a.tiles[unit % units / sixteens];              // units of a tile side by side: the first finds its rank rows for all
     if (tile.z == 0) continue;
-    const bool fits = tile.x >= 0 && tile.x < a.n_adapters && tile.y >= 0 && tile.z > 0 && tile.z <= 16 && tile.y <= a.n_tokens - tile.z;
+    const bool fits = tile_fits(a, tile);
+    const int skip = unit % sixteens * 16;
+    if (skip > 0 && (!fits || skip >= tile.z)) continue;      // a bad tile is reported by the first of its units
+    tile.y += skip;
+    tile.z = min(16, tile.z - skip);
     int row0 = 0, r = 0, tok0 = -1, tok1 = -1;                // this lane's tokens: rows g and g + 8 of the tile
     float scale = 0.f;
     if (fits) {
@@ -651,11 +659,8 @@ struct Many {
 };
 
 // Whether tile v continues the run of tile u before it.
-__device__ __forceinline__ bool fits(const RunArgs& a, const int4& v) {
-  return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
-}
 __device__ __forceinline__ bool follows(const RunArgs& a, const int4& u, const int4& v) {
-  return fits(a, u) && fits(a, v) && u.x == v.x && u.z == a.tile && u.y + u.z == v.y;
+  return tile_fits(a, u) && tile_fits(a, v) && u.x == v.x && u.z == a.tile && u.y + u.z == v.y;
 }
 
 template <int NB, int Y>
@@ -693,7 +698,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 2 : 3) lora_first_kerne
     if (first % a.window && follows(a, a.tiles[first - 1], tile)) continue;   // another unit's
     int row0 = 0, r = 0;
     float scale = 1.f;                                        // 16-bit y: part of these values; fp32: of the second product's sums
-    const bool good = fits(a, tile);
+    const bool good = tile_fits(a, tile);
     if (good) {
       row0 = a.table[2 * tile.x];
       r = a.table[2 * tile.x + 1];
@@ -861,7 +866,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
       const int first = base + j++;
       const int4 tile = a.tiles[first];
       if (tile.z == 0) break;
-      if (!fits(a, tile)) continue;                           // reported by the first kernel, as is a bad adapter
+      if (!tile_fits(a, tile)) continue;                           // reported by the first kernel, as is a bad adapter
       const int row0 = a.table[2 * tile.x], r = a.table[2 * tile.x + 1];
       float scale = 1.f;                                      // 16-bit y: the finished values have it
       if constexpr (F32) scale = a.scale[tile.x];
@@ -1030,8 +1035,8 @@ Choice choose(int max_rank) {
   return max_rank <= 16 ? choice_of<2, Y>() : max_rank <= 32 ? choice_of<4, Y>() : max_rank <= 64 ? choice_of<8, Y>() : choice_of<16, Y>();
 }
 
-// Whether a call is one of many tokens per adapter: its tiles then have 64 tokens, and it takes the two kernels. With 16-token
-// tiles and with these, us: 1536 tokens of 5 adapters, rank 64, K 5120, q|k|v 61 and 52, gate|up 157 and 120; of 60 adapters, rank
+// Whether a call is one of many tokens per adapter (its tiles have 64 tokens), which takes the two kernels. With the one kernel
+// and with these, us: 1536 tokens of 5 adapters, rank 64, K 5120, q|k|v 61 and 52, gate|up 157 and 120; of 60 adapters, rank
 // 16, N 5120 28 and 36; of 200 adapters, rank 64 67 and 108; 1000 tokens of one adapter, rank 64, gate|up 90 and 98.
 bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1024 && n_tokens >= 64 * n_adapters; }
 
@@ -1042,11 +1047,11 @@ using namespace qmv;
 
 extern "C" {
 
-int32_t lora_tile(int64_t n_tokens, int64_t n_adapters) { return many_tokens(n_tokens, n_adapters) ? kLargeTile : kSmallTile; }
+int32_t lora_tile(int64_t n_tokens) { return n_tokens < 1024 ? kSmallTile : kLargeTile; }
 
 int64_t lora_max_tiles(int64_t n_tokens, int64_t n_adapters) {
   if (n_tokens <= 0 || n_adapters <= 0) return 0;
-  return n_tokens / lora_tile(n_tokens, n_adapters) + (n_tokens < n_adapters ? n_tokens : n_adapters);
+  return n_tokens / lora_tile(n_tokens) + (n_tokens < n_adapters ? n_tokens : n_adapters);
 }
 
 size_t lora_workspace_size(int64_t n_tokens, int64_t n_adapters, int32_t max_rank, int32_t n_tasks) {
@@ -1067,7 +1072,7 @@ int lora_plan(const lora_plan_args* g, void* stream) {
   if (g->max_tiles == 0) return QMV_OK;
   int* err = device_error_word();
   if (!err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
-  PlanArgs a{g->ids, g->order, reinterpret_cast<int4*>(g->tiles), err, g->n_tokens, g->n_adapters, lora_tile(g->n_tokens, g->n_adapters), g->max_tiles};
+  PlanArgs a{g->ids, g->order, reinterpret_cast<int4*>(g->tiles), err, g->n_tokens, g->n_adapters, lora_tile(g->n_tokens), g->max_tiles};
   const void* f = reinterpret_cast<const void*>(lora_plan_kernel);
   // a warp for every 128 tokens, up to 32: fewer counters to clear and to sum where there are few
   const int warps = g->n_tokens >= 4096 ? 32 : g->n_tokens >= 512 ? 16 : 8;
@@ -1134,7 +1139,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (need && !aligned16(g->workspace)) return fail(QMV_ERR_ALIGN, "workspace must be 16-byte aligned");
   a.err = device_error_word();
   if (!a.err) return fail(QMV_ERR_CUDA, "cannot locate the device error word");
-  a.tile = lora_tile(g->n_tokens, g->n_adapters);
+  a.tile = lora_tile(g->n_tokens);
   const int type = tasks[0].y_type;
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank) : choose<QMV_F16>(g->max_rank);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1146,13 +1151,15 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (!many_tokens(g->n_tokens, g->n_adapters)) {
     int rc = kernel_fit(c.few, kLoraThreads, c.few_smem, &per_sm);
     if (rc) return rc;
-    // Few units are cut into eight blocks each, as long as all are resident at once; more of them into four, up to two rounds, or
+    // A unit is 16 tokens of a tile and a projection. Few units are cut into eight blocks each, as long as all are resident at once; more of them into four, up to two rounds, or
     // two, since a unit has two meetings of its cluster whatever its size. us with 8, 4 and 2: 80 tokens of 12 adapters, rank 16,
     // gate|up 11.9, 12.7, 20.1; 512 of 8, rank 64, gate|up 57, 41, 48; 64 of 48, rank 64, q|k|v 33.0, 24.4, 27.7; 1000 of one, rank 64,
     // gate|up 89, 79, 73; 1023 of 8, rank 32, q|k|v 51, 33, 27.
     const int64_t blocks = (int64_t)sm_count() * per_sm;
-    a.cluster = units * kCluster <= blocks + blocks / 4 ? kCluster : units * 4 <= 2 * blocks + blocks / 8 ? 4 : 2;
-    const int64_t most = 8 * blocks / a.cluster, clusters = units < most ? units : most;
+    // Counted without the units that are empty because a tile of 64 tokens has fewer.
+    const int64_t full = (g->n_tokens / 16 + (int64_t)(g->n_tokens < g->n_adapters ? g->n_tokens : g->n_adapters)) * n_tasks;
+    a.cluster = full * kCluster <= blocks + blocks / 4 ? kCluster : full * 4 <= 2 * blocks + blocks / 8 ? 4 : 2;
+    const int64_t all = units * (a.tile / 16), most = 8 * blocks / a.cluster, clusters = all < most ? all : most;
     cudaError_t e = kv8::launch_early(c.few, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.few_smem, s, a.cluster);
     if (e != cudaSuccess) return cuda_fail(e, "lora_run launch");
     return QMV_OK;

@@ -131,7 +131,7 @@ def test_plan(env, T, A):
         else:
             ids = g.integers(-3, min(A, 2), T)
         p = _plan(env, ids, A)
-        order, tiles = step.plan(ids, A, q.lora_tile(T, A), q.lora_max_tiles(T, A))
+        order, tiles = step.plan(ids, A, q.lora_tile(T), q.lora_max_tiles(T, A))
         assert np.array_equal(p.order.cpu().numpy(), order) and np.array_equal(p.tiles.cpu().numpy(), tiles)
     assert q.qmv_check_status() == 0
 
