@@ -751,7 +751,7 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * (or place) is left out.
  * workspace: device, 16-byte aligned, lora_workspace_size(n_tokens, n_adapters,
  * max_rank, n_tasks) bytes, which is 0 where the call needs none (below
- * 1024 tokens, or 64 per adapter). It needs no clearing; calls that overlap on the GPU need one each.
+ * 1280 tokens, or 64 per adapter). It needs no clearing; calls that overlap on the GPU need one each.
  */
 typedef struct {
   const void* a;             /* bf16 [pool_rows][lda] */

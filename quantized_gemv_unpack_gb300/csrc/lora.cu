@@ -1035,10 +1035,10 @@ Choice choose(int max_rank) {
   return max_rank <= 16 ? choice_of<2, Y>() : max_rank <= 32 ? choice_of<4, Y>() : max_rank <= 64 ? choice_of<8, Y>() : choice_of<16, Y>();
 }
 
-// Whether a call is one of many tokens per adapter (its tiles have 64 tokens), which takes the two kernels. With the one kernel
-// and with these, us: 1536 tokens of 5 adapters, rank 64, K 5120, q|k|v 61 and 52, gate|up 157 and 120; of 60 adapters, rank
-// 16, N 5120 28 and 36; of 200 adapters, rank 64 67 and 108; 1000 tokens of one adapter, rank 64, gate|up 90 and 98.
-bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1024 && n_tokens >= 64 * n_adapters; }
+// Whether a call is one of many tokens per adapter, which takes the two kernels. us with the one kernel and with these, K 5120: 1024
+// tokens of 5 adapters, rank 64, gate|up 80 and 88, q|k|v 42 and 35; 1536 of 5, gate|up 139 and 102; 4096 of 5, gate|up 278 and 199;
+// 4096 of 60, rank 16, N 5120 50 and 56; 3000 of 200, rank 64, N 5120, bf16 77 and 115.
+bool many_tokens(int64_t n_tokens, int64_t n_adapters) { return n_tokens >= 1280 && n_tokens >= 64 * n_adapters; }
 
 }  // namespace
 }  // namespace qmv

@@ -205,7 +205,7 @@ def _lora_case(env, ids, ranks, K, Ns, kind, seed, max_rank=None, ldx=None, ldy=
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("T,A", [(1, 1), (5, 3), (16, 1), (17, 1), (64, 40), (200, 5), (1024, 3), (1100, 60), (4000, 61)])
+@pytest.mark.parametrize("T,A", [(1, 1), (5, 3), (16, 1), (17, 1), (64, 40), (200, 5), (1024, 3), (1100, 60), (1300, 3), (4000, 61)])
 @pytest.mark.parametrize("K,N,rank", [(8, 1, 1), (72, 33, 16), (512, 640, 8), (1000, 257, 64), (200, 96, 128), (2048, 72, 17)])
 def test_lora(env, kind, T, A, K, N, rank):
     g = np.random.default_rng(T + K)
@@ -224,7 +224,7 @@ def test_lora_several_projections_and_strides(env, T):
         _lora_case(env, ids, [4, 16, 0, 33, 64, 9], 640, [320, 64, 61], "bf16", T + ldy, ldy=ldy)
 
 
-@pytest.mark.parametrize("T", [1, 16, 33, 1025])
+@pytest.mark.parametrize("T", [1, 16, 33, 1025, 2049])
 @pytest.mark.parametrize("max_rank", [16, 32, 64, 128])
 def test_lora_same_result_whatever_the_neighbours(env, T, max_rank):
     """A token's result has the same bits in another order and, where K is cut alike (few tiles), in a call of its own."""
@@ -247,7 +247,7 @@ def test_lora_same_result_whatever_the_neighbours(env, T, max_rank):
 def test_lora_infinite_and_nan_tokens_stay_by_themselves(env):
     q, torch, dev = env
     g = np.random.default_rng(1)
-    for T in (16, 1040):
+    for T in (16, 1040, 2080):
         x = torch.randn((T, 256), device=dev).to(torch.bfloat16)
         x[3, 7], x[5, 9], x[7] = math.nan, math.inf, 3e38
         A = torch.randn((16, 256), device=dev).to(torch.bfloat16)
@@ -274,7 +274,7 @@ def test_lora_infinite_and_nan_tokens_stay_by_themselves(env):
     assert y[0].tolist() == [math.inf, -math.inf, math.inf, math.inf]
 
 
-@pytest.mark.parametrize("T", [20, 1100])
+@pytest.mark.parametrize("T", [20, 1100, 2100])
 @pytest.mark.parametrize("what", ["rows", "negative", "rank", "below", "tile", "count", "place", "adapter"])
 def test_lora_leaves_out_what_is_corrupt(env, T, what):
     """A table, tile or place outside its array is reported, nothing of it is read or written, and the others are served."""
@@ -318,7 +318,7 @@ def test_lora_leaves_out_what_is_corrupt(env, T, what):
 def test_lora_more_tiles_than_blocks(env):
     """Clusters take several tiles each: many adapters with a token each, and empty entries of the list between the tasks."""
     g = np.random.default_rng(9)
-    for T, A in [(1024, 1024), (1000, 600)]:
+    for T, A in [(1024, 1024), (1000, 600), (2000, 1000)]:
         ids = g.permutation(A)[np.arange(T) % A]
         _lora_case(env, ids, g.integers(1, 9, A), 64, [40, 24, 8], "f32", T)
     _lora_case(env, np.zeros(1024, dtype=int), np.full(1024, 3), 64, [40, 24], "f32", 4)
@@ -611,7 +611,7 @@ def test_rows_past_32_bits(env):
     assert torch.equal(out[[0, 2, 3, 4]], w[[15, 0, 9, 14]]) and not bool(out[1].any())
     del big, out
     # adapters of one tile and of many: rows of x, A, B and y
-    for T, ld in ((3, 2 ** 31 + 8), (1030, 2 ** 23)):
+    for T, ld in ((3, 2 ** 31 + 8), (1300, 2 ** 23)):
         x, y = far(T, 64, ld, torch.bfloat16), far(T, 72, ld, torch.bfloat16)
         a, b = far(3, 64, 2 ** 31 + 8, torch.bfloat16), far(3, 72, 2 ** 31 + 8, torch.bfloat16)
         for t in (x, y, a, b):

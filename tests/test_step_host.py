@@ -21,11 +21,11 @@ def _err(rc, want, text=""):
 
 
 def test_lora_tiles_bound_every_split(L):
-    for T in (1, 2, 15, 16, 17, 100, 1023, 1024, 1025, 5000):
+    for T in (1, 2, 15, 16, 17, 100, 1023, 1024, 1025, 1279, 1280, 5000):
         tile = q.lora_tile(T)
         assert tile == (16 if T < 1024 else 64)
         for A in (1, 2, 7, 78, 79, 300, 1024):
-            assert (q.lora_workspace_size(T, A, 16, 1) > 0) == (T >= 1024 and T >= 64 * A)
+            assert (q.lora_workspace_size(T, A, 16, 1) > 0) == (T >= 1280 and T >= 64 * A)
             # the most tiles: as many adapters as can have one token each, the rest in full tiles beside them
             n = min(T, A)
             worst = n + (T - n) // tile
