@@ -642,7 +642,10 @@ int logprob_run(const logprob_args* g, void* stream) {
   a.scale2 = g->scale * kLog2E;
   const int N = 16 / xs;
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && (int64_t)g->n_rows * a.cluster < 2 * sm_count() && g->V / (2 * a.cluster) >= kManyThreads * N) a.cluster *= 2;
+  // A row is cut while there are then at most 3.5 blocks per SM, so that all are resident at once: more of them only repeat the first
+  // steps of the lists and the joins. 128257 values fp32, top 5, us with 8, 4 and 2 blocks per row: 38 rows 12.3, 13.7, 17.6; 64 rows
+  // 15.3, 14.5, 17.8; 100 rows 21.8, 17.5, 20.9; 150 rows 30.1, 26.4, 21.2.
+  while (a.cluster < kMaxCluster && 4 * (int64_t)g->n_rows * a.cluster <= 7 * (int64_t)sm_count() && g->V / (2 * a.cluster) >= kManyThreads * N) a.cluster *= 2;
   const bool few = (int64_t)g->n_rows * a.cluster <= sm_count();   // a block per SM: twice the threads, all of a row's loads at once
   // positions of a row and of the skew before it, in vectors
   const int64_t vectors = (g->V + 2 * (int64_t)N - 2) / N;
