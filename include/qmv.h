@@ -738,13 +738,13 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * scales, have one y_type, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
  * and ldx multiples of 8; y: [n_tokens][ldy] of y_type, as the projection left
  * it (rows of 16-byte alignment are fastest). n_tokens, n_adapters and max_tiles
- * are the plan's. max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
+ * are the plan's (entries past lora_max_tiles are not read). max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
  * chooses the kernel; an adapter may have rank 0.
  * Products are exact and sums fp32; the r values between the two products are
  * rounded to 2^-27 of themselves for an fp32 y (three bf16 parts) and to 2^-18
  * for the others, and y once. The result is reproducible bit for bit. A token's
  * does not depend on the values, the adapters or the places of the others, but
- * the sizes of the call (n_tokens, n_adapters, max_tiles, max_rank, the tasks)
+ * the sizes of the call (n_tokens, n_adapters, max_rank, the tasks)
  * choose in which order sums over K are formed.
  * A tile, place or adapter outside its array, a rank over max_rank or rows
  * outside the pool set QMV_ERR_CORRUPT in the device error word, and that tile

@@ -631,7 +631,9 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
 //
 // lora_first_kernel: a cluster takes a run of up to 128 tokens of one adapter and one projection, each block a share of K.
 // The product is one of the fifth-generation tensor cores (the tokens' 128 rows of x by the rank rows of A, 64 columns at a
-// time, sums in tensor memory), so that the warps only copy; the blocks' sums meet in distributed shared memory.
+// time, sums in tensor memory), so that the warps only copy; the blocks' sums meet in distributed shared memory. They wait for one
+// another with tensor memory in hand: beside a block of another kernel that wants all of it an SM never has room for two of
+// them (attention over prompts has 98 KB of shared memory or more), so that none is behind it for the other's.
 //
 // lora_second_kernel: a block takes 256 columns and a window of tokens. A warp owns 32 columns: their values of B stay in its
 // registers while the tokens pass by; y comes through a ring in which each lane finds what it has asked for itself (registers
@@ -1115,7 +1117,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   a.n_tokens = g->n_tokens;
   a.n_adapters = g->n_adapters;
   a.pool_rows = g->pool_rows;
-  a.max_tiles = g->max_tiles;
+  a.max_tiles = (int32_t)lora_max_tiles(g->n_tokens, g->n_adapters);   // what the workspace has room for: a longer list is empty from there on
   a.n_tasks = n_tasks;
   for (int i = 0; i < n_tasks; ++i) {
     const lora_task& k = tasks[i];
@@ -1133,7 +1135,6 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
     a.t[i] = {static_cast<const __nv_bfloat16*>(k.a), static_cast<const __nv_bfloat16*>(k.b), k.y, k.lda, k.ldb, k.ldy, k.N, (int32_t)(k.ldy * ys % 16 == 0)};
   }
   if (g->n_tokens == 0) return QMV_OK;
-  if ((int64_t)g->max_tiles * n_tasks > INT32_MAX / 64) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d tasks", g->max_tiles, n_tasks);
   const size_t need = lora_workspace_size(g->n_tokens, g->n_adapters, g->max_rank, n_tasks);
   if (need && (!g->workspace || g->ws_bytes < need)) return fail(QMV_ERR_ARG, "workspace of %zu bytes, lora_workspace_size is %zu", g->ws_bytes, need);
   if (need && !aligned16(g->workspace)) return fail(QMV_ERR_ALIGN, "workspace must be 16-byte aligned");
@@ -1144,7 +1145,7 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   const Choice c = type == QMV_F32 ? choose<QMV_F32>(g->max_rank) : type == QMV_BF16 ? choose<QMV_BF16>(g->max_rank) : choose<QMV_F16>(g->max_rank);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* args[] = {&a};
-  const int64_t units = (int64_t)g->max_tiles * n_tasks;
+  const int64_t units = (int64_t)a.max_tiles * n_tasks;
   int per_sm = 0;
   // Clusters and blocks are one for every unit, up to eight rounds of them: the device hands them out as others end (units differ
   // by rank and N). Past that they take several each, so that a list with many empty tiles costs few launches of blocks.
@@ -1177,9 +1178,9 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (rc) return rc;
   // the second kernel's windows: up to 1024 tokens, as long as there are four blocks of them for each that is resident
   a.window2 = kMostBlocks * 16 / a.tile;
-  while (a.window2 > 1 && (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices < 4 * (int64_t)sm_count() * per_sm) a.window2 /= 2;
-  const int64_t pieces = (int64_t)((g->max_tiles + a.window2 - 1) / a.window2) * a.slices, most2 = 64 * (int64_t)sm_count() * per_sm;
-  if (pieces > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d slices of columns", g->max_tiles, a.slices);
+  while (a.window2 > 1 && (int64_t)((a.max_tiles + a.window2 - 1) / a.window2) * a.slices < 4 * (int64_t)sm_count() * per_sm) a.window2 /= 2;
+  const int64_t pieces = (int64_t)((a.max_tiles + a.window2 - 1) / a.window2) * a.slices, most2 = 64 * (int64_t)sm_count() * per_sm;
+  if (pieces > INT32_MAX) return fail(QMV_ERR_UNSUPPORTED, "max_tiles=%d of %d slices of columns", a.max_tiles, a.slices);
   cudaError_t e = kv8::launch_early(c.first, dim3((unsigned)(clusters * a.cluster)), kLoraThreads, args, c.first_smem, s, a.cluster);
   if (e != cudaSuccess) return cuda_fail(e, "lora_run launch (first product)");
   e = kv8::launch_early(c.second, dim3((unsigned)(pieces < most2 ? pieces : most2)), kLoraThreads, args, c.second_smem, s);

@@ -737,3 +737,32 @@ def test_lora_many_tokens_in_graphs_and_on_streams(env):
     s.check()
     other.check()
     assert q.qmv_check_status() == 0
+
+
+@pytest.mark.parametrize("T", [40, 1100, 1500])
+def test_lora_of_a_longer_list_of_tiles(env, T):
+    """max_tiles past what the split can need: the plan empties the rest, and the workspace does not have to grow with it."""
+    q, torch, dev = env
+    g = torch.Generator(device=dev).manual_seed(T)
+    new = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    x, a, b = new(T, 128), new(20, 128), new(20, 72)
+    ids = torch.randint(-1, 3, (T,), generator=g, device=dev).to(torch.int32)
+    table, scale = torch.tensor([[0, 8], [8, 5], [13, 7]], dtype=torch.int32, device=dev), torch.ones(3, device=dev)
+    want, y = torch.ones((T, 72), device=dev), torch.ones((T, 72), device=dev)
+    plan = q.LoraPlan(ids, 3)
+    plan.run()
+    q.Lora(plan, table, scale, x, [(a, b, want)], max_rank=8).run()
+    few = plan.tiles
+    plan.tiles = torch.full((few.shape[0] + 500, 4), -9, dtype=torch.int32, device=dev)
+    plan.args.tiles, plan.args.max_tiles = plan.tiles.data_ptr(), plan.tiles.shape[0]
+    plan.run()
+    assert torch.equal(plan.tiles[:few.shape[0]], few) and not bool(plan.tiles[few.shape[0]:].any())
+    call = q.Lora(plan, table, scale, x, [(a, b, y)], max_rank=8)
+    assert call.args.max_tiles == few.shape[0] + 500 and call.workspace.numel() == q.lora_workspace_size(T, 3, 8, 1)
+    room = torch.full((call.workspace.numel() + 4096,), 7, dtype=torch.uint8, device=dev)
+    call.workspace = room
+    if call.args.workspace:
+        call.args.workspace = room.data_ptr()
+    call.run()
+    assert torch.equal(y, want) and bool((room[-4096:] == 7).all())
+    assert q.qmv_check_status() == 0
