@@ -266,13 +266,26 @@ struct Vec<__half> : Vec16<__half, __half2> {
 
 constexpr int kAhead = 4, kGroups = 2;   // vectors of a thread at a time, and such groups on their way
 
+constexpr int kFound = 64;       // candidates that are sorted at once
 template <int WARPS>
 struct TopShared {
   Key list[WARPS][32];
   Key lists[kMaxCluster][32];     // of the cluster's blocks, in its first
-  unsigned least;                 // k values of the block reach it (order_of)
-  unsigned jth[WARPS];            // j values of the warp reach it
+  Key found[kFound];              // candidates, in no order
+  uint32_t most[WARPS][32];       // threads' largest values (order_of), each warp's and then several warps' in order
+  uint16_t parts[32][32 * WARPS]; // threads' largest values in each part of what they read: the upper half of order_of
+  int count;                      // of candidates
 };
+// The 32 largest of two lists of values.
+__device__ __forceinline__ uint32_t join_lists32(uint32_t a, uint32_t b, int lane) {
+  uint32_t k = max(a, __shfl_sync(0xFFFFFFFFu, b, 31 - lane));
+#pragma unroll
+  for (int j = 16; j; j >>= 1) {
+    const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, k, j);
+    k = (lane & j) == 0 ? max(k, o) : min(k, o);
+  }
+  return k;
+}
 
 // A list takes one key, the same in all lanes.
 __device__ __forceinline__ Key insert(Key list, Key k, int lane) {
@@ -322,8 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   const int C = a.cluster, part = C > 1 ? (int)cluster_rank() : 0;
   const int64_t row = blockIdx.x / C;
   if constexpr (TOP) {
-    if (tid == 0) ts.least = 0;
-    __syncthreads();
+    if (tid == 0) ts.count = 0;
   }
   if (C > 1) cluster_arrive();                              // waited for before the first access to another block's memory
   follow_previous();
@@ -350,26 +362,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
     }
     copies_end();
   };
-#pragma unroll
-  for (int i = 0; i < kGroups; ++i) ask(lo + i * kStep, i);
   int token = -1;
   if (a.tokens) token = a.tokens[row];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) ask(lo + i * kStep, i);
   if (token >= a.V) {
     if (part == 0 && tid == 0) atomicCAS(a.err, 0, (int)QMV_ERR_CORRUPT);
     token = -1;
   }
-  float given = INFINITY;                                   // no token: nothing to count
-  if (token >= 0) given = fmaxf(to_f(x[token]), -INFINITY);  // NaN ranks as -inf
+  T own_value = T(0.f);                                     // on its way, with a list, while the first values are summed
+  if (token >= 0) own_value = x[token];
   const int given_at = min(hi, token + skew);               // positions before it come first among equals
-  // given is -inf, which all values before its place precede, or an ordinary value, with one below it that compares as such
-  const bool lowest = given == -INFINITY, counted = fabsf(given) > 1e-4f;
-  const typename V::Bound at_given = V::bound(given), under_given = V::below(given);
+  float given = INFINITY;                                   // no token: nothing to count
+  bool lowest = false, counted = false;
+  typename V::Bound at_given = V::bound(0.f), under_given = at_given;
+  const auto know_given = [&]() {
+    if (token < 0) return;
+    given = fmaxf(to_f(own_value), -INFINITY);              // NaN ranks as -inf
+    // given is -inf, which all values before its place precede, or an ordinary value, with one below it that compares as such
+    lowest = given == -INFINITY, counted = fabsf(given) > 1e-4f;
+    at_given = V::bound(given), under_given = V::below(given);
+  };
+  if constexpr (!TOP) know_given();                         // its wait is hidden by other blocks, and the loop leaner without it
   const Scale scale{a.scale2, a.scale2 >= 0.05f && a.scale2 <= 1e6f ? V::kMost : -1.f};
   Sums t{-INFINITY, 0.f, 0.f};
   int ahead = 0;
-  Key list = 0, least = 0;                                  // the warp's list and its k-th key
-  float floor = -INFINITY;                                  // values below it are in no list
+  Key list = 0;
   int place = 0;
+  // a thread's groups in up to 32 parts
+  const int groups = (hi - lo + kStep - 1) / kStep, per_part = (groups + 31) / 32;
+  float part_most = -INFINITY;
+  int part_at = 0, in_part = 0;
   for (int g0 = lo; g0 < hi; g0 += kStep) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
     const bool inside = g0 >= skew && g0 + kStep <= hi;
@@ -441,6 +464,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
     parts(u2, u0, u1);
     t.s += s0 + s1;
     t.u += u0 + u1;
+    if (TOP && g0 == lo) know_given();
     if (m >= given) {
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
@@ -460,56 +484,14 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       }
     }
     if constexpr (TOP) {
-      const int j = (a.top + WARPS - 1) / WARPS;
-      if (g0 == lo) {
-        // as many lanes of the warp have seen a value of at least their k-th, or j-th, largest
-        const uint32_t o = sort_down32(order_of(m), lane);
-        if (lane == a.top - 1) atomicMax(&ts.least, o);
-        if (lane == j - 1) ts.jth[warp] = o;
-        __syncthreads();
-      }
-      const uint32_t low = __reduce_min_sync(0xFFFFFFFFu, ((volatile unsigned*)ts.jth)[lane % WARPS]);
-      floor = fmaxf(floor, value_of(max(low, *(volatile unsigned*)&ts.least)));
-      uint32_t passes = 0;                                  // this lane's values that are candidates
-#pragma unroll
-      for (int v = 0; v < kAhead; ++v) {
-        if (!__any_sync(0xFFFFFFFFu, vmax[v] >= floor)) continue;
-        const int p = g0 + (v * THREADS + tid) * N;
-        float z[N];
-        V::values(w[v], z);
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (fmaxf(z[i], -INFINITY) >= floor && (inside || (p + i >= skew && p + i < hi))) passes |= 1u << (v * N + i);
-      }
-      bool changed = false;
-      while (uint32_t lanes = __ballot_sync(0xFFFFFFFFu, passes != 0)) {
-        const int i = __ffs(passes) - 1, v = i / N;
-        const uint4 y = v == 0 ? w[0] : v == 1 ? w[1] : v == 2 ? w[2] : w[3];
-        Key k = passes ? key_of(V::value(y, i % N), g0 + (v * THREADS + tid) * N + i % N - skew) : 0;
-        passes &= passes - 1;
-        if (k <= least) k = 0;
-        lanes = __ballot_sync(0xFFFFFFFFu, k != 0);
-        if (!lanes) continue;
-        if (__popc(lanes) <= 8) {
-          for (; lanes; lanes &= lanes - 1) list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(lanes) - 1), lane);
-        } else {
-          list = join_lists(list, sort_down(k, lane), lane);
-        }
-        least = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
-        changed = true;
-      }
-      if (changed) {
-        const uint32_t now = (uint32_t)(__shfl_sync(0xFFFFFFFFu, list, j - 1) >> 32), kth = (uint32_t)(least >> 32);
-        if (kth) floor = fmaxf(floor, value_of(kth));
-        if (lane == 0) {
-          if (now > ts.jth[warp]) ((volatile unsigned*)ts.jth)[warp] = now;
-          if (kth) atomicMax(&ts.least, kth);
-        }
-      }
+      part_most = in_part == 0 ? m : fmaxf(part_most, m);
+      ts.parts[part_at][tid] = (uint16_t)(order_of(part_most) >> 16);
+      if (++in_part == per_part) in_part = 0, ++part_at;
     }
   }
 
   // the block's results
+  const uint32_t my_most = order_of(t.m);
   t = join(t, scale);
   ahead = __reduce_add_sync(0xFFFFFFFFu, ahead);
   if (lane == 0) {
@@ -523,6 +505,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       ahead = __reduce_add_sync(0xFFFFFFFFu, lane < n ? c[lane] : 0);
     }
     if constexpr (TOP) {
+      if (l == nullptr) return;
       for (int d = n / 2; d; d >>= 1) {
         if (warp < d) {
           list = join_lists(l[warp][lane], l[warp + d][lane], lane);
@@ -532,10 +515,108 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
       }
     }
   };
-  if constexpr (TOP) ts.list[warp][lane] = list;
-  __syncthreads();
   Key (*own)[32] = nullptr, (*others)[32] = nullptr;
-  if constexpr (TOP) own = ts.list, others = ts.lists;
+  if constexpr (TOP) {
+    others = ts.lists;
+    // as many threads have a value of at least the k-th of their largest ones: what is below it is in no list
+    uint32_t most = sort_down32(my_most, lane);
+    ts.most[warp][lane] = most;
+    __syncthreads();
+    for (int d = WARPS / 2; d; d >>= 1) {
+      if (warp < d) {
+        most = join_lists32(most, ts.most[warp + d][lane], lane);
+        ts.most[warp][lane] = most;
+      }
+      __syncthreads();
+    }
+    const uint32_t least_most = ts.most[0][a.top - 1];
+    const float floor = value_of(least_most);
+    const int vectors = groups * kAhead;                      // of a thread
+    // Vector i of thread `of` at its position p, which is `end` where there is none; and which of its values are candidates.
+    const auto read = [&](int i, int of, uint4& y, int& p) {
+      p = lo + i / kAhead * kStep + (i % kAhead * THREADS + of) * N;
+      if (i >= vectors || p >= hi || p + N <= skew) {
+        p = end;
+      } else if (p >= skew && p + N <= hi) {
+        y = *reinterpret_cast<const uint4*>(base + p);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) V::put(y, e, p + e >= skew && p + e < hi ? to_f(base[p + e]) : -INFINITY);
+      }
+    };
+    const auto candidates = [&](const uint4& y, int p) {
+      uint32_t passes = 0;
+      if (p == end || V::largest(y) < floor) return passes;
+      float z[N];
+      V::values(y, z);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (fmaxf(z[e], -INFINITY) >= floor && p + e >= skew && p + e < hi) passes |= 1u << e;
+      return passes;
+    };
+    // the parts of each thread that have one, read again by its warp
+    unsigned have = __ballot_sync(0xFFFFFFFFu, my_most >= least_most);
+    for (; have; have &= have - 1) {
+      const int of = warp * 32 + __ffs(have) - 1;
+      unsigned where = __ballot_sync(0xFFFFFFFFu, lane * per_part < groups && ts.parts[lane][of] >= least_most >> 16);
+      for (; where; where &= where - 1) {
+        const int first = (__ffs(where) - 1) * per_part * kAhead;
+        for (int i = lane; i < per_part * kAhead; i += 32) {
+          uint4 y;
+          int p;
+          read(first + i, of, y, p);
+          for (uint32_t passes = candidates(y, p); passes; passes &= passes - 1) {
+            const int e = __ffs(passes) - 1, at = atomicAdd(&ts.count, 1);
+            if (at >= kFound) break;
+            ts.found[at] = key_of(V::value(y, e), p + e - skew);
+          }
+        }
+      }
+      // the warp as one: its lanes meet again in the next vote
+      if (__any_sync(0xFFFFFFFFu, *(volatile int*)&ts.count > kFound)) break;
+    }
+    __syncthreads();
+    const int count = ts.count;
+    if (count <= kFound) {
+      if (warp < 2) {
+        list = 32 * warp + lane < count ? ts.found[32 * warp + lane] : 0;
+        if (warp == 0 || count > 32) ts.list[warp][lane] = list = sort_down(list, lane);
+      }
+      if (count > 32) {
+        __syncthreads();
+        if (warp == 0) list = join_lists(list, ts.list[1][lane], lane);
+      }
+    } else {
+      // more of them (equal values, or fewer than k that are not masked): each warp keeps a list, its lanes' values one by one
+      own = ts.list;
+      list = 0;
+      Key least = 0;                                        // its k-th key
+      for (int i = 0; i < vectors; ++i) {
+        uint4 y;
+        int p;
+        read(i, tid, y, p);
+        uint32_t passes = candidates(y, p);
+        while (__any_sync(0xFFFFFFFFu, passes != 0)) {
+          const int e = __ffs(passes) - 1;
+          Key k = passes ? key_of(V::value(y, e), p + e - skew) : 0;
+          passes &= passes - 1;
+          if (k <= least) k = 0;
+          unsigned lanes = __ballot_sync(0xFFFFFFFFu, k != 0);
+          if (!lanes) continue;
+          if (__popc(lanes) <= 8) {
+            for (; lanes; lanes &= lanes - 1) list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(lanes) - 1), lane);
+          } else {
+            list = join_lists(list, sort_down(k, lane), lane);
+          }
+          least = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
+        }
+      }
+      ts.list[warp][lane] = list;
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
   join_all(sums, aheads, own, WARPS);
   if (C > 1) {
     cluster_wait();
