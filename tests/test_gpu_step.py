@@ -766,3 +766,27 @@ def test_lora_of_a_longer_list_of_tiles(env, T):
     call.run()
     assert torch.equal(y, want) and bool((room[-4096:] == 7).all())
     assert q.qmv_check_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,V", [(1, 131073), (70, 70001), (400, 40000)])
+def test_logprob_alternatives_among_equal_values(env, kind, T, V):
+    """More values at the threshold than are sorted at once, fewer that are not masked than alternatives, and exactly as many."""
+    q, torch, dev = env
+    g = torch.Generator(device=dev).manual_seed(V)
+    rows = [torch.round(torch.randn((T, V), generator=g, device=dev) * 2), torch.full((T, V), -math.inf, device=dev), torch.full((T, V), 1.5, device=dev),
+            torch.randn((T, V), generator=g, device=dev)]
+    rows[1][:, [5, V // 2, V - 1]] = torch.tensor([1.0, 3.0, 1.0], device=dev)
+    for n in (63, 64, 65, 300):                         # that many values share the first place
+        x = torch.randn((T, V), generator=g, device=dev).clamp(max=3)
+        x.scatter_(1, torch.rand((T, V), generator=g, device=dev).topk(n, dim=1).indices, 4.0)
+        rows.append(x)
+    for x in rows:
+        x = x.to(_type(torch, kind))
+        want = torch.sort(x, dim=1, descending=True, stable=True).indices
+        for top in (1, 5, 32):
+            call = q.LogProb(x, top=top)
+            call.run()
+            assert torch.equal(call.top_index.long(), want[:, :top])
+            assert torch.equal(call.top_logprob.isinf(), torch.gather(x, 1, want[:, :top]).isinf())
+    assert q.qmv_check_status() == 0
