@@ -6,9 +6,10 @@
 // give lse = scale M + ln S and the entropy ln S - ln 2 U / S. Partial results of
 // threads, warps and blocks join by S = sum S_p 2^D_p, U = sum (U_p + D_p S_p) 2^D_p,
 // D_p their M less the largest. d is one fused multiply-add from the rounded product
-// M scale log2 e (what the rounding took is put back into ln S); where M is so large that
-// the product could overflow (a row masked by its type's lowest value), the difference
-// comes first.
+// M scale log2 e, and what the rounding took is put back into ln S. That is a part of every
+// d, the largest value's own among them, and half a step of the product: from products of
+// 2^32 on it would take powers past fp32's range. So beyond 2^20 (a finite mask, a row
+// of its type's lowest value) the difference comes first; up to there it is 2^-4 at most.
 //
 // The top k (k <= 32) come from the threads' largest values: at least k values of a block reach the k-th of its threads'
 // maxima, and hardly more do. So the pass keeps maxima alone, of each thread and of up to 32 parts of what it reads, and
@@ -52,7 +53,7 @@ struct Args {
   int* err;
   int64_t ldx;
   int32_t V, top, cluster, piece;   // piece: values of a block, a multiple of a vector
-  float scale, scale2;              // scale2 = scale * log2 e
+  float scale, scale2, most;        // scale2 = scale * log2 e; most: see Scale
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -72,15 +73,18 @@ struct Sums {
   float m, s, u;
 };
 
-// What a kernel knows of the scale: values up to `most` keep clear of overflow, and so does what lies `gap` or more below them.
+// Sums are taken against the rounded product of a largest value with scale2 as long as its magnitude is at most `most` (-1: never),
+// else against the value itself.
 struct Scale {
   float scale2, most;
   __device__ __forceinline__ bool plain(float m) const { return fabsf(m) <= most; }
-  // distance in powers of 2 between what two sums were taken against: the rounded products, or the values
+  // distance in powers of 2 between what the sums of v and of m were taken against; a product that was not rounded is not here either
   __device__ __forceinline__ float between(float v, float m) const {
-    return plain(m) ? __fsub_rn(__fmul_rn(v, scale2), __fmul_rn(m, scale2)) : (v - m) * scale2;
+    if (plain(m)) return plain(v) ? __fsub_rn(__fmul_rn(v, scale2), __fmul_rn(m, scale2)) : fmaf(v, scale2, -__fmul_rn(m, scale2));
+    return plain(v) ? -fmaf(m, scale2, -__fmul_rn(v, scale2)) : (v - m) * scale2;
   }
 };
+constexpr float kPlainProduct = 1048576.f;   // 2^20
 
 // The sum of the lanes' parts, in every lane.
 __device__ __forceinline__ Sums join(Sums t, const Scale& k) {
@@ -170,13 +174,14 @@ __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
 
-// Sixteen bytes of a row. least: a value that is taken in the place of -inf, so far below `most` that its power is 0.
+// Sixteen bytes of a row. In 16 bits lift puts a value in the place of -inf (and of what is below it) that is so far below `-most` that
+// its power is 0, so that no distance is infinite; kMost: what `most` is held to for that.
 template <typename T>
 struct Vec;
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  static constexpr float kMost = 1e28f;
+  static constexpr float kMost = INFINITY;
   static __device__ __forceinline__ void values(const uint4& w, float (&v)[4]) {
     v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
   }
@@ -231,7 +236,7 @@ struct Vec16 {
 };
 template <>
 struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {
-  static constexpr float kMost = 1e28f;
+  static constexpr float kMost = INFINITY;                  // 2^20 / 0.05 is far enough from -1e30
   static __device__ __forceinline__ void values(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -246,6 +251,7 @@ struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {
 };
 template <>
 struct Vec<__half> : Vec16<__half, __half2> {
+  // 5504 below it is the least value, whose power is then 0 for a scale2 of 0.05 and more
   static constexpr float kMost = 60000.f;
   static __device__ __forceinline__ void values(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
     at_given = V::bound(given), under_given = V::below(given);
   };
   if constexpr (!TOP) know_given();                         // its wait is hidden by other blocks, and the loop leaner without it
-  const Scale scale{a.scale2, a.scale2 >= 0.05f && a.scale2 <= 1e6f ? V::kMost : -1.f};
+  const Scale scale{a.scale2, fminf(a.most, V::kMost)};
   Sums t{-INFINITY, 0.f, 0.f};
   int ahead = 0;
   Key list = 0;
@@ -729,6 +735,7 @@ int logprob_run(const logprob_args* g, void* stream) {
   a.top = g->top;
   a.scale = g->scale;
   a.scale2 = g->scale * kLog2E;
+  a.most = a.scale2 >= 0.05f && a.scale2 <= 1e6f ? kPlainProduct / a.scale2 : -1.f;
   const int N = 16 / xs;
   a.cluster = 1;
   // A row is cut while there are then at most 3.5 blocks per SM, so that all are resident at once: more of them only repeat the first

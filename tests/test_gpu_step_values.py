@@ -1,0 +1,127 @@
+"""GPU values of logprob_run and lora_run outside the ordinary: finite masks and logits of any magnitude, infinite factors, what
+the fp32 values between the products keep, large sizes and pools, empty entries in a list of tiles. Against the definitions in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = [pytest.mark.gpu, pytest.mark.filterwarnings("ignore::RuntimeWarning")]
+
+
+@pytest.fixture(scope="module")
+def env():
+    import torch
+
+    import __graft_entry__
+    __graft_entry__.build()
+    import quantized_gemv_unpack_gb300 as q
+    assert torch.cuda.is_available()
+    q.qmv_check_status()
+    return q, torch, torch.device("cuda:0")
+
+
+def _type(torch, name):
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+# ----------------------------------------------------------------------------- log probabilities
+
+def _logprob(x, scale, token, top):
+    """(lse, entropy, log probability, top's log probabilities, top's indices, rank) of a row without NaN and +inf."""
+    z = x * scale
+    m = z.max()
+    if m == -math.inf:
+        return -math.inf, 0.0, -math.inf, np.full(top, -math.inf), np.arange(top), token
+    e = np.exp(z - m)
+    ln_s = math.log(math.fsum(e))
+    lp = (z - m) - ln_s
+    seq = np.lexsort((np.arange(len(x)), -x))
+    return m + ln_s, math.fsum(-np.exp(v) * v for v in lp[lp > -800]), lp[token], lp[seq[:top]], seq[:top], int(np.flatnonzero(seq == token)[0])
+
+
+def _logprob_rows(env, rows, kind, scale, tokens, top, copies):
+    """Rows, each `copies` times, against the definition. Copies lie alike in memory and have the same bits."""
+    q, torch, dev = env
+    n, V = rows.shape
+    ld = (V + 15) // 8 * 8
+    x = torch.full((n * copies, ld), math.nan, dtype=_type(torch, kind), device=dev)[:, :V]
+    x.copy_(torch.from_numpy(np.tile(rows, (copies, 1))))
+    call = q.LogProb(x, torch.tensor(list(tokens) * copies, dtype=torch.int32, device=dev), top=top, scale=scale)
+    call.run()
+    assert q.qmv_check_status() == 0
+    outs = [call.lse, call.entropy, call.logprob, call.rank] + ([call.top_logprob, call.top_index] if top else [])
+    for o in outs:
+        assert torch.equal(o.view(torch.int32)[n:], o.view(torch.int32)[:n].repeat((copies - 1,) + (1,) * (o.dim() - 1)))
+    xv, scale = _f64(x[:n]), float(np.float32(scale))
+    for i in range(n):
+        lse, h, lp, best, at, rank = _logprob(xv[i], scale, tokens[i], top)
+        # fp32: a power 2^d, d = (x - m) scale log2 e, is off by 3 steps of 2^-24 |d| (difference, product, constant) and by 2^-22 (exp2), and
+        # by 2^-27 (what the maximum's product was rounded by, up to 2^-4, is a part of d). A sum of n = V / 256 + 64 terms in a row by
+        # n 2^-24. Weighted by p, |d| is at most log2 V + 1. Then the last sums and products, each within 2^-24 of the result or of ln S.
+        bits = math.log2(V) + 1
+        rel = 2.0 ** -22 + 2.0 ** -27 + (V / 256 + 64) * 2.0 ** -24 + 3 * 2.0 ** -24 * bits
+        pairs = [(float(call.lse[i]), lse, rel), (float(call.logprob[i]), lp, rel), (float(call.entropy[i]), h, 3 * rel * bits)]
+        pairs += [(float(call.top_logprob[i, j]), best[j], rel) for j in range(top)]
+        for k, (got, want, off) in enumerate(pairs):
+            if abs(want) < 3.4e38:
+                assert abs(got - want) <= off + 3 * 2.0 ** -24 * (abs(want) + bits), (i, k, got, want)
+            else:
+                assert got == math.copysign(math.inf, want), (i, k, got, want)
+        assert int(call.rank[i]) == rank, i
+        if top:
+            assert call.top_index[i].tolist() == at.tolist(), i
+
+
+MASKS = {"f32": [-1e9, -1e10, -3e10, -1e12, -1e15, -1e20, -1e27, 1e10], "bf16": [-1e9, -1e10, -3e10, -1e12, -1e15, -1e20, -1e27, 1e10],
+         "f16": [-65504.0, -60000.0, -49000.0, -2048.0, 60000.0]}
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [0.8, 1.0, 1.25, 1e5, 5e5])
+@pytest.mark.parametrize("V,copies", [(9001, 1), (9001, 40), (70001, 1)])
+def test_logprob_of_large_finite_values(env, kind, scale, V, copies):
+    """Rows masked by a finite value: all of them, a thread's first values, a tail, nine tenths, all but a few; and likely values so large."""
+    g = np.random.default_rng(V)
+    for mask in MASKS[kind] if V < 10000 else MASKS[kind][1:4:2]:
+        some = g.standard_normal((9, V)) * 3
+        rows = some.copy()
+        rows[0] = mask
+        rows[1] = mask
+        rows[1, V // 2] = some[1, 0]
+        rows[2, :V * 2 // 3] = mask
+        rows[3, V // 2:] = mask
+        rows[4, g.random(V) < 0.9] = mask
+        rows[5, g.random(V) < 0.999] = mask
+        rows[6] = mask * (1 + np.round(some[6]) / 64) if kind != "f16" else mask + 32 * np.abs(np.round(some[6]))   # near one another, and large
+        rows[7, g.random(V) < 0.5] = mask
+        rows[7, g.random(V) < 0.5] = -math.inf
+        rows[8, g.random(V) < 0.5] = -abs(mask) * 0.75
+        if kind == "f16":
+            rows = np.clip(rows, np.where(np.isinf(rows), -math.inf, -65504.0), 65504.0)
+        tokens = [int(t) for t in g.integers(0, V, 9)]
+        tokens[1], tokens[4] = V // 2, int(rows[4].argmax())
+        for top in (0, 5):
+            _logprob_rows(env, rows, kind, scale, tokens, top, copies)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scale", [1.0, 0.4, 1e5])
+@pytest.mark.parametrize("copies", [1, 40])
+def test_logprob_across_the_plain_bound(env, kind, scale, copies):
+    """Values on both sides of where the maximum's product is 2^20 (and of half and twice it), in orders that cross it inside a thread, a warp and a block."""
+    V = 9001
+    g = np.random.default_rng(3)
+    at = 2.0 ** 20 / (scale * math.log2(math.e))
+    rows = []
+    for centre in (at, -at, 2 * at, -2 * at, at / 2):
+        up = centre + np.linspace(-30.0, 30.0, V) / scale
+        rows += [up, up[::-1], g.permutation(up), np.where(g.random(V) < 0.5, up, -math.inf)]
+    rows = np.stack(rows)
+    if kind == "f16":
+        rows = np.clip(rows, np.where(np.isinf(rows), -math.inf, -65504.0), 65504.0)
+    for top in (0, 3):
+        _logprob_rows(env, rows, kind, scale, [int(t) for t in g.integers(0, V, len(rows))], top, copies)
