@@ -73,6 +73,9 @@ struct Sums {
   float m, s, u;
 };
 
+// Half of v - m: the whole may pass fp32's range where its product with a small scale does not.
+__device__ __forceinline__ float half_difference(float v, float m) { return fmaf(v, 0.5f, -0.5f * m); }
+
 // Sums are taken against the rounded product of a largest value with scale2 as long as its magnitude is at most `most` (-1: never),
 // else against the value itself.
 struct Scale {
@@ -80,8 +83,9 @@ struct Scale {
   __device__ __forceinline__ bool plain(float m) const { return fabsf(m) <= most; }
   // distance in powers of 2 between what the sums of v and of m were taken against; a product that was not rounded is not here either
   __device__ __forceinline__ float between(float v, float m) const {
-    if (plain(m)) return plain(v) ? __fsub_rn(__fmul_rn(v, scale2), __fmul_rn(m, scale2)) : fmaf(v, scale2, -__fmul_rn(m, scale2));
-    return plain(v) ? -fmaf(m, scale2, -__fmul_rn(v, scale2)) : (v - m) * scale2;
+    const float pv = __fmul_rn(v, scale2), pm = __fmul_rn(m, scale2);
+    if (plain(fmaxf(fabsf(v), fabsf(m)))) return __fsub_rn(pv, pm);
+    return plain(m) ? fmaf(v, scale2, -pm) : plain(v) ? -fmaf(m, scale2, -pv) : half_difference(v, m) * (2.f * scale2);
   }
 };
 constexpr float kPlainProduct = 1048576.f;   // 2^20
@@ -450,14 +454,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
         }
       }
     } else {
-      const float r = t.m == -INFINITY ? 0.f : -t.m;
+      const float m0 = t.m == -INFINITY ? 0.f : t.m;
 #pragma unroll
       for (int v = 0; v < kAhead; ++v) {
         float z[N];
         V::values(w[v], z);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-          const float d0 = max_nan((z[i] + r) * a.scale2, -256.f), d1 = max_nan((z[i + 1] + r) * a.scale2, -256.f);
+          const float d0 = max_nan(half_difference(z[i], m0) * (2.f * a.scale2), -256.f);
+          const float d1 = max_nan(half_difference(z[i + 1], m0) * (2.f * a.scale2), -256.f);
           const Pair e = pair(exp2_fast(d0), exp2_fast(d1));
           s2 = add2(s2, e);
           u2 = fma2(e, pair(d0, d1), u2);
@@ -663,7 +668,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   const bool none = t.s == 0.f;                             // every value is -inf
   const auto log_p = [&](float v) {
     if (none) return -INFINITY;
-    return v == -INFINITY ? (ln_s == ln_s ? -INFINITY : ln_s) : fmaf(v - t.m, a.scale, -ln_s);
+    return v == -INFINITY ? (ln_s == ln_s ? -INFINITY : ln_s) : fmaf(half_difference(v, t.m), 2.f * a.scale, -ln_s);
   };
   if (lane == 0) {
     if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(t.m, a.scale, ln_s);

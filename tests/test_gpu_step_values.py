@@ -125,3 +125,15 @@ def test_logprob_across_the_plain_bound(env, kind, scale, copies):
         rows = np.clip(rows, np.where(np.isinf(rows), -math.inf, -65504.0), 65504.0)
     for top in (0, 3):
         _logprob_rows(env, rows, kind, scale, [int(t) for t in g.integers(0, V, len(rows))], top, copies)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("copies", [1, 40])
+def test_logprob_of_the_largest_values_under_a_small_scale(env, kind, copies):
+    """The distance of two values is past what fp32 holds, their logits' is not."""
+    V = 3001
+    g = np.random.default_rng(5)
+    for most, scale in [(3.3e38, 2e-38), (3.3e38, 1e-36), (1e38, 0.04)]:
+        rows = np.stack([g.uniform(-most, most, V), np.where(g.random(V) < 0.5, most, -most), np.linspace(-most, most, V), np.linspace(most, -most, V)])
+        for top in (0, 4):
+            _logprob_rows(env, rows, kind, scale, [0, 5, V - 1, V - 1], top, copies)
