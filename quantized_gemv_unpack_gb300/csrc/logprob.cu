@@ -662,9 +662,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   if (warp != 0) return;
   t = total;
   ahead = total_ahead;
-  const float log2_s = log2f(t.s);
+  const float log_s = logf(t.s);
   // the sum against the value itself: what the product's rounding took is put back
-  const float ln_s = (log2_s - (scale.plain(t.m) ? fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)) : 0.f)) * kLn2;
+  const float ln_s = scale.plain(t.m) ? fmaf(-kLn2, fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)), log_s) : log_s;
   const bool none = t.s == 0.f;                             // every value is -inf
   const auto log_p = [&](float v) {
     if (none) return -INFINITY;
@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   };
   if (lane == 0) {
     if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(t.m, a.scale, ln_s);
-    if (a.entropy) a.entropy[row] = none ? 0.f : (log2_s - t.u / t.s) * kLn2;
+    if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kLn2, t.u / t.s, log_s);
     if (a.logprob) a.logprob[row] = token < 0 ? 0.f : log_p(given);
     if (a.rank) a.rank[row] = token < 0 ? -1 : ahead;
   }

@@ -137,3 +137,19 @@ def test_logprob_of_the_largest_values_under_a_small_scale(env, kind, copies):
         rows = np.stack([g.uniform(-most, most, V), np.where(g.random(V) < 0.5, most, -most), np.linspace(-most, most, V), np.linspace(most, -most, V)])
         for top in (0, 4):
             _logprob_rows(env, rows, kind, scale, [0, 5, V - 1, V - 1], top, copies)
+
+
+def test_logprob_last_step(env):
+    """n equal values in a row that is otherwise -inf: S = n exactly, so that of ln n only the logarithm is rounded."""
+    q, torch, dev = env
+    V, T = 5000, 600
+    x = torch.full((T, V), -math.inf, device=dev)
+    n = torch.arange(2, T + 2, device=dev)
+    x[torch.arange(V, device=dev) * 7919 % V < n[:, None]] = 0.0
+    call = q.LogProb(x, torch.zeros(T, dtype=torch.int32, device=dev), top=1)
+    call.run()
+    assert bool((call.rank == 0).all())
+    want = torch.log(n.double())
+    step = torch.exp2(torch.floor(torch.log2(want)) - 23)
+    for got in (call.lse, call.entropy, -call.logprob, -call.top_logprob[:, 0]):
+        assert bool(((got.double() - want).abs() <= step).all())                      # a logarithm is within a step
