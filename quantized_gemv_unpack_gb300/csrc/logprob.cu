@@ -28,6 +28,7 @@
 // which a thread finds what it has asked for itself; in 16 bits the exponentials (16 per
 // clock and SM) take three quarters of the time that the loads do. Few rows are cut over
 // a cluster of up to eight blocks that join in distributed shared memory.
+#include "cluster.cuh"
 #include "kv8.cuh"
 
 #include <type_traits>
@@ -35,6 +36,7 @@
 namespace qmv {
 namespace {
 
+using namespace cluster;
 using kv8::follow_previous;
 
 constexpr int kManyThreads = 256, kFewThreads = 512;
@@ -302,31 +304,8 @@ __device__ __forceinline__ Key insert(Key list, Key k, int lane) {
   return list > k ? list : lane == 0 || up > k ? k : up;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void st_remote32(uint32_t p, uint32_t v) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(p), "r"(v) : "memory"); }
 __device__ __forceinline__ void st_remote64(uint32_t p, Key v) { asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(p), "l"(v) : "memory"); }
-
-__device__ __forceinline__ void copy16(uint32_t to, const void* p) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <typename T, bool TOP, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const __grid_constant__ Args a) {

@@ -25,12 +25,14 @@
 // 1023 of 24, ranks up to 128, K 13824, N 5120 53 (137 MB, 2.6 TB/s); 8190 of 5, rank 64, gate|up, bf16 189 (918 MB, 4.9 TB/s).
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "kv8.cuh"
 #include "tcgen05.cuh"
 
 namespace qmv {
 namespace {
 
+using namespace cluster;
 using kv8::follow_previous;
 
 constexpr int kMaxAdapters = QMV_LORA_MAX_ADAPTERS;
@@ -200,21 +202,6 @@ struct RunArgs {
 __device__ __forceinline__ bool tile_fits(const RunArgs& a, const int4& v) {
   return v.x >= 0 && v.x < a.n_adapters && v.y >= 0 && v.z > 0 && v.z <= a.tile && v.y <= a.n_tokens - v.z;
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ float4 sum(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 __device__ __forceinline__ void st_remote(uint32_t p, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(p), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
@@ -227,12 +214,6 @@ __device__ __forceinline__ float4 ld_remote(uint32_t p) {
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p) : "memory");
   return v;
 }
-// Sixteen bytes from memory to shared memory, asynchronously.
-__device__ __forceinline__ void copy16(uint32_t to, const void* p) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
-}
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }   // all of this thread's
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -785,8 +766,9 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 2 : 3) lora_first_kerne
       core::mbar_wait(&done[use % G], (use / G) & 1, a.err);  // the last stage's products, and with them all
     }
     begun += n_stages;
-    umma::fence_after();
     copies_wait();
+    __syncwarp();                                             // a warp reads tensor memory as a whole
+    umma::fence_after();
     // tensor memory has a token per lane; `mine` the order of the second product's fragments
     {
       const int row = warp % 4 * 32 + lane, b = row / 16, g = row % 8, high = row % 16 / 8;
