@@ -228,6 +228,13 @@ __device__ __forceinline__ uint32_t split(float& x, float& y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Words of the values between the products, whose columns are rank rows j, j + 1, j, j + 1: 0 past the rank. There the first product
+// has multiplied zeros, which an infinite value of x makes NaN.
+__device__ __forceinline__ void keep_rank(float4& v, int j, int r) {
+  if (j >= r) v.x = v.z = 0.f;
+  if (j + 1 >= r) v.y = v.w = 0.f;
+}
+
 template <int Y>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (Y == QMV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -492,7 +499,10 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
       }
       return v;
     };
-    const auto parts_of = [&](float4 u, float4 v, uint4 (&f)[P3]) {
+    const auto parts_of = [&](int item, float4 u, float4 v, uint4 (&f)[P3]) {
+      const int j = item / 32 * 16 + 2 * (item % 4);
+      keep_rank(u, j, r);
+      keep_rank(v, j + 8, r);
 #pragma unroll
       for (int k = 0; k < P3; ++k) {
         f[k].x = split(u.x, u.y);
@@ -519,7 +529,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
         if (j + 8 < r)
           for (int c = 0; c < C; ++c) v = sum(v, mine[(2 * c + 1) * per + at]);
         uint4 f[P3];
-        parts_of(u, v, f);
+        parts_of(item, u, v, f);
 #pragma unroll
         for (int k = 0; k < P3; ++k) st_remote(remote(frag + (item / 32 * P3 + k) * 32 + item % 32, tid / per), f[k]);
       }
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
           v = sum(v, ld_remote(p + 32 * 16));
         }
         uint4 f[P3];
-        parts_of(u, v, f);
+        parts_of(i, u, v, f);
 #pragma unroll
         for (int k = 0; k < P3; ++k) frag[(i / 32 * P3 + k) * 32 + i % 32] = f[k];
       }
@@ -804,6 +814,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 ? 2 : 3) lora_first_kerne
         u.x += e.x, u.y += e.y, u.z += e.z, u.w += e.w;
         v.x += f.x, v.y += f.y, v.z += f.z, v.w += f.w;
       }
+      keep_rank(u, 16 * s + 2 * (i % 4), r);
+      keep_rank(v, 16 * s + 8 + 2 * (i % 4), r);
       if constexpr (!S::F32) {
         u.x *= scale, u.y *= scale, u.z *= scale, u.w *= scale;
         v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;

@@ -153,3 +153,73 @@ def test_logprob_last_step(env):
     step = torch.exp2(torch.floor(torch.log2(want)) - 23)
     for got in (call.lse, call.entropy, -call.logprob, -call.top_logprob[:, 0]):
         assert bool(((got.double() - want).abs() <= step).all())                      # a logarithm is within a step
+
+
+# ----------------------------------------------------------------------------- adapters
+
+def _call(env, ids, table, scale, x, a, b, y, max_rank):
+    q, torch, dev = env
+    plan = q.LoraPlan(torch.as_tensor(np.asarray(ids, dtype=np.int32), device=dev), len(table))
+    plan.run()
+    call = q.Lora(plan, torch.as_tensor(np.asarray(table, dtype=np.int32), device=dev), torch.as_tensor(np.asarray(scale, dtype=np.float32), device=dev),
+                  x, [(a, b, y)], max_rank=max_rank)
+    call.run()
+    assert q.qmv_check_status() == 0
+    return call, plan
+
+
+def _follows(got, want, bound):
+    """got has want's NaN and infinities, and is within the bound elsewhere."""
+    there = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isposinf(got), np.isposinf(want))
+    assert np.array_equal(np.isneginf(got), np.isneginf(want)) and np.all(np.abs(got - want)[there] <= bound[there])
+
+
+def _infinite_case(env, T, rank, max_rank, kind, seed, spoil):
+    """Small whole factors of which spoil(x, a, b) makes some infinite: y as the definition has it."""
+    q, torch, dev = env
+    g = np.random.default_rng(seed)
+    K, N, A = 64, 72, 3
+    rows = A * rank + 2
+    draw = lambda *s: g.integers(1, 4, s) * g.choice([-1.0, 1.0], s)  # noqa: E731
+    x, a, b, y = draw(T, K), draw(rows, K), draw(rows, N), draw(T, N)
+    spoil(x, a, b)
+    x, a, b = (torch.from_numpy(v).to(torch.bfloat16).double().numpy() for v in (x, a, b))
+    ids = np.arange(T) % A
+    table = [(1 + i * rank, rank) for i in range(A)]
+    scale = [1.0, -2.0, 0.5]
+    t = lambda v, k="bf16": torch.from_numpy(v).to(_type(torch, k)).to(dev)  # noqa: E731
+    yt = t(y, kind)
+    _call(env, ids, table, scale, t(x), t(a), t(b), yt, max_rank)
+    h = np.stack([a[f:f + r] @ x[i] for i in range(T) for f, r in [table[ids[i]]]])
+    # value by value: a product of matrices may leave out what is 0
+    own = [(f, f + r) for f, r in (table[i] for i in ids)]
+    by = np.array(scale)[ids][:, None]
+    want = y + by * np.stack([(h[i][:, None] * b[f:e]).sum(0) for i, (f, e) in enumerate(own)])
+    s2 = np.abs(by) * np.stack([np.abs(h[i][:, None] * b[f:e]).sum(0) for i, (f, e) in enumerate(own)])
+    # h is exact (64 products of 16 bits, of up to 9.3); then rank / 16 times three products with 16 additions inside, each within 2^-23 of what
+    # is summed up; two parts leave 2^-17; y and its type
+    bound = (3 * 8 + 16 + 2) * 2.0 ** -23 * s2 + (0 if kind == "f32" else 2.0 ** -17) * s2
+    bound += (2.0 ** -23 if kind == "f32" else 2.0 ** -8 + 2.0 ** -24) * (np.abs(want) + bound)
+    _follows(_f64(yt), want, bound)
+
+
+SIZES = [(5, 16), (5, 32), (40, 64), (40, 128), (1300, 16), (1300, 32), (1300, 64), (1300, 128)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,max_rank", SIZES)
+@pytest.mark.parametrize("rank", [1, 2, 8, 9, 12, 16, 17, 40, 100])
+def test_lora_of_infinite_activations(env, kind, T, max_rank, rank):
+    """An infinite x (or value of A) makes the values between infinite, of the ranks that there are and no others."""
+    if rank > max_rank:
+        rank = max_rank - 1
+
+    def spoil(x, a, b):
+        x[1, 5] = math.inf
+        x[3, 63] = -math.inf
+        a[1 + 2 * rank, 9] = math.inf                   # the first rank row of the third adapter
+        b[:, ::2] = np.abs(b[:, ::2])                   # columns in which infinities may agree
+        a[:, 5] = np.abs(a[:, 5])
+
+    _infinite_case(env, T, rank, max_rank, kind, T + rank, spoil)
