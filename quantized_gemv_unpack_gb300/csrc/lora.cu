@@ -311,6 +311,74 @@ __device__ __forceinline__ void add_row_part(void* p, int n, float s, const floa
   }
 }
 
+// Infinite values of B. A value between the products is a sum of bf16 parts, and the parts after the first may be 0 or of the other
+// sign: each of them times an infinite value of B is NaN, where the value itself gives an infinity. Where there are any, the values
+// of B that are not finite meet the values between the products as a whole, one by one.
+
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float most(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Few tokens: a lane's sums of the second product that are NaN, once more, value by value: rank rows j < r of b, from the lane's first column on, with the
+// parts of rows g and g + 8 as the fragments have them.
+template <int Y, int P3>
+__device__ __noinline__ void sums_again(float* d, const uint4* frag, const __nv_bfloat16* b, int64_t ldb, int r, int cols, int lane) {
+  const uint32_t* parts = reinterpret_cast<const uint32_t*>(frag);
+  for (int c = 0; c < 8; ++c) {
+    const int at = Y == QMV_F32 ? c % 4 + c / 4 * 16 : c;
+    if (at >= cols) break;
+    for (int hi = 0; hi < 2; ++hi) {
+      float* to = d + c % 4 * 4 + 2 * hi + c / 4;
+      if (*to == *to) continue;
+      float sum = 0.f;
+      for (int j = 0; j < r; ++j) {
+        const float w = __bfloat162float(b[j * ldb + at]);
+        for (int k = P3 - 1; k >= 0; --k) {
+          const uint32_t two = parts[((j / 16 * P3 + k) * 32 + lane / 4 * 4 + j % 8 / 2) * 4 + j % 16 / 8 * 2 + hi];
+          const float h = __uint_as_float(j & 1 ? two & 0xFFFF0000u : two << 16);
+          if (k == 0 || fabsf(w) < INFINITY) sum = fmaf(h, w, sum);
+        }
+      }
+      *to = sum;
+    }
+  }
+}
+
+// Many tokens: in B's registers +-1 stands for a value that is not finite, so that an infinite value between keeps its sign,
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7F80u) == 0x7F80u) w = (w & 0xFFFF8000u) | 0x3F80u;
+  if ((w & 0x7F800000u) == 0x7F800000u) w = (w & 0x8000FFFFu) | 0x3F800000u;
+  return w;
+}
+// and what it stands for is added to y afterwards. A lane's column, of `count` tokens whose rows of y are row_y bytes away; values: the
+// finished values of the run, KS * P3 * 32 words for each 16 tokens.
+template <int Y, int KS, int P3>
+__device__ __noinline__ void add_infinite(char* y, const int64_t* row_y, int count, const uint4* values, const __nv_bfloat16* b, int64_t ldb, int r, float scale) {
+  const uint32_t* parts = reinterpret_cast<const uint32_t*>(values);
+  for (int j = 0; j < r; ++j) {
+    const float w = __bfloat162float(b[j * ldb]);
+    if (fabsf(w) < INFINITY) continue;
+    for (int i = 0; i < count; ++i) {
+      if (row_y[i] < 0) continue;
+      float h = 0.f;
+      for (int k = P3 - 1; k >= 0; --k) {
+        const uint32_t two = parts[(((int64_t)(i / 16 * KS + j / 16) * P3 + k) * 32 + i % 8 * 4 + j % 8 / 2) * 4 + j % 16 / 8 * 2 + i % 16 / 8];
+        h += __uint_as_float(j & 1 ? two & 0xFFFF0000u : two << 16);
+      }
+      char* q = y + row_y[i];
+      if constexpr (Y == QMV_F32) {
+        *reinterpret_cast<float*>(q) += scale * (h * w);
+      } else if constexpr (Y == QMV_BF16) {
+        *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(__bfloat162float(*reinterpret_cast<__nv_bfloat16*>(q)) + scale * (h * w));
+      } else {
+        *reinterpret_cast<__half*>(q) = __float2half_rn(__half2float(*reinterpret_cast<__half*>(q)) + scale * (h * w));
+      }
+    }
+  }
+}
+
 // ---- few tokens of an adapter
 //
 // A cluster takes up to 16 tokens of a tile. Each warp streams through its own ring of asynchronous copies: k32 steps of x and
@@ -599,6 +667,16 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_short_kernel(const __gri
             for (int i = 0; i < 4; ++i) mma(d[i], f.x, f.y, f.z, f.w, b[i][0], b[i][1]);
           }
         }
+      }
+      const float any = most(most(most(d[0][0], d[0][1], d[0][2]), most(d[0][3], d[1][0], d[1][1]), most(d[1][2], d[1][3], d[2][0])),
+                             most(d[2][1], d[2][2], d[2][3]), most(most(d[3][0], d[3][1], d[3][2]), d[3][3], d[3][3]));
+      if (any != any) {                                       // an infinite value of B, or what is NaN all the same
+        float e[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) e[i] = d[i / 4][i % 4];
+        sums_again<Y, P3>(e, frag, t.b + (int64_t)row0 * t.ldb + n, t.ldb, r, t.N - n, lane);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) d[i / 4][i % 4] = e[i];
       }
       if (t.wide && (F32 ? n0 + 32 : n + 8) <= t.N) {
         uint32_t v[WORDS];
@@ -913,6 +991,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
       };
       for (int i = 0; i < AY - 1; ++i) ask();
       uint32_t b[KS][4][2];
+      __nv_bfloat162 seen = __floats2bfloat162_rn(0.f, 0.f);  // 0 times every value of b: NaN where one is not finite
       const __nv_bfloat16* pb = t.b + (int64_t)(row0 + 2 * t4) * t.ldb + col;
       const int cols = t.N - col;                             // from this lane's first on
 #pragma unroll
@@ -934,12 +1013,23 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
           }
         }
 #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+          seen = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[i].x), zero, seen);
+          seen = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[i].y), zero, seen);
+        }
+#pragma unroll
         for (int i = 0; i < 2; ++i) {
           b[s][0][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x5410);
           b[s][1][i] = __byte_perm(w[2 * i].x, w[2 * i + 1].x, 0x7632);
           b[s][2][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x5410);
           b[s][3][i] = __byte_perm(w[2 * i].y, w[2 * i + 1].y, 0x7632);
         }
+      }
+      const bool finite = !__any_sync(0xFFFFFFFFu, __hisnan(seen.x) || __hisnan(seen.y));
+      if (!finite) {
+#pragma unroll
+        for (int i = 0; i < 8 * KS; ++i) b[i / 8][i / 2 % 4][i % 2] = finite2(b[i / 8][i / 2 % 4][i % 2]);
       }
       // Block m: fp32 values of y are added in the end (one rounding), 16-bit ones are what the products are added to.
       const auto block = [&](auto plain, int m, const uint4* h) {
@@ -1010,6 +1100,10 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
         }
       }
       copies_wait();
+      if (!finite) {
+        __syncwarp();                                         // the warp's rows of y are written
+        if (n0 + lane < t.N) add_infinite<Y, KS, P3>(y + (int64_t)(n0 + lane) * size, row_y, count, values, t.b + (int64_t)row0 * t.ldb + n0 + lane, t.ldb, r, scale);
+      }
     }
   }
 }

@@ -223,3 +223,43 @@ def test_lora_of_infinite_activations(env, kind, T, max_rank, rank):
         a[:, 5] = np.abs(a[:, 5])
 
     _infinite_case(env, T, rank, max_rank, kind, T + rank, spoil)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,max_rank", SIZES)
+@pytest.mark.parametrize("rank", [1, 5, 16, 17, 64, 100])
+def test_lora_of_infinite_columns(env, kind, T, max_rank, rank):
+    """An infinite value of B makes its column infinite by the sign of the value that it is multiplied by, whatever parts that is held in."""
+    if rank > max_rank:
+        rank = max_rank - 1
+
+    def spoil(x, a, b):
+        b[0] = b[-1] = math.inf                         # rows of no adapter
+        b[1, [0, 9, 31, 71]] = math.inf                 # of the first
+        b[2 * rank, 8] = -math.inf                      # the second's last
+        b[1 + 2 * rank, 40] = math.nan
+        x[2, 7] = math.inf                              # meets it
+        x *= 1 + 2.0 ** -7                              # values between of more bits than one part holds, rests of either sign
+        a *= 1 + 2.0 ** -6 * (np.arange(64) % 2)
+
+    _infinite_case(env, T, rank, max_rank, kind, T + rank, spoil)
+
+
+@pytest.mark.parametrize("T", [20, 1300])
+def test_lora_infinite_columns_leave_the_others(env, T):
+    """Columns and tokens that an infinite value does not reach keep their bits."""
+    q, torch, dev = env
+    x, a, b = (torch.randn(s, device=dev).to(torch.bfloat16) for s in ((T, 200), (30, 200), (30, 104)))
+    ids = np.arange(T) % 2
+    ys = []
+    for bad in (False, True):
+        if bad:
+            b[3, 17], x[4, 0] = math.inf, math.nan
+        y = torch.ones((T, 104), device=dev)
+        _call(env, ids, [(0, 12), (12, 18)], [1.0, 0.5], x, a, b, y, 32)
+        ys.append(y)
+    keep = torch.ones((T, 104), dtype=torch.bool, device=dev)
+    keep[::2, 17] = False
+    keep[4] = False
+    assert torch.equal(ys[0][keep], ys[1][keep]) and not bool(torch.isfinite(ys[1][::2, 17]).any()) and bool(torch.isnan(ys[1][4]).all())
+    assert not bool(torch.isnan(ys[1][::2, 17]).sum() > 1)
