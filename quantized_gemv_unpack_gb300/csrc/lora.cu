@@ -939,8 +939,7 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
     for (int j = 0; j < tiles;) {
       const int first = base + j++;
       const int4 tile = a.tiles[first];
-      if (tile.z == 0) break;
-      if (!tile_fits(a, tile)) continue;                           // reported by the first kernel, as is a bad adapter
+      if (!tile_fits(a, tile)) continue;                           // an empty entry, or reported by the first kernel, as is a bad adapter
       const int row0 = a.table[2 * tile.x], r = a.table[2 * tile.x + 1];
       float scale = 1.f;                                      // 16-bit y: the finished values have it
       if constexpr (F32) scale = a.scale[tile.x];

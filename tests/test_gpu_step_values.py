@@ -263,3 +263,34 @@ def test_lora_infinite_columns_leave_the_others(env, T):
     keep[4] = False
     assert torch.equal(ys[0][keep], ys[1][keep]) and not bool(torch.isfinite(ys[1][::2, 17]).any()) and bool(torch.isnan(ys[1][4]).all())
     assert not bool(torch.isnan(ys[1][::2, 17]).sum() > 1)
+
+
+@pytest.mark.parametrize("T,N", [(40, 300), (1100, 300), (2100, 300), (40000, 1100)])
+def test_lora_empty_entries_inside_a_list(env, T, N):
+    """An entry of no tokens is passed over, wherever it stands, by every kernel alike."""
+    q, torch, dev = env
+    x, a, b = (torch.randn(s, device=dev).to(torch.bfloat16) for s in ((T, 128), (20, 128), (20, 1104)))
+    b = b[:, :N]
+    ids = np.minimum(np.arange(T) // 16, 2)
+    want, y = torch.ones((T, N), device=dev), torch.ones((T, N), device=dev)
+    call, plan = _call(env, ids, [(0, 8), (8, 5), (13, 7)], [1.0, 0.5, 2.0], x, a, b, want, 16)
+    call.tasks[0].y = y.data_ptr()
+    used = int((plan.tiles[:, 2] > 0).sum())
+    assert used > 2
+    if used == plan.tiles.shape[0]:                     # no room for an empty one: the list's last is left out, and its tokens
+        used -= 1
+    t, n, o = plan.tiles[used - 1:used, 1:3].sum(), used, plan.order.long()
+    gone = o[int(t):]
+    gone = gone[gone >= 0]
+    for at in (0, 1, 2):
+        y.fill_(1)
+        moved = torch.cat([plan.tiles[:at], torch.zeros_like(plan.tiles[:1]), plan.tiles[at:n], torch.zeros_like(plan.tiles[n + 1:])])
+        keep = plan.tiles.clone()
+        plan.tiles.copy_(moved)
+        call.run()
+        torch.cuda.synchronize()
+        plan.tiles.copy_(keep)
+        left = want.clone()
+        left[gone] = 1
+        assert torch.equal(y, left), at
+    assert q.qmv_check_status() == 0
