@@ -294,3 +294,63 @@ def test_lora_empty_entries_inside_a_list(env, T, N):
         left[gone] = 1
         assert torch.equal(y, left), at
     assert q.qmv_check_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 20, 1300])
+@pytest.mark.parametrize("rank", [1, 16, 30, 64, 128])
+def test_lora_values_between_keep_their_bits(env, T, rank):
+    """fp32 y: the values between the products have 24 bits, of which three bf16 parts keep all. One rank row of each adapter is at work, B is +-1 there:
+    y is the value itself."""
+    q, torch, dev = env
+    g = np.random.default_rng(T + rank)
+    K, N = 256, 96
+    at = g.integers(0, rank, 2)                         # the rank rows at work
+    a, b = np.zeros((2 * rank, K)), g.standard_normal((2 * rank, N))
+    for i in range(2):
+        # bytes with their upper bit set at three places of x: sums of whole numbers below 2^24, exact in any order
+        a[i * rank + at[i], [3, 100, 250]] = g.integers(128, 256, 3)
+        b[i * rank + at[i]] = g.choice([-1.0, 1.0], N)
+    x = np.zeros((T, K))
+    x[:, [3, 100, 250]] = [65536.0, 256.0, 1.0]
+    x *= g.choice([0.25, 1.0, 2.0], (T, 1))
+    ids = np.arange(T) % 2
+    t = lambda v: torch.from_numpy(v).to(torch.bfloat16).to(dev)  # noqa: E731
+    y = torch.zeros((T, N), device=dev)
+    _call(env, ids, [(0, rank), (rank, rank)], [1.0, 1.0], t(x), t(a), t(b), y, rank)
+    h = np.array([a[i * rank + at[i]] @ x[k] for k, i in enumerate(ids)])
+    two = torch.from_numpy(h).to(torch.bfloat16).double()
+    two += (torch.from_numpy(h) - two).to(torch.bfloat16).double()
+    # a matrix product may cut what it adds at two bits below an fp32 sum's last: 2^-22. Two parts would be off by more.
+    assert np.all(np.abs(_f64(y) - h[:, None] * b[ids * rank + at[ids]]) <= 2.0 ** -22 * h[:, None])
+    assert T == 1 or np.max(np.abs(two.numpy() - h) / h) > 2.0 ** -22
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,A,pool,K,N,rank", [(70, 6, 6, 13824, 5120, 128), (1300, 4, 4, 5120, 13824, 64), (3, 2, 2, 5120, 13824, 16),
+                                               (2000, 5, 512, 512, 1499, 16), (4100, 5, 1024, 256, 520, 24), (50, 5, 1024, 4096, 4096, 16)])
+def test_lora_of_large_sizes_and_pools(env, kind, T, A, pool, K, N, rank):
+    """Projections of a large model, and pools of many more adapters than a step uses, on which the kernels' choice goes."""
+    q, torch, dev = env
+    g = torch.Generator(device=dev).manual_seed(T)
+    new = lambda *s: torch.randn(s, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    x, a, b = new(T, K), new(pool * rank, K), new(pool * rank, (N + 7) // 8 * 8)[:, :N]
+    y0 = (torch.randn((T, N), generator=g, device=dev) * 30).to(_type(torch, kind))
+    used = torch.randperm(pool, generator=g, device=dev)[:A].cpu().numpy()
+    ids = used[np.sort(np.arange(T) * 7919 % A)]
+    ranks = np.where(np.arange(pool) % 3 == 1, max(1, rank - 5), rank)
+    table, scale = np.stack([np.arange(pool) * rank, ranks], 1), 0.5 + np.arange(pool) % 4
+    y = y0.clone()
+    _call(env, ids, table, scale, x, a, b, y, rank)
+    for i in used:
+        t = torch.from_numpy(np.flatnonzero(ids == i)).to(dev)
+        f, r = table[i]
+        A64, B64, X = a[f:f + r].double(), b[f:f + r].double(), x[t].double()
+        h = X @ A64.T
+        want = y0[t].double() + float(scale[i]) * (h @ B64)
+        s1, s2 = float(scale[i]) * ((X.abs() @ A64.abs().T) @ B64.abs()), float(scale[i]) * (h.abs() @ B64.abs())
+        # fp32 sums, each addition within a step (2^-23) of what is summed up: K / 16 matrix products with 16 additions inside and 16 joins, then
+        # rank / 16 times three of them; two parts leave 2^-17 of the values between, three nothing; y once more and to its type
+        bound = (K / 16 + 32) * 2.0 ** -23 * s1 + (3 * 8 + 16 + 2) * 2.0 ** -23 * s2 + (0 if kind == "f32" else 2.0 ** -17) * s2
+        bound += (2.0 ** -24 + (0 if kind == "f32" else 2.0 ** -8)) * (want.abs() + bound)
+        assert bool(((y[t].double() - want).abs() <= bound).all())
+    assert q.qmv_check_status() == 0
