@@ -6,10 +6,13 @@
 // give lse = scale M + ln S and the entropy ln S - ln 2 U / S. Partial results of
 // threads, warps and blocks join by S = sum S_p 2^D_p, U = sum (U_p + D_p S_p) 2^D_p,
 // D_p their M less the largest. d is one fused multiply-add from the rounded product
-// M scale log2 e, and what the rounding took is put back into ln S. That is a part of every
-// d, the largest value's own among them, and half a step of the product: from products of
-// 2^32 on it would take powers past fp32's range. So beyond 2^20 (a finite mask, a row
-// of its type's lowest value) the difference comes first; up to there it is 2^-4 at most.
+// M scale log2 e, and what the rounding took is put back into the results. That is a part of
+// every d, the largest value's own among them, and up to half a step of the product: with
+// products of 2^32 and more it would take powers past fp32's range. So from 2^31 on (a mask of
+// -1e10, a row of its type's lowest value) the difference comes first, which is slower; up to
+// there it is at most 2^6, and a mask of -1e9 keeps to the fast path (1000 rows of 131072
+// values bf16, all but one in a thousand masked so: 58 us, 84 where the difference is taken
+// from 2^20 on).
 //
 // The top k (k <= 32) come from the threads' largest values: at least k values of a block reach the k-th of its threads'
 // maxima, and hardly more do. So the pass keeps maxima alone, of each thread and of up to 32 parts of what it reads, and
@@ -90,7 +93,7 @@ struct Scale {
     return plain(m) ? fmaf(v, scale2, -pm) : plain(v) ? -fmaf(m, scale2, -pv) : half_difference(v, m) * (2.f * scale2);
   }
 };
-constexpr float kPlainProduct = 1048576.f;   // 2^20
+constexpr float kPlainProduct = 2147483648.f;   // 2^31
 
 // The sum of the lanes' parts, in every lane.
 __device__ __forceinline__ Sums join(Sums t, const Scale& k) {
@@ -242,7 +245,7 @@ struct Vec16 {
 };
 template <>
 struct Vec<__nv_bfloat16> : Vec16<__nv_bfloat16, __nv_bfloat162> {
-  static constexpr float kMost = INFINITY;                  // 2^20 / 0.05 is far enough from -1e30
+  static constexpr float kMost = INFINITY;                  // 2^31 / 0.05 is far enough from -1e30
   static __device__ __forceinline__ void values(const uint4& w, float (&v)[8]) {
     const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -641,9 +644,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   if (warp != 0) return;
   t = total;
   ahead = total_ahead;
-  const float log_s = logf(t.s);
-  // the sum against the value itself: what the product's rounding took is put back
-  const float ln_s = scale.plain(t.m) ? fmaf(-kLn2, fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)), log_s) : log_s;
+  // the sums against the value itself: what the product's rounding took is put back, its whole part exactly
+  const float rest = scale.plain(t.m) ? fmaf(t.m, a.scale2, -__fmul_rn(t.m, a.scale2)) : 0.f, whole = rintf(rest);
+  const float ln_s = fmaf(-kLn2, rest - whole, logf(ldexpf(t.s, -(int)whole)));
   const bool none = t.s == 0.f;                             // every value is -inf
   const auto log_p = [&](float v) {
     if (none) return -INFINITY;
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprob_kernel(const 
   };
   if (lane == 0) {
     if (a.lse) a.lse[row] = none ? -INFINITY : fmaf(t.m, a.scale, ln_s);
-    if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kLn2, t.u / t.s, log_s);
+    if (a.entropy) a.entropy[row] = none ? 0.f : fmaf(-kLn2, t.u / t.s - rest, ln_s);
     if (a.logprob) a.logprob[row] = token < 0 ? 0.f : log_p(given);
     if (a.rank) a.rank[row] = token < 0 ? -1 : ahead;
   }

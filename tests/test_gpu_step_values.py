@@ -59,12 +59,15 @@ def _logprob_rows(env, rows, kind, scale, tokens, top, copies):
     xv, scale = _f64(x[:n]), float(np.float32(scale))
     for i in range(n):
         lse, h, lp, best, at, rank = _logprob(xv[i], scale, tokens[i], top)
-        # fp32: a power 2^d, d = (x - m) scale log2 e, is off by 3 steps of 2^-24 |d| (difference, product, constant) and by 2^-22 (exp2), and
-        # by 2^-27 (what the maximum's product was rounded by, up to 2^-4, is a part of d). A sum of n = V / 256 + 64 terms in a row by
-        # n 2^-24. Weighted by p, |d| is at most log2 V + 1. Then the last sums and products, each within 2^-24 of the result or of ln S.
-        bits = math.log2(V) + 1
-        rel = 2.0 ** -22 + 2.0 ** -27 + (V / 256 + 64) * 2.0 ** -24 + 3 * 2.0 ** -24 * bits
-        pairs = [(float(call.lse[i]), lse, rel), (float(call.logprob[i]), lp, rel), (float(call.entropy[i]), h, 3 * rel * bits)]
+        # fp32: a power 2^d, d = (x - m) scale log2 e, is off by 3 steps of 2^-24 |d| (difference, product, constant) and by 2^-22 (exp2). Where d is
+        # taken from the rounded product P of the maximum it has what the rounding took, r <= P 2^-24, in it: another step of 2^-24 |d|, since
+        # values that differ from the maximum are at least as far from it. A sum of n = V / 256 + 64 terms in a row is off by n 2^-24, the
+        # entropy's by that of r too, which is at most 2^6. Weighted by p, |d| is at most log2 V + 1. Then the last sums and products, each
+        # within 2^-24 of the result or of ln S.
+        n_sum, bits = V / 256 + 64, math.log2(V) + 1
+        rel = 2.0 ** -22 + n_sum * 2.0 ** -24 + 4 * 2.0 ** -24 * bits
+        rest = min(2.0 ** 6, abs(float(xv[i].max())) * scale * math.log2(math.e) * 2.0 ** -24)
+        pairs = [(float(call.lse[i]), lse, rel), (float(call.logprob[i]), lp, rel), (float(call.entropy[i]), h, 3 * rel * bits + n_sum * 2.0 ** -24 * rest)]
         pairs += [(float(call.top_logprob[i, j]), best[j], rel) for j in range(top)]
         for k, (got, want, off) in enumerate(pairs):
             if abs(want) < 3.4e38:
@@ -111,14 +114,15 @@ def test_logprob_of_large_finite_values(env, kind, scale, V, copies):
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("scale", [1.0, 0.4, 1e5])
 @pytest.mark.parametrize("copies", [1, 40])
-def test_logprob_across_the_plain_bound(env, kind, scale, copies):
-    """Values on both sides of where the maximum's product is 2^20 (and of half and twice it), in orders that cross it inside a thread, a warp and a block."""
+@pytest.mark.parametrize("bound,reach", [(20, 30.0), (24, 60.0), (27, 300.0), (31, 3000.0)])
+def test_logprob_across_the_plain_bound(env, kind, scale, copies, bound, reach):
+    """Values on both sides of where the maximum's product is 2^bound (and of half and twice it), in orders that cross it inside a thread, a warp and a block."""
     V = 9001
     g = np.random.default_rng(3)
-    at = 2.0 ** 20 / (scale * math.log2(math.e))
+    at = 2.0 ** bound / (scale * math.log2(math.e))
     rows = []
     for centre in (at, -at, 2 * at, -2 * at, at / 2):
-        up = centre + np.linspace(-30.0, 30.0, V) / scale
+        up = centre + np.linspace(-reach, reach, V) / scale
         rows += [up, up[::-1], g.permutation(up), np.where(g.random(V) < 0.5, up, -math.inf)]
     rows = np.stack(rows)
     if kind == "f16":
