@@ -738,20 +738,24 @@ int lora_plan(const lora_plan_args* args, void* stream);
  * scales, have one y_type, and must not write overlapping y ranges. x: bf16 [n_tokens][ldx], K
  * and ldx multiples of 8; y: [n_tokens][ldy] of y_type, as the projection left
  * it (rows of 16-byte alignment are fastest). n_tokens, n_adapters and max_tiles
- * are the plan's (entries past lora_max_tiles are not read). max_rank (up to QMV_LORA_MAX_RANK) bounds the ranks and
- * chooses the kernel; an adapter may have rank 0.
- * Products are exact and sums fp32; the r values between the two products are
- * rounded to 2^-27 of themselves for an fp32 y (three bf16 parts) and to 2^-18
- * for the others, and y once. The result is reproducible bit for bit. A token's
+ * are the plan's (entries past lora_max_tiles are not read). max_rank (up to
+ * QMV_LORA_MAX_RANK) bounds the ranks and chooses the kernel; an adapter may
+ * have rank 0. n_adapters chooses it too, with n_tokens: long prompts of a few
+ * adapters out of a large pool are served fastest with a table of those few.
+ * Products are exact and sums fp32; the r values between the two products keep
+ * their 24 bits for an fp32 y (three bf16 parts) and are rounded to 2^-17 of
+ * themselves for the others, and y once. Infinities and NaN in x, A and B give
+ * what the formula gives. The result is reproducible bit for bit. A token's
  * does not depend on the values, the adapters or the places of the others, but
  * the sizes of the call (n_tokens, n_adapters, max_rank, the tasks)
  * choose in which order sums over K are formed.
  * A tile, place or adapter outside its array, a rank over max_rank or rows
  * outside the pool set QMV_ERR_CORRUPT in the device error word, and that tile
- * (or place) is left out.
+ * (or place) is left out. An entry of no tokens is passed over.
  * workspace: device, 16-byte aligned, lora_workspace_size(n_tokens, n_adapters,
  * max_rank, n_tasks) bytes, which is 0 where the call needs none (below
- * 1280 tokens, or 64 per adapter). It needs no clearing; calls that overlap on the GPU need one each.
+ * 1280 tokens, or 64 per adapter). It needs no clearing; calls that overlap on
+ * the GPU need one each.
  */
 typedef struct {
   const void* a;             /* bf16 [pool_rows][lda] */
@@ -792,8 +796,9 @@ int lora_run(const lora_args* args, const lora_task* tasks, int n_tasks, void* s
  * probability 0 (a masked token); a row of nothing else has lse and log
  * probabilities -inf and entropy 0. A NaN or +inf in a row makes its lse,
  * entropy and log probabilities NaN; its order stands.
- * Sums are fp32, taken against the row's largest value. The result is
- * reproducible bit for bit.
+ * Sums are fp32, taken against the row's largest value. Finite values may have
+ * any magnitude, masks of -1e10 or of the type's lowest value among them; results
+ * past fp32's range are infinite. The result is reproducible bit for bit.
  */
 #define QMV_LOGPROB_MAX_V 16777216
 #define QMV_LOGPROB_MAX_TOP 32

@@ -761,7 +761,8 @@ class Lora:
     """lora_run: each token's adapter added to the outputs of projections that share x [tokens][K] (bf16). table [adapters][2]
     (int32): an adapter's first rank row and its rank; scale [adapters] (fp32). tasks: (a, b, y) per projection: the pools of
     rank rows a [rows][K] and b [rows][N] (bf16), and y [tokens][N], to which the projection has written. max_rank bounds
-    the ranks in the table; a lower bound gives a leaner kernel. The plan's run() comes first, once per step. Calls of many
+    the ranks in the table; a lower bound gives a leaner kernel. Long prompts of a few adapters of a large pool are served fastest
+    with a plan and a table of those few. The plan's run() comes first, once per step. Calls of many
     tokens need a workspace of lora_workspace_size bytes: one is made where none is given; layers of one stream should share it
     (its `workspace`)."""
 
@@ -811,7 +812,7 @@ class Lora:
 
 
 class LogProb:
-    """logprob_run: log probabilities of logits [rows][V] (fp32, bf16 or fp16), times scale. run() fills lse and entropy
+    """logprob_run: log probabilities of logits [rows][V] (fp32, bf16 or fp16, the first row on 16 bytes), times scale. run() fills lse and entropy
     [rows], with tokens [rows] (int32) logprob and rank [rows], with top (up to 32) top_index and top_logprob [rows][top]."""
 
     def __init__(self, logits, tokens=None, top: int = 0, scale: float = 1.0):

@@ -17,12 +17,13 @@
 // * second product: a lane's 8 bytes of a row of B are four consecutive n of one rank row; two rows zipped by byte permutes
 //   are the pairs of four n8 blocks, so that a lane's sums are two runs of four columns of y (fp32), or one of eight (16 bits).
 // The r values between the products are fp32 sums, handed on as bf16 parts, each the rounding of what the ones before it have
-// left: three for an fp32 y (2^-27 of the value is lost at most, less than an fp32 sum's own rounding), two for a 16-bit y
-// (2^-18, where y itself is rounded to 2^-9 or 2^-12). One part would put 2^-9 of the adapter's whole product on y.
+// left: three for an fp32 y, which hold all 24 bits, two for a 16-bit y, which leave 2^-17 (what the first leaves is below 2^-8 of the
+// value's power of two, and rounded by half a step of at most 2^-17), where y itself is rounded to 2^-8 or 2^-11. One part would put
+// 2^-8 of the adapter's whole product on y.
 //
-// Measured, us per call in a stream of calls (bytes that have to be moved, at their rate): one token of rank 16, K = N = 4096 4.6;
-// 64 tokens of 48 adapters of ranks up to 64, K 5120, q|k|v 26 (75 MB, 2.9 TB/s); 80 of 12, rank 16, gate|up 12.1 (33 MB, 2.8 TB/s);
-// 1023 of 24, ranks up to 128, K 13824, N 5120 53 (137 MB, 2.6 TB/s); 8190 of 5, rank 64, gate|up, bf16 189 (918 MB, 4.9 TB/s).
+// Measured, us per call in a stream of calls (bytes that have to be moved, at their rate): one token of rank 16, K = N = 4096 5.1;
+// 64 tokens of 48 adapters of ranks up to 64, K 5120, q|k|v 26 (75 MB, 2.9 TB/s); 80 of 12, rank 16, gate|up 12.6 (33 MB, 2.6 TB/s);
+// 1023 of 24, ranks up to 128, K 13824, N 5120 57 (137 MB, 2.4 TB/s); 8190 of 5, rank 64, gate|up, bf16 188 (918 MB, 4.9 TB/s).
 #include <type_traits>
 
 #include "cluster.cuh"
@@ -321,8 +322,9 @@ __device__ __forceinline__ float most(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-// Few tokens: a lane's sums of the second product that are NaN, once more, value by value: rank rows j < r of b, from the lane's first column on, with the
-// parts of rows g and g + 8 as the fragments have them.
+// Few tokens: a lane's sums of the second product that are NaN, once more, value by value: rank rows j < r of b, from the lane's first
+// column on, with the parts of rows g and g + 8 as the fragments have them. One look at the sums per step of 32 columns costs a token
+// of rank 16 (K = N = 4096) 0.1 of 5.1 us.
 template <int Y, int P3>
 __device__ __noinline__ void sums_again(float* d, const uint4* frag, const __nv_bfloat16* b, int64_t ldb, int r, int cols, int lane) {
   const uint32_t* parts = reinterpret_cast<const uint32_t*>(frag);
@@ -346,16 +348,19 @@ __device__ __noinline__ void sums_again(float* d, const uint4* frag, const __nv_
   }
 }
 
-// Many tokens: in B's registers +-1 stands for a value that is not finite, so that an infinite value between keeps its sign,
+// Many tokens: in B's registers +-1 stands for a value that is not finite, so that an infinite value between keeps its sign, and what
+// it stands for is added to y afterwards (B with 0 in its place beside B itself, for the later parts, took registers that the
+// second kernel does not have: 4096 tokens, rank 128, fp32 169 -> 206 us).
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
   if ((w & 0x7F80u) == 0x7F80u) w = (w & 0xFFFF8000u) | 0x3F80u;
   if ((w & 0x7F800000u) == 0x7F800000u) w = (w & 0x8000FFFFu) | 0x3F800000u;
   return w;
 }
-// and what it stands for is added to y afterwards. A lane's column, of `count` tokens whose rows of y are row_y bytes away; values: the
-// finished values of the run, KS * P3 * 32 words for each 16 tokens.
+// A lane's column, of `count` tokens whose rows of y are row_y bytes away; values: the finished values of the run, KS * P3 * 32 words for
+// each 16 tokens.
 template <int Y, int KS, int P3>
-__device__ __noinline__ void add_infinite(char* y, const int64_t* row_y, int count, const uint4* values, const __nv_bfloat16* b, int64_t ldb, int r, float scale) {
+__device__ __noinline__ void add_infinite(char* y, const int64_t* row_y, int count, const uint4* values, const __nv_bfloat16* b, int64_t ldb,
+                                          int r, float scale) {
   const uint32_t* parts = reinterpret_cast<const uint32_t*>(values);
   for (int j = 0; j < r; ++j) {
     const float w = __bfloat162float(b[j * ldb]);
@@ -386,7 +391,8 @@ __device__ __noinline__ void add_infinite(char* y, const int64_t* row_y, int cou
 // copies just what its own fragments need, so a step needs no barrier of the block (B in pieces of 16 bytes, which a lane
 // shares with others of its warp: 64 tokens of 48 adapters 26 us, with 8-byte pieces of its own 30).
 // Bound by a unit's chain: its tile, table and tokens (1.1 us), the first loads, the meeting (2.5 us) and the steps, two or
-// three of which a warp has in flight; beyond 16 tokens per adapter also by L2, from which every tile reads its rank rows again. NB blocks of eight rank rows (the call's largest rank).
+// three of which a warp has in flight; beyond 16 tokens per adapter also by L2, from which every tile reads its rank rows again. NB blocks
+// of eight rank rows (the call's largest rank).
 template <int NB, int Y>
 struct Short {
   static constexpr bool F32 = Y == QMV_F32;
@@ -933,7 +939,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
     while (slice >= (a.t[task].N + 255) / 256) slice -= (a.t[task++].N + 255) / 256;
     const Task& t = a.t[task];
     const int base = unit / a.slices * a.window2, tiles = min(a.window2, a.max_tiles - base);
-    const int n0 = slice * 256 + warp * 32, n = n0 + own_column<Y>(t4), col = n0 + block_column<Y>(g);   // this warp's columns; the first of this lane's sums, and of its loads of B
+    // this warp's columns; the first of this lane's sums, and of its loads of B
+    const int n0 = slice * 256 + warp * 32, n = n0 + own_column<Y>(t4), col = n0 + block_column<Y>(g);
     const bool whole = t.wide && (F32 ? n0 + 32 : n + 8) <= t.N;
     char* y = static_cast<char*>(t.y);
     for (int j = 0; j < tiles;) {
@@ -1101,7 +1108,8 @@ __global__ void __launch_bounds__(kLoraThreads, NB > 8 || Y == QMV_F32 ? 2 : 3) 
       copies_wait();
       if (!finite) {
         __syncwarp();                                         // the warp's rows of y are written
-        if (n0 + lane < t.N) add_infinite<Y, KS, P3>(y + (int64_t)(n0 + lane) * size, row_y, count, values, t.b + (int64_t)row0 * t.ldb + n0 + lane, t.ldb, r, scale);
+        if (n0 + lane < t.N)
+          add_infinite<Y, KS, P3>(y + (int64_t)(n0 + lane) * size, row_y, count, values, t.b + (int64_t)row0 * t.ldb + n0 + lane, t.ldb, r, scale);
       }
     }
   }
@@ -1239,10 +1247,10 @@ int lora_run(const lora_args* g, const lora_task* tasks, int n_tasks, void* stre
   if (!many_tokens(g->n_tokens, g->n_adapters)) {
     int rc = kernel_fit(c.few, kLoraThreads, c.few_smem, &per_sm);
     if (rc) return rc;
-    // A unit is 16 tokens of a tile and a projection. Few units are cut into eight blocks each, as long as all are resident at once; more of them into four, up to two rounds, or
-    // two, since a unit has two meetings of its cluster whatever its size. us with 8, 4 and 2: 80 tokens of 12 adapters, rank 16,
-    // gate|up 11.9, 12.7, 20.1; 512 of 8, rank 64, gate|up 57, 41, 48; 64 of 48, rank 64, q|k|v 33.0, 24.4, 27.7; 1000 of one, rank 64,
-    // gate|up 89, 79, 73; 1023 of 8, rank 32, q|k|v 51, 33, 27.
+    // A unit is 16 tokens of a tile and a projection. Few units are cut into eight blocks each, as long as all are resident at once;
+    // more of them into four, up to two rounds, or two, since a unit has two meetings of its cluster whatever its size. us with 8, 4
+    // and 2: 80 tokens of 12 adapters, rank 16, gate|up 11.9, 12.7, 20.1; 512 of 8, rank 64, gate|up 57, 41, 48; 64 of 48, rank 64,
+    // q|k|v 33.0, 24.4, 27.7; 1000 of one, rank 64, gate|up 89, 79, 73; 1023 of 8, rank 32, q|k|v 51, 33, 27.
     const int64_t blocks = (int64_t)sm_count() * per_sm;
     // Counted without the units that are empty because a tile of 64 tokens has fewer.
     const int64_t full = (g->n_tokens / 16 + (int64_t)(g->n_tokens < g->n_adapters ? g->n_tokens : g->n_adapters)) * n_tasks;
